@@ -75,8 +75,10 @@ typedef enum pa_dtype {
     PA_DTYPE_F32 = 0,
     PA_DTYPE_BF16 = 1,
     PA_DTYPE_FP8_E4M3 = 2,
-    PA_DTYPE_INT8 = 3 /* cache type only: int8 codes with one fp32 scale per (row, KV head);
-                         pa_reshape_and_cache_int8, pa_decode_int8 */
+    PA_DTYPE_INT8 = 3, /* cache type only: int8 codes with one fp32 scale per (row, KV head);
+                          pa_reshape_and_cache_int8, pa_decode_int8 */
+    PA_DTYPE_INT4 = 4  /* cache type only: 4-bit codes, two to a byte, with one bf16 pair
+                          (lo, s) per (row, KV head); pa_reshape_and_cache_int4, pa_decode_int4 */
 } pa_dtype;
 
 /* Bits the kernels OR into *error_word. */
@@ -84,6 +86,7 @@ typedef enum pa_dtype {
 #define PA_DEVERR_SLOT 0x2      /* a slot >= num_blocks * block_size */
 #define PA_DEVERR_CONTEXT 0x4   /* context_len < 0, or > max_context_len, or past the table */
 #define PA_DEVERR_TIMEOUT 0x8   /* a shared-memory barrier wait gave up after its limit */
+#define PA_DEVERR_POSITION 0x10 /* a position outside [0, max_position) (pa_norm_rope*) */
 
 /*
  * Append one K and one V row per token into the paged pool:
@@ -171,7 +174,10 @@ pa_status pa_decode_int8(const void* q, const void* k_cache, const void* v_cache
  * error; never blocks. For an INT8 cache (dtype PA_DTYPE_INT8) this copies
  * the codes; copy the row scales with a second call on the two scale arrays
  * viewed as fp32 pools of one KV head, one row and num_kv_heads * block_size
- * values per block (num_kv_heads * block_size a multiple of 4).
+ * values per block (num_kv_heads * block_size a multiple of 4). For an INT4
+ * cache (dtype PA_DTYPE_INT4, head_dim the number of dims, a multiple of 32)
+ * it copies the packed codes; the (lo, s) pairs, 4 bytes each, likewise take
+ * a second call as fp32 pools.
  */
 pa_status pa_copy_blocks(void* k_cache, void* v_cache, const int64_t* block_mapping,
                          int num_pairs, int num_kv_heads, int head_dim, int block_size,
@@ -461,6 +467,150 @@ pa_status pa_test_withhold_tile(const void* q, const void* k_cache, const void* 
                                 void* workspace, size_t workspace_bytes, int32_t* error_word,
                                 int withhold_tile, struct CUstream_st* stream);
 
+/*
+ * 4-bit caches. A row (one token, one KV head) of K or V holds head_dim codes
+ * c in 0..15, two to a byte (dim 2j in the low nibble of byte j, dim 2j + 1
+ * in its high nibble), and one pair (lo, s): the cached value is lo + s * c.
+ *   codes   uint8 [num_blocks][num_kv_heads][block_size][head_dim / 2]
+ *   params  bf16  [num_blocks][num_kv_heads][block_size][2], (lo, s)
+ * head_dim / 2 + 4 bytes a row: 0.27 of a bf16 cache's at head_dim 128.
+ * Codes and params are 16-byte aligned.
+ *
+ * pa_reshape_and_cache_int4 -- quantising append:
+ *   lo = min_d x[d] rounded down to bf16, s = (max_d x[d] - lo) / 15 rounded
+ *   up to bf16, c[d] = round_half_even((x[d] - lo) / s) clamped to 0..15
+ * for the new K row x = k_new[t][h] (and V), every difference and quotient in
+ * fp32 (IEEE); s = 0 (all x equal to lo) gives codes 0. The directed roundings
+ * keep every x inside [lo, lo + 15 s], so a value is off by at most s / 2
+ * (plus fp32 rounding). Rows must be finite with a finite max - lo; a row that
+ * is not gives unspecified codes and params for itself alone. new_dtype
+ * PA_DTYPE_F32 or PA_DTYPE_BF16; head_dim a multiple of 32, at most 256. Slots
+ * as in pa_reshape_and_cache.
+ */
+pa_status pa_reshape_and_cache_int4(const void* k_new, const void* v_new, pa_dtype new_dtype,
+                                    const int64_t* slot_mapping, void* k_cache, void* v_cache,
+                                    void* k_params, void* v_params, int num_tokens,
+                                    int num_kv_heads, int head_dim, int block_size,
+                                    int num_blocks, int32_t* error_word,
+                                    struct CUstream_st* stream);
+
+/*
+ * The cached rows of every sequence as plain values, one after another:
+ *   k_out[row_starts[s] + i][h][:] = lo + s * c of row i of sequence s, KV head h
+ * (same for V) for i < context_lens[s], an fp32 sum rounded to out_dtype
+ * (PA_DTYPE_F32 or PA_DTYPE_BF16). Attention over a prompt that is processed in
+ * chunks reads its earlier chunks this way. k_out, v_out: [num_rows]
+ * [num_kv_heads][head_dim]; row_starts: int64 [num_seqs]. Output rows that no
+ * sequence covers are left as they are. A context length outside
+ * [0, max_context_len], or rows outside [0, num_rows), flag
+ * PA_DEVERR_CONTEXT and leave that sequence's rows out; a block-table entry
+ * outside the pool flags PA_DEVERR_BLOCK_ID and leaves that block's rows out.
+ * Sequences whose output rows overlap race. Any block_size >= 1; head_dim a
+ * multiple of 32, at most 256. No workspace.
+ */
+pa_status pa_gather_int4(const void* k_cache, const void* v_cache, const void* k_params,
+                         const void* v_params, const int32_t* block_tables,
+                         const int32_t* context_lens, const int64_t* row_starts, void* k_out,
+                         void* v_out, pa_dtype out_dtype, int64_t num_rows, int num_seqs,
+                         int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                         int max_blocks_per_seq, int max_context_len, int32_t* error_word,
+                         struct CUstream_st* stream);
+
+/*
+ * Decode attention over a 4-bit cache, bf16 q and out. num_queries (Q) new
+ * tokens per sequence, the last Q of its n = context_lens[s] rows (1: plain
+ * decode); query token j sits at row n - Q + j and attends to the rows
+ * i <= n - Q + j, with window > 0 only to the last `window` of them
+ * (i > n - Q + j - window; 0: all):
+ *   out[s][j][qh][:] = sum_i softmax_i(scale * <q[s][j][qh], K_i>) * V_i[:]
+ * q, out: [num_seqs][num_queries][num_heads][head_dim]. n == 0 gives zero
+ * rows; 0 < n < Q is flagged PA_DEVERR_CONTEXT (those rows are left as they
+ * are). Scores, softmax and sums are fp32; q is held in f16 (exactly, but for
+ * elements more than 2^20 below their head's largest), a probability times its
+ * row's s is rounded to f16 once. Partitions of 512 rows merged as in
+ * pa_decode: a sequence's result does not depend on the rest of the batch.
+ * Workspace: pa_decode_workspace_size_multi(num_seqs, num_queries, num_heads,
+ * head_dim, max_context_len) bytes, used as in pa_decode. Supported: head_dim
+ * 64 or 128, block_size a multiple of 16, (num_heads / num_kv_heads) *
+ * num_queries <= 8 (else PA_ERR_UNSUPPORTED).
+ */
+pa_status pa_decode_int4(const void* q, const void* k_cache, const void* v_cache,
+                         const void* k_params, const void* v_params, const int32_t* block_tables,
+                         const int32_t* context_lens, float scale, int window, void* out,
+                         int num_seqs, int num_queries, int num_heads, int num_kv_heads,
+                         int head_dim, int block_size, int num_blocks, int max_blocks_per_seq,
+                         int max_context_len, void* workspace, size_t workspace_bytes,
+                         int32_t* error_word, struct CUstream_st* stream);
+
+/*
+ * Norms of queries and keys for each head, and the rotation by position, in
+ * one pass: for every token t and every q head (and K head, with k_weight)
+ *   y = x * (mean_d x[d]^2 + eps)^(-1/2) * (weight[d] + weight_offset)
+ *       (a null weight: y = x),
+ *   pair i < rot_dim / 2 of y is turned by its angle:
+ *       (a, b) -> (a cos - b sin, b cos + a sin),
+ *       (a, b) = (y[i], y[i + rot_dim / 2]), or with interleaved != 0
+ *       (y[2 i], y[2 i + 1]);
+ *       cos = cos_sin[p][i], sin = cos_sin[p][rot_dim / 2 + i],
+ *       p = positions[pair_axis[i]][t];
+ *   dims past rot_dim are not turned.
+ * All in fp32, rounded once to dtype on the way out.
+ */
+typedef struct pa_norm_rope_args {
+    const void* q;            /* dtype [num_tokens][num_heads][head_dim] */
+    const void* k;            /* dtype [num_tokens][num_kv_heads][head_dim] */
+    int64_t q_stride;         /* elements from a token's q (k) to the next token's, at least */
+    int64_t k_stride;         /*   heads * head_dim: parts of a fused projection fit as they are */
+    void* q_out;              /* dtype, like q; q itself with q_stride works in place */
+    int64_t q_out_stride;
+    const void* q_weight;     /* weight_dtype [head_dim], null: no norm of q */
+    const void* k_weight;     /* weight_dtype [head_dim], null: no norm of k */
+    float eps;                /* >= 0 and finite */
+    float weight_offset;      /* added to the weights: 0, or 1 where weights are kept around 0 */
+    const float* cos_sin;     /* fp32 [max_position][rot_dim]: rot_dim / 2 cosines, then sines */
+    const int32_t* positions; /* [num_axes][num_tokens] */
+    const uint8_t* pair_axis; /* HOST memory, read during the call: rot_dim / 2 axis numbers
+                                 < num_axes (time, height, width for images and video);
+                                 null: every pair turns by axis 0 */
+    int num_tokens, num_heads, num_kv_heads, head_dim;
+    int rot_dim;              /* 0..head_dim, a multiple of 16; 0: no rotation (cos_sin,
+                                 positions and pair_axis unused) */
+    int max_position;
+    int num_axes;             /* 1..4 */
+    int interleaved;
+    int dtype;                /* PA_DTYPE_F32 or PA_DTYPE_BF16: q, k, v and the outputs */
+    int weight_dtype;         /* PA_DTYPE_F32 or PA_DTYPE_BF16 */
+} pa_norm_rope_args;
+
+/*
+ * pa_norm_rope writes the q rows to q_out and the K rows to k_out (in place
+ * where k_out is k, with k_stride). pa_norm_rope_append writes the K rows into
+ * their slots of a paged pool of `dtype`, with V beside them (a bit copy of
+ * v, v_stride elements between tokens). pa_norm_rope_append_int4 rounds the K
+ * rows to dtype and quantises them and V into a 4-bit cache: codes and params
+ * are those of pa_norm_rope followed by pa_reshape_and_cache_int4.
+ * Slots as in pa_reshape_and_cache (q is written whatever the slot). A token
+ * with a position outside [0, max_position) on any axis is flagged
+ * PA_DEVERR_POSITION; nothing of it is written.
+ * head_dim a multiple of 16 (of 32 for the 4-bit cache), at most 256; every
+ * buffer 16-byte aligned, positions 4-byte, and strides multiples of 16 bytes
+ * (else PA_ERR_INVALID_ARG). Apart from the in-place uses outputs must not
+ * overlap inputs.
+ */
+pa_status pa_norm_rope(const pa_norm_rope_args* args, void* k_out, int64_t k_out_stride,
+                       int32_t* error_word, struct CUstream_st* stream);
+
+pa_status pa_norm_rope_append(const pa_norm_rope_args* args, const void* v, int64_t v_stride,
+                              const int64_t* slot_mapping, void* k_cache, void* v_cache,
+                              int block_size, int num_blocks, int32_t* error_word,
+                              struct CUstream_st* stream);
+
+pa_status pa_norm_rope_append_int4(const pa_norm_rope_args* args, const void* v,
+                                   int64_t v_stride, const int64_t* slot_mapping, void* k_cache,
+                                   void* v_cache, void* k_params, void* v_params, int block_size,
+                                   int num_blocks, int32_t* error_word,
+                                   struct CUstream_st* stream);
+
 /* Human-readable name of a status. Never NULL. */
 const char* pa_status_string(pa_status status);
 
@@ -471,7 +621,7 @@ pa_status pa_check_error_word(int32_t error_word_value);
 int pa_version(void);
 
 /* Rows per split-K partition the decode calls use for a cache of this type
- * when none is requested: 512 for fp32, bf16 and INT8, 1024 for FP8 (the same
+ * when none is requested: 512 for fp32, bf16, INT8 and INT4, 1024 for FP8 (the same
  * bytes per partition as 512 bf16 rows). 0 for a type no cache holds. The
  * workspace size functions assume 512, which covers every case. */
 int pa_default_partition_size(pa_dtype cache_dtype);

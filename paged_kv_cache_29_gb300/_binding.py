@@ -28,6 +28,7 @@ PA_DEVERR_BLOCK_ID = 0x1
 PA_DEVERR_SLOT = 0x2
 PA_DEVERR_CONTEXT = 0x4
 PA_DEVERR_TIMEOUT = 0x8
+PA_DEVERR_POSITION = 0x10
 
 KERNELS = {"auto": 0, "simt": 1, "mma": 2, "generic": 3, "tc": 4}
 DEFAULT_PARTITION = 512
@@ -45,6 +46,21 @@ class PagedAttentionError(RuntimeError):
 class _Options(ctypes.Structure):
     _fields_ = [("kernel", ctypes.c_int), ("partition_size", ctypes.c_int),
                 ("long_partition_size", ctypes.c_int), ("long_partition_from", ctypes.c_int)]
+
+
+class _NormRopeArgs(ctypes.Structure):
+    """pa_norm_rope_args."""
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("q_stride", ctypes.c_int64),
+                ("k_stride", ctypes.c_int64), ("q_out", ctypes.c_void_p),
+                ("q_out_stride", ctypes.c_int64), ("q_weight", ctypes.c_void_p),
+                ("k_weight", ctypes.c_void_p), ("eps", ctypes.c_float),
+                ("weight_offset", ctypes.c_float), ("cos_sin", ctypes.c_void_p),
+                ("positions", ctypes.c_void_p), ("pair_axis", ctypes.c_char_p),
+                ("num_tokens", ctypes.c_int), ("num_heads", ctypes.c_int),
+                ("num_kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("rot_dim", ctypes.c_int), ("max_position", ctypes.c_int),
+                ("num_axes", ctypes.c_int), ("interleaved", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("weight_dtype", ctypes.c_int)]
 
 
 def lib() -> ctypes.CDLL:
@@ -105,6 +121,21 @@ def lib() -> ctypes.CDLL:
         L.pa_decode_workspace_size.restype = S
         L.pa_decode_workspace_size_ex.argtypes = [I, I, I, I, I]
         L.pa_decode_workspace_size_ex.restype = S
+        L.pa_reshape_and_cache_int4.argtypes = [P, P, I, P, P, P, P, P, I, I, I, I, I, P, P]
+        L.pa_reshape_and_cache_int4.restype = I
+        L.pa_gather_int4.argtypes = [P, P, P, P, P, P, P, P, P, I, ctypes.c_int64, I, I, I, I, I,
+                                     I, I, P, P]
+        L.pa_gather_int4.restype = I
+        L.pa_decode_int4.argtypes = [P, P, P, P, P, P, P, F, I, P, I, I, I, I, I, I, I, I, I, P, S,
+                                     P, P]
+        L.pa_decode_int4.restype = I
+        NR = ctypes.POINTER(_NormRopeArgs)
+        L.pa_norm_rope.argtypes = [NR, P, ctypes.c_int64, P, P]
+        L.pa_norm_rope.restype = I
+        L.pa_norm_rope_append.argtypes = [NR, P, ctypes.c_int64, P, P, P, I, I, P, P]
+        L.pa_norm_rope_append.restype = I
+        L.pa_norm_rope_append_int4.argtypes = [NR, P, ctypes.c_int64, P, P, P, P, P, I, I, P, P]
+        L.pa_norm_rope_append_int4.restype = I
         L.pa_status_string.argtypes = [I]
         L.pa_status_string.restype = ctypes.c_char_p
         L.pa_check_error_word.argtypes = [ctypes.c_int32]
@@ -138,8 +169,8 @@ def pa_version() -> int:
 
 def pa_default_partition_size(cache_dtype: str) -> int:
     """Rows per split-K partition used when none is requested, for a cache
-    of this type ("f32", "bf16", "fp8" or "int8")."""
-    codes = {"f32": 0, "bf16": 1, "fp8": 2, "int8": 3}
+    of this type ("f32", "bf16", "fp8", "int8" or "int4")."""
+    codes = {"f32": 0, "bf16": 1, "fp8": 2, "int8": 3, "int4": 4}
     if cache_dtype not in codes:
         raise ValueError(f"unknown cache dtype {cache_dtype!r}")
     return lib().pa_default_partition_size(codes[cache_dtype])
@@ -491,8 +522,9 @@ def pa_decode_int8(q, k_cache, v_cache, k_scales, v_scales, block_tables, contex
 def pa_copy_blocks(k_cache, v_cache, block_mapping, error_word=None, stream=None) -> None:
     """Copy-on-write: block dst := block src of both pools for each (src, dst)
     row of block_mapping (int64 [n][2]); negative entries skip a pair. The
-    pools are [NB][Hkv][bs][D]; for an INT8 cache call it again on the row
-    scales viewed as [NB][1][1][Hkv * bs]."""
+    pools are [NB][Hkv][bs][D] (an INT4 cache's [NB][Hkv][bs][D / 2] bytes); for
+    an INT8 cache call it again on the row scales viewed as [NB][1][1][Hkv * bs],
+    for an INT4 cache on the params viewed as [NB][1][1][Hkv * bs * 2]."""
     import torch
     _check_cuda("k_cache", k_cache, ndim=4)
     _check_cuda("v_cache", v_cache, k_cache.dtype, 4)
@@ -715,3 +747,250 @@ def pa_decode_noalloc(q, k_cache, v_cache, block_tables, context_lens, scale, ou
             what += (f" (needs {need} bytes of scratch, the fixed scratch holds "
                      f"{NOALLOC_SCRATCH_BYTES}; pass a workspace to pa_decode instead)")
         raise PagedAttentionError(rc, what)
+
+
+def _check_int4_pool(k_cache, v_cache, k_params, v_params):
+    """(NB, Hkv, bs, D) of a 4-bit pool."""
+    import torch
+    _check_cuda("k_cache", k_cache, torch.uint8, 4)
+    _check_cuda("v_cache", v_cache, torch.uint8, 4)
+    _check_cuda("k_params", k_params, torch.bfloat16, 4)
+    _check_cuda("v_params", v_params, torch.bfloat16, 4)
+    nb, hkv, bs, half = k_cache.shape
+    if v_cache.shape != k_cache.shape or tuple(k_params.shape) != (nb, hkv, bs, 2) \
+            or v_params.shape != k_params.shape:
+        raise ValueError("INT4 pools are [NB][Hkv][bs][D / 2] codes with [NB][Hkv][bs][2] params")
+    return nb, hkv, bs, 2 * half
+
+
+def pa_reshape_and_cache_int4(k_new, v_new, slot_mapping, k_cache, v_cache, k_params, v_params,
+                              error_word=None, stream=None) -> None:
+    """Quantising append into a 4-bit cache: k_new/v_new (bf16 or fp32,
+    [T][Hkv][D]) -> codes (uint8 [NB][Hkv][bs][D / 2]) and one bf16 pair (lo, s)
+    per row (params, [NB][Hkv][bs][2]); value = lo + s * code."""
+    import torch
+    nb, hkv, bs, d = _check_int4_pool(k_cache, v_cache, k_params, v_params)
+    _check_cuda("k_new", k_new, ndim=3)
+    _check_cuda("v_new", v_new, k_new.dtype, 3)
+    _check_cuda("slot_mapping", slot_mapping, torch.int64, 1)
+    if error_word is not None:
+        _check_cuda("error_word", error_word, torch.int32)
+    if tuple(k_new.shape[1:]) != (hkv, d) or k_new.shape != v_new.shape \
+            or slot_mapping.shape[0] != k_new.shape[0]:
+        raise ValueError("shape mismatch between k_new/v_new/slot_mapping and the caches")
+    _check_device(stream, k_new, v_new, slot_mapping, k_cache, v_cache, k_params, v_params,
+                  error_word)
+    rc = lib().pa_reshape_and_cache_int4(_ptr(k_new), _ptr(v_new), _dtype_code(k_new),
+                                         _ptr(slot_mapping), _ptr(k_cache), _ptr(v_cache),
+                                         _ptr(k_params), _ptr(v_params), int(k_new.shape[0]), hkv,
+                                         d, bs, nb, _ptr(error_word), _stream(stream))
+    if rc != PA_OK:
+        raise PagedAttentionError(rc, "pa_reshape_and_cache_int4")
+
+
+def pa_gather_int4(k_cache, v_cache, k_params, v_params, block_tables, context_lens, row_starts,
+                   k_out, v_out, max_context_len, error_word=None, stream=None) -> None:
+    """The cached rows of every sequence as plain values: rows row_starts[s] ..
+    row_starts[s] + context_lens[s] - 1 of k_out/v_out ([rows][Hkv][D], bf16 or
+    fp32). row_starts: int64 [B]. Rows that no sequence covers stay as they are."""
+    import torch
+    nb, hkv, bs, d = _check_int4_pool(k_cache, v_cache, k_params, v_params)
+    _check_cuda("block_tables", block_tables, torch.int32, 2)
+    _check_cuda("context_lens", context_lens, torch.int32, 1)
+    _check_cuda("row_starts", row_starts, torch.int64, 1)
+    _check_cuda("k_out", k_out, ndim=3)
+    _check_cuda("v_out", v_out, k_out.dtype, 3)
+    if error_word is not None:
+        _check_cuda("error_word", error_word, torch.int32)
+    B = context_lens.shape[0]
+    if block_tables.shape[0] != B or row_starts.shape[0] != B or k_out.shape != v_out.shape \
+            or tuple(k_out.shape[1:]) != (hkv, d):
+        raise ValueError("shape mismatch between the outputs, the tables and the caches")
+    _check_device(stream, k_cache, v_cache, k_params, v_params, block_tables, context_lens,
+                  row_starts, k_out, v_out, error_word)
+    rc = lib().pa_gather_int4(_ptr(k_cache), _ptr(v_cache), _ptr(k_params), _ptr(v_params),
+                              _ptr(block_tables), _ptr(context_lens), _ptr(row_starts),
+                              _ptr(k_out), _ptr(v_out), _dtype_code(k_out), int(k_out.shape[0]),
+                              B, hkv, d, bs, nb, int(block_tables.shape[1]),
+                              int(max_context_len), _ptr(error_word), _stream(stream))
+    if rc != PA_OK:
+        raise PagedAttentionError(rc, "pa_gather_int4")
+
+
+def pa_decode_int4(q, k_cache, v_cache, k_params, v_params, block_tables, context_lens, scale,
+                   out, max_context_len, window: int = 0, workspace=None, error_word=None,
+                   stream=None) -> None:
+    """Decode attention over a 4-bit cache. q/out: bf16 [B][Hq][D], or
+    [B][Q][Hq][D] for the last Q tokens of every sequence (token j attends to
+    rows 0 .. n - Q + j). window > 0: each token attends to its last `window`
+    rows only. workspace: a CUDA tensor of at least
+    pa_decode_workspace_size_multi(B, Q, Hq, D, max_context_len) bytes; when
+    None, one is allocated from torch's caching allocator for this call."""
+    import torch
+    nb, hkv, bs, d = _check_int4_pool(k_cache, v_cache, k_params, v_params)
+    _check_cuda("q", q, torch.bfloat16)
+    _check_cuda("out", out, torch.bfloat16)
+    _check_cuda("block_tables", block_tables, torch.int32, 2)
+    _check_cuda("context_lens", context_lens, torch.int32, 1)
+    if error_word is not None:
+        _check_cuda("error_word", error_word, torch.int32)
+    if q.dim() == 3:
+        (B, hq, dq), Q = q.shape, 1
+    elif q.dim() == 4:
+        B, Q, hq, dq = q.shape
+    else:
+        raise ValueError(f"q must have 3 or 4 dimensions, got {q.dim()}")
+    if dq != d or out.shape != q.shape or block_tables.shape[0] != B or context_lens.shape[0] != B:
+        raise ValueError("shape mismatch between q/out/block_tables/context_lens and the caches")
+    _check_device(stream, q, out, k_cache, v_cache, k_params, v_params, block_tables,
+                  context_lens, error_word, workspace)
+    if workspace is None:
+        need = pa_decode_workspace_size_multi(B, Q, hq, d, int(max_context_len))
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+    _check_cuda("workspace", workspace)
+    rc = lib().pa_decode_int4(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_params),
+                              _ptr(v_params), _ptr(block_tables), _ptr(context_lens),
+                              float(scale), int(window), _ptr(out), B, Q, hq, hkv, d, bs, nb,
+                              int(block_tables.shape[1]), int(max_context_len), _ptr(workspace),
+                              workspace.numel() * workspace.element_size(), _ptr(error_word),
+                              _stream(stream))
+    if rc != PA_OK:
+        raise PagedAttentionError(rc, "pa_decode_int4")
+
+
+def _check_heads(name, t, dtype=None):
+    """A CUDA tensor [T][H][D] whose tokens may lie any distance apart (a part
+    of a fused projection's output); returns that distance in elements."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must have 3 dimensions, got {t.dim()}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    T, H, D = t.shape
+    st, sh, sd = t.stride()
+    if (sd != 1 and D > 1) or (sh != D and H > 1):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return st if T > 1 else H * D
+
+
+def _norm_rope_args(q, k, positions, cos_sin, q_out, q_weight, k_weight, eps, weight_offset,
+                    interleaved, pair_axis, error_word):
+    import torch
+    q_stride = _check_heads("q", q)
+    k_stride = _check_heads("k", k, q.dtype)
+    q_out_stride = _check_heads("q_out", q_out, q.dtype)
+    dtype = _dtype_code(q)
+    T, hq, d = q.shape
+    if k.shape[0] != T or k.shape[2] != d or q_out.shape != q.shape:
+        raise ValueError("shape mismatch between q, k and q_out")
+    weight_dtype = 0
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _check_cuda(name, w, ndim=1)
+            if w.shape[0] != d:
+                raise ValueError(f"{name} must hold head_dim elements")
+            weight_dtype = _dtype_code(w)
+    if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
+        raise TypeError("q_weight and k_weight must have the same type")
+    rot, max_position, axes, axis_bytes = 0, 0, 1, None
+    if cos_sin is not None:
+        _check_cuda("cos_sin", cos_sin, torch.float32, 2)
+        _check_cuda("positions", positions, torch.int32)
+        max_position, rot = cos_sin.shape
+        axes = 1 if positions.dim() == 1 else positions.shape[0]
+        if positions.dim() not in (1, 2) or positions.shape[-1] != T:
+            raise ValueError("positions must be [T] or [axes][T]")
+        if pair_axis is not None:
+            axis_bytes = bytes(pair_axis)
+            if len(axis_bytes) != rot // 2:
+                raise ValueError("pair_axis must hold rot_dim / 2 axis numbers")
+    elif positions is not None or pair_axis is not None:
+        raise ValueError("positions and pair_axis need cos_sin")
+    if error_word is not None:
+        _check_cuda("error_word", error_word, torch.int32)
+    return _NormRopeArgs(_ptr(q), _ptr(k), q_stride, k_stride, _ptr(q_out), q_out_stride,
+                         _ptr(q_weight), _ptr(k_weight), float(eps), float(weight_offset),
+                         _ptr(cos_sin), _ptr(positions), axis_bytes, T, hq, k.shape[1], d, rot,
+                         max_position, axes, int(bool(interleaved)), dtype, weight_dtype)
+
+
+def pa_norm_rope(q, k, positions, cos_sin, q_out, k_out, q_weight=None, k_weight=None, eps=1e-6,
+                 weight_offset=0.0, interleaved=False, pair_axis=None, error_word=None,
+                 stream=None) -> None:
+    """Per-head RMS norms of q ([T][Hq][D]) and k ([T][Hkv][D]) with their
+    weights ([D]; None: no norm) and the rotation by position, in one pass into
+    q_out and k_out (in place where they are q and k). The tokens of q, k and
+    the outputs may lie any distance apart (parts of a fused projection).
+
+    positions: int32 [T], or [axes][T] with pair_axis the axis number of each of
+    the rot_dim / 2 pairs. cos_sin: fp32 [max_position][rot_dim], cosines then
+    sines; None (with positions None): no rotation. interleaved: pairs are
+    (2i, 2i + 1), else (i, i + rot_dim / 2)."""
+    args = _norm_rope_args(q, k, positions, cos_sin, q_out, q_weight, k_weight, eps,
+                           weight_offset, interleaved, pair_axis, error_word)
+    k_out_stride = _check_heads("k_out", k_out, k.dtype)
+    if k_out.shape != k.shape:
+        raise ValueError("shape mismatch between k and k_out")
+    _check_device(stream, q, k, positions, cos_sin, q_out, k_out, q_weight, k_weight, error_word)
+    rc = lib().pa_norm_rope(ctypes.byref(args), _ptr(k_out), k_out_stride, _ptr(error_word),
+                            _stream(stream))
+    if rc != PA_OK:
+        raise PagedAttentionError(rc, "pa_norm_rope")
+
+
+def _check_append_rows(k, v, slot_mapping, hkv, d):
+    import torch
+    v_stride = _check_heads("v", v, k.dtype)
+    _check_cuda("slot_mapping", slot_mapping, torch.int64, 1)
+    if v.shape != k.shape or tuple(k.shape[1:]) != (hkv, d) or slot_mapping.shape[0] != k.shape[0]:
+        raise ValueError("shape mismatch between k/v/slot_mapping and the caches")
+    return v_stride
+
+
+def pa_norm_rope_append(q, k, v, positions, cos_sin, slot_mapping, q_out, k_cache, v_cache,
+                        q_weight=None, k_weight=None, eps=1e-6, weight_offset=0.0,
+                        interleaved=False, pair_axis=None, error_word=None, stream=None) -> None:
+    """pa_norm_rope whose K rows go into their slots of the paged pool
+    ([NB][Hkv][bs][D], q's type), with the V rows beside them (a bit copy).
+    slot_mapping: int64 [T], negative = no append."""
+    _check_cuda("k_cache", k_cache, ndim=4)
+    _check_cuda("v_cache", v_cache, k_cache.dtype, 4)
+    args = _norm_rope_args(q, k, positions, cos_sin, q_out, q_weight, k_weight, eps,
+                           weight_offset, interleaved, pair_axis, error_word)
+    nb, hkv, bs, d = k_cache.shape
+    if k_cache.dtype != q.dtype:
+        raise TypeError(f"k_cache must be {q.dtype}, got {k_cache.dtype}")
+    if v_cache.shape != k_cache.shape:
+        raise ValueError("v_cache must match k_cache")
+    v_stride = _check_append_rows(k, v, slot_mapping, hkv, d)
+    _check_device(stream, q, k, v, positions, cos_sin, slot_mapping, q_out, k_cache, v_cache,
+                  q_weight, k_weight, error_word)
+    rc = lib().pa_norm_rope_append(ctypes.byref(args), _ptr(v), v_stride, _ptr(slot_mapping),
+                                   _ptr(k_cache), _ptr(v_cache), bs, nb, _ptr(error_word),
+                                   _stream(stream))
+    if rc != PA_OK:
+        raise PagedAttentionError(rc, "pa_norm_rope_append")
+
+
+def pa_norm_rope_append_int4(q, k, v, positions, cos_sin, slot_mapping, q_out, k_cache, v_cache,
+                             k_params, v_params, q_weight=None, k_weight=None, eps=1e-6,
+                             weight_offset=0.0, interleaved=False, pair_axis=None,
+                             error_word=None, stream=None) -> None:
+    """pa_norm_rope whose K rows are quantised into a 4-bit cache, with the V
+    rows (codes and params as of pa_reshape_and_cache_int4 on pa_norm_rope's
+    K rows). slot_mapping: int64 [T], negative = no append."""
+    nb, hkv, bs, d = _check_int4_pool(k_cache, v_cache, k_params, v_params)
+    args = _norm_rope_args(q, k, positions, cos_sin, q_out, q_weight, k_weight, eps,
+                           weight_offset, interleaved, pair_axis, error_word)
+    v_stride = _check_append_rows(k, v, slot_mapping, hkv, d)
+    _check_device(stream, q, k, v, positions, cos_sin, slot_mapping, q_out, k_cache, v_cache,
+                  k_params, v_params, q_weight, k_weight, error_word)
+    rc = lib().pa_norm_rope_append_int4(ctypes.byref(args), _ptr(v), v_stride, _ptr(slot_mapping),
+                                        _ptr(k_cache), _ptr(v_cache), _ptr(k_params),
+                                        _ptr(v_params), bs, nb, _ptr(error_word),
+                                        _stream(stream))
+    if rc != PA_OK:
+        raise PagedAttentionError(rc, "pa_norm_rope_append_int4")

@@ -13,7 +13,7 @@ namespace {
 
 using pa::DecodeParams;
 
-constexpr int kVersion = 10100;   // 1.1.0
+constexpr int kVersion = 10200;   // 1.2.0
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr size_t kMaxDynamicSmem = 227 * 1024;
 
@@ -331,7 +331,7 @@ pa_status pa_check_error_word(int32_t error_word_value) {
 int pa_version(void) { return kVersion; }
 
 int pa_default_partition_size(pa_dtype cache_dtype) {
-    if (!valid_decode_cache_dtype(cache_dtype)) return 0;
+    if (!valid_decode_cache_dtype(cache_dtype) && cache_dtype != PA_DTYPE_INT4) return 0;
     return cache_dtype == PA_DTYPE_FP8_E4M3 ? pa::kDefaultPartition8 : pa::kDefaultPartition;
 }
 
@@ -375,9 +375,10 @@ pa_status pa_copy_blocks(void* k_cache, void* v_cache, const int64_t* block_mapp
                          int num_blocks, pa_dtype dtype, int32_t* error_word,
                          struct CUstream_st* stream) {
     if (num_pairs < 0 || num_kv_heads <= 0 || head_dim <= 0 || block_size <= 0 ||
-        num_blocks <= 0 || !valid_decode_cache_dtype(dtype))
+        num_blocks <= 0 || (!valid_decode_cache_dtype(dtype) && dtype != PA_DTYPE_INT4))
         return PA_ERR_INVALID_ARG;
-    const int row_bytes = head_dim * elem_bytes(dtype);
+    if (dtype == PA_DTYPE_INT4 && head_dim % 2 != 0) return PA_ERR_UNSUPPORTED;
+    const int row_bytes = dtype == PA_DTYPE_INT4 ? head_dim / 2 : head_dim * elem_bytes(dtype);
     if (row_bytes % 16 != 0) return PA_ERR_UNSUPPORTED;
     if (num_pairs == 0) return PA_OK;
     if (!k_cache || !v_cache || !block_mapping) return PA_ERR_INVALID_ARG;

@@ -34,6 +34,8 @@ struct DecodeParams {
     float v_scale;                 // FP8 caches: V value = v_scale * e4m3(code) (else 1)
     const float* k_row_scales;     // INT8 caches: [num_blocks][num_kv_heads][block_size] (else null)
     const float* v_row_scales;
+    const uint32_t* k_pairs;       // INT4 caches: a row's (lo, s), likewise laid out (else null)
+    const uint32_t* v_pairs;
     int num_seqs;
     int num_queries;               // query tokens per sequence, the last rows of each (>= 1)
     int window;                    // sliding window: attend to the last `window` rows (0 = all)
@@ -98,6 +100,55 @@ cudaError_t launch_append_int8(const void* k_new, const void* v_new, pa_dtype ne
                                float* k_scales, float* v_scales, int num_tokens,
                                int num_kv_heads, int head_dim, int block_size, int num_blocks,
                                int32_t* error_word, cudaStream_t stream);
+
+// Quantising append into a 4-bit cache, and the gather of its rows.
+cudaError_t launch_append_int4(const void* k_new, const void* v_new, pa_dtype new_dtype,
+                               const int64_t* slot_mapping, void* k_cache, void* v_cache,
+                               void* k_params, void* v_params, int num_tokens, int num_kv_heads,
+                               int head_dim, int block_size, int num_blocks, int32_t* error_word,
+                               cudaStream_t stream);
+cudaError_t launch_gather_int4(const void* k_cache, const void* v_cache, const void* k_params,
+                               const void* v_params, const int32_t* block_tables,
+                               const int32_t* context_lens, const int64_t* row_starts,
+                               void* k_out, void* v_out, pa_dtype out_dtype, long long num_rows,
+                               int num_seqs, int num_kv_heads, int head_dim, int block_size,
+                               int num_blocks, int max_blocks_per_seq, int max_context_len,
+                               int32_t* error_word, cudaStream_t stream);
+
+// 4-bit cache, bf16 q/out (head dim 64 or 128, at most 8 query columns per KV
+// head). p.window counts the rows that any query token sees.
+cudaError_t launch_decode_int4(const DecodeParams& p, cudaStream_t stream);
+
+// Norms and rotation of q and k rows (pa_norm_rope_args in the header); the K
+// rows go to k_out, or with k_cache set into their slots, or with k_params set
+// quantised into a 4-bit cache.
+struct NormRopeParams {
+    const void* q;
+    const void* k;
+    const void* v;
+    void* q_out;
+    void* k_out;
+    long long q_stride, k_stride, v_stride, q_out_stride, k_out_stride;   // elements per token
+    const void* q_weight;
+    const void* k_weight;
+    const float* cos_sin;
+    const int32_t* positions;
+    const int64_t* slot_mapping;
+    void* k_cache;
+    void* v_cache;
+    void* k_params;
+    void* v_params;
+    int32_t* error_word;
+    long long num_slots;
+    float eps, weight_offset;
+    int weight_bf16;
+    int num_tokens, num_heads, num_kv_heads, head_dim;
+    int rot_dim, max_position, num_axes, interleaved;
+    int block_size;
+    int splits;                    // warps per token
+    uint8_t pair_axis[128];        // rot_dim / 2 <= 128
+};
+cudaError_t launch_norm_rope(const NormRopeParams& p, pa_dtype dtype, cudaStream_t stream);
 
 // Quantising append into an FP8 cache (new rows fp32 or bf16).
 cudaError_t launch_append_fp8(const void* k_new, const void* v_new, pa_dtype new_dtype,
