@@ -527,7 +527,7 @@ pa_status pa_gather_int4(const void* k_cache, const void* v_cache, const void* k
  * rows; 0 < n < Q is flagged PA_DEVERR_CONTEXT (those rows are left as they
  * are). Scores, softmax and sums are fp32; q is held in f16 (exactly, but for
  * elements more than 2^20 below their head's largest), a probability times its
- * row's s is rounded to f16 once. Partitions of 512 rows merged as in
+ * row's s is rounded to f16 once. Partitions of 1024 rows merged as in
  * pa_decode: a sequence's result does not depend on the rest of the batch.
  * Workspace: pa_decode_workspace_size_multi(num_seqs, num_queries, num_heads,
  * head_dim, max_context_len) bytes, used as in pa_decode. Supported: head_dim
@@ -621,8 +621,8 @@ pa_status pa_check_error_word(int32_t error_word_value);
 int pa_version(void);
 
 /* Rows per split-K partition the decode calls use for a cache of this type
- * when none is requested: 512 for fp32, bf16, INT8 and INT4, 1024 for FP8 (the same
- * bytes per partition as 512 bf16 rows). 0 for a type no cache holds. The
+ * when none is requested: 512 for fp32, bf16 and INT8, 1024 for FP8 (the same
+ * bytes per partition as 512 bf16 rows) and INT4. 0 for a type no cache holds. The
  * workspace size functions assume 512, which covers every case. */
 int pa_default_partition_size(pa_dtype cache_dtype);
 

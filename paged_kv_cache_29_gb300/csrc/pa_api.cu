@@ -331,7 +331,8 @@ pa_status pa_check_error_word(int32_t error_word_value) {
 int pa_version(void) { return kVersion; }
 
 int pa_default_partition_size(pa_dtype cache_dtype) {
-    if (!valid_decode_cache_dtype(cache_dtype) && cache_dtype != PA_DTYPE_INT4) return 0;
+    if (cache_dtype == PA_DTYPE_INT4) return pa::kDefaultPartition4;
+    if (!valid_decode_cache_dtype(cache_dtype)) return 0;
     return cache_dtype == PA_DTYPE_FP8_E4M3 ? pa::kDefaultPartition8 : pa::kDefaultPartition;
 }
 

@@ -165,7 +165,7 @@ pa_status pa_decode_int4(const void* q, const void* k_cache, const void* v_cache
         !aligned(block_tables, 4) || !aligned(context_lens, 4) ||
         !pool4_ok(k_cache, v_cache, k_params, v_params))
         return PA_ERR_INVALID_ARG;
-    constexpr int P = pa::kDefaultPartition;
+    constexpr int P = pa::kDefaultPartition4;
     const long long parts = max_context_len > 0 ? ceil_div(max_context_len, P) : 1;
     const long long chunk = num_seqs < pa::kPlanMaxSeqs ? num_seqs : pa::kPlanMaxSeqs;
     if (parts * chunk * num_kv_heads > 0x3fffffffLL) return PA_ERR_UNSUPPORTED;

@@ -8,31 +8,39 @@
 // and 16 dims x 16 rows of V codes x 8 columns per m16n8k16 f16 MMA.
 //
 // Codes as f16 without a conversion: the bits 0x000c are the f16 subnormal
-// c * 2^-24 and the bits 0x00c0 are 16 c * 2^-24, exact MMA operands both. So
-// one AND gives the codes of two dims (K) or two rows (V), and one shift by 8
-// the next two of a word: 5 instructions for 8 codes. The factor 16 of the odd
-// dims is taken out of q (K) and out of the output (V), 2^24 out of the
-// score's and the output's scale.
-//   K words need nothing more: nibbles (0, 4), (1, 5), (2, 6), (3, 7) of a word
-//   are pairs of dims of one row, and q is dealt the same way.
-//   V pairs two rows of one dim: one byte permute puts the halves of two rows'
-//   words side by side (6 instructions for 8 codes).
+// c * 2^-24, the bits 0x00c0 are 16 c * 2^-24 and a byte 0x00dc is their sum,
+// exact MMA operands all three. 2^24 is taken out of the score's and the
+// output's scale.
+//   K: nibbles (0, 4), (1, 5), (2, 6), (3, 7) of a word are pairs of dims of one
+//   row, and q is dealt the same way, divided by 16 for the second and fourth
+//   pair: 4 ANDs and a shift for 8 codes.
+//   V: a transposing 8-bit ldmatrix gives a lane the bytes of four rows of one
+//   byte column (two dims); w & 0x000f000f (and the other two rows') is the
+//   even dim's operand, w & 0x00ff00ff the odd dim's, whose output is even + 16
+//   odd and is taken apart at the end: 4 instructions for 8 codes.
+// (ANDs and permutes run at half rate, and their pipe is the busiest. A byte
+// 0..15 is also the e4m3 value c * 2^-9, one AND for four codes; but the e4m3 MMA
+// converts its operands to f16 itself: 125 instructions a tile for q . c
+// instead of 48.)
 //
 // q is scaled by a power of two per head to [2^12, 2^13) before it becomes f16
-// (exact: bf16 has fewer bits), whatever its size. A probability times its
-// row's s_i is the V operand: with s_i = 2^e_i u_i (u_i < 2) the running
-// reference M bounds T_i = S_i + e_i, so that 2^(T_i - M) u_i stays in f16's
-// range for any sizes of the steps. M is raised only when a T exceeds it by
-// more than 8 (operands up to 2^9 are as exact): most tiles need no cross-lane
+// (exact: bf16 has fewer bits), whatever its size; sum q' is the product with a
+// row of ones.
+// A probability times its row's step is the V operand in f16: the steps are
+// taken relative to 2^e, e the largest step's exponent so far, and M is a
+// reference that the scores exceed by at most 8, so operands stay below 2^9
+// whatever the sizes of scores and steps. M and e are raised, and the output
+// rescaled, only when a row goes past them: most units need no cross-lane
 // maximum and no rescale. Sums, z = sum p lo, scores and outputs are fp32.
 //
-// Work: items of at most 512 rows (sequence, KV head, partition) dealt to
-// persistent CTAs (pa_plan.cuh); warp w of a CTA takes the 16-row tiles w,
-// w + 4, ... of each item. Every warp streams its own tiles through its own
-// shared-memory ring with 16-byte cp.async, STAGES - 1 tiles ahead and across
-// item boundaries: a tile is 1 KB of K codes, 1 KB of V codes and 128 bytes of
-// pairs, too small for one producer warp to keep four consumers fed. At an
-// item's end the warps' states are merged through shared memory.
+// Work: items of at most kItemRows rows (sequence, KV head, partition) dealt to
+// persistent CTAs (pa_plan.cuh); warp w of a CTA takes units w, w + 4, ... of
+// 32 rows (two 16-row tiles, each inside one block) of each item. Every warp
+// streams its own units through its own shared-memory ring with 16-byte
+// cp.async, STAGES - 1 units ahead and across item boundaries: a tile is 1 KB of
+// K codes, 1 KB of V codes and 128 bytes of pairs, too small for one producer
+// warp to keep four consumers fed. At an item's end the warps' states are
+// merged through shared memory.
 #include <atomic>
 
 #include "pa_decode_stream.cuh"
@@ -45,13 +53,21 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads4 = kWarps * 32;
-constexpr int kItemRows = kDefaultPartition;
-constexpr int kWarpTiles = kItemRows / kTileRows / kWarps;   // a warp's tiles of an item
-constexpr float kRaise = 8.f;                                // see M above
-static_assert(kWarpTiles <= 32, "a lane per tile holds its place in the pool");
+constexpr int kItemRows = kDefaultPartition4;
+constexpr int kUnitRows = 2 * kTileRows;
+constexpr int kWarpUnits = kItemRows / kUnitRows / kWarps;   // a warp's units of an item
+constexpr float kRaise = 8.f;                                // M lags by at most this (base 2)
+static_assert(2 * kWarpUnits <= 32, "a lane per tile holds its place in the pool");
 
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_16_if(bool on, uint32_t dst, const void* src) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %2, 0;\n\t"
+        "@p cp.async.cg.shared.global [%0], [%1], 16;\n\t}" ::"r"(dst), "l"(src), "r"(static_cast<int>(on))
+        : "memory");
 }
 template <int N>
 __device__ __forceinline__ void cp_async_wait_group() {
@@ -61,17 +77,6 @@ __device__ __forceinline__ uint2 lds64(uint32_t addr) {
     uint2 v;
     asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
     return v;
-}
-__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
-    uint32_t v;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
-    return v;
-}
-// e + 127 of a V row: its step's exponent, but at least its lo's less 20 (then
-// lo 2^-e stays below 2^21, and a step that loses bits as an f16 operand adds
-// less than 2^-30 of lo) and at least -100 (2^-e and its sums stay finite).
-__device__ __forceinline__ uint32_t value_exponent(uint32_t pair) {
-    return max(pair >> 23, max((pair >> 7) & 0xffu, 47u) - 20u);
 }
 // An 8 x 8 matrix of 16-bit elements, two per lane, transposed.
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
@@ -83,18 +88,19 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
 template <int D, int NC, int STAGES>
 struct Smem4 {
     static constexpr int kCodes = kTileRows * D / 2;                 // K or V codes of a tile
-    static constexpr int kStage = 2 * kCodes + 2 * kTileRows * 4;
+    static constexpr int kTile = 2 * kCodes + 2 * kTileRows * 4;
+    static constexpr int kStage = 2 * kTile;
     static constexpr int kRing = kWarps * STAGES * kStage;
-    // A warp's output of one column: lane group gid holds dims gid * D / 8 ..;
-    // two floats of padding per group and four per column spread the float2
-    // stores of a half-warp over all banks.
-    static constexpr int kLaneDims = D / 8;
-    static constexpr int kCol = 8 * (kLaneDims + 2) + 4;
+    // A warp's outputs of one column; four floats of padding spread the float2
+    // stores of a half-warp (4 dim pairs x 4 column pairs) over all banks.
+    static constexpr int kCol = D + 4;
     static constexpr int kState = NC * (kCol + 2);                   // o, then m, l
     static constexpr int kMerge = kWarps * kState * 4;
-    static constexpr int kBytes = kRing + kMerge + 2 * 16;
+    static constexpr int kQ = kRing + kMerge;                        // q fragments [D / 32][lane]
+    static constexpr int kFirst = kQ + (D / 32) * 32 * 16;           // the first two items
+    static constexpr int kBytes = kFirst + 2 * 16 + 8 * 4 + 8 * 4;   // columns' rows and factors
     static_assert(kMerge >= 4 * plan_scratch_ints(kThreads4), "the plan's scratch lives there");
-    static_assert((kRing + kMerge) % 16 == 0, "the first items follow");
+    static_assert((kRing + kMerge) % 16 == 0, "16-byte fragments follow");
 };
 
 // D: head dim. NC: query columns the state holds (an item uses ncols <= NC).
@@ -102,16 +108,18 @@ template <int D, int NC, int STAGES, int MIN_CTAS>
 __global__ void __launch_bounds__(kThreads4, MIN_CTAS) decode_int4_kernel(const DecodeParams p) {
     using Smem = Smem4<D, NC, STAGES>;
     constexpr int kKWords = D / 32;       // words of K codes per lane and row
-    constexpr int kVWords = D / 64;       // words of V codes per lane and row
     constexpr int kMt = D / 16;           // m-tiles of the output
-    constexpr int kLaneDims = Smem::kLaneDims;
 
     extern __shared__ __align__(128) uint8_t smem_raw[];
     float* merge = reinterpret_cast<float*>(smem_raw + Smem::kRing);
-    int4* first_items = reinterpret_cast<int4*>(smem_raw + Smem::kRing + Smem::kMerge);
+    uint4* q_frag = reinterpret_cast<uint4*>(smem_raw + Smem::kQ);
+    int4* first_items = reinterpret_cast<int4*>(smem_raw + Smem::kFirst);
+    int* col_row = reinterpret_cast<int*>(first_items + 2);   // column c's row beside column 0's
+    float* col_f = reinterpret_cast<float*>(col_row + 8);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int gid = lane >> 2, t4 = lane & 3;
     const uint32_t ring = smem_addr(smem_raw) + warp * STAGES * Smem::kStage;
+    const uint32_t ring_end = ring + STAGES * Smem::kStage;
 
     grid_dependency_wait();
     grid_launch_dependents();
@@ -120,32 +128,40 @@ __global__ void __launch_bounds__(kThreads4, MIN_CTAS) decode_int4_kernel(const 
     const int Hkv = p.num_kv_heads, bs = p.block_size, Q = p.num_queries;
     const int grp = p.num_heads / Hkv, ncols = grp * Q;
     const int window = p.window > 0 ? p.window - (Q - 1) : 0;   // of one query token
+    // Query column c = G j + g is head g of the group, query token j.
+    if (threadIdx.x < 8) col_row[threadIdx.x] = threadIdx.x / grp * p.num_heads + threadIdx.x % grp;
 
-    // ---- the warp's stream of tiles: item desc, this lane's tile in the pool
-    // (tile units of 16 rows; lane i: the warp's i-th tile), next tile, count.
+    const int bs_log2 = (bs & (bs - 1)) == 0 ? __ffs(bs) - 1 : -1;
+
+    // ---- the warp's stream of units: this lane's tile in the pool (tile units of
+    // 16 rows; lane i: the warp's i-th tile of the item), the next unit, units.
     uint32_t place = 0;
-    int next_tile = 0, num_tiles = 0;
+    int next_unit = 0, num_units = 0;
     // The item after it: descriptor and this lane's block id; then one more.
     int4 d_next = make_int4(-1, 0, 0, 0), d_after = make_int4(-1, 0, 0, 0);
     int id_next = 0, off_next = 0;
-    int issue_stage = 0;
+    uint32_t issue_at = ring;
 
-    auto tiles_of = [&](const int4& d, int& lo) {
-        const int base = seq_row_base(d.w, p.window);
-        lo = base + d.z * kItemRows;
-        const int hi = min(d.w, lo + kItemRows);
-        const int nt = (hi - lo + kTileRows - 1) / kTileRows;
-        return (nt - warp + kWarps - 1) / kWarps;            // tiles warp, warp + W, ...
+    // The warp's units of item d, its first row, and the warp's tiles (the last
+    // unit may have one).
+    auto units_of = [&](const int4& d, int& lo, int& tiles) {
+        lo = seq_row_base(d.w, p.window) + d.z * kItemRows;
+        const int nt = (min(d.w, lo + kItemRows) - lo + kTileRows - 1) / kTileRows;
+        const int nu = (nt + 1) / 2;
+        const int cnt = (nu - warp + kWarps - 1) / kWarps;
+        // Only the item's very last unit can be half a one.
+        tiles = 2 * cnt - ((nt & 1) && cnt > 0 && warp + kWarps * (cnt - 1) == nu - 1 ? 1 : 0);
+        return cnt;
     };
     // Requests the block id of this lane's tile of item d.
     auto fetch = [&](const int4& d) {
         id_next = 0;
         if (d.x < 0) return;
-        int lo;
-        const int cnt = tiles_of(d, lo);
-        if (lane < cnt) {
-            const int tok = lo + kTileRows * (warp + kWarps * lane);
-            const int col = tok / bs;
+        int lo, tiles;
+        units_of(d, lo, tiles);
+        if (lane < tiles) {
+            const int tok = lo + kUnitRows * (warp + kWarps * (lane >> 1)) + kTileRows * (lane & 1);
+            const int col = bs_log2 >= 0 ? tok >> bs_log2 : tok / bs;
             off_next = (tok - col * bs) / kTileRows;
             id_next = __ldg(p.block_tables + static_cast<size_t>(d.x) * p.max_blocks_per_seq + col);
         }
@@ -154,37 +170,39 @@ __global__ void __launch_bounds__(kThreads4, MIN_CTAS) decode_int4_kernel(const 
     // the pool is flagged and replaced: the output is unspecified, every read
     // stays inside the pool.
     auto enter = [&](const int4& d) {
-        int lo;
-        num_tiles = tiles_of(d, lo);
-        next_tile = 0;
+        int lo, num_tiles;
+        num_units = units_of(d, lo, num_tiles);
+        next_unit = 0;
         int id = id_next;
         if (id < 0 || id >= p.num_blocks) {
             raise_error(p.error_word, PA_DEVERR_BLOCK_ID);
             id = 0;
         }
-        place = (static_cast<uint32_t>(id) * Hkv + d.y) * (bs / kTileRows) + off_next;
+        // A unit's missing second tile is the pool's first one: in bounds, and
+        // every row of it is masked.
+        place = lane < num_tiles ? (static_cast<uint32_t>(id) * Hkv + d.y) * (bs / kTileRows) + off_next : 0u;
     };
-    // Copies one tile into the given stage (one commit group).
-    auto copy_tile = [&](uint32_t tile) {
-        const uint32_t dst = ring + issue_stage * Smem::kStage;
-        const size_t at = static_cast<size_t>(tile) * Smem::kCodes;
-        const uint8_t* ks = static_cast<const uint8_t*>(p.k_cache) + at + lane * 16;
-        const uint8_t* vs = static_cast<const uint8_t*>(p.v_cache) + at + lane * 16;
-        // V chunks are permuted within their 128 bytes so that the reads of
-        // rows 2 t4 + const by the lanes (gid, t4) hit every bank once.
-        const int line = lane >> 3;
-        const int sw = D == 128 ? (line << 1) : ((line & 1) << 1);
-        const uint32_t vd = dst + Smem::kCodes + line * 128 + (((lane & 7) ^ sw) << 4);
-        cp_async_16(dst + lane * 16, ks);
-        cp_async_16(vd, vs);
-        if constexpr (D == 128) {
-            cp_async_16(dst + 512 + lane * 16, ks + 512);
-            cp_async_16(vd + 512, vs + 512);
-        }
-        if (lane < 8) {
-            const uint32_t* pairs = lane < 4 ? p.k_pairs : p.v_pairs;
-            cp_async_16(dst + 2 * Smem::kCodes + lane * 16,
-                        pairs + static_cast<size_t>(tile) * kTileRows + (lane & 3) * 4);
+    // Copies one tile. A lane takes 16-byte chunk `lane` (and lane + 32) of the K
+    // and of the V codes, rows in order; chunks are permuted within each 128
+    // bytes so that the reads below hit every bank once: K rows 2 gid + const by
+    // lanes (gid, t4), V chunks of 8 rows in order.
+    const int line = lane >> 3;            // of 128 bytes: 2 rows (D = 128) or 4
+    const uint32_t k_to = line * 128 + (((lane & 7) ^ ((line & 1) << (D == 128 ? 2 : 1))) << 4);
+    const uint32_t v_to = Smem::kCodes + line * 128 + (((lane & 7) ^ (D == 128 ? line : line & 1)) << 4);
+    const uint8_t* const k_from = static_cast<const uint8_t*>(p.k_cache) + lane * 16;
+    const uint8_t* const v_from = static_cast<const uint8_t*>(p.v_cache) + lane * 16;
+    // Pairs of both tiles in one instruction: lanes 0-7 the first tile's, 8-15
+    // the second's (4 chunks of K, 4 of V each).
+    const uint32_t* const pairs_from = ((lane & 4) ? p.v_pairs : p.k_pairs) + (lane & 3) * 4;
+    const uint32_t pairs_to = ((lane >> 3) & 1) * Smem::kTile + 2 * Smem::kCodes + (lane & 7) * 16;
+    auto copy_codes = [&](uint32_t tile, uint32_t to) {
+        const uint8_t* ks = k_from + static_cast<size_t>(tile) * Smem::kCodes;
+        const uint8_t* vs = v_from + static_cast<size_t>(tile) * Smem::kCodes;
+        cp_async_16(to + k_to, ks);
+        cp_async_16(to + v_to, vs);
+        if constexpr (D == 128) {          // 4 lines on: both permutations repeat
+            cp_async_16(to + k_to + 512, ks + 512);
+            cp_async_16(to + v_to + 512, vs + 512);
         }
     };
     int total = 0, j_next = 1;
@@ -193,87 +211,88 @@ __global__ void __launch_bounds__(kThreads4, MIN_CTAS) decode_int4_kernel(const 
         if (k >= total) return make_int4(-1, 0, 0, 0);
         return j < 2 ? first_items[j] : p.items[k];
     };
-    // The next tile of the stream, if any; a commit group in any case.
+    // The next unit of the stream, if any; a commit group in any case.
     auto issue = [&]() {
-        while (next_tile == num_tiles && d_next.x >= 0) {
+        while (next_unit == num_units && d_next.x >= 0) {
             enter(d_next);
             d_next = d_after;
             fetch(d_next);
             ++j_next;
             d_after = own_item(j_next + 1);
         }
-        if (next_tile < num_tiles) {
-            copy_tile(__shfl_sync(0xffffffffu, place, next_tile));
-            ++next_tile;
+        if (next_unit < num_units) {
+            const uint32_t a = __shfl_sync(0xffffffffu, place, 2 * next_unit);
+            const uint32_t b = __shfl_sync(0xffffffffu, place, 2 * next_unit + 1);
+            copy_codes(a, issue_at);
+            copy_codes(b, issue_at + Smem::kTile);
+            cp_async_16_if(lane < 16, issue_at + pairs_to,
+                           pairs_from + static_cast<size_t>((lane & 8) ? b : a) * kTileRows);
+            ++next_unit;
         }
         cp_async_commit();
-        issue_stage = issue_stage + 1 == STAGES ? 0 : issue_stage + 1;
+        issue_at += Smem::kStage;
+        if (issue_at == ring_end) issue_at = ring;
     };
 
-    // ---- q of an item: raw rows (lane (gid, t4): column gid, D / 4 dims from
-    // t4 * D / 4), then the MMA's B fragments and the column's scale and sum.
-    uint4 q_raw[D / 32];
+    // ---- q of an item. Warp w deals columns 2 w and 2 w + 1: 16 lanes each (8
+    // with D = 64), 8 dims a lane, as f16 into the B fragments of the MMAs' lanes
+    // (gid = column, t4 = the lane's quarter of the dims).
+    constexpr int kQLanes = D / 8;
+    const int q_col = 2 * warp + lane / 16, q_part = lane % 16;
+    const bool q_mine = q_col < ncols && q_part < kQLanes;
+    const int q_row = q_mine ? q_col / grp * p.num_heads + q_col % grp : 0;
+    uint4 q_raw = make_uint4(0u, 0u, 0u, 0u);
     auto load_q = [&](const int4& d) {
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) q_raw[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (d.x >= 0 && gid < ncols) {
-            const uint4* src = reinterpret_cast<const uint4*>(
-                static_cast<const __nv_bfloat16*>(p.q) + query_row(p, d.x, d.y, gid, grp) * D + t4 * (D / 4));
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) q_raw[i] = __ldg(src + i);
-        }
+        if (d.x >= 0 && q_mine)
+            q_raw = __ldg(reinterpret_cast<const uint4*>(
+                static_cast<const __nv_bfloat16*>(p.q) +
+                (static_cast<size_t>(d.x) * Q * p.num_heads + d.y * grp + q_row) * D) + q_part);
     };
-    uint32_t qb[2 * kKWords][2];
-    float qf[2], qsum[2];                  // of columns 2 t4 and 2 t4 + 1
     auto deal_q = [&]() {
-        float mx = 0.f, sum = 0.f;
+        const uint32_t w[4] = {q_raw.x, q_raw.y, q_raw.z, q_raw.w};
+        float x[8], mx = 0.f;
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-            const uint32_t w[4] = {q_raw[i].x, q_raw[i].y, q_raw[i].z, q_raw[i].w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float a = bf16_lo(w[e]), b = bf16_hi(w[e]);
-                mx = fmaxf(mx, fmaxf(fabsf(a), fabsf(b)));
-                sum += a + b;
-            }
+        for (int e = 0; e < 4; ++e) {
+            x[2 * e] = bf16_lo(w[e]);
+            x[2 * e + 1] = bf16_hi(w[e]);
+            mx = fmaxf(mx, fmaxf(fabsf(x[2 * e]), fabsf(x[2 * e + 1])));
         }
 #pragma unroll
-        for (int off = 1; off < 4; off <<= 1) {
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-            sum += __shfl_xor_sync(0xffffffffu, sum, off);
-        }
-        // f = 2^k with mx * f in [2^12, 2^13); 1 / f = 2^-k.
+        for (int off = 8; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+        // f = 2^k with mx * f in [2^12, 2^13); 1 / f = 2^-k. A negative scale
+        // turns q, so that the factor F below is positive.
         const int ex = max(13, min(253, static_cast<int>(__float_as_uint(mx) >> 23)));
-        const float f = __uint_as_float(static_cast<uint32_t>(min(254, 266 - ex)) << 23);
-        const float inv = __uint_as_float(static_cast<uint32_t>(max(1, ex - 12)) << 23);
+        const float f = copysignf(__uint_as_float(static_cast<uint32_t>(266 - ex) << 23), p.scale_log2);
+        const float inv = __uint_as_float(static_cast<uint32_t>(ex - 12) << 23);
+        const float g = f * 0.0625f;
+        if (q_col < 8 && q_part < kQLanes)
+            q_frag[q_part % kKWords * 32 + q_col * 4 + q_part / kKWords] =
+                make_uint4(pack_f16x2(x[0] * f, x[4] * f), pack_f16x2(x[1] * g, x[5] * g),
+                           pack_f16x2(x[2] * f, x[6] * f), pack_f16x2(x[3] * g, x[7] * g));
+        // S = F S', S' = s acc + lo qsum, acc = f 2^-24 q . c, qsum = f 2^-24 q . 1,
+        // F = |scale| 2^24 / f (kept above 0: scale 0 gives equal weights).
+        if (q_part == 0) col_f[q_col] = fmaxf(fabsf(p.scale_log2) * (inv * 16777216.f), 1e-30f);
+    };
+    uint32_t qb[kKWords][4];
+    float qf[2], qsum[2];                  // of columns 2 t4 and 2 t4 + 1
+    auto take_q = [&]() {
+        float ones[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < kKWords; ++i) {
-            const uint32_t w[4] = {q_raw[i].x, q_raw[i].y, q_raw[i].z, q_raw[i].w};
-            float x[8];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                x[2 * e] = bf16_lo(w[e]) * f;
-                x[2 * e + 1] = bf16_hi(w[e]) * f;
-            }
-            qb[2 * i][0] = pack_f16x2(x[0], x[4]);
-            qb[2 * i][1] = pack_f16x2(x[1] * 0.0625f, x[5] * 0.0625f);
-            qb[2 * i + 1][0] = pack_f16x2(x[2], x[6]);
-            qb[2 * i + 1][1] = pack_f16x2(x[3] * 0.0625f, x[7] * 0.0625f);
+            const uint4 v = q_frag[i * 32 + lane];
+            qb[i][0] = v.x; qb[i][1] = v.y; qb[i][2] = v.z; qb[i][3] = v.w;
+            mma_16816_f16(ones, 0x00010001u, 0x00010001u, 0x00100010u, 0x00100010u, v.x, v.y);
+            mma_16816_f16(ones, 0x00010001u, 0x00010001u, 0x00100010u, 0x00100010u, v.z, v.w);
         }
-        // S = F (s acc + lo sum'), acc = f 2^-24 q . c: F = scale 2^24 / f.
-        const float F = p.scale_log2 * (inv * 16777216.f);
-        const float sp = sum * (f * (1.f / 16777216.f));
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            qf[i] = __shfl_sync(0xffffffffu, F, 8 * t4 + 4 * i);
-            qsum[i] = __shfl_sync(0xffffffffu, sp, 8 * t4 + 4 * i);
-        }
+        const float2 F = *reinterpret_cast<const float2*>(col_f + 2 * t4);
+        qf[0] = F.x; qf[1] = F.y;
+        qsum[0] = ones[0]; qsum[1] = ones[1];
     };
 
     // The first item where the warp can find it without the plan: its tiles
     // and q are on their way while the CTA computes its work list.
     const int4 first = first_item_by_warp(p, c, lane);
-    static_assert(STAGES - 1 <= kWarpTiles, "a full partition fills the ring");
+    static_assert(STAGES - 1 <= kWarpUnits, "a full partition fills the ring");
     if (first.x >= 0) {
         fetch(first);
         enter(first);
@@ -299,148 +318,158 @@ __global__ void __launch_bounds__(kThreads4, MIN_CTAS) decode_int4_kernel(const 
 #pragma unroll 1
         for (int i = 0; i < STAGES - 1; ++i) issue();
     }
-    __syncthreads();                       // the plan's scratch becomes the merge area
+    deal_q();
+    __syncthreads();                       // q is dealt; the plan's scratch becomes the merge area
 
-    int stage = 0;
+    uint32_t at = ring;                    // the stage of the next unit
     const int j0 = (2 * t4) / grp, j1 = (2 * t4 + 1) / grp;   // the columns' query tokens
+    // This lane's offsets into a tile: K rows 2 gid and 2 gid + 1, the V row that
+    // it points ldmatrix at (lanes 16-31: the next 16 bytes of the same rows).
+    const int k_unit = D == 128 ? t4 ^ ((gid & 1) << 2) : (((gid & 1) << 2) | (t4 >> 1)) ^ (gid & 2);
+    const uint32_t k_at = D == 128 ? gid * 128 : (gid >> 1) * 128 + (t4 & 1) * 8;
+    const int vr = lane & 15;
+    const uint32_t v_row = D == 128 ? (vr >> 1) * 128 : (vr >> 2) * 128;
+    const int v_unit = D == 128 ? (((vr & 1) << 2) | (lane >> 4)) ^ ((vr >> 1) & 3)
+                                : (((vr & 3) << 1) | (lane >> 4)) ^ ((vr >> 2) & 1);
     int4 it_next = own_item(1);
     for (int j = 0; it.x >= 0; ++j) {
         const int n = it.w;
-        int lo;
-        const int cnt = tiles_of(it, lo);
+        int lo, tiles;
+        const int cnt = units_of(it, lo, tiles);
         const int4 it_after = own_item(j + 2);
-        deal_q();
+        take_q();
         float o[kMt][4];
 #pragma unroll
         for (int mt = 0; mt < kMt; ++mt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[mt][e] = 0.f;
-        float m0 = -INFINITY, m1 = -INFINITY, ref0 = 0.f, ref1 = 0.f;
+        // References in units of S'; r = -F m (0 while a column has seen no row).
+        float m0 = -INFINITY, m1 = -INFINITY, r0 = 0.f, r1 = 0.f;
         float l0 = 0.f, l1 = 0.f, z0 = 0.f, z1 = 0.f;
+        int ve = 1;                        // e + 127
+        float vinv = 0.f;                  // 2^-e
+        float vtop = -1.f;                 // 2^(e + 1); -1: raise at the next unit
 
         for (int i = 0; i < cnt; ++i) {
             issue();
             cp_async_wait_group<STAGES - 1>();
             __syncwarp();
-            const uint32_t kb = ring + stage * Smem::kStage;
-            const uint32_t vb = kb + Smem::kCodes;
-            const uint32_t pb = vb + Smem::kCodes;
-            const int row0 = lo + kTileRows * (warp + kWarps * i);
+            const int row0 = lo + kUnitRows * (warp + kWarps * i);
 
-            // ---- acc = q . c, rows gid and gid + 8, columns 2 t4 and 2 t4 + 1
-            uint32_t kw[2][kKWords];
-            if constexpr (D == 128) {
-                const uint4 a = lds128(kb + lane * 16), b = lds128(kb + 512 + lane * 16);
-                kw[0][0] = a.x; kw[0][1] = a.y; kw[0][2] = a.z; kw[0][3] = a.w;
-                kw[1][0] = b.x; kw[1][1] = b.y; kw[1][2] = b.z; kw[1][3] = b.w;
-            } else {
-                const uint2 a = lds64(kb + lane * 8), b = lds64(kb + 256 + lane * 8);
-                kw[0][0] = a.x; kw[0][1] = a.y;
-                kw[1][0] = b.x; kw[1][1] = b.y;
-            }
-            float acc[4] = {0.f, 0.f, 0.f, 0.f}, bcc[4] = {0.f, 0.f, 0.f, 0.f};
+            // ---- S' of rows 2 gid, 2 gid + 1 of both tiles, columns 2 t4, 2 t4 + 1
+            float S[2][4];
+            uint2 vp[2];
 #pragma unroll
-            for (int u = 0; u < kKWords; ++u) {
-                const uint32_t a = kw[0][u], b = kw[1][u], a8 = a >> 8, b8 = b >> 8;
-                mma_16816_f16(acc, a & 0x000f000fu, b & 0x000f000fu, a & 0x00f000f0u, b & 0x00f000f0u,
-                              qb[2 * u][0], qb[2 * u][1]);
-                mma_16816_f16(bcc, a8 & 0x000f000fu, b8 & 0x000f000fu, a8 & 0x00f000f0u,
-                              b8 & 0x00f000f0u, qb[2 * u + 1][0], qb[2 * u + 1][1]);
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t kb = at + h * Smem::kTile + k_at, pb = at + h * Smem::kTile + 2 * Smem::kCodes;
+                uint32_t kw[2][kKWords];
+                if constexpr (D == 128) {
+                    const uint4 a = lds128(kb + k_unit * 16), b = lds128(kb + (k_unit ^ 4) * 16);
+                    kw[0][0] = a.x; kw[0][1] = a.y; kw[0][2] = a.z; kw[0][3] = a.w;
+                    kw[1][0] = b.x; kw[1][1] = b.y; kw[1][2] = b.z; kw[1][3] = b.w;
+                } else {
+                    const uint2 a = lds64(kb + k_unit * 16), b = lds64(kb + (k_unit ^ 2) * 16);
+                    kw[0][0] = a.x; kw[0][1] = a.y;
+                    kw[1][0] = b.x; kw[1][1] = b.y;
+                }
+                float acc[4] = {0.f, 0.f, 0.f, 0.f}, bcc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int u = 0; u < kKWords; ++u) {
+                    const uint32_t a = kw[0][u], b = kw[1][u], a8 = a >> 8, b8 = b >> 8;
+                    mma_16816_f16(acc, a & 0x000f000fu, b & 0x000f000fu, a & 0x00f000f0u,
+                                  b & 0x00f000f0u, qb[u][0], qb[u][1]);
+                    mma_16816_f16(bcc, a8 & 0x000f000fu, b8 & 0x000f000fu, a8 & 0x00f000f0u,
+                                  b8 & 0x00f000f0u, qb[u][2], qb[u][3]);
+                }
+                const uint2 kp = lds64(pb + 8 * gid);
+                vp[h] = lds64(pb + 64 + 8 * gid);
+                S[h][0] = fmaf(int4_step(kp.x), acc[0] + bcc[0], int4_lo(kp.x) * qsum[0]);
+                S[h][1] = fmaf(int4_step(kp.x), acc[1] + bcc[1], int4_lo(kp.x) * qsum[1]);
+                S[h][2] = fmaf(int4_step(kp.y), acc[2] + bcc[2], int4_lo(kp.y) * qsum[0]);
+                S[h][3] = fmaf(int4_step(kp.y), acc[3] + bcc[3], int4_lo(kp.y) * qsum[1]);
             }
-            const uint32_t kp0 = lds32(pb + 4 * gid), kp1 = lds32(pb + 32 + 4 * gid);
-            uint32_t vp0 = lds32(pb + 64 + 4 * gid), vp1 = lds32(pb + 96 + 4 * gid);
-            bool see[4] = {true, true, true, true};
-            const bool edge = row0 + kTileRows - 1 > n - Q || (window > 0 && row0 <= n - 1 - window);
-            if (edge) {
+            if (row0 + kUnitRows - 1 > n - Q || (window > 0 && row0 <= n - 1 - window)) {
+                // Some token does not see some row of the unit (whose second tile
+                // may not be there at all).
                 const int top0 = n - Q + j0, top1 = n - Q + j1;
-                const int r = row0 + gid;
                 const int w = window > 0 ? window : INT_MAX;
-                // differences of rows fit: both are below 2^31
-                see[0] = r <= top0 && top0 - r < w;
-                see[1] = r <= top1 && top1 - r < w;
-                see[2] = r + 8 <= top0 && top0 - r - 8 < w;
-                see[3] = r + 8 <= top1 && top1 - r - 8 < w;
-                // Rows that no token sees may hold any pair.
-                if (r >= n || n - Q - r >= w) vp0 = 0u;
-                if (r + 8 >= n || n - Q - r - 8 >= w) vp1 = 0u;
-            }
-            // ---- T = S + e
-            const uint32_t e0 = value_exponent(vp0), e1 = value_exponent(vp1);
-            const float x0 = static_cast<float>(static_cast<int>(e0) - 127);
-            const float x1 = static_cast<float>(static_cast<int>(e1) - 127);
-            const float i0 = __uint_as_float((254u - e0) << 23), i1 = __uint_as_float((254u - e1) << 23);
-            float T[4];
-            T[0] = fmaf(fmaf(int4_step(kp0), acc[0] + bcc[0], int4_lo(kp0) * qsum[0]), qf[0], x0);
-            T[1] = fmaf(fmaf(int4_step(kp0), acc[1] + bcc[1], int4_lo(kp0) * qsum[1]), qf[1], x0);
-            T[2] = fmaf(fmaf(int4_step(kp1), acc[2] + bcc[2], int4_lo(kp1) * qsum[0]), qf[0], x1);
-            T[3] = fmaf(fmaf(int4_step(kp1), acc[3] + bcc[3], int4_lo(kp1) * qsum[1]), qf[1], x1);
-            if (edge) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (!see[e]) T[e] = -INFINITY;
+                for (int h = 0; h < 2; ++h) {
+                    const int r = row0 + kTileRows * h + 2 * gid;
+                    if (!(r <= top0 && top0 - r < w)) S[h][0] = -INFINITY;
+                    if (!(r <= top1 && top1 - r < w)) S[h][1] = -INFINITY;
+                    if (!(r + 1 <= top0 && top0 - r - 1 < w)) S[h][2] = -INFINITY;
+                    if (!(r + 1 <= top1 && top1 - r - 1 < w)) S[h][3] = -INFINITY;
+                    // Rows that no token sees may hold any pair.
+                    if (r >= n || n - Q - r >= w) vp[h].x = 0u;
+                    if (r + 1 >= n || n - Q - r - 1 >= w) vp[h].y = 0u;
+                }
             }
-            float mx0 = fmaxf(T[0], T[2]), mx1 = fmaxf(T[1], T[3]);
-            if (__any_sync(0xffffffffu, mx0 > m0 + kRaise || mx1 > m1 + kRaise)) {
+            const float smax = fmaxf(fmaxf(int4_step(vp[0].x), int4_step(vp[0].y)),
+                                     fmaxf(int4_step(vp[1].x), int4_step(vp[1].y)));
+            float mx0 = fmaxf(fmaxf(S[0][0], S[0][2]), fmaxf(S[1][0], S[1][2]));
+            float mx1 = fmaxf(fmaxf(S[0][1], S[0][3]), fmaxf(S[1][1], S[1][3]));
+            if (__any_sync(0xffffffffu, fmaxf(fmaf(mx0, qf[0], r0), fmaf(mx1, qf[1], r1)) > kRaise || smax >= vtop)) {
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1) {
                     mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, off));
                     mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
                 }
                 const float n0 = fmaxf(m0, mx0), n1 = fmaxf(m1, mx1);
-                // A column that has seen no row keeps M = -inf and sums of 0.
-                ref0 = n0 == -INFINITY ? 0.f : n0;
-                ref1 = n1 == -INFINITY ? 0.f : n1;
-                const float a0 = fast_exp2(m0 - ref0), a1 = fast_exp2(m1 - ref1);
-                m0 = n0;
-                m1 = n1;
-                l0 *= a0; z0 *= a0; l1 *= a1; z1 *= a1;
+                const float q0 = n0 == -INFINITY ? 0.f : -(n0 * qf[0]);
+                const float q1 = n1 == -INFINITY ? 0.f : -(n1 * qf[1]);
+                const float a0 = m0 == -INFINITY ? 0.f : fast_exp2(q0 - r0);
+                const float a1 = m1 == -INFINITY ? 0.f : fast_exp2(q1 - r1);
+                m0 = n0; m1 = n1; r0 = q0; r1 = q1;
+                const int ne = max(ve, min(253, static_cast<int>(__reduce_max_sync(0xffffffffu,
+                                                                  __float_as_uint(smax)) >> 23)));
+                const float ae = __uint_as_float(static_cast<uint32_t>(max(0, 127 + ve - ne)) << 23);
+                ve = ne;
+                vinv = __uint_as_float(static_cast<uint32_t>(254 - ne) << 23);
+                // A column that has seen no row yet takes its first reference
+                // from the next unit.
+                vtop = __any_sync(0xffffffffu, m0 == -INFINITY || m1 == -INFINITY)
+                           ? -1.f : __uint_as_float(static_cast<uint32_t>(ne + 1) << 23);
+                if (i > 0) {               // else every sum is 0
+                    l0 *= a0; z0 *= a0; l1 *= a1; z1 *= a1;
+                    const float b0 = a0 * ae, b1 = a1 * ae;
 #pragma unroll
-                for (int mt = 0; mt < kMt; ++mt) {
-                    o[mt][0] *= a0; o[mt][1] *= a1; o[mt][2] *= a0; o[mt][3] *= a1;
+                    for (int mt = 0; mt < kMt; ++mt) {
+                        o[mt][0] *= b0; o[mt][1] *= b1; o[mt][2] *= b0; o[mt][3] *= b1;
+                    }
                 }
             }
-            const float E0 = fast_exp2(T[0] - ref0), E1 = fast_exp2(T[1] - ref1);
-            const float E2 = fast_exp2(T[2] - ref0), E3 = fast_exp2(T[3] - ref1);
-            const float u0 = int4_step(vp0) * i0, u1 = int4_step(vp1) * i1;
-            const float y0 = int4_lo(vp0) * i0, y1 = int4_lo(vp1) * i1;
-            l0 = fmaf(E2, i1, fmaf(E0, i0, l0));
-            l1 = fmaf(E3, i1, fmaf(E1, i0, l1));
-            z0 = fmaf(E2, y1, fmaf(E0, y0, z0));
-            z1 = fmaf(E3, y1, fmaf(E1, y0, z1));
-            // B operand: lane (gid, t4) takes column gid, rows 2 t4, 2 t4 + 1 (+ 8)
-            const uint32_t b0 = transpose8x8(pack_f16x2(E0 * u0, E1 * u0));
-            const uint32_t b1 = transpose8x8(pack_f16x2(E2 * u1, E3 * u1));
-
-            // ---- o += codes(V)^T . P, rows 2 t4, 2 t4 + 1, 2 t4 + 8, 2 t4 + 9
-            uint32_t vw[4][kVWords];
+            // ---- o += codes(V)^T . P, tile by tile
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                if constexpr (D == 128) {
-                    const int line = t4 + 4 * (q >> 1);
-                    const int unit = (((q & 1) << 2) | (gid >> 1)) ^ (t4 << 1);
-                    const uint2 v = lds64(vb + line * 128 + unit * 16 + (gid & 1) * 8);
-                    vw[q][0] = v.x; vw[q][1] = v.y;
-                } else {
-                    const int r = 2 * t4 + (q & 1) + 8 * (q >> 1);
-                    const int unit = (((r & 3) << 1) | (gid >> 2)) ^ (((r >> 2) & 1) << 1);
-                    vw[q][0] = lds32(vb + (r >> 2) * 128 + unit * 16 + (gid & 3) * 4);
-                }
-            }
+            for (int h = 0; h < 2; ++h) {
+                const float E0 = fast_exp2(fmaf(S[h][0], qf[0], r0)), E1 = fast_exp2(fmaf(S[h][1], qf[1], r1));
+                const float E2 = fast_exp2(fmaf(S[h][2], qf[0], r0)), E3 = fast_exp2(fmaf(S[h][3], qf[1], r1));
+                const float u0 = int4_step(vp[h].x) * vinv, u1 = int4_step(vp[h].y) * vinv;
+                const float y0 = int4_lo(vp[h].x), y1 = int4_lo(vp[h].y);
+                l0 += E0 + E2;
+                l1 += E1 + E3;
+                z0 = fmaf(E2, y1, fmaf(E0, y0, z0));
+                z1 = fmaf(E3, y1, fmaf(E1, y0, z1));
+                // B operand: lane (gid, t4) takes column gid, the rows of lane groups
+                // 2 t4 and 2 t4 + 1: rows 4 t4, 4 t4 + 2 (b0) and 4 t4 + 1, 4 t4 + 3 (b1)
+                const uint32_t b0 = transpose8x8(pack_f16x2(E0 * u0, E1 * u0));
+                const uint32_t b1 = transpose8x8(pack_f16x2(E2 * u1, E3 * u1));
+                const uint32_t vb = at + h * Smem::kTile + Smem::kCodes + v_row;
 #pragma unroll
-            for (int u = 0; u < kVWords; ++u) {
+                for (int u = 0; u < D / 64; ++u) {
+                    // Rows 4 t4 .. + 3 (bytes 0..3) of byte columns 32 u + gid, + 8, + 16, + 24.
+                    uint32_t w[4];
+                    ldsm_x2_trans_b8(vb + ((v_unit ^ (2 * u)) << 4), w[0], w[1], w[2], w[3]);
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    const uint32_t sel = hf ? 0x7632u : 0x5410u;
-                    const uint32_t x = prmt(vw[0][u], vw[1][u], sel), y = prmt(vw[2][u], vw[3][u], sel);
-                    const uint32_t x8 = x >> 8, y8 = y >> 8;
-                    mma_16816_f16(o[4 * u + 2 * hf], x & 0x000f000fu, x & 0x00f000f0u,
-                                  y & 0x000f000fu, y & 0x00f000f0u, b0, b1);
-                    mma_16816_f16(o[4 * u + 2 * hf + 1], x8 & 0x000f000fu, x8 & 0x00f000f0u,
-                                  y8 & 0x000f000fu, y8 & 0x00f000f0u, b0, b1);
+                    for (int q = 0; q < 4; ++q) {
+                        const uint32_t x = w[q] & 0x00ff00ffu, y = prmt(w[q], 0u, 0x4341u);
+                        mma_16816_f16(o[4 * u + q], x & 0x000f000fu, x, y & 0x000f000fu, y, b0, b1);
+                    }
                 }
             }
             __syncwarp();                  // the stage may be filled again
-            stage = stage + 1 == STAGES ? 0 : stage + 1;
+            at += Smem::kStage;
+            if (at == ring_end) at = ring;
         }
 
         // ---- the warp's state, then the next item's q while the CTA merges
@@ -454,50 +483,61 @@ __global__ void __launch_bounds__(kThreads4, MIN_CTAS) decode_int4_kernel(const 
         float* st = merge + warp * Smem::kState;
         float* ml = st + NC * Smem::kCol;
         const int c0 = 2 * t4, c1 = 2 * t4 + 1;
-        if (gid == 0) {
-            if (c0 < NC) { ml[c0] = m0; ml[NC + c0] = l0; }
-            if (c1 < NC) { ml[c1] = m1; ml[NC + c1] = l1; }
-        }
         if (c0 < NC) {                     // NC is even: c1 < NC too
+            if (gid == 0) {
+                ml[c0] = m0 == -INFINITY ? -INFINITY : -r0;
+                ml[c1] = m1 == -INFINITY ? -INFINITY : -r1;
+                ml[NC + c0] = l0;
+                ml[NC + c1] = l1;
+            }
+            // even dims: o 2^e 2^24; odd ones: (o - even's) 2^e 2^20
+            const float ve2 = __uint_as_float(static_cast<uint32_t>(ve) << 23);
 #pragma unroll
             for (int mt = 0; mt < kMt; ++mt) {
-                const int at = gid * (kLaneDims + 2) + 2 * mt;   // dims gid * kLaneDims + 2 mt, + 1
-                *reinterpret_cast<float2*>(st + c0 * Smem::kCol + at) =
-                    make_float2(fmaf(o[mt][0], 16777216.f, z0), fmaf(o[mt][2], 1048576.f, z0));
-                *reinterpret_cast<float2*>(st + c1 * Smem::kCol + at) =
-                    make_float2(fmaf(o[mt][1], 16777216.f, z1), fmaf(o[mt][3], 1048576.f, z1));
+                const int d = 16 * mt + 2 * gid;   // dims d and d + 1
+                *reinterpret_cast<float2*>(st + c0 * Smem::kCol + d) =
+                    make_float2(fmaf(o[mt][0] * 16777216.f, ve2, z0),
+                                fmaf((o[mt][2] - o[mt][0]) * 1048576.f, ve2, z0));
+                *reinterpret_cast<float2*>(st + c1 * Smem::kCol + d) =
+                    make_float2(fmaf(o[mt][1] * 16777216.f, ve2, z1),
+                                fmaf((o[mt][3] - o[mt][1]) * 1048576.f, ve2, z1));
             }
         }
         load_q(it_next);
         __syncthreads();
         const int nparts = (n - seq_row_base(n, p.window) + kItemRows - 1) / kItemRows;
-        for (int idx = threadIdx.x; idx < ncols * D; idx += kThreads4) {
-            const int g = idx / D, d = idx - g * D;
-            const float* col = merge + g * Smem::kCol + d / kLaneDims * (kLaneDims + 2) + d % kLaneDims;
+        // Four dims of a column per thread.
+        for (int idx = threadIdx.x; idx < ncols * (D / 4); idx += kThreads4) {
+            const int g = idx / (D / 4), d = idx % (D / 4) * 4;
+            const float* col = merge + g * Smem::kCol + d;
             const float* mlg = merge + NC * Smem::kCol + g;
             float M = -INFINITY;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) M = fmaxf(M, mlg[w * Smem::kState]);
             const float ref = M == -INFINITY ? 0.f : M;
-            float L = 0.f, O = 0.f;
+            float L = 0.f, O[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
                 const float cw = fast_exp2(mlg[w * Smem::kState] - ref);
+                const float2 a = *reinterpret_cast<const float2*>(col + w * Smem::kState);
+                const float2 b = *reinterpret_cast<const float2*>(col + w * Smem::kState + 2);
                 L = fmaf(cw, mlg[w * Smem::kState + NC], L);
-                O = fmaf(cw, col[w * Smem::kState], O);
+                O[0] = fmaf(cw, a.x, O[0]);
+                O[1] = fmaf(cw, a.y, O[1]);
+                O[2] = fmaf(cw, b.x, O[2]);
+                O[3] = fmaf(cw, b.y, O[3]);
             }
-            const size_t row = query_row(p, it.x, it.y, g, grp);
+            const size_t row = static_cast<size_t>(it.x) * Q * p.num_heads + it.y * grp + col_row[g];
             if (nparts == 1) {
-                static_cast<__nv_bfloat16*>(p.out)[row * D + d] = __float2bfloat16_rn(O / L);
+                *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + row * D + d) =
+                    make_uint2(pack_bf16x2(O[0] / L, O[1] / L), pack_bf16x2(O[2] / L, O[3] / L));
             } else {
                 const size_t slot = row * p.max_parts + it.z;
-                p.part_o[slot * D + d] = O;
-                if (d == 0) {
-                    p.part_ml[2 * slot] = M;
-                    p.part_ml[2 * slot + 1] = L;
-                }
+                *reinterpret_cast<float4*>(p.part_o + slot * D + d) = make_float4(O[0], O[1], O[2], O[3]);
+                if (d == 0) *reinterpret_cast<float2*>(p.part_ml + 2 * slot) = make_float2(M, L);
             }
         }
+        deal_q();
         __syncthreads();                   // the next item's states overwrite the merge area
         it = it_next;
         it_next = it_after;
@@ -554,8 +594,8 @@ cudaError_t launch_decode_int4(const DecodeParams& p, cudaStream_t stream) {
     }
     const int ncols = p.num_heads / p.num_kv_heads * p.num_queries;
     if (p.head_dim == 128)
-        return ncols <= 4 ? run<128, 4, 5, 4>(p, sms, stream) : run<128, 8, 4, 4>(p, sms, stream);
-    return ncols <= 4 ? run<64, 4, 6, 4>(p, sms, stream) : run<64, 8, 6, 4>(p, sms, stream);
+        return ncols <= 4 ? run<128, 4, 3, 3>(p, sms, stream) : run<128, 8, 3, 3>(p, sms, stream);
+    return ncols <= 4 ? run<64, 4, 4, 3>(p, sms, stream) : run<64, 8, 4, 3>(p, sms, stream);
 }
 
 }  // namespace pa

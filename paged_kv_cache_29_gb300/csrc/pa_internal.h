@@ -191,6 +191,10 @@ constexpr int kDefaultPartition = 512;
 // than CTAs a small batch waits for its largest item, and there 1024 rows
 // measured slower.
 constexpr int kDefaultPartition8 = 1024;
+// INT4 caches: about the bytes of 512 bf16 rows again (139 KB at head dim 128).
+// An item's fixed work (q, the warps' merge, its partial) is that of four
+// 32-row units per warp: 8b_gqa 51.3 us at 1024 rows, 58.0 at 512.
+constexpr int kDefaultPartition4 = 1024;
 constexpr int kNoLongPartitions = 0x7fffffff;   // partition_long_from: one size for all
 // Kernel of pa_decode_fp8 and pa_append_decode_fp8 when none is requested.
 constexpr pa_kernel kFp8DefaultKernel = PA_KERNEL_MMA;

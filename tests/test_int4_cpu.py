@@ -175,7 +175,7 @@ def test_int4_pools_copy_by_their_byte_rows(lib):
     def copy(d):
         return lib.pa_copy_blocks(None, None, None, 1, 2, d, 16, 8, 4, None, None)
     assert copy(48) == UNSUPPORTED and copy(33) == UNSUPPORTED and copy(64) == INVALID   # null pools
-    assert pa.pa_default_partition_size("int4") == 512
+    assert pa.pa_default_partition_size("int4") == 1024
 
 
 # ------------------------------------------------------------------ binding
