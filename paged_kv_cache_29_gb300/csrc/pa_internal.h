@@ -146,7 +146,7 @@ struct NormRopeParams {
     int rot_dim, max_position, num_axes, interleaved;
     int block_size;
     int splits;                    // warps per token
-    uint8_t pair_axis[128];        // rot_dim / 2 <= 128
+    alignas(4) uint8_t pair_axis[128];   // rot_dim / 2 <= 128; read four at a time
 };
 cudaError_t launch_norm_rope(const NormRopeParams& p, pa_dtype dtype, cudaStream_t stream);
 

@@ -7,11 +7,13 @@
 //
 // fp32 throughout, one rounding at the store.
 //
-// TPR lanes hold a row, 8 dims each; a pair's other half is 8 lanes' worth
-// away (halves) or in the same lane (interleaved). A warp works on one token:
-// its cosines and sines are loaded once and stay in registers for all the rows
-// that the warp takes of it (rows part, part + splits, ... of the token's q, K
-// and V heads).
+// TPR lanes hold a row, 8 dims each, dealt so that both halves of a pair are in
+// one lane: with pairs (i, i + rot / 2) lane c < rot / 8 holds dims 4 c .. + 3
+// and rot / 2 + 4 c .. + 3, every other lane dims 8 c .. + 7. Either way a lane
+// turns pairs 4 c .. 4 c + 3, so four cosines and four sines, loaded once per
+// token, serve every row that the warp takes of it; nothing but the sum of
+// squares crosses lanes. A warp works on one token: passes part, part + splits,
+// ... of its q, K and V rows, U passes' loads in flight.
 #include "pa_int4.cuh"
 #include "pa_internal.h"
 
@@ -20,18 +22,46 @@ namespace pa {
 namespace {
 
 constexpr int kThreads = 128;
+#ifndef PA_NW
+#define PA_NW 4864
+#endif
+constexpr long long kNormRopeWarps = PA_NW;
 
 enum Dest { kOut, kPool, kPool4 };
 
-__device__ __forceinline__ float round_to(float x, const float*) { return x; }
-__device__ __forceinline__ float round_to(float x, const __nv_bfloat16*) {
-    return __bfloat162float(__float2bfloat16_rn(x));
-}
+// Four consecutive elements.
+template <typename T>
+struct Quad;
+template <>
+struct Quad<__nv_bfloat16> {
+    using Raw = uint2;
+    __device__ static __forceinline__ void unpack(const Raw& r, float* x) {
+        x[0] = bf16_lo(r.x); x[1] = bf16_hi(r.x); x[2] = bf16_lo(r.y); x[3] = bf16_hi(r.y);
+    }
+    __device__ static __forceinline__ Raw pack(const float* x) {
+        return make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+    }
+};
+template <>
+struct Quad<float> {
+    using Raw = uint4;
+    __device__ static __forceinline__ void unpack(const Raw& r, float* x) {
+        x[0] = __uint_as_float(r.x); x[1] = __uint_as_float(r.y);
+        x[2] = __uint_as_float(r.z); x[3] = __uint_as_float(r.w);
+    }
+    __device__ static __forceinline__ Raw pack(const float* x) {
+        return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
+                          __float_as_uint(x[3]));
+    }
+};
 
 template <typename T, int TPR, Dest DEST>
 __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    constexpr int kRowsPerWarp = 32 / TPR;
+    using Q = Quad<T>;
+    using Raw = typename Q::Raw;
+    constexpr int kRowsPerPass = 32 / TPR;
+    constexpr int U = sizeof(T) == 2 ? 4 : 2;            // passes in flight
     const int lane = threadIdx.x & 31;
     const int sub = lane / TPR, c = lane % TPR;
     const long long warp = static_cast<long long>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
@@ -39,18 +69,12 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
     const int part = static_cast<int>(warp - t * p.splits);
     if (t >= p.num_tokens) return;                       // whole warps
 
-    const int D = p.head_dim;
-    const bool live = 8 * c < D;
-    const int half = p.rot_dim / 2;
-    const bool turned = 8 * c < p.rot_dim;
-    const bool second = !p.interleaved && 8 * c >= half;  // holds b's
-    // This lane's cosines, and sines with the sign that its element takes.
-    float cs[8], sn[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        cs[e] = 1.f;
-        sn[e] = 0.f;
-    }
+    const int D = p.head_dim, half = p.rot_dim / 2;
+    const bool live = 8 * c < D, turned = 8 * c < p.rot_dim;
+    const bool split = turned && !p.interleaved;         // the lane holds two halves' quads
+    const int d0 = split ? 4 * c : 8 * c, d1 = split ? half + 4 * c : 8 * c + 4;
+
+    float cs[4] = {1.f, 1.f, 1.f, 1.f}, sn[4] = {0.f, 0.f, 0.f, 0.f};
     if (p.rot_dim > 0) {
         bool ok = true;
         for (int a = 0; a < p.num_axes; ++a) {
@@ -62,107 +86,173 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
             return;
         }
         if (turned) {
+            const uint32_t axes = *reinterpret_cast<const uint32_t*>(p.pair_axis + 4 * c);
+            if (axes == (axes & 0xffu) * 0x01010101u) {  // one axis: whole quads of the table
+                const int pos = __ldg(p.positions + static_cast<long long>(axes & 0xffu) * p.num_tokens + t);
+                const float* row = p.cos_sin + static_cast<long long>(pos) * p.rot_dim + 4 * c;
+                const float4 a = __ldg(reinterpret_cast<const float4*>(row));
+                const float4 b = __ldg(reinterpret_cast<const float4*>(row + half));
+                cs[0] = a.x; cs[1] = a.y; cs[2] = a.z; cs[3] = a.w;
+                sn[0] = b.x; sn[1] = b.y; sn[2] = b.z; sn[3] = b.w;
+            } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int i = p.interleaved ? 4 * c + e / 2 : 8 * c - (second ? half : 0) + e;
-                const long long axis = p.pair_axis[i];
-                const int pos = __ldg(p.positions + axis * p.num_tokens + t);
-                const float* row = p.cos_sin + static_cast<long long>(pos) * p.rot_dim;
-                const bool b = p.interleaved ? (e & 1) : second;
-                cs[e] = __ldg(row + i);
-                const float s = __ldg(row + half + i);
-                sn[e] = b ? s : -s;
+                for (int i = 0; i < 4; ++i) {
+                    const long long axis = (axes >> (8 * i)) & 0xffu;
+                    const int pos = __ldg(p.positions + axis * p.num_tokens + t);
+                    const float* row = p.cos_sin + static_cast<long long>(pos) * p.rot_dim + 4 * c + i;
+                    cs[i] = __ldg(row);
+                    sn[i] = __ldg(row + half);
+                }
             }
         }
     }
-    long long slot = -1;
+    long long row0 = 0;                                  // the slot's row of KV head 0 in the pool
+    bool append = false;
     if constexpr (DEST != kOut) {
-        slot = __ldg(p.slot_mapping + t);
-        if (slot >= p.num_slots) {
-            if (part == 0 && lane == 0) raise_error(p.error_word, PA_DEVERR_SLOT);
-            slot = -1;
-        }
+        const long long slot = __ldg(p.slot_mapping + t);
+        append = slot >= 0 && slot < p.num_slots;
+        if (slot >= p.num_slots && part == 0 && lane == 0) raise_error(p.error_word, PA_DEVERR_SLOT);
+        const long long blk = append ? slot / p.block_size : 0;
+        row0 = blk * p.num_kv_heads * p.block_size + (append ? slot - blk * p.block_size : 0);
     }
-    const long long blk = slot >= 0 ? slot / p.block_size : 0;
-    const int off = slot >= 0 ? static_cast<int>(slot - blk * p.block_size) : 0;
-    const int Hq = p.num_heads, Hkv = p.num_kv_heads;
-    const int rows = DEST == kOut ? Hq + Hkv : slot >= 0 ? Hq + 2 * Hkv : Hq;
-    const int partner = p.interleaved ? 0 : (lane - c) + (second ? c - half / 8 : c + half / 8);
 
-    for (int r0 = part * kRowsPerWarp; r0 < rows; r0 += p.splits * kRowsPerWarp) {
-        const int r = r0 + sub;
-        const bool on = r < rows && live;
-        const bool is_q = r < Hq, is_v = r >= Hq + Hkv;
-        const int h = is_q ? r : is_v ? r - Hq - Hkv : r - Hq;
-        // The row's 8 elements as they are (V is copied bit for bit), and as fp32.
-        constexpr int kVecs = sizeof(T) / 2;
-        uint4 raw[kVecs];
-        float x[8];
-#pragma unroll
-        for (int i = 0; i < kVecs; ++i) raw[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (on) {
-            const T* src = is_q   ? static_cast<const T*>(p.q) + t * p.q_stride
-                           : is_v ? static_cast<const T*>(p.v) + t * p.v_stride
-                                  : static_cast<const T*>(p.k) + t * p.k_stride;
-            const uint4* at = reinterpret_cast<const uint4*>(src + static_cast<long long>(h) * D + 8 * c);
-#pragma unroll
-            for (int i = 0; i < kVecs; ++i) raw[i] = at[i];
-        }
-#pragma unroll
-        for (int i = 0; i < kVecs; ++i) ElemTraits<T>::unpack(raw[i], x + i * ElemTraits<T>::kPerChunk);
-        const void* weight = is_q ? p.q_weight : is_v ? nullptr : p.k_weight;
-        float ss = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-#pragma unroll
-        for (int o = TPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        float y[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = x[e];
+    // Normed and turned rows of q or K.
+    auto turn_rows = [&](const void* from, int rows, const void* weight, auto&& put) {
+        float w[8];
         if (weight != nullptr && live) {
-            const float inv = 1.0f / sqrtf(ss / static_cast<float>(D) + p.eps);
-            float w[8];
-            if (p.weight_bf16)
-                load8(static_cast<const __nv_bfloat16*>(weight) + 8 * c, w);
-            else
-                load8(static_cast<const float*>(weight) + 8 * c, w);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = x[e] * inv * (w[e] + p.weight_offset);
-        }
-        float z[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float far = __shfl_sync(0xffffffffu, y[e], partner & 31);
-            const float other = p.interleaved ? y[e ^ 1] : far;
-            z[e] = turned ? fmaf(y[e], cs[e], other * sn[e]) : y[e];
-        }
-        if (is_q) {
-            if (on)
-                store8(static_cast<T*>(p.q_out) + t * p.q_out_stride + static_cast<long long>(h) * D + 8 * c, z);
-        } else if (DEST == kOut) {
-            if (on)
-                store8(static_cast<T*>(p.k_out) + t * p.k_out_stride + static_cast<long long>(h) * D + 8 * c, z);
-        }
-        if constexpr (DEST != kOut) {
-            const long long row = (blk * Hkv + h) * p.block_size + off;
-            if constexpr (DEST == kPool) {
-                if (on && is_v) {
-                    uint4* at = reinterpret_cast<uint4*>(static_cast<T*>(p.v_cache) + row * D + 8 * c);
-#pragma unroll
-                    for (int i = 0; i < kVecs; ++i) at[i] = raw[i];
-                } else if (on && !is_q) {
-                    store8(static_cast<T*>(p.k_cache) + row * D + 8 * c, z);
-                }
+            if (p.weight_bf16) {
+                const __nv_bfloat16* s = static_cast<const __nv_bfloat16*>(weight);
+                Quad<__nv_bfloat16>::unpack(__ldg(reinterpret_cast<const uint2*>(s + d0)), w);
+                Quad<__nv_bfloat16>::unpack(__ldg(reinterpret_cast<const uint2*>(s + d1)), w + 4);
             } else {
-                float u[8];
+                const float* s = static_cast<const float*>(weight);
+                Quad<float>::unpack(__ldg(reinterpret_cast<const uint4*>(s + d0)), w);
+                Quad<float>::unpack(__ldg(reinterpret_cast<const uint4*>(s + d1)), w + 4);
+            }
 #pragma unroll
-                for (int e = 0; e < 8; ++e) u[e] = is_v ? x[e] : round_to(z[e], static_cast<const T*>(nullptr));
-                const uint32_t pair = int4_row_pair<TPR>(u, live);
-                if (on && !is_q) {
-                    reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache) +
-                                                row * (D / 2))[c] = int4_codes(u, pair);
-                    if (c == 0) static_cast<uint32_t*>(is_v ? p.v_params : p.k_params)[row] = pair;
+            for (int e = 0; e < 8; ++e) w[e] += p.weight_offset;
+        }
+        for (int pass = part; pass * kRowsPerPass < rows; pass += U * p.splits) {
+            Raw raw[U][2];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int h = (pass + u * p.splits) * kRowsPerPass + sub;
+                raw[u][0] = raw[u][1] = Raw{};
+                if (h < rows && live) {
+                    const T* row = static_cast<const T*>(from) + static_cast<long long>(h) * D;
+                    raw[u][0] = *reinterpret_cast<const Raw*>(row + d0);
+                    raw[u][1] = *reinterpret_cast<const Raw*>(row + d1);
                 }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int first = (pass + u * p.splits) * kRowsPerPass;
+                if (first >= rows) break;                // whole warps
+                float x[8];
+                Q::unpack(raw[u][0], x);
+                Q::unpack(raw[u][1], x + 4);
+                if (weight != nullptr) {
+                    float ss = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+#pragma unroll
+                    for (int o = TPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                    const float inv = 1.0f / sqrtf(ss / static_cast<float>(D) + p.eps);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] *= inv * w[e];
+                }
+                if (split) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float a = x[i], b = x[i + 4];
+                        x[i] = fmaf(a, cs[i], -(b * sn[i]));
+                        x[i + 4] = fmaf(b, cs[i], a * sn[i]);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float a = x[2 * i], b = x[2 * i + 1];
+                        x[2 * i] = fmaf(a, cs[i], -(b * sn[i]));
+                        x[2 * i + 1] = fmaf(b, cs[i], a * sn[i]);
+                    }
+                }
+                put(first + sub, first + sub < rows && live, x);
+            }
+        }
+    };
+    auto store_row = [&](void* to, bool on, const float* x) {
+        if (on) {
+            *reinterpret_cast<Raw*>(static_cast<T*>(to) + d0) = Q::pack(x);
+            *reinterpret_cast<Raw*>(static_cast<T*>(to) + d1) = Q::pack(x + 4);
+        }
+    };
+    // A row's 8 values of this lane as codes (dims a .. + 3 and b .. + 3).
+    auto store_row4 = [&](bool v, long long row, bool on, const float* x, int a, int b) {
+        const uint32_t pair = int4_row_pair<TPR>(x, on);
+        if (on) {
+            const uint32_t codes = int4_codes(x, pair);
+            uint8_t* to = static_cast<uint8_t*>(v ? p.v_cache : p.k_cache) + row * (D / 2);
+            *reinterpret_cast<uint16_t*>(to + a / 2) = static_cast<uint16_t>(codes);
+            *reinterpret_cast<uint16_t*>(to + b / 2) = static_cast<uint16_t>(codes >> 16);
+            if (c == 0) static_cast<uint32_t*>(v ? p.v_params : p.k_params)[row] = pair;
+        }
+    };
+
+    T* const q_out = static_cast<T*>(p.q_out) + t * p.q_out_stride;
+    turn_rows(static_cast<const T*>(p.q) + t * p.q_stride, p.num_heads, p.q_weight,
+              [&](int h, bool on, const float* x) { store_row(q_out + static_cast<long long>(h) * D, on, x); });
+    const T* const k = static_cast<const T*>(p.k) + t * p.k_stride;
+    if constexpr (DEST == kOut) {
+        T* const k_out = static_cast<T*>(p.k_out) + t * p.k_out_stride;
+        turn_rows(k, p.num_kv_heads, p.k_weight,
+                  [&](int h, bool on, const float* x) { store_row(k_out + static_cast<long long>(h) * D, on, x); });
+    } else {
+        if (!append) return;
+        const T* const v = static_cast<const T*>(p.v) + t * p.v_stride;
+        if constexpr (DEST == kPool) {
+            turn_rows(k, p.num_kv_heads, p.k_weight, [&](int h, bool on, const float* x) {
+                store_row(static_cast<T*>(p.k_cache) + (row0 + static_cast<long long>(h) * p.block_size) * D, on, x);
+            });
+            // V as it is, 16 bytes a lane.
+            constexpr int kVecs = sizeof(T) / 2;
+            for (int pass = part; pass * kRowsPerPass < p.num_kv_heads; pass += U * p.splits) {
+                uint4 raw[U][kVecs];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int h = (pass + u * p.splits) * kRowsPerPass + sub;
+                    if (h < p.num_kv_heads && live) {
+                        const uint4* at = reinterpret_cast<const uint4*>(v + static_cast<long long>(h) * D + 8 * c);
+#pragma unroll
+                        for (int i = 0; i < kVecs; ++i) raw[u][i] = at[i];
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int h = (pass + u * p.splits) * kRowsPerPass + sub;
+                    if (h < p.num_kv_heads && live) {
+                        uint4* at = reinterpret_cast<uint4*>(
+                            static_cast<T*>(p.v_cache) + (row0 + static_cast<long long>(h) * p.block_size) * D + 8 * c);
+#pragma unroll
+                        for (int i = 0; i < kVecs; ++i) at[i] = raw[u][i];
+                    }
+                }
+            }
+        } else {
+            turn_rows(k, p.num_kv_heads, p.k_weight, [&](int h, bool on, float* x) {
+                // The codes are those of the row as pa_norm_rope would store it.
+                float y[8];
+                Q::unpack(Q::pack(x), y);
+                Q::unpack(Q::pack(x + 4), y + 4);
+                store_row4(false, row0 + static_cast<long long>(h) * p.block_size, on, y, d0, d1);
+            });
+            for (int first = part * kRowsPerPass; first < p.num_kv_heads; first += p.splits * kRowsPerPass) {
+                const int h = first + sub;
+                const bool on = h < p.num_kv_heads && live;
+                float x[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = 0.f;
+                if (on) load8(v + static_cast<long long>(h) * D + 8 * c, x);
+                store_row4(true, row0 + static_cast<long long>(h) * p.block_size, on, x, 8 * c, 8 * c + 4);
             }
         }
     }
@@ -171,9 +261,11 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
 template <typename T, Dest DEST>
 cudaError_t run(NormRopeParams p, cudaStream_t stream) {
     const int tpr = p.head_dim <= 64 ? 8 : p.head_dim <= 128 ? 16 : 32;
-    const int rows = p.num_heads + p.num_kv_heads * (DEST == kOut ? 1 : 2);
-    const int passes = (rows * tpr + 31) / 32;
-    p.splits = passes < 4 ? passes : 4;
+    // Warps per token: enough to fill the device when there are few tokens, one
+    // when there are many (a warp's table rows and weights then serve every row).
+    const int passes = (p.num_heads * tpr + 31) / 32;
+    const long long want = (kNormRopeWarps + p.num_tokens - 1) / p.num_tokens;
+    p.splits = static_cast<int>(want < passes ? want : passes);
     const long long warps = static_cast<long long>(p.num_tokens) * p.splits;
     const long long blocks = (warps * 32 + kThreads - 1) / kThreads;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
