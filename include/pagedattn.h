@@ -482,7 +482,7 @@ pa_status pa_test_withhold_tile(const void* q, const void* k_cache, const void* 
  * for the new K row x = k_new[t][h] (and V), every difference and quotient in
  * fp32 (IEEE); s = 0 (all x equal to lo) gives codes 0. The directed roundings
  * keep every x inside [lo, lo + 15 s], so a value is off by at most s / 2
- * (plus fp32 rounding). Rows must be finite with a finite max - lo; a row that
+ * (plus fp32 rounding). A zero lo is +0. Rows must be finite with a finite max - lo; a row that
  * is not gives unspecified codes and params for itself alone. new_dtype
  * PA_DTYPE_F32 or PA_DTYPE_BF16; head_dim a multiple of 32, at most 256. Slots
  * as in pa_reshape_and_cache.
@@ -497,8 +497,8 @@ pa_status pa_reshape_and_cache_int4(const void* k_new, const void* v_new, pa_dty
 /*
  * The cached rows of every sequence as plain values, one after another:
  *   k_out[row_starts[s] + i][h][:] = lo + s * c of row i of sequence s, KV head h
- * (same for V) for i < context_lens[s], an fp32 sum rounded to out_dtype
- * (PA_DTYPE_F32 or PA_DTYPE_BF16). Attention over a prompt that is processed in
+ * (same for V) for i < context_lens[s], the exact sum rounded once to
+ * out_dtype (PA_DTYPE_F32 or PA_DTYPE_BF16). Attention over a prompt that is processed in
  * chunks reads its earlier chunks this way. k_out, v_out: [num_rows]
  * [num_kv_heads][head_dim]; row_starts: int64 [num_seqs]. Output rows that no
  * sequence covers are left as they are. A context length outside

@@ -20,25 +20,51 @@ namespace pa {
 __device__ __forceinline__ float int4_lo(uint32_t pair) { return __uint_as_float(pair << 16); }
 __device__ __forceinline__ float int4_step(uint32_t pair) { return __uint_as_float(pair & 0xffff0000u); }
 
-// The pair of a row from its smallest and largest element.
+// The pair of a row from its smallest and largest element (a zero lo is +0).
 __device__ __forceinline__ uint32_t int4_pair(float mn, float mx) {
-    const uint32_t lo = __bfloat16_as_ushort(__float2bfloat16_rd(mn));
+    const uint32_t lo = __bfloat16_as_ushort(__float2bfloat16_rd(__fadd_rn(mn, 0.f)));
     const float step = __fdiv_rn(__fsub_rn(mx, int4_lo(lo)), 15.0f);
     return lo | (static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_ru(step))) << 16);
 }
 
-// Eight consecutive dims' codes, dim e in nibble e.
+// Eight consecutive dims' codes, dim e in nibble e. One reciprocal serves all
+// quotients: with r the correctly rounded 1 / s, q0 = d r and the remainder
+// m = d - q0 s (exact in an FMA), q0 + m r rounds to the IEEE quotient d / s
+// (P. Markstein, "Computation of elementary functions on the IBM RISC
+// System/6000 processor", IBM J. Res. Dev. 34, 1990; the one exception there, a
+// divisor whose fp32 significand is all ones, is no bf16 value). That needs s
+// and the remainder away from underflow: rows whose step is below 2^-90 or above
+// 2^90 divide instead. A finite row's quotients lie in 0..15 (lo is at most its
+// minimum, lo + 15 s at least its maximum but for rounding that rint removes).
 __device__ __forceinline__ uint32_t int4_codes(const float* x, uint32_t pair) {
     const float lo = int4_lo(pair), step = int4_step(pair);
-    uint32_t w = 0u;
-    if (step > 0.f) {
+    if (!(step > 0.f)) return 0u;
+    float c[8];
+    if (step > 0x1p-90f && step < 0x1p90f) {
+        const float r = __frcp_rn(step);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const int c = __float2int_rn(__fdiv_rn(__fsub_rn(x[e], lo), step));
-            w |= static_cast<uint32_t>(max(0, min(15, c))) << (4 * e);
+            const float d = __fsub_rn(x[e], lo);
+            const float q = __fmul_rn(d, r);
+            c[e] = __fmaf_rn(__fmaf_rn(-q, step, d), r, q);
         }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) c[e] = __fdiv_rn(__fsub_rn(x[e], lo), step);
     }
-    return w;
+    // Adding 1.5 * 2^23 rounds to an integer, half to even; four codes are put
+    // together in fp32 (below 2^16: exact) and read from the low bits.
+    constexpr float kRound = 12582912.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) c[e] = __fsub_rn(__fadd_rn(c[e], kRound), kRound);
+    uint32_t w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float* k = c + 4 * i;
+        const float v = __fmaf_rn(k[3], 4096.f, __fmaf_rn(k[2], 256.f, __fmaf_rn(k[1], 16.f, k[0])));
+        w[i] = __float_as_uint(__fadd_rn(v, 8388608.f));
+    }
+    return __byte_perm(w[0], w[1], 0x5410);
 }
 
 // A row spread over TPR consecutive lanes, 8 dims each (live: this lane holds

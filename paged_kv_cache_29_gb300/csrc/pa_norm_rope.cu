@@ -22,10 +22,10 @@ namespace pa {
 namespace {
 
 constexpr int kThreads = 128;
-#ifndef PA_NW
-#define PA_NW 4864
-#endif
-constexpr long long kNormRopeWarps = PA_NW;
+// Warps that fill the device (16 per SM): more tokens than this take one warp
+// each. Prompt of 4,099 tokens, 48 rows each, three axes: 18.3 us with one warp
+// per token, 22.5 with two, 35.2 with eight.
+constexpr long long kNormRopeWarps = 2432;
 
 enum Dest { kOut, kPool, kPool4 };
 
@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
     using Q = Quad<T>;
     using Raw = typename Q::Raw;
     constexpr int kRowsPerPass = 32 / TPR;
-    constexpr int U = sizeof(T) == 2 ? 4 : 2;            // passes in flight
+    constexpr int U = 2;                                 // passes of a batch
     const int lane = threadIdx.x & 31;
     const int sub = lane / TPR, c = lane % TPR;
     const long long warp = static_cast<long long>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
@@ -73,6 +73,25 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
     const bool live = 8 * c < D, turned = 8 * c < p.rot_dim;
     const bool split = turned && !p.interleaved;         // the lane holds two halves' quads
     const int d0 = split ? 4 * c : 8 * c, d1 = split ? half + 4 * c : 8 * c + 4;
+
+    // Rows of q and K are loaded a batch of U passes ahead of their use, the
+    // first batch of q before the positions are known.
+    Raw raw[U][2];
+    auto load_batch = [&](const T* from, int rows, int pass) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int h = (pass + u * p.splits) * kRowsPerPass + sub;
+            raw[u][0] = raw[u][1] = Raw{};
+            if (h < rows && live) {
+                const T* row = from + static_cast<long long>(h) * D;
+                raw[u][0] = *reinterpret_cast<const Raw*>(row + d0);
+                raw[u][1] = *reinterpret_cast<const Raw*>(row + d1);
+            }
+        }
+    };
+    const T* const q = static_cast<const T*>(p.q) + t * p.q_stride;
+    const T* const k = static_cast<const T*>(p.k) + t * p.k_stride;
+    load_batch(q, p.num_heads, part);
 
     float cs[4] = {1.f, 1.f, 1.f, 1.f}, sn[4] = {0.f, 0.f, 0.f, 0.f};
     if (p.rot_dim > 0) {
@@ -116,8 +135,9 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
         row0 = blk * p.num_kv_heads * p.block_size + (append ? slot - blk * p.block_size : 0);
     }
 
-    // Normed and turned rows of q or K.
-    auto turn_rows = [&](const void* from, int rows, const void* weight, auto&& put) {
+    // Normed and turned rows of q or K; raw holds the first batch, and the first
+    // batch of `then` (then_rows rows) at the end.
+    auto turn_rows = [&](const T* from, int rows, const void* weight, const T* then, int then_rows, auto&& put) {
         float w[8];
         if (weight != nullptr && live) {
             if (p.weight_bf16) {
@@ -133,24 +153,21 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
             for (int e = 0; e < 8; ++e) w[e] += p.weight_offset;
         }
         for (int pass = part; pass * kRowsPerPass < rows; pass += U * p.splits) {
-            Raw raw[U][2];
+            float in[U][8];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int h = (pass + u * p.splits) * kRowsPerPass + sub;
-                raw[u][0] = raw[u][1] = Raw{};
-                if (h < rows && live) {
-                    const T* row = static_cast<const T*>(from) + static_cast<long long>(h) * D;
-                    raw[u][0] = *reinterpret_cast<const Raw*>(row + d0);
-                    raw[u][1] = *reinterpret_cast<const Raw*>(row + d1);
-                }
+                Q::unpack(raw[u][0], in[u]);
+                Q::unpack(raw[u][1], in[u] + 4);
             }
+            if ((pass + U * p.splits) * kRowsPerPass < rows)
+                load_batch(from, rows, pass + U * p.splits);
+            else if (then != nullptr)
+                load_batch(then, then_rows, part);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int first = (pass + u * p.splits) * kRowsPerPass;
                 if (first >= rows) break;                // whole warps
-                float x[8];
-                Q::unpack(raw[u][0], x);
-                Q::unpack(raw[u][1], x + 4);
+                float* const x = in[u];
                 if (weight != nullptr) {
                     float ss = 0.f;
 #pragma unroll
@@ -199,46 +216,45 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
     };
 
     T* const q_out = static_cast<T*>(p.q_out) + t * p.q_out_stride;
-    turn_rows(static_cast<const T*>(p.q) + t * p.q_stride, p.num_heads, p.q_weight,
+    turn_rows(q, p.num_heads, p.q_weight, DEST == kOut || append ? k : nullptr, p.num_kv_heads,
               [&](int h, bool on, const float* x) { store_row(q_out + static_cast<long long>(h) * D, on, x); });
-    const T* const k = static_cast<const T*>(p.k) + t * p.k_stride;
     if constexpr (DEST == kOut) {
         T* const k_out = static_cast<T*>(p.k_out) + t * p.k_out_stride;
-        turn_rows(k, p.num_kv_heads, p.k_weight,
+        turn_rows(k, p.num_kv_heads, p.k_weight, nullptr, 0,
                   [&](int h, bool on, const float* x) { store_row(k_out + static_cast<long long>(h) * D, on, x); });
     } else {
         if (!append) return;
         const T* const v = static_cast<const T*>(p.v) + t * p.v_stride;
         if constexpr (DEST == kPool) {
-            turn_rows(k, p.num_kv_heads, p.k_weight, [&](int h, bool on, const float* x) {
+            turn_rows(k, p.num_kv_heads, p.k_weight, nullptr, 0, [&](int h, bool on, const float* x) {
                 store_row(static_cast<T*>(p.k_cache) + (row0 + static_cast<long long>(h) * p.block_size) * D, on, x);
             });
             // V as it is, 16 bytes a lane.
-            constexpr int kVecs = sizeof(T) / 2;
-            for (int pass = part; pass * kRowsPerPass < p.num_kv_heads; pass += U * p.splits) {
-                uint4 raw[U][kVecs];
+            constexpr int kVecs = sizeof(T) / 2, UV = 4;
+            for (int pass = part; pass * kRowsPerPass < p.num_kv_heads; pass += UV * p.splits) {
+                uint4 vec[UV][kVecs];
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
+                for (int u = 0; u < UV; ++u) {
                     const int h = (pass + u * p.splits) * kRowsPerPass + sub;
                     if (h < p.num_kv_heads && live) {
                         const uint4* at = reinterpret_cast<const uint4*>(v + static_cast<long long>(h) * D + 8 * c);
 #pragma unroll
-                        for (int i = 0; i < kVecs; ++i) raw[u][i] = at[i];
+                        for (int i = 0; i < kVecs; ++i) vec[u][i] = at[i];
                     }
                 }
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
+                for (int u = 0; u < UV; ++u) {
                     const int h = (pass + u * p.splits) * kRowsPerPass + sub;
                     if (h < p.num_kv_heads && live) {
                         uint4* at = reinterpret_cast<uint4*>(
                             static_cast<T*>(p.v_cache) + (row0 + static_cast<long long>(h) * p.block_size) * D + 8 * c);
 #pragma unroll
-                        for (int i = 0; i < kVecs; ++i) at[i] = raw[u][i];
+                        for (int i = 0; i < kVecs; ++i) at[i] = vec[u][i];
                     }
                 }
             }
         } else {
-            turn_rows(k, p.num_kv_heads, p.k_weight, [&](int h, bool on, float* x) {
+            turn_rows(k, p.num_kv_heads, p.k_weight, nullptr, 0, [&](int h, bool on, float* x) {
                 // The codes are those of the row as pa_norm_rope would store it.
                 float y[8];
                 Q::unpack(Q::pack(x), y);

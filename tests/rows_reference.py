@@ -21,10 +21,22 @@ def bf16_value(bits):
     return (np.asarray(bits, dtype=np.uint32) << 16).view(np.float32)
 
 
+def bf16_of_double(x):
+    """64-bit values rounded once to bf16 (bits)."""
+    x = np.asarray(x, dtype=np.float64)
+    f = x.astype(np.float32)
+    # fp32 towards zero with the lost bits in the last place: rounding that to
+    # bf16 is rounding x.
+    over = np.abs(f.astype(np.float64)) > np.abs(x)
+    f = np.where(over, np.nextafter(f, np.float32(0)), f)
+    b = np.ascontiguousarray(f).view(np.uint32) | (f.astype(np.float64) != x).astype(np.uint32)
+    return bf16_bits(b.view(np.float32))
+
+
 def quantise4(x):
     """Codes (uint8, packed) and pairs (uint16 bf16 bits, [..., 2]) of rows x (fp32)."""
     x = np.asarray(x, dtype=np.float32)
-    lo_bits = bf16_bits(x.min(-1), "down")
+    lo_bits = bf16_bits(x.min(-1) + np.float32(0), "down")     # a zero is +0
     lo = bf16_value(lo_bits)
     s_bits = bf16_bits((x.max(-1) - lo) / np.float32(15), "up")
     s = bf16_value(s_bits)
