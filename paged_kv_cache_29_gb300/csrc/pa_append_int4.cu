@@ -1,8 +1,8 @@
 // pa_append_int4.cu -- the quantising append into a 4-bit cache and the gather
 // of its rows as plain values (row format: pa_int4.cuh). Both are one pass over
 // memory. A warp works on one token (or one row of one sequence) and goes over
-// its KV heads, TPR lanes per head with 8 dims each: the token's slot (the row's
-// block) is looked up once, reads of new rows and writes of values run over
+// its KV heads, TPR lanes per head: the token's slot (the row's block) is looked
+// up once, reads of new rows and writes of values run over
 // consecutive heads, contiguous.
 #include "pa_int4.cuh"
 #include "pa_internal.h"
@@ -16,53 +16,79 @@ constexpr int kWarpsPerCta = kThreads / 32;
 // Warps that fill the device (16 per SM); with fewer tokens than that, several
 // warps share a token's heads.
 constexpr long long kFillWarps = 2432;
-#ifndef PA_GX
-#define PA_GX 4864
-#endif
+// CTAs of the gather (32 per SM): a batch of prompts 226 us with 4,864, 283 with
+// 2,432.
+constexpr long long kGatherCtas = 4864;
 
-// Eight elements as they are loaded, their fp32 values, and the row's pair.
+// Sixteen elements as they are loaded, their fp32 values, and the row's pair.
 template <typename T, int TPR>
-struct Eight;
+struct Sixteen;
 template <int TPR>
-struct Eight<float, TPR> {
-    float4 a, b;
+struct Sixteen<float, TPR> {
+    float4 v[4];
     __device__ __forceinline__ void load(const float* p) {
-        a = __ldg(reinterpret_cast<const float4*>(p));
-        b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = __ldg(reinterpret_cast<const float4*>(p) + i);
     }
-    __device__ __forceinline__ void clear() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
     __device__ __forceinline__ void values(float* x) const {
-        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[4 * i] = v[i].x; x[4 * i + 1] = v[i].y; x[4 * i + 2] = v[i].z; x[4 * i + 3] = v[i].w;
+        }
     }
     __device__ __forceinline__ uint32_t pair(bool on) const {
-        float x[8];
-        values(x);
-        return int4_row_pair<TPR>(x, on);
+        float mn = INFINITY, mx = -INFINITY;
+        if (on) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                mn = fminf(fminf(fminf(mn, v[i].x), fminf(v[i].y, v[i].z)), v[i].w);
+                mx = fmaxf(fmaxf(fmaxf(mx, v[i].x), fmaxf(v[i].y, v[i].z)), v[i].w);
+            }
+        }
+#pragma unroll
+        for (int off = TPR / 2; off > 0; off >>= 1) {
+            mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, off));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+        }
+        return int4_pair<false>(mn, mx);
     }
 };
 template <int TPR>
-struct Eight<__nv_bfloat16, TPR> {
-    uint4 v;
-    __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = __ldg(reinterpret_cast<const uint4*>(p)); }
-    __device__ __forceinline__ void clear() { v = make_uint4(0u, 0u, 0u, 0u); }
-    __device__ __forceinline__ void values(float* x) const { ElemTraits<__nv_bfloat16>::unpack(v, x); }
+struct Sixteen<__nv_bfloat16, TPR> {
+    uint4 v[2];
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+        v[0] = __ldg(reinterpret_cast<const uint4*>(p));
+        v[1] = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+    }
+    __device__ __forceinline__ void clear() { v[0] = v[1] = make_uint4(0u, 0u, 0u, 0u); }
+    __device__ __forceinline__ void values(float* x) const {
+        ElemTraits<__nv_bfloat16>::unpack(v[0], x);
+        ElemTraits<__nv_bfloat16>::unpack(v[1], x + 8);
+    }
     // The minimum and minus the maximum side by side as bf16: one shuffle and
     // one packed minimum per level.
     __device__ __forceinline__ uint32_t pair(bool on) const {
         auto h2 = [](uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); };
         auto u = [](__nv_bfloat162 h) { return *reinterpret_cast<const uint32_t*>(&h); };
-        const uint32_t mn = u(__hmin2(__hmin2(h2(v.x), h2(v.y)), __hmin2(h2(v.z), h2(v.w))));
-        const uint32_t mx = u(__hmax2(__hmax2(h2(v.x), h2(v.y)), __hmax2(h2(v.z), h2(v.w)))) ^ 0x80008000u;
+        auto lo4 = [&](const uint4& a) { return __hmin2(__hmin2(h2(a.x), h2(a.y)), __hmin2(h2(a.z), h2(a.w))); };
+        auto hi4 = [&](const uint4& a) { return __hmax2(__hmax2(h2(a.x), h2(a.y)), __hmax2(h2(a.z), h2(a.w))); };
+        const uint32_t mn = u(__hmin2(lo4(v[0]), lo4(v[1])));
+        const uint32_t mx = u(__hmax2(hi4(v[0]), hi4(v[1]))) ^ 0x80008000u;
         uint32_t m = u(__hmin2(h2(__byte_perm(mn, mx, 0x5410)), h2(__byte_perm(mn, mx, 0x7632))));
         if (!on) m = 0x7f807f80u;                        // +inf twice
 #pragma unroll
         for (int off = TPR / 2; off > 0; off >>= 1)
             m = u(__hmin2(h2(m), h2(__shfl_xor_sync(0xffffffffu, m, off))));
-        return int4_pair(bf16_lo(m), -bf16_hi(m));
+        return int4_pair<true>(bf16_lo(m), -bf16_hi(m));
     }
 };
 
+// 16 dims a lane: the pair and its reciprocal, which every lane of a row works
+// out, cost four rows of a pass once.
 template <typename TIn, int TPR>
 __global__ void __launch_bounds__(kThreads)
 append_int4_kernel(const TIn* __restrict__ k_new, const TIn* __restrict__ v_new,
@@ -72,48 +98,53 @@ append_int4_kernel(const TIn* __restrict__ k_new, const TIn* __restrict__ v_new,
                    int num_kv_heads, int block_size, long long num_slots, int32_t* error_word) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     constexpr int kRowsPerPass = 32 / TPR;
-    constexpr int U = sizeof(TIn) == 2 ? 4 : 2;          // passes in flight
+    constexpr int U = sizeof(TIn) == 2 ? 2 : 1;          // passes in flight
     const int lane = threadIdx.x & 31;
     const int sub = lane / TPR, c = lane % TPR;
-    const bool live = 8 * c < head_dim;
-    const long long warp = static_cast<long long>(blockIdx.x) * kWarpsPerCta + (threadIdx.x >> 5);
-    const long long t = warp / splits;
+    const bool live = 16 * c < head_dim;
+    // Unsigned: the last CTA's warps may pass 2^31.
+    const uint32_t warp = blockIdx.x * kWarpsPerCta + (threadIdx.x >> 5);
+    const uint32_t t = splits == 1 ? warp : warp / static_cast<uint32_t>(splits);
     const int part = static_cast<int>(warp - t * splits);
-    if (t >= num_tokens) return;
+    if (t >= static_cast<uint32_t>(num_tokens)) return;
     const long long slot = __ldg(slot_mapping + t);
     if (slot < 0) return;
     if (slot >= num_slots) {
         if (part == 0 && lane == 0) raise_error(error_word, PA_DEVERR_SLOT);
         return;
     }
-    const long long blk = slot / block_size;
-    const long long row0 = blk * num_kv_heads * block_size + (slot - blk * block_size);
-    const long long from = t * num_kv_heads * head_dim + 8 * c;
-    // The K heads, then the V heads.
-    const int rows = 2 * num_kv_heads;
-    for (int pass = part; pass * kRowsPerPass < rows; pass += U * splits) {
-        Eight<TIn, TPR> in[U];
+    const long long row0 = slot_row(slot, num_slots, num_kv_heads, block_size);
+    // Passes 0 .. n - 1 are the K heads', n .. 2 n - 1 the V heads'.
+    const int n = (num_kv_heads + kRowsPerPass - 1) / kRowsPerPass;
+    const size_t from = static_cast<size_t>(t) * num_kv_heads * head_dim + 16 * c;
+    const size_t codes0 = static_cast<size_t>(row0) * (head_dim / 2) + 8 * c;
+    const size_t code_stride = static_cast<size_t>(block_size) * (head_dim / 2);   // between heads
+    for (int pass = part; pass < 2 * n; pass += U * splits) {
+        Sixteen<TIn, TPR> in[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int r = (pass + u * splits) * kRowsPerPass + sub;
-            const bool v = r >= num_kv_heads;
+            const int at = pass + u * splits;
+            const bool v = at >= n;
+            const int h = (v ? at - n : at) * kRowsPerPass + sub;
             in[u].clear();
-            if (r < rows && live)
-                in[u].load((v ? v_new : k_new) + from + static_cast<long long>(v ? r - num_kv_heads : r) * head_dim);
+            if (at < 2 * n && h < num_kv_heads && live) in[u].load((v ? v_new : k_new) + from + h * head_dim);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int first = (pass + u * splits) * kRowsPerPass;
-            if (first >= rows) break;                    // whole warps
-            const int r = first + sub;
-            const bool v = r >= num_kv_heads, on = r < rows && live;
+            const int at = pass + u * splits;
+            if (at >= 2 * n) break;                      // whole warps
+            const bool v = at >= n;
+            const int h = (v ? at - n : at) * kRowsPerPass + sub;
+            const bool on = h < num_kv_heads && live;
             const uint32_t pair = in[u].pair(on);
             if (on) {
-                float x[8];
+                float x[16];
                 in[u].values(x);
-                const long long row = row0 + static_cast<long long>(v ? r - num_kv_heads : r) * block_size;
-                reinterpret_cast<uint32_t*>((v ? v_cache : k_cache) + row * (head_dim / 2))[c] = int4_codes(x, pair);
-                if (c == 0) (v ? v_params : k_params)[row] = pair;
+                uint32_t codes[2];
+                int4_codes<16>(x, pair, codes);
+                *reinterpret_cast<uint2*>((v ? v_cache : k_cache) + codes0 + h * code_stride) =
+                    make_uint2(codes[0], codes[1]);
+                if (c == 0) (v ? v_params : k_params)[row0 + static_cast<long long>(h) * block_size] = pair;
             }
         }
     }
@@ -143,7 +174,7 @@ __device__ __forceinline__ void put_values(float* p, uint32_t w, uint32_t pair) 
 }
 
 template <typename TOut, int TPR>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 3)
 gather_int4_kernel(const uint8_t* __restrict__ k_cache, const uint8_t* __restrict__ v_cache,
                    const uint32_t* __restrict__ k_params, const uint32_t* __restrict__ v_params,
                    const int32_t* __restrict__ block_tables,
@@ -154,7 +185,7 @@ gather_int4_kernel(const uint8_t* __restrict__ k_cache, const uint8_t* __restric
                    int32_t* error_word) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     constexpr int kRowsPerPass = 32 / TPR;
-    constexpr int U = 4;                                 // passes in flight
+    constexpr int U = 4;                           // passes in flight
     const int s = blockIdx.y;
     const int n = __ldg(context_lens + s);
     const long long start = __ldg(row_starts + s);
@@ -166,15 +197,19 @@ gather_int4_kernel(const uint8_t* __restrict__ k_cache, const uint8_t* __restric
     const int sub = lane / TPR, c = lane % TPR;
     const bool live = 8 * c < head_dim;
     const int32_t* table = block_tables + static_cast<size_t>(s) * max_blocks_per_seq;
-    const int stride = gridDim.x * kWarpsPerCta;
-    for (int row = blockIdx.x * kWarpsPerCta + (threadIdx.x >> 5); row < n; row += stride) {
-        const int col = row / block_size;
-        const int id = __ldg(table + col);
+    const uint32_t stride = gridDim.x * kWarpsPerCta;
+    // Unsigned: the row after the last may pass 2^31. Block ids a row ahead.
+    const uint32_t un = static_cast<uint32_t>(n), ubs = static_cast<uint32_t>(block_size);
+    uint32_t row = blockIdx.x * kWarpsPerCta + (threadIdx.x >> 5);
+    int id_next = row < un ? __ldg(table + row / ubs) : 0;
+    for (; row < un; row += stride) {
+        const int id = id_next;
+        if (row + stride < un) id_next = __ldg(table + (row + stride) / ubs);
         if (id < 0 || id >= num_blocks) {
             if (lane == 0) raise_error(error_word, PA_DEVERR_BLOCK_ID);
             continue;
         }
-        const size_t in0 = static_cast<size_t>(id) * num_kv_heads * block_size + (row - col * block_size);
+        const size_t in0 = static_cast<size_t>(id) * num_kv_heads * block_size + row % ubs;
         const size_t out0 = (static_cast<size_t>(start) + row) * num_kv_heads * head_dim + 8 * c;
         for (int pass = 0; pass * kRowsPerPass < num_kv_heads; pass += U) {
             uint32_t w[U][2], pair[U][2];
@@ -202,8 +237,6 @@ gather_int4_kernel(const uint8_t* __restrict__ k_cache, const uint8_t* __restric
     }
 }
 
-int lanes_per_row(int head_dim) { return head_dim <= 64 ? 8 : head_dim <= 128 ? 16 : 32; }
-
 }  // namespace
 
 cudaError_t launch_append_int4(const void* k_new, const void* v_new, pa_dtype new_dtype,
@@ -212,13 +245,12 @@ cudaError_t launch_append_int4(const void* k_new, const void* v_new, pa_dtype ne
                                int head_dim, int block_size, int num_blocks, int32_t* error_word,
                                cudaStream_t stream) {
     if (num_tokens == 0) return cudaSuccess;
-    const int tpr = lanes_per_row(head_dim);
-    const long long passes = (2LL * num_kv_heads * tpr + 31) / 32;
+    const int tpr = head_dim <= 64 ? 4 : head_dim <= 128 ? 8 : 16;
+    const long long passes = 2LL * ((static_cast<long long>(num_kv_heads) * tpr + 31) / 32);
     const long long want = (kFillWarps + num_tokens - 1) / num_tokens;
     const int splits = static_cast<int>(want < passes ? want : passes);
     const long long blocks =
         (static_cast<long long>(num_tokens) * splits + kWarpsPerCta - 1) / kWarpsPerCta;
-    if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     auto run = [&](auto kernel, auto tag) {
         using TIn = decltype(tag);
         kernel<<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(
@@ -231,9 +263,9 @@ cudaError_t launch_append_int4(const void* k_new, const void* v_new, pa_dtype ne
     };
     auto pick = [&](auto tag) {
         using TIn = decltype(tag);
-        return tpr == 8    ? run(append_int4_kernel<TIn, 8>, tag)
-               : tpr == 16 ? run(append_int4_kernel<TIn, 16>, tag)
-                           : run(append_int4_kernel<TIn, 32>, tag);
+        return tpr == 4   ? run(append_int4_kernel<TIn, 4>, tag)
+               : tpr == 8 ? run(append_int4_kernel<TIn, 8>, tag)
+                          : run(append_int4_kernel<TIn, 16>, tag);
     };
     return new_dtype == PA_DTYPE_BF16 ? pick(__nv_bfloat16{}) : pick(float{});
 }
@@ -246,11 +278,11 @@ cudaError_t launch_gather_int4(const void* k_cache, const void* v_cache, const v
                                int num_blocks, int max_blocks_per_seq, int max_context_len,
                                int32_t* error_word, cudaStream_t stream) {
     if (num_seqs == 0) return cudaSuccess;
-    const int tpr = lanes_per_row(head_dim);
+    const int tpr = head_dim <= 64 ? 8 : head_dim <= 128 ? 16 : 32;
     // Rows beyond a sequence's length cost nothing but a CTA's look at it, so the
     // sequences share a bounded number of CTAs, at most one warp per row.
     long long bx = (max_context_len + kWarpsPerCta - 1) / kWarpsPerCta;
-    const long long share = (PA_GX + num_seqs - 1) / num_seqs;
+    const long long share = (kGatherCtas + num_seqs - 1) / num_seqs;
     if (bx > share) bx = share;
     if (bx < 1) bx = 1;
     auto run = [&](auto kernel, auto tag) {

@@ -20,56 +20,67 @@ namespace pa {
 __device__ __forceinline__ float int4_lo(uint32_t pair) { return __uint_as_float(pair << 16); }
 __device__ __forceinline__ float int4_step(uint32_t pair) { return __uint_as_float(pair & 0xffff0000u); }
 
-// The pair of a row from its smallest and largest element (a zero lo is +0).
+// IEEE quotients d / s by one divisor: with r the correctly rounded 1 / s and
+// q0 = d r, the remainder m = d - q0 s is exact in an FMA, and q0 + m r is rounded
+// once (the correction step of P. Markstein, "Computation of elementary functions
+// on the IBM RISC System/6000 processor", IBM J. Res. Dev. 34, 1990). Before that
+// rounding it is within 2^-22 of a last place of the quotient, and s, 15 or a
+// bf16 value, has at most 8 significant bits, so that no quotient comes nearer
+// than 2^-9 of a place to a rounding boundary. That needs s, and d where it
+// counts, away from underflow.
+__device__ __forceinline__ float int4_quotient(float d, float s, float r) {
+    const float q = __fmul_rn(d, r);
+    return __fmaf_rn(__fmaf_rn(-q, s, d), r, q);
+}
+// Steps (and a row's max - lo) outside these bounds divide instead.
+constexpr float kInt4Small = 0x1p-80f, kInt4Large = 0x1p80f;
+
+// The pair of a row from its smallest and largest element (a zero lo is +0), lo
+// being exact where the row is bf16.
+template <bool BF16>
 __device__ __forceinline__ uint32_t int4_pair(float mn, float mx) {
-    const uint32_t lo = __bfloat16_as_ushort(__float2bfloat16_rd(__fadd_rn(mn, 0.f)));
-    const float step = __fdiv_rn(__fsub_rn(mx, int4_lo(lo)), 15.0f);
-    return lo | (static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_ru(step))) << 16);
+    mn = __fadd_rn(mn, 0.f);
+    uint32_t lo = __float_as_uint(mn);
+    // Down to bf16: towards zero, and one step on where that went up.
+    if constexpr (!BF16) lo = (lo + ((lo >> 31) ? 0xffffu : 0u)) & 0xffff0000u;
+    const float d = __fsub_rn(mx, __uint_as_float(lo));
+    float s = int4_quotient(d, 15.0f, 1.0f / 15.0f);
+    if (!(d >= kInt4Small) && d != 0.f) s = __fdiv_rn(d, 15.0f);
+    // Up to bf16 (s is not negative); an infinite or NaN row stays itself.
+    const uint32_t up = (__float_as_uint(s) + 0xffffu) & 0xffff0000u;
+    return (lo >> 16) | up;
 }
 
-// Eight consecutive dims' codes, dim e in nibble e. One reciprocal serves all
-// quotients: with r the correctly rounded 1 / s, q0 = d r and the remainder
-// m = d - q0 s (exact in an FMA), q0 + m r rounds to the IEEE quotient d / s
-// (P. Markstein, "Computation of elementary functions on the IBM RISC
-// System/6000 processor", IBM J. Res. Dev. 34, 1990; the one exception there, a
-// divisor whose fp32 significand is all ones, is no bf16 value). That needs s
-// and the remainder away from underflow: rows whose step is below 2^-90 or above
-// 2^90 divide instead. A finite row's quotients lie in 0..15 (lo is at most its
-// minimum, lo + 15 s at least its maximum but for rounding that rint removes).
-__device__ __forceinline__ uint32_t int4_codes(const float* x, uint32_t pair) {
+// N consecutive dims' codes (N = 8 or 16), dim e in nibble e. A finite row's
+// quotients lie in 0..15: lo is at most its minimum, lo + 15 s at least its
+// maximum but for rounding that the rounding to an integer removes.
+template <int N>
+__device__ __forceinline__ void int4_codes(const float* x, uint32_t pair, uint32_t* codes) {
     const float lo = int4_lo(pair), step = int4_step(pair);
-    if (!(step > 0.f)) return 0u;
-    float c[8];
-    if (step > 0x1p-90f && step < 0x1p90f) {
-        const float r = __frcp_rn(step);
+    const float r = step > 0.f ? __frcp_rn(step) : 0.f;   // a row of one value: differences 0
+    float q[N];
+    if (step == 0.f || (step > kInt4Small && step < kInt4Large)) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float d = __fsub_rn(x[e], lo);
-            const float q = __fmul_rn(d, r);
-            c[e] = __fmaf_rn(__fmaf_rn(-q, step, d), r, q);
-        }
+        for (int e = 0; e < N; ++e) q[e] = int4_quotient(__fsub_rn(x[e], lo), step, r);
     } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) c[e] = __fdiv_rn(__fsub_rn(x[e], lo), step);
+        for (int e = 0; e < N; ++e) q[e] = __fdiv_rn(__fsub_rn(x[e], lo), step);
     }
-    // Adding 1.5 * 2^23 rounds to an integer, half to even; four codes are put
-    // together in fp32 (below 2^16: exact) and read from the low bits.
-    constexpr float kRound = 12582912.f;
+    // Adding 1.5 * 2^23 rounds to an integer, half to even, into the low bits; the
+    // integers' common upper bits are taken off the sum below, mod 2^32.
+    constexpr uint32_t kBits = 0x4b400000u;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) c[e] = __fsub_rn(__fadd_rn(c[e], kRound), kRound);
-    uint32_t w[2];
+    for (int i = 0; i < N / 8; ++i) {
+        uint32_t w = 0u;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const float* k = c + 4 * i;
-        const float v = __fmaf_rn(k[3], 4096.f, __fmaf_rn(k[2], 256.f, __fmaf_rn(k[1], 16.f, k[0])));
-        w[i] = __float_as_uint(__fadd_rn(v, 8388608.f));
+        for (int e = 7; e >= 0; --e) w = w * 16u + __float_as_uint(__fadd_rn(q[8 * i + e], 12582912.f));
+        codes[i] = w - kBits * 0x11111111u;
     }
-    return __byte_perm(w[0], w[1], 0x5410);
 }
 
 // A row spread over TPR consecutive lanes, 8 dims each (live: this lane holds
 // dims of the row): the row's pair, in every lane.
-template <int TPR>
+template <int TPR, bool BF16>
 __device__ __forceinline__ uint32_t int4_row_pair(const float* x, bool live) {
     float mn = INFINITY, mx = -INFINITY;
     if (live) {
@@ -84,7 +95,20 @@ __device__ __forceinline__ uint32_t int4_row_pair(const float* x, bool live) {
         mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, off));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
     }
-    return int4_pair(mn, mx);
+    return int4_pair<BF16>(mn, mx);
+}
+
+// Row of KV head 0 of a slot in a pool [block][kv_head][block_size]. A 64-bit
+// division is some 70 instructions, so only pools that need one pay for it.
+__device__ __forceinline__ long long slot_row(long long slot, long long num_slots, int num_kv_heads,
+                                              int block_size) {
+    if (num_slots <= 0x7fffffffLL) {
+        const uint32_t s = static_cast<uint32_t>(slot), bs = static_cast<uint32_t>(block_size);
+        const uint32_t blk = s / bs;
+        return static_cast<long long>(blk) * num_kv_heads * block_size + (s - blk * bs);
+    }
+    const long long blk = slot / block_size;
+    return blk * num_kv_heads * block_size + (slot - blk * block_size);
 }
 
 // Eight consecutive elements as fp32, and eight fp32 values rounded and stored.

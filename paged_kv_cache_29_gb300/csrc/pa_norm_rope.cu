@@ -64,10 +64,12 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
     constexpr int U = 2;                                 // passes of a batch
     const int lane = threadIdx.x & 31;
     const int sub = lane / TPR, c = lane % TPR;
-    const long long warp = static_cast<long long>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
-    const long long t = warp / p.splits;
-    const int part = static_cast<int>(warp - t * p.splits);
-    if (t >= p.num_tokens) return;                       // whole warps
+    // Unsigned: the last CTA's warps may pass 2^31.
+    const uint32_t warp = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    const uint32_t token = p.splits == 1 ? warp : warp / static_cast<uint32_t>(p.splits);
+    const int part = static_cast<int>(warp - token * p.splits);
+    if (token >= static_cast<uint32_t>(p.num_tokens)) return;   // whole warps
+    const long long t = token;
 
     const int D = p.head_dim, half = p.rot_dim / 2;
     const bool live = 8 * c < D, turned = 8 * c < p.rot_dim;
@@ -131,8 +133,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
         const long long slot = __ldg(p.slot_mapping + t);
         append = slot >= 0 && slot < p.num_slots;
         if (slot >= p.num_slots && part == 0 && lane == 0) raise_error(p.error_word, PA_DEVERR_SLOT);
-        const long long blk = append ? slot / p.block_size : 0;
-        row0 = blk * p.num_kv_heads * p.block_size + (append ? slot - blk * p.block_size : 0);
+        if (append) row0 = slot_row(slot, p.num_slots, p.num_kv_heads, p.block_size);
     }
 
     // Normed and turned rows of q or K; raw holds the first batch, and the first
@@ -205,9 +206,10 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
     };
     // A row's 8 values of this lane as codes (dims a .. + 3 and b .. + 3).
     auto store_row4 = [&](bool v, long long row, bool on, const float* x, int a, int b) {
-        const uint32_t pair = int4_row_pair<TPR>(x, on);
+        const uint32_t pair = int4_row_pair<TPR, sizeof(T) == 2>(x, on);
         if (on) {
-            const uint32_t codes = int4_codes(x, pair);
+            uint32_t codes;
+            int4_codes<8>(x, pair, &codes);
             uint8_t* to = static_cast<uint8_t*>(v ? p.v_cache : p.k_cache) + row * (D / 2);
             *reinterpret_cast<uint16_t*>(to + a / 2) = static_cast<uint16_t>(codes);
             *reinterpret_cast<uint16_t*>(to + b / 2) = static_cast<uint16_t>(codes >> 16);
@@ -284,7 +286,6 @@ cudaError_t run(NormRopeParams p, cudaStream_t stream) {
     p.splits = static_cast<int>(want < passes ? want : passes);
     const long long warps = static_cast<long long>(p.num_tokens) * p.splits;
     const long long blocks = (warps * 32 + kThreads - 1) / kThreads;
-    if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     auto go = [&](auto kernel) {
         kernel<<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(p);
         return cudaGetLastError();
