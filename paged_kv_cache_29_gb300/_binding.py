@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import struct
 import threading
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -61,6 +62,11 @@ class _NormRopeArgs(ctypes.Structure):
                 ("rot_dim", ctypes.c_int), ("max_position", ctypes.c_int),
                 ("num_axes", ctypes.c_int), ("interleaved", ctypes.c_int),
                 ("dtype", ctypes.c_int), ("weight_dtype", ctypes.c_int)]
+
+
+# The same layout as a struct format: packing it takes a fifth of the time that
+# filling the ctypes structure does.
+_norm_rope_pack = struct.Struct("@PPqqPqPPffPPP10i").pack
 
 
 def lib() -> ctypes.CDLL:
@@ -129,12 +135,11 @@ def lib() -> ctypes.CDLL:
         L.pa_decode_int4.argtypes = [P, P, P, P, P, P, P, F, I, P, I, I, I, I, I, I, I, I, I, P, S,
                                      P, P]
         L.pa_decode_int4.restype = I
-        NR = ctypes.POINTER(_NormRopeArgs)
-        L.pa_norm_rope.argtypes = [NR, P, ctypes.c_int64, P, P]
+        L.pa_norm_rope.argtypes = [P, P, ctypes.c_int64, P, P]
         L.pa_norm_rope.restype = I
-        L.pa_norm_rope_append.argtypes = [NR, P, ctypes.c_int64, P, P, P, I, I, P, P]
+        L.pa_norm_rope_append.argtypes = [P, P, ctypes.c_int64, P, P, P, I, I, P, P]
         L.pa_norm_rope_append.restype = I
-        L.pa_norm_rope_append_int4.argtypes = [NR, P, ctypes.c_int64, P, P, P, P, P, I, I, P, P]
+        L.pa_norm_rope_append_int4.argtypes = [P, P, ctypes.c_int64, P, P, P, P, P, I, I, P, P]
         L.pa_norm_rope_append_int4.restype = I
         L.pa_status_string.argtypes = [I]
         L.pa_status_string.restype = ctypes.c_char_p
@@ -749,18 +754,70 @@ def pa_decode_noalloc(q, k_cache, v_cache, block_tables, context_lens, scale, ou
         raise PagedAttentionError(rc, what)
 
 
-def _check_int4_pool(k_cache, v_cache, k_params, v_params):
-    """(NB, Hkv, bs, D) of a 4-bit pool."""
+# The calls below check each tensor on the way to its pointer: on a decode step the
+# host's part of a call is as long as a small kernel, and these attributes are
+# most of it.
+
+def _arg(name, t, dev, dtype=None, ndim=None):
+    """The pointer of a contiguous CUDA tensor on device `dev` (torch's current
+    one) with the given type and dimensions, or the checks' error."""
+    try:
+        if t.get_device() == dev and t.is_contiguous() and (dtype is None or t.dtype is dtype) \
+                and (ndim is None or t.dim() == ndim):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _check_cuda(name, t, dtype, ndim)
+    _check_device(None, t)
+    return t.data_ptr()
+
+
+def _opt_arg(name, t, dev, dtype=None, ndim=None):
+    return None if t is None else _arg(name, t, dev, dtype, ndim)
+
+
+def _heads_arg(name, t, dev, dtype=None):
+    """Pointer and token stride (elements) of a CUDA tensor [T][H][D] whose
+    tokens may lie any distance apart (a part of a fused projection's output)."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must have 3 dimensions, got {t.dim()}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    T, H, D = t.shape
+    st, sh, sd = t.stride()
+    if (sd != 1 and D > 1) or (sh != D and H > 1):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    if t.device.index != dev:
+        _check_device(None, t)
+    return t.data_ptr(), (st if T > 1 else H * D)
+
+
+def _stream_on(stream, dev):
+    """The raw stream: the given one (on device `dev`), else torch's current one."""
+    if stream is None:
+        import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        return (raw(dev) or None) if raw is not None else _stream(None)
+    _check_device(stream)
+    return _stream(stream)
+
+
+def _int4_pool(k_cache, v_cache, k_params, v_params, dev):
+    """((NB, Hkv, bs, D), the four pointers) of a 4-bit pool."""
     import torch
-    _check_cuda("k_cache", k_cache, torch.uint8, 4)
-    _check_cuda("v_cache", v_cache, torch.uint8, 4)
-    _check_cuda("k_params", k_params, torch.bfloat16, 4)
-    _check_cuda("v_params", v_params, torch.bfloat16, 4)
-    nb, hkv, bs, half = k_cache.shape
-    if v_cache.shape != k_cache.shape or tuple(k_params.shape) != (nb, hkv, bs, 2) \
-            or v_params.shape != k_params.shape:
+    ptrs = (_arg("k_cache", k_cache, dev, torch.uint8, 4), _arg("v_cache", v_cache, dev, torch.uint8, 4),
+            _arg("k_params", k_params, dev, torch.bfloat16, 4),
+            _arg("v_params", v_params, dev, torch.bfloat16, 4))
+    shape = k_cache.shape
+    nb, hkv, bs, half = shape
+    pairs = k_params.shape
+    if v_cache.shape != shape or v_params.shape != pairs or tuple(pairs) != (nb, hkv, bs, 2):
         raise ValueError("INT4 pools are [NB][Hkv][bs][D / 2] codes with [NB][Hkv][bs][2] params")
-    return nb, hkv, bs, 2 * half
+    return (nb, hkv, bs, 2 * half), ptrs
 
 
 def pa_reshape_and_cache_int4(k_new, v_new, slot_mapping, k_cache, v_cache, k_params, v_params,
@@ -769,21 +826,17 @@ def pa_reshape_and_cache_int4(k_new, v_new, slot_mapping, k_cache, v_cache, k_pa
     [T][Hkv][D]) -> codes (uint8 [NB][Hkv][bs][D / 2]) and one bf16 pair (lo, s)
     per row (params, [NB][Hkv][bs][2]); value = lo + s * code."""
     import torch
-    nb, hkv, bs, d = _check_int4_pool(k_cache, v_cache, k_params, v_params)
-    _check_cuda("k_new", k_new, ndim=3)
-    _check_cuda("v_new", v_new, k_new.dtype, 3)
-    _check_cuda("slot_mapping", slot_mapping, torch.int64, 1)
-    if error_word is not None:
-        _check_cuda("error_word", error_word, torch.int32)
-    if tuple(k_new.shape[1:]) != (hkv, d) or k_new.shape != v_new.shape \
-            or slot_mapping.shape[0] != k_new.shape[0]:
+    dev = torch.cuda.current_device()
+    (nb, hkv, bs, d), (kc, vc, kp, vp) = _int4_pool(k_cache, v_cache, k_params, v_params, dev)
+    kn = _arg("k_new", k_new, dev, None, 3)
+    vn = _arg("v_new", v_new, dev, k_new.dtype, 3)
+    slots = _arg("slot_mapping", slot_mapping, dev, torch.int64, 1)
+    T, h, dn = k_new.shape
+    if h != hkv or dn != d or v_new.shape != k_new.shape or slot_mapping.shape[0] != T:
         raise ValueError("shape mismatch between k_new/v_new/slot_mapping and the caches")
-    _check_device(stream, k_new, v_new, slot_mapping, k_cache, v_cache, k_params, v_params,
-                  error_word)
-    rc = lib().pa_reshape_and_cache_int4(_ptr(k_new), _ptr(v_new), _dtype_code(k_new),
-                                         _ptr(slot_mapping), _ptr(k_cache), _ptr(v_cache),
-                                         _ptr(k_params), _ptr(v_params), int(k_new.shape[0]), hkv,
-                                         d, bs, nb, _ptr(error_word), _stream(stream))
+    rc = lib().pa_reshape_and_cache_int4(kn, vn, _dtype_code(k_new), slots, kc, vc, kp, vp, T, hkv,
+                                         d, bs, nb, _opt_arg("error_word", error_word, dev, torch.int32),
+                                         _stream_on(stream, dev))
     if rc != PA_OK:
         raise PagedAttentionError(rc, "pa_reshape_and_cache_int4")
 
@@ -794,25 +847,22 @@ def pa_gather_int4(k_cache, v_cache, k_params, v_params, block_tables, context_l
     row_starts[s] + context_lens[s] - 1 of k_out/v_out ([rows][Hkv][D], bf16 or
     fp32). row_starts: int64 [B]. Rows that no sequence covers stay as they are."""
     import torch
-    nb, hkv, bs, d = _check_int4_pool(k_cache, v_cache, k_params, v_params)
-    _check_cuda("block_tables", block_tables, torch.int32, 2)
-    _check_cuda("context_lens", context_lens, torch.int32, 1)
-    _check_cuda("row_starts", row_starts, torch.int64, 1)
-    _check_cuda("k_out", k_out, ndim=3)
-    _check_cuda("v_out", v_out, k_out.dtype, 3)
-    if error_word is not None:
-        _check_cuda("error_word", error_word, torch.int32)
-    B = context_lens.shape[0]
-    if block_tables.shape[0] != B or row_starts.shape[0] != B or k_out.shape != v_out.shape \
-            or tuple(k_out.shape[1:]) != (hkv, d):
+    dev = torch.cuda.current_device()
+    (nb, hkv, bs, d), (kc, vc, kp, vp) = _int4_pool(k_cache, v_cache, k_params, v_params, dev)
+    bt = _arg("block_tables", block_tables, dev, torch.int32, 2)
+    cl = _arg("context_lens", context_lens, dev, torch.int32, 1)
+    rs = _arg("row_starts", row_starts, dev, torch.int64, 1)
+    ko = _arg("k_out", k_out, dev, None, 3)
+    vo = _arg("v_out", v_out, dev, k_out.dtype, 3)
+    B, mb = block_tables.shape
+    rows, h, do = k_out.shape
+    if context_lens.shape[0] != B or row_starts.shape[0] != B or v_out.shape != k_out.shape \
+            or h != hkv or do != d:
         raise ValueError("shape mismatch between the outputs, the tables and the caches")
-    _check_device(stream, k_cache, v_cache, k_params, v_params, block_tables, context_lens,
-                  row_starts, k_out, v_out, error_word)
-    rc = lib().pa_gather_int4(_ptr(k_cache), _ptr(v_cache), _ptr(k_params), _ptr(v_params),
-                              _ptr(block_tables), _ptr(context_lens), _ptr(row_starts),
-                              _ptr(k_out), _ptr(v_out), _dtype_code(k_out), int(k_out.shape[0]),
-                              B, hkv, d, bs, nb, int(block_tables.shape[1]),
-                              int(max_context_len), _ptr(error_word), _stream(stream))
+    rc = lib().pa_gather_int4(kc, vc, kp, vp, bt, cl, rs, ko, vo, _dtype_code(k_out), rows, B, hkv, d,
+                              bs, nb, mb, int(max_context_len),
+                              _opt_arg("error_word", error_word, dev, torch.int32),
+                              _stream_on(stream, dev))
     if rc != PA_OK:
         raise PagedAttentionError(rc, "pa_gather_int4")
 
@@ -827,94 +877,77 @@ def pa_decode_int4(q, k_cache, v_cache, k_params, v_params, block_tables, contex
     pa_decode_workspace_size_multi(B, Q, Hq, D, max_context_len) bytes; when
     None, one is allocated from torch's caching allocator for this call."""
     import torch
-    nb, hkv, bs, d = _check_int4_pool(k_cache, v_cache, k_params, v_params)
-    _check_cuda("q", q, torch.bfloat16)
-    _check_cuda("out", out, torch.bfloat16)
-    _check_cuda("block_tables", block_tables, torch.int32, 2)
-    _check_cuda("context_lens", context_lens, torch.int32, 1)
-    if error_word is not None:
-        _check_cuda("error_word", error_word, torch.int32)
-    if q.dim() == 3:
-        (B, hq, dq), Q = q.shape, 1
-    elif q.dim() == 4:
-        B, Q, hq, dq = q.shape
+    dev = torch.cuda.current_device()
+    (nb, hkv, bs, d), (kc, vc, kp, vp) = _int4_pool(k_cache, v_cache, k_params, v_params, dev)
+    qp = _arg("q", q, dev, torch.bfloat16)
+    op = _arg("out", out, dev, torch.bfloat16)
+    bt = _arg("block_tables", block_tables, dev, torch.int32, 2)
+    cl = _arg("context_lens", context_lens, dev, torch.int32, 1)
+    shape = q.shape
+    if len(shape) == 3:
+        (B, hq, dq), Q = shape, 1
+    elif len(shape) == 4:
+        B, Q, hq, dq = shape
     else:
-        raise ValueError(f"q must have 3 or 4 dimensions, got {q.dim()}")
-    if dq != d or out.shape != q.shape or block_tables.shape[0] != B or context_lens.shape[0] != B:
+        raise ValueError(f"q must have 3 or 4 dimensions, got {len(shape)}")
+    rows, mb = block_tables.shape
+    if dq != d or out.shape != shape or rows != B or context_lens.shape[0] != B:
         raise ValueError("shape mismatch between q/out/block_tables/context_lens and the caches")
-    _check_device(stream, q, out, k_cache, v_cache, k_params, v_params, block_tables,
-                  context_lens, error_word, workspace)
     if workspace is None:
         need = pa_decode_workspace_size_multi(B, Q, hq, d, int(max_context_len))
         workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
-    _check_cuda("workspace", workspace)
-    rc = lib().pa_decode_int4(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_params),
-                              _ptr(v_params), _ptr(block_tables), _ptr(context_lens),
-                              float(scale), int(window), _ptr(out), B, Q, hq, hkv, d, bs, nb,
-                              int(block_tables.shape[1]), int(max_context_len), _ptr(workspace),
-                              workspace.numel() * workspace.element_size(), _ptr(error_word),
-                              _stream(stream))
+    ws = _arg("workspace", workspace, dev)
+    rc = lib().pa_decode_int4(qp, kc, vc, kp, vp, bt, cl, float(scale), int(window), op, B, Q, hq, hkv,
+                              d, bs, nb, mb, int(max_context_len), ws,
+                              workspace.numel() * workspace.element_size(),
+                              _opt_arg("error_word", error_word, dev, torch.int32),
+                              _stream_on(stream, dev))
     if rc != PA_OK:
         raise PagedAttentionError(rc, "pa_decode_int4")
 
 
-def _check_heads(name, t, dtype=None):
-    """A CUDA tensor [T][H][D] whose tokens may lie any distance apart (a part
-    of a fused projection's output); returns that distance in elements."""
-    if t is None:
-        raise ValueError(f"{name} is required")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() != 3:
-        raise ValueError(f"{name} must have 3 dimensions, got {t.dim()}")
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    T, H, D = t.shape
-    st, sh, sd = t.stride()
-    if (sd != 1 and D > 1) or (sh != D and H > 1):
-        raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return st if T > 1 else H * D
-
-
 def _norm_rope_args(q, k, positions, cos_sin, q_out, q_weight, k_weight, eps, weight_offset,
-                    interleaved, pair_axis, error_word):
+                    interleaved, pair_axis, dev):
     import torch
-    q_stride = _check_heads("q", q)
-    k_stride = _check_heads("k", k, q.dtype)
-    q_out_stride = _check_heads("q_out", q_out, q.dtype)
-    dtype = _dtype_code(q)
-    T, hq, d = q.shape
-    if k.shape[0] != T or k.shape[2] != d or q_out.shape != q.shape:
+    qp, q_stride = _heads_arg("q", q, dev)
+    dt = q.dtype
+    kp, k_stride = _heads_arg("k", k, dev, dt)
+    op, q_out_stride = (qp, q_stride) if q_out is q else _heads_arg("q_out", q_out, dev, dt)
+    shape, k_shape = q.shape, k.shape
+    T, hq, d = shape
+    if k_shape[0] != T or k_shape[2] != d or q_out.shape != shape:
         raise ValueError("shape mismatch between q, k and q_out")
-    weight_dtype = 0
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+    weight_dtype, wp = 0, [None, None]
+    for i, (name, w) in enumerate((("q_weight", q_weight), ("k_weight", k_weight))):
         if w is not None:
-            _check_cuda(name, w, ndim=1)
+            wp[i] = _arg(name, w, dev, None, 1)
             if w.shape[0] != d:
                 raise ValueError(f"{name} must hold head_dim elements")
             weight_dtype = _dtype_code(w)
     if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
         raise TypeError("q_weight and k_weight must have the same type")
-    rot, max_position, axes, axis_bytes = 0, 0, 1, None
+    rot, max_position, axes, axis_bytes, cs, pos = 0, 0, 1, None, None, None
+    axis_ptr = 0
     if cos_sin is not None:
-        _check_cuda("cos_sin", cos_sin, torch.float32, 2)
-        _check_cuda("positions", positions, torch.int32)
+        cs = _arg("cos_sin", cos_sin, dev, torch.float32, 2)
+        pos = _arg("positions", positions, dev, torch.int32)
         max_position, rot = cos_sin.shape
-        axes = 1 if positions.dim() == 1 else positions.shape[0]
-        if positions.dim() not in (1, 2) or positions.shape[-1] != T:
+        pos_shape = positions.shape
+        if len(pos_shape) not in (1, 2) or pos_shape[-1] != T:
             raise ValueError("positions must be [T] or [axes][T]")
+        axes = 1 if len(pos_shape) == 1 else pos_shape[0]
         if pair_axis is not None:
             axis_bytes = bytes(pair_axis)
             if len(axis_bytes) != rot // 2:
                 raise ValueError("pair_axis must hold rot_dim / 2 axis numbers")
+            axis_ptr = ctypes.cast(axis_bytes, ctypes.c_void_p).value
     elif positions is not None or pair_axis is not None:
         raise ValueError("positions and pair_axis need cos_sin")
-    if error_word is not None:
-        _check_cuda("error_word", error_word, torch.int32)
-    return _NormRopeArgs(_ptr(q), _ptr(k), q_stride, k_stride, _ptr(q_out), q_out_stride,
-                         _ptr(q_weight), _ptr(k_weight), float(eps), float(weight_offset),
-                         _ptr(cos_sin), _ptr(positions), axis_bytes, T, hq, k.shape[1], d, rot,
-                         max_position, axes, int(bool(interleaved)), dtype, weight_dtype)
+    # The second is what the first points at: it has to outlive the call.
+    return _norm_rope_pack(qp, kp, q_stride, k_stride, op, q_out_stride, wp[0] or 0, wp[1] or 0, eps,
+                           weight_offset, cs or 0, pos or 0, axis_ptr, T, hq, k_shape[1], d, rot,
+                           max_position, axes, 1 if interleaved else 0, _dtype_code(q),
+                           weight_dtype), axis_bytes
 
 
 def pa_norm_rope(q, k, positions, cos_sin, q_out, k_out, q_weight=None, k_weight=None, eps=1e-6,
@@ -929,25 +962,28 @@ def pa_norm_rope(q, k, positions, cos_sin, q_out, k_out, q_weight=None, k_weight
     the rot_dim / 2 pairs. cos_sin: fp32 [max_position][rot_dim], cosines then
     sines; None (with positions None): no rotation. interleaved: pairs are
     (2i, 2i + 1), else (i, i + rot_dim / 2)."""
-    args = _norm_rope_args(q, k, positions, cos_sin, q_out, q_weight, k_weight, eps,
-                           weight_offset, interleaved, pair_axis, error_word)
-    k_out_stride = _check_heads("k_out", k_out, k.dtype)
+    import torch
+    dev = torch.cuda.current_device()
+    args, _axes = _norm_rope_args(q, k, positions, cos_sin, q_out, q_weight, k_weight, eps,
+                           weight_offset, interleaved, pair_axis, dev)
+    ko, k_out_stride = _heads_arg("k_out", k_out, dev, k.dtype)
     if k_out.shape != k.shape:
         raise ValueError("shape mismatch between k and k_out")
-    _check_device(stream, q, k, positions, cos_sin, q_out, k_out, q_weight, k_weight, error_word)
-    rc = lib().pa_norm_rope(ctypes.byref(args), _ptr(k_out), k_out_stride, _ptr(error_word),
-                            _stream(stream))
+    rc = lib().pa_norm_rope(args, ko, k_out_stride,
+                            _opt_arg("error_word", error_word, dev, torch.int32),
+                            _stream_on(stream, dev))
     if rc != PA_OK:
         raise PagedAttentionError(rc, "pa_norm_rope")
 
 
-def _check_append_rows(k, v, slot_mapping, hkv, d):
+def _append_args(k, v, slot_mapping, hkv, d, dev):
     import torch
-    v_stride = _check_heads("v", v, k.dtype)
-    _check_cuda("slot_mapping", slot_mapping, torch.int64, 1)
-    if v.shape != k.shape or tuple(k.shape[1:]) != (hkv, d) or slot_mapping.shape[0] != k.shape[0]:
+    vp, v_stride = _heads_arg("v", v, dev, k.dtype)
+    slots = _arg("slot_mapping", slot_mapping, dev, torch.int64, 1)
+    T, h, dk = k.shape
+    if v.shape != k.shape or h != hkv or dk != d or slot_mapping.shape[0] != T:
         raise ValueError("shape mismatch between k/v/slot_mapping and the caches")
-    return v_stride
+    return vp, v_stride, slots
 
 
 def pa_norm_rope_append(q, k, v, positions, cos_sin, slot_mapping, q_out, k_cache, v_cache,
@@ -956,21 +992,19 @@ def pa_norm_rope_append(q, k, v, positions, cos_sin, slot_mapping, q_out, k_cach
     """pa_norm_rope whose K rows go into their slots of the paged pool
     ([NB][Hkv][bs][D], q's type), with the V rows beside them (a bit copy).
     slot_mapping: int64 [T], negative = no append."""
-    _check_cuda("k_cache", k_cache, ndim=4)
-    _check_cuda("v_cache", v_cache, k_cache.dtype, 4)
-    args = _norm_rope_args(q, k, positions, cos_sin, q_out, q_weight, k_weight, eps,
-                           weight_offset, interleaved, pair_axis, error_word)
+    import torch
+    dev = torch.cuda.current_device()
+    args, _axes = _norm_rope_args(q, k, positions, cos_sin, q_out, q_weight, k_weight, eps,
+                           weight_offset, interleaved, pair_axis, dev)
+    kc = _arg("k_cache", k_cache, dev, q.dtype, 4)
+    vc = _arg("v_cache", v_cache, dev, q.dtype, 4)
     nb, hkv, bs, d = k_cache.shape
-    if k_cache.dtype != q.dtype:
-        raise TypeError(f"k_cache must be {q.dtype}, got {k_cache.dtype}")
     if v_cache.shape != k_cache.shape:
         raise ValueError("v_cache must match k_cache")
-    v_stride = _check_append_rows(k, v, slot_mapping, hkv, d)
-    _check_device(stream, q, k, v, positions, cos_sin, slot_mapping, q_out, k_cache, v_cache,
-                  q_weight, k_weight, error_word)
-    rc = lib().pa_norm_rope_append(ctypes.byref(args), _ptr(v), v_stride, _ptr(slot_mapping),
-                                   _ptr(k_cache), _ptr(v_cache), bs, nb, _ptr(error_word),
-                                   _stream(stream))
+    vp, v_stride, slots = _append_args(k, v, slot_mapping, hkv, d, dev)
+    rc = lib().pa_norm_rope_append(args, vp, v_stride, slots, kc, vc, bs, nb,
+                                   _opt_arg("error_word", error_word, dev, torch.int32),
+                                   _stream_on(stream, dev))
     if rc != PA_OK:
         raise PagedAttentionError(rc, "pa_norm_rope_append")
 
@@ -982,15 +1016,14 @@ def pa_norm_rope_append_int4(q, k, v, positions, cos_sin, slot_mapping, q_out, k
     """pa_norm_rope whose K rows are quantised into a 4-bit cache, with the V
     rows (codes and params as of pa_reshape_and_cache_int4 on pa_norm_rope's
     K rows). slot_mapping: int64 [T], negative = no append."""
-    nb, hkv, bs, d = _check_int4_pool(k_cache, v_cache, k_params, v_params)
-    args = _norm_rope_args(q, k, positions, cos_sin, q_out, q_weight, k_weight, eps,
-                           weight_offset, interleaved, pair_axis, error_word)
-    v_stride = _check_append_rows(k, v, slot_mapping, hkv, d)
-    _check_device(stream, q, k, v, positions, cos_sin, slot_mapping, q_out, k_cache, v_cache,
-                  k_params, v_params, q_weight, k_weight, error_word)
-    rc = lib().pa_norm_rope_append_int4(ctypes.byref(args), _ptr(v), v_stride, _ptr(slot_mapping),
-                                        _ptr(k_cache), _ptr(v_cache), _ptr(k_params),
-                                        _ptr(v_params), bs, nb, _ptr(error_word),
-                                        _stream(stream))
+    import torch
+    dev = torch.cuda.current_device()
+    (nb, hkv, bs, d), (kc, vc, kp, vq) = _int4_pool(k_cache, v_cache, k_params, v_params, dev)
+    args, _axes = _norm_rope_args(q, k, positions, cos_sin, q_out, q_weight, k_weight, eps,
+                           weight_offset, interleaved, pair_axis, dev)
+    vp, v_stride, slots = _append_args(k, v, slot_mapping, hkv, d, dev)
+    rc = lib().pa_norm_rope_append_int4(args, vp, v_stride, slots, kc, vc, kp, vq, bs, nb,
+                                        _opt_arg("error_word", error_word, dev, torch.int32),
+                                        _stream_on(stream, dev))
     if rc != PA_OK:
         raise PagedAttentionError(rc, "pa_norm_rope_append_int4")

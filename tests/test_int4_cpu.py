@@ -152,6 +152,15 @@ def test_norm_rope_refusals(lib, kw, status):
     assert _norm(lib, **kw) == status
 
 
+def test_packed_arguments_are_the_header_s_struct():
+    import struct
+    assert struct.calcsize("@PPqqPqPPffPPP10i") == ctypes.sizeof(pa._NormRopeArgs)
+    values = list(range(1, 9)) + [0.5, 0.25] + list(range(9, 12)) + list(range(20, 30))
+    s = pa._NormRopeArgs.from_buffer_copy(pa._norm_rope_pack(*values))
+    got = [getattr(s, n) for n, _ in s._fields_ if n != "pair_axis"]
+    assert got == values[:12] + values[13:]
+
+
 def test_norm_rope_append_refusals(lib):
     def pool(v=FAKE, v_stride=256, slots=FAKE, kc=FAKE, vc=FAKE, bs=16, nb=4, **kw):
         args = pa._NormRopeArgs(**{**NORM, **kw})
