@@ -34,7 +34,7 @@
 // maximum and no rescale. Sums, z = sum p lo, scores and outputs are fp32.
 //
 // Work: items of at most kItemRows rows (sequence, KV head, partition) dealt to
-// persistent CTAs (pa_plan.cuh); warp w of a CTA takes units w, w + 4, ... of
+// persistent CTAs in the order of pa_plan.cuh (plan4 below); warp w of a CTA takes units w, w + 4, ... of
 // 32 rows (two 16-row tiles, each inside one block) of each item. Every warp
 // streams its own units through its own shared-memory ring with 16-byte
 // cp.async, STAGES - 1 units ahead and across item boundaries: a tile is 1 KB of
@@ -43,8 +43,8 @@
 // merged through shared memory.
 #include <atomic>
 
-#include "pa_decode_stream.cuh"
 #include "pa_int4.cuh"
+#include "pa_plan.cuh"
 #include "pa_tile_math_quant.cuh"
 
 namespace pa {
@@ -85,6 +85,140 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     return r;
 }
 
+__device__ __forceinline__ void grid_dependency_wait() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void grid_launch_dependents() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+// The work list of one CTA, in the order of pa_plan.cuh: every full partition by
+// sequence, partition and KV head, then the partial last partitions in 16 size
+// buckets, largest first, by sequence within a bucket; dealt in a snake. Warp w
+// takes the w-th quarter of the sequences, 32 at a time, so that one barrier
+// joins the warps' counts: 1.2 us at 128 sequences where the general plan (two
+// partition sizes, barriers per 128 sequences) takes 4.2, all of it before the
+// first tile is used.
+constexpr int kListItems = 32;                 // of the CTA's items in shared memory
+constexpr int kItemShift = 10;
+static_assert(kItemRows == 1 << kItemShift && kPlanBuckets == 16 && kWarps == 4, "");
+struct Plan4 {
+    int4 list[kListItems];                     // the CTA's items; the rest in p.items
+    int full[kWarps];                          // full partitions of a warp's sequences
+    int hist[kWarps][kPlanBuckets];            // partial ones by bucket
+    float col_f[2][8];                         // q columns' factors, two items' in turn
+    int col_row[8];                            // column c's row beside column 0's
+};
+
+// All threads of the CTA; returns the launch's item count. The lists may be
+// read after the next __syncthreads.
+__device__ int plan4(const DecodeParams& p, int c, int C, Plan4* sm) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int B = p.num_seqs, Hkv = p.num_kv_heads;
+    const int per_warp = (B + kThreads4 - 1) / kThreads4 * 32;
+    const int begin = warp * per_warp, end = min(B, begin + per_warp);
+    const float inv_c = 1.0f / static_cast<float>(C);
+    if (lane < kPlanBuckets) sm->hist[warp][lane] = 0;
+    __syncwarp();
+
+    int full = 0, n_kept = -1;
+    for (int s0 = begin; s0 < end; s0 += 32) {
+        const int s = s0 + lane;
+        const bool mine = s < end && (s < C ? s : s % C) == c;
+        const int n = s < end ? plan_len(p, s, mine) : -1;
+        n_kept = n;
+        const int span = n > 0 ? n - seq_row_base(n, p.window) : 0;
+        full += __reduce_add_sync(0xffffffffu, span >> kItemShift);
+        const int r = span & (kItemRows - 1);
+        if (r > 0) atomicAdd(&sm->hist[warp][(kItemRows - r) * kPlanBuckets >> kItemShift], 1);
+        // The output rows of empty sequences are zeros.
+        unsigned empty = __ballot_sync(0xffffffffu, mine && n == 0);
+        while (empty != 0u) {
+            const int e = s0 + __ffs(empty) - 1;
+            empty &= empty - 1u;
+            const int chunks = p.num_queries * p.num_heads * p.head_dim / 8;   // of 16 bytes
+            uint4* rows = static_cast<uint4*>(p.out) + static_cast<size_t>(e) * chunks;
+            for (int i = lane; i < chunks; i += 32) rows[i] = make_uint4(0u, 0u, 0u, 0u);
+        }
+    }
+    if (lane == 0) sm->full[warp] = full;
+    __syncthreads();
+
+    int full_at = 0, full_all = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) full_at += sm->full[w];
+        full_all += sm->full[w];
+    }
+    // Lane b < 16: where this warp's partial partitions of bucket b start.
+    int part_at = 0, part_all = 0;
+    {
+        int before = 0, count = 0;
+        if (lane < kPlanBuckets) {
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const int h = sm->hist[w][lane];
+                if (w < warp) before += h;
+                count += h;
+            }
+        }
+        int incl = count;
+#pragma unroll
+        for (int off = 1; off < kPlanBuckets; off <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += u;
+        }
+        part_at = incl - count + before;
+        part_all = __shfl_sync(0xffffffffu, incl, kPlanBuckets - 1);
+    }
+    // Puts those of items a .. e - 1 that are this CTA's. The first round is
+    // found in fp32 and may come out one early, never late.
+    auto put = [&](int a, int e, auto&& item) {
+        if (a >= e) return;
+        for (int j = max(0, static_cast<int>(static_cast<float>(a) * inv_c * 0.999999f) - 1); j * C < e; ++j) {
+            const int k = snake_item(c, j, C);
+            if (k < a || k >= e) continue;
+            if (j < kListItems)
+                sm->list[j] = item(k - a);
+            else
+                p.items[k] = item(k - a);
+        }
+    };
+    const unsigned below = (1u << lane) - 1u;
+    for (int s0 = begin; s0 < end; s0 += 32) {
+        const int s = s0 + lane;
+        const int n = per_warp == 32 ? n_kept : s < end ? plan_len(p, s, false) : -1;
+        const int span = n > 0 ? n - seq_row_base(n, p.window) : 0;
+        const int nf = span >> kItemShift, r = span & (kItemRows - 1);
+        int incl = nf;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += u;
+        }
+        const int a = (full_at + incl - nf) * Hkv;
+        put(a, a + nf * Hkv, [&](int i) { return make_int4(s, i % Hkv, i / Hkv, n); });
+        full_at += __shfl_sync(0xffffffffu, incl, 31);
+
+        const int b = r > 0 ? (kItemRows - r) * kPlanBuckets >> kItemShift : kPlanBuckets;
+        const unsigned same = __match_any_sync(0xffffffffu, b);
+        const int start = __shfl_sync(0xffffffffu, part_at, b & (kPlanBuckets - 1));
+        if (r > 0) {
+            const int f = (full_all + start + __popc(same & below)) * Hkv;
+            put(f, f + Hkv, [&](int i) { return make_int4(s, i, nf, n); });
+        }
+        if (per_warp > 32) {
+#pragma unroll
+            for (int k = 0; k < kPlanBuckets; ++k) {
+                const unsigned m = __ballot_sync(0xffffffffu, b == k);
+                if (lane == k) part_at += __popc(m);
+            }
+        }
+    }
+    return (full_all + part_all) * Hkv;
+}
+
 template <int D, int NC, int STAGES>
 struct Smem4 {
     static constexpr int kCodes = kTileRows * D / 2;                 // K or V codes of a tile
@@ -96,10 +230,13 @@ struct Smem4 {
     static constexpr int kCol = D + 4;
     static constexpr int kState = NC * (kCol + 2);                   // o, then m, l
     static constexpr int kMerge = kWarps * kState * 4;
-    static constexpr int kQ = kRing + kMerge;                        // q fragments [D / 32][lane]
-    static constexpr int kFirst = kQ + (D / 32) * 32 * 16;           // the first two items
-    static constexpr int kBytes = kFirst + 2 * 16 + 8 * 4 + 8 * 4;   // columns' rows and factors
-    static_assert(kMerge >= 4 * plan_scratch_ints(kThreads4), "the plan's scratch lives there");
+    // Two merge areas in turn, where they leave room for three CTAs on an SM:
+    // one barrier per item instead of two.
+    static constexpr int kMerges = NC <= 4 ? 2 : 1;
+    static constexpr int kQFrag = (D / 32) * 32 * 16;                // q fragments [D / 32][lane]
+    static constexpr int kQ = kRing + kMerges * kMerge;              // two items' in turn
+    static constexpr int kPlan = kQ + 2 * kQFrag;
+    static constexpr int kBytes = kPlan + static_cast<int>(sizeof(Plan4));
     static_assert((kRing + kMerge) % 16 == 0, "16-byte fragments follow");
 };
 
@@ -112,10 +249,9 @@ __global__ void __launch_bounds__(kThreads4, MIN_CTAS) decode_int4_kernel(const 
 
     extern __shared__ __align__(128) uint8_t smem_raw[];
     float* merge = reinterpret_cast<float*>(smem_raw + Smem::kRing);
-    uint4* q_frag = reinterpret_cast<uint4*>(smem_raw + Smem::kQ);
-    int4* first_items = reinterpret_cast<int4*>(smem_raw + Smem::kFirst);
-    int* col_row = reinterpret_cast<int*>(first_items + 2);   // column c's row beside column 0's
-    float* col_f = reinterpret_cast<float*>(col_row + 8);
+    uint4* q_frags = reinterpret_cast<uint4*>(smem_raw + Smem::kQ);
+    Plan4* const plan = reinterpret_cast<Plan4*>(smem_raw + Smem::kPlan);
+    int* const col_row = plan->col_row;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int gid = lane >> 2, t4 = lane & 3;
     const uint32_t ring = smem_addr(smem_raw) + warp * STAGES * Smem::kStage;
@@ -209,7 +345,7 @@ __global__ void __launch_bounds__(kThreads4, MIN_CTAS) decode_int4_kernel(const 
     auto own_item = [&](int j) -> int4 {
         const int k = snake_item(c, j, C);
         if (k >= total) return make_int4(-1, 0, 0, 0);
-        return j < 2 ? first_items[j] : p.items[k];
+        return j < kListItems ? plan->list[j] : p.items[k];
     };
     // The next unit of the stream, if any; a commit group in any case.
     auto issue = [&]() {
@@ -241,14 +377,15 @@ __global__ void __launch_bounds__(kThreads4, MIN_CTAS) decode_int4_kernel(const 
     const int q_col = 2 * warp + lane / 16, q_part = lane % 16;
     const bool q_mine = q_col < ncols && q_part < kQLanes;
     const int q_row = q_mine ? q_col / grp * p.num_heads + q_col % grp : 0;
-    uint4 q_raw = make_uint4(0u, 0u, 0u, 0u);
+    uint4 q_raw = make_uint4(0u, 0u, 0u, 0u);   // of the next item to deal
     auto load_q = [&](const int4& d) {
         if (d.x >= 0 && q_mine)
             q_raw = __ldg(reinterpret_cast<const uint4*>(
                 static_cast<const __nv_bfloat16*>(p.q) +
                 (static_cast<size_t>(d.x) * Q * p.num_heads + d.y * grp + q_row) * D) + q_part);
     };
-    auto deal_q = [&]() {
+    auto deal_q = [&](int buf) {
+        uint4* q_frag = q_frags + buf * (Smem::kQFrag / 16);
         const uint32_t w[4] = {q_raw.x, q_raw.y, q_raw.z, q_raw.w};
         float x[8], mx = 0.f;
 #pragma unroll
@@ -271,11 +408,12 @@ __global__ void __launch_bounds__(kThreads4, MIN_CTAS) decode_int4_kernel(const 
                            pack_f16x2(x[2] * f, x[6] * f), pack_f16x2(x[3] * g, x[7] * g));
         // S = F S', S' = s acc + lo qsum, acc = f 2^-24 q . c, qsum = f 2^-24 q . 1,
         // F = |scale| 2^24 / f (kept above 0: scale 0 gives equal weights).
-        if (q_part == 0) col_f[q_col] = fmaxf(fabsf(p.scale_log2) * (inv * 16777216.f), 1e-30f);
+        if (q_part == 0) plan->col_f[buf][q_col] = fmaxf(fabsf(p.scale_log2) * (inv * 16777216.f), 1e-30f);
     };
     uint32_t qb[kKWords][4];
     float qf[2], qsum[2];                  // of columns 2 t4 and 2 t4 + 1
-    auto take_q = [&]() {
+    auto take_q = [&](int buf) {
+        const uint4* q_frag = q_frags + buf * (Smem::kQFrag / 16);
         float ones[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < kKWords; ++i) {
@@ -284,42 +422,25 @@ __global__ void __launch_bounds__(kThreads4, MIN_CTAS) decode_int4_kernel(const 
             mma_16816_f16(ones, 0x00010001u, 0x00010001u, 0x00100010u, 0x00100010u, v.x, v.y);
             mma_16816_f16(ones, 0x00010001u, 0x00010001u, 0x00100010u, 0x00100010u, v.z, v.w);
         }
-        const float2 F = *reinterpret_cast<const float2*>(col_f + 2 * t4);
+        const float2 F = *reinterpret_cast<const float2*>(&plan->col_f[buf][2 * t4]);
         qf[0] = F.x; qf[1] = F.y;
         qsum[0] = ones[0]; qsum[1] = ones[1];
     };
 
-    // The first item where the warp can find it without the plan: its tiles
-    // and q are on their way while the CTA computes its work list.
-    const int4 first = first_item_by_warp(p, c, lane);
-    static_assert(STAGES - 1 <= kWarpUnits, "a full partition fills the ring");
-    if (first.x >= 0) {
-        fetch(first);
-        enter(first);
-#pragma unroll
-        for (int i = 0; i < STAGES - 1; ++i) issue();
-        load_q(first);
-    }
-    total = plan_cta<__nv_bfloat16, kThreads4>(p, c, C, reinterpret_cast<int*>(merge), first_items);
+    total = plan4(p, c, C, plan);
+    __syncthreads();
     int4 it = own_item(0);
-    if (it.x < 0) {
-        cp_async_wait_group<0>();
-        return;
-    }
-    if (first.x < 0) {
-        fetch(it);
-        enter(it);
-        load_q(it);
-    }
+    if (it.x < 0) return;
+    fetch(it);
+    enter(it);
+    load_q(it);
     d_next = own_item(1);
     fetch(d_next);
     d_after = own_item(2);
-    if (first.x < 0) {
 #pragma unroll 1
-        for (int i = 0; i < STAGES - 1; ++i) issue();
-    }
-    deal_q();
-    __syncthreads();                       // q is dealt; the plan's scratch becomes the merge area
+    for (int i = 0; i < STAGES - 1; ++i) issue();
+    deal_q(0);
+    __syncthreads();
 
     uint32_t at = ring;                    // the stage of the next unit
     const int j0 = (2 * t4) / grp, j1 = (2 * t4 + 1) / grp;   // the columns' query tokens
@@ -337,7 +458,8 @@ __global__ void __launch_bounds__(kThreads4, MIN_CTAS) decode_int4_kernel(const 
         int lo, tiles;
         const int cnt = units_of(it, lo, tiles);
         const int4 it_after = own_item(j + 2);
-        take_q();
+        take_q(j & 1);
+        load_q(it_next);                   // dealt at this item's end
         float o[kMt][4];
 #pragma unroll
         for (int mt = 0; mt < kMt; ++mt)
@@ -472,7 +594,7 @@ __global__ void __launch_bounds__(kThreads4, MIN_CTAS) decode_int4_kernel(const 
             if (at == ring_end) at = ring;
         }
 
-        // ---- the warp's state, then the next item's q while the CTA merges
+        // ---- the warp's state and its share of the next item's q
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) {
             l0 += __shfl_xor_sync(0xffffffffu, l0, off);
@@ -480,7 +602,8 @@ __global__ void __launch_bounds__(kThreads4, MIN_CTAS) decode_int4_kernel(const 
             z0 += __shfl_xor_sync(0xffffffffu, z0, off);
             z1 += __shfl_xor_sync(0xffffffffu, z1, off);
         }
-        float* st = merge + warp * Smem::kState;
+        float* const area = merge + (j & (Smem::kMerges - 1)) * (Smem::kMerge / 4);
+        float* st = area + warp * Smem::kState;
         float* ml = st + NC * Smem::kCol;
         const int c0 = 2 * t4, c1 = 2 * t4 + 1;
         if (c0 < NC) {                     // NC is even: c1 < NC too
@@ -503,14 +626,17 @@ __global__ void __launch_bounds__(kThreads4, MIN_CTAS) decode_int4_kernel(const 
                                 fmaf((o[mt][3] - o[mt][1]) * 1048576.f, ve2, z1));
             }
         }
-        load_q(it_next);
+        deal_q((j + 1) & 1);
+        // The states and the next q are complete. With two areas, a warp that
+        // writes its next state here has passed the next item's barrier, which
+        // every warp reaches only after this merge.
         __syncthreads();
         const int nparts = (n - seq_row_base(n, p.window) + kItemRows - 1) / kItemRows;
         // Four dims of a column per thread.
         for (int idx = threadIdx.x; idx < ncols * (D / 4); idx += kThreads4) {
             const int g = idx / (D / 4), d = idx % (D / 4) * 4;
-            const float* col = merge + g * Smem::kCol + d;
-            const float* mlg = merge + NC * Smem::kCol + g;
+            const float* col = area + g * Smem::kCol + d;
+            const float* mlg = area + NC * Smem::kCol + g;
             float M = -INFINITY;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) M = fmaxf(M, mlg[w * Smem::kState]);
@@ -537,8 +663,7 @@ __global__ void __launch_bounds__(kThreads4, MIN_CTAS) decode_int4_kernel(const 
                 if (d == 0) *reinterpret_cast<float2*>(p.part_ml + 2 * slot) = make_float2(M, L);
             }
         }
-        deal_q();
-        __syncthreads();                   // the next item's states overwrite the merge area
+        if constexpr (Smem::kMerges == 1) __syncthreads();   // the next states overwrite the area
         it = it_next;
         it_next = it_after;
     }
