@@ -779,6 +779,13 @@ def _opt_arg(name, t, dev, dtype=None, ndim=None):
 def _heads_arg(name, t, dev, dtype=None):
     """Pointer and token stride (elements) of a CUDA tensor [T][H][D] whose
     tokens may lie any distance apart (a part of a fused projection's output)."""
+    try:
+        T, H, D = t.shape
+        st, sh, sd = t.stride()
+        if t.get_device() == dev and sd == 1 and (sh == D or H == 1) and (dtype is None or t.dtype is dtype):
+            return t.data_ptr(), (st if T > 1 else H * D)
+    except (AttributeError, ValueError):
+        pass
     if t is None:
         raise ValueError(f"{name} is required")
     if not t.is_cuda:
@@ -791,31 +798,48 @@ def _heads_arg(name, t, dev, dtype=None):
     st, sh, sd = t.stride()
     if (sd != 1 and D > 1) or (sh != D and H > 1):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    if t.device.index != dev:
-        _check_device(None, t)
+    _check_device(None, t)
     return t.data_ptr(), (st if T > 1 else H * D)
+
+
+_raw_stream_of = None
 
 
 def _stream_on(stream, dev):
     """The raw stream: the given one (on device `dev`), else torch's current one."""
-    if stream is None:
+    global _raw_stream_of
+    if stream is not None:
+        _check_device(stream)
+        return _stream(stream)
+    if _raw_stream_of is None:
         import torch
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        return (raw(dev) or None) if raw is not None else _stream(None)
-    _check_device(stream)
-    return _stream(stream)
+        _raw_stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda d: torch.cuda.current_stream(d).cuda_stream)
+    return _raw_stream_of(dev) or None
+
+
+_plain_codes = {}
+
+
+def _plain_dtype_code(t):
+    """_dtype_code of a tensor, float32 and bfloat16 by one lookup."""
+    if not _plain_codes:
+        import torch
+        _plain_codes.update({torch.float32: 0, torch.bfloat16: 1})
+    code = _plain_codes.get(t.dtype)
+    return _dtype_code(t) if code is None else code
 
 
 def _int4_pool(k_cache, v_cache, k_params, v_params, dev):
     """((NB, Hkv, bs, D), the four pointers) of a 4-bit pool."""
     import torch
-    ptrs = (_arg("k_cache", k_cache, dev, torch.uint8, 4), _arg("v_cache", v_cache, dev, torch.uint8, 4),
-            _arg("k_params", k_params, dev, torch.bfloat16, 4),
-            _arg("v_params", v_params, dev, torch.bfloat16, 4))
+    ptrs = (_arg("k_cache", k_cache, dev, torch.uint8, 4), _arg("v_cache", v_cache, dev, torch.uint8),
+            _arg("k_params", k_params, dev, torch.bfloat16),
+            _arg("v_params", v_params, dev, torch.bfloat16))
     shape = k_cache.shape
     nb, hkv, bs, half = shape
     pairs = k_params.shape
-    if v_cache.shape != shape or v_params.shape != pairs or tuple(pairs) != (nb, hkv, bs, 2):
+    if v_cache.shape != shape or v_params.shape != pairs or pairs != (nb, hkv, bs, 2):
         raise ValueError("INT4 pools are [NB][Hkv][bs][D / 2] codes with [NB][Hkv][bs][2] params")
     return (nb, hkv, bs, 2 * half), ptrs
 
@@ -834,7 +858,7 @@ def pa_reshape_and_cache_int4(k_new, v_new, slot_mapping, k_cache, v_cache, k_pa
     T, h, dn = k_new.shape
     if h != hkv or dn != d or v_new.shape != k_new.shape or slot_mapping.shape[0] != T:
         raise ValueError("shape mismatch between k_new/v_new/slot_mapping and the caches")
-    rc = lib().pa_reshape_and_cache_int4(kn, vn, _dtype_code(k_new), slots, kc, vc, kp, vp, T, hkv,
+    rc = lib().pa_reshape_and_cache_int4(kn, vn, _plain_dtype_code(k_new), slots, kc, vc, kp, vp, T, hkv,
                                          d, bs, nb, _opt_arg("error_word", error_word, dev, torch.int32),
                                          _stream_on(stream, dev))
     if rc != PA_OK:
@@ -859,7 +883,7 @@ def pa_gather_int4(k_cache, v_cache, k_params, v_params, block_tables, context_l
     if context_lens.shape[0] != B or row_starts.shape[0] != B or v_out.shape != k_out.shape \
             or h != hkv or do != d:
         raise ValueError("shape mismatch between the outputs, the tables and the caches")
-    rc = lib().pa_gather_int4(kc, vc, kp, vp, bt, cl, rs, ko, vo, _dtype_code(k_out), rows, B, hkv, d,
+    rc = lib().pa_gather_int4(kc, vc, kp, vp, bt, cl, rs, ko, vo, _plain_dtype_code(k_out), rows, B, hkv, d,
                               bs, nb, mb, int(max_context_len),
                               _opt_arg("error_word", error_word, dev, torch.int32),
                               _stream_on(stream, dev))
@@ -923,7 +947,7 @@ def _norm_rope_args(q, k, positions, cos_sin, q_out, q_weight, k_weight, eps, we
             wp[i] = _arg(name, w, dev, None, 1)
             if w.shape[0] != d:
                 raise ValueError(f"{name} must hold head_dim elements")
-            weight_dtype = _dtype_code(w)
+            weight_dtype = _plain_dtype_code(w)
     if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
         raise TypeError("q_weight and k_weight must have the same type")
     rot, max_position, axes, axis_bytes, cs, pos = 0, 0, 1, None, None, None
@@ -946,7 +970,7 @@ def _norm_rope_args(q, k, positions, cos_sin, q_out, q_weight, k_weight, eps, we
     # The second is what the first points at: it has to outlive the call.
     return _norm_rope_pack(qp, kp, q_stride, k_stride, op, q_out_stride, wp[0] or 0, wp[1] or 0, eps,
                            weight_offset, cs or 0, pos or 0, axis_ptr, T, hq, k_shape[1], d, rot,
-                           max_position, axes, 1 if interleaved else 0, _dtype_code(q),
+                           max_position, axes, 1 if interleaved else 0, _plain_dtype_code(q),
                            weight_dtype), axis_bytes
 
 

@@ -183,8 +183,11 @@ pa_status pa_decode_int4(const void* q, const void* k_cache, const void* v_cache
     base.v_cache = v_cache;
     base.items = reinterpret_cast<int4*>(ws + 256);
     if (parts > 1) {
+        // The outputs are written 16 bytes at a time, so they start on such a
+        // boundary: 8 bytes more at most, and the size asked for is for half the
+        // partition size.
         base.part_ml = reinterpret_cast<float*>(ws + 256 + 16 * units);
-        base.part_o = base.part_ml + 2 * units * num_queries;
+        base.part_o = base.part_ml + (2 * units * num_queries + 3) / 4 * 4;
     }
     base.error_word = error_word;
     base.scale_log2 = scale * kLog2e;

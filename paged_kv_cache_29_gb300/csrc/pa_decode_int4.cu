@@ -97,9 +97,12 @@ __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commi
 // sequence, partition and KV head, then the partial last partitions in 16 size
 // buckets, largest first, by sequence within a bucket; dealt in a snake. Warp w
 // takes the w-th quarter of the sequences, 32 at a time, so that one barrier
-// joins the warps' counts: 1.2 us at 128 sequences where the general plan (two
-// partition sizes, barriers per 128 sequences) takes 4.2, all of it before the
-// first tile is used.
+// joins the warps' counts: the list is there 2.0 us into the launch at 128
+// sequences (the context lengths' own latency is most of it), where the general
+// plan (two partition sizes, barriers per 128 sequences) took 6.3. Tried and
+// slower: one CTA of three such groups per SM that take its items in turn from a
+// counter (the GQA batch 53.8 us against 50.6: the CTAs' ends then agree, at the
+// time at which the last of them ended before).
 constexpr int kListItems = 32;                 // of the CTA's items in shared memory
 constexpr int kItemShift = 10;
 static_assert(kItemRows == 1 << kItemShift && kPlanBuckets == 16 && kWarps == 4, "");
@@ -107,7 +110,7 @@ struct Plan4 {
     int4 list[kListItems];                     // the CTA's items; the rest in p.items
     int full[kWarps];                          // full partitions of a warp's sequences
     int hist[kWarps][kPlanBuckets];            // partial ones by bucket
-    float col_f[2][8];                         // q columns' factors, two items' in turn
+    alignas(8) float col_f[2][8];              // q columns' factors, two items' in turn; read in pairs
     int col_row[8];                            // column c's row beside column 0's
 };
 

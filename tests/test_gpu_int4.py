@@ -186,6 +186,14 @@ def test_flagged_sequences_leave_the_others_alone():
     b.check(got, skip=(0, 1, 2, 3))
 
 
+@pytest.mark.parametrize("hq,lens,Q", [(1, [2100], 1), (3, [2100], 1), (1, [1025, 3000, 40], 3), (5, [1100, 2049, 7], 1)])
+def test_odd_numbers_of_partials(hq, lens, Q):
+    """Partials whose maxima and sums end off a 16-byte boundary."""
+    b = Batch(lens, hq=hq, hkv=1, d=128, Q=Q, seed=hq).upload()
+    b.check(b.decode())
+    assert int(b.err.item()) == 0
+
+
 def test_batch_invariance_is_bitwise():
     lens = [700, 33, 4000, 1, 515, 0, 2047]
     b = Batch(lens, hq=8, hkv=2, seed=13).upload()
