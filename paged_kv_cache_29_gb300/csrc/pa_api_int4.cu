@@ -157,8 +157,12 @@ pa_status pa_decode_int4(const void* q, const void* k_cache, const void* v_cache
         return PA_ERR_INVALID_ARG;
     if (static_cast<long long>(max_context_len) > static_cast<long long>(max_blocks_per_seq) * block_size)
         return PA_ERR_INVALID_ARG;
+    // Row numbers stay below 2^31 with an item's rows added, tile numbers of the
+    // pool below 2^32.
     if ((head_dim != 64 && head_dim != 128) || block_size % 16 != 0 ||
-        static_cast<long long>(num_heads / num_kv_heads) * num_queries > 8)
+        static_cast<long long>(num_heads / num_kv_heads) * num_queries > 8 ||
+        max_context_len > INT_MAX - 4096 ||
+        static_cast<double>(num_blocks) * num_kv_heads * (block_size / 16) >= 4294967296.0)
         return PA_ERR_UNSUPPORTED;
     if (num_seqs == 0) return PA_OK;
     if (!q || !out || !block_tables || !context_lens || !aligned16(q) || !aligned16(out) ||

@@ -154,6 +154,36 @@ def test_decode_peaked_softmax():
     b.check(b.decode())
 
 
+@pytest.mark.parametrize("factor", [-1.0, 0.0, -40.0])
+def test_negative_and_zero_scales(factor):
+    b = Batch([5, 600, 1500], hq=8, hkv=2, seed=25)
+    b.scale *= factor
+    b.upload()
+    b.check(b.decode())
+
+
+def test_infinite_and_nan_queries_stay_in_their_rows():
+    b = Batch([40, 700, 1300], hq=8, hkv=2, seed=26)
+    clean = b.q.copy()
+    b.q[0, 0, 1, 5], b.q[1, 0, 4, 0], b.q[2, 0, 7, 127] = 0x7FC0, 0x7F80, 0xFF80      # NaN, inf, -inf
+    got = b.upload().decode()
+    b.q = clean
+    for s, h in ((0, 1), (1, 4), (2, 7)):
+        assert not np.isfinite(got[s, 0, h]).all()
+        want, _ = ref.attention4(value(b.q[s]), b.pools, b.table[s], b.lens[s], b.scale, b.bs)
+        got[s, 0, h] = want[0, h]
+    b.check(got)
+
+
+def test_a_sequence_with_a_nan_row_leaves_the_others_alone():
+    b = Batch([600, 40, 1100], hq=8, hkv=2, seed=27)
+    for pairs in b.pools[2:]:
+        pairs[b.table[0, 3], 1, 5] = [0x7FC0, 0x7F80]
+    got = b.upload().decode()
+    assert np.isnan(got[0, 0, 4:]).all()                            # the heads of KV head 1
+    b.check(got, skip=(0,))
+
+
 def test_garbage_past_the_end_does_not_leak():
     lens = [1, 17, 40, 600]
     b = Batch(lens, hq=8, hkv=2, seed=11)
@@ -217,6 +247,14 @@ def test_more_sequences_than_one_launch_holds():
     rng = np.random.default_rng(15)
     b = Batch([int(n) for n in rng.integers(0, 40, 4400)], hq=2, hkv=1, d=64, seed=16).upload()
     b.check(b.decode())
+    assert int(b.err.item()) == 0
+
+
+def test_more_items_than_a_cta_keeps_in_shared_memory():
+    rng = np.random.default_rng(28)
+    lens = [int(n) for n in rng.integers(0, 36, 3000)]
+    b = Batch(lens, hq=8, hkv=8, d=64, seed=29).upload()            # some 50 items for each of 456 CTAs
+    b.check(b.decode(), skip=set(range(3000)) - set(rng.permutation(3000)[:400].tolist()))
     assert int(b.err.item()) == 0
 
 

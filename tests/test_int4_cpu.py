@@ -112,7 +112,8 @@ def _decode(lib, **kw):
     (dict(hq=6, hkv=4), INVALID), (dict(scale=float("nan")), INVALID), (dict(scale=float("inf")), INVALID),
     (dict(window=-1), INVALID), (dict(Q=0), INVALID), (dict(mcl=641), INVALID), (dict(B=-1), INVALID),
     (dict(d=96), UNSUPPORTED), (dict(d=256), UNSUPPORTED), (dict(bs=8), UNSUPPORTED), (dict(hq=18, hkv=2), UNSUPPORTED),
-    (dict(Q=3), UNSUPPORTED), (dict(B=0, q=None), pa.PA_OK), (dict(), WORKSPACE), (dict(ws=FAKE, wsb=100), WORKSPACE),
+    (dict(Q=3), UNSUPPORTED), (dict(mcl=2 ** 31 - 16, mb=2 ** 27), UNSUPPORTED), (dict(nb=2 ** 31 - 1, hkv=4), UNSUPPORTED),
+    (dict(B=0, q=None), pa.PA_OK), (dict(), WORKSPACE), (dict(ws=FAKE, wsb=100), WORKSPACE),
     (dict(ws=FAKE + 8, wsb=1 << 30), WORKSPACE),
 ])
 def test_decode_refusals(lib, kw, status):
