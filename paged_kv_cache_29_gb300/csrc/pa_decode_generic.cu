@@ -193,11 +193,12 @@ __global__ void __launch_bounds__(kCombineMaxWarps * 32) combine_kernel(const De
     const int n = __ldg(p.context_lens + s);
     const int span = n - seq_row_base(n, p.window);       // rows of the partitions
     const int P = seq_partition(p, span);
-    const bool merge = n <= p.context_cap && n >= p.num_queries && span > P;   // else flagged or one partition
+    const bool merge = n <= p.context_cap && n >= p.num_queries &&
+                       span > P + p.partition_tail;           // else flagged or one partition
     if (!merge && (blockIdx.x | blockIdx.y) != 0) return;
     asm volatile("griddepcontrol.wait;" ::: "memory");    // the partials are the decode kernel's output
     if (!merge) return;
-    const int np = (span + P - 1) / P;
+    const int np = (span - p.partition_tail + P - 1) / P;
     const int nw = HPB > 1 ? 1 : combine_warps(np);
     const int D = p.head_dim;
     const size_t row = static_cast<size_t>(sq) * p.num_heads + qh;

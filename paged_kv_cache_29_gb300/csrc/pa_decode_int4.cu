@@ -33,8 +33,9 @@
 // rescaled, only when a row goes past them: most units need no cross-lane
 // maximum and no rescale. Sums, z = sum p lo, scores and outputs are fp32.
 //
-// Work: items of at most kItemRows rows (sequence, KV head, partition) dealt to
-// persistent CTAs in the order of pa_plan.cuh (plan4 below); warp w of a CTA takes units w, w + 4, ... of
+// Work: items (sequence, KV head, partition) of kItemRows rows, a sequence's last
+// one of up to kTailRows more, dealt to persistent CTAs in the order of
+// pa_plan.cuh (plan4 below); warp w of a CTA takes units w, w + 4, ... of
 // 32 rows (two 16-row tiles, each inside one block) of each item. Every warp
 // streams its own units through its own shared-memory ring with 16-byte
 // cp.async, STAGES - 1 units ahead and across item boundaries: a tile is 1 KB of
@@ -55,7 +56,8 @@ constexpr int kWarps = 4;
 constexpr int kThreads4 = kWarps * 32;
 constexpr int kItemRows = kDefaultPartition4;
 constexpr int kUnitRows = 2 * kTileRows;
-constexpr int kWarpUnits = kItemRows / kUnitRows / kWarps;   // a warp's units of an item
+constexpr int kTailRows = kPartitionTail4;
+constexpr int kWarpUnits = (kItemRows + kTailRows + kUnitRows * kWarps - 1) / (kUnitRows * kWarps);   // of an item, at most
 constexpr float kRaise = 8.f;                                // M lags by at most this (base 2)
 static_assert(2 * kWarpUnits <= 32, "a lane per tile holds its place in the pool");
 
@@ -93,8 +95,8 @@ __device__ __forceinline__ void grid_launch_dependents() {
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
-// The work list of one CTA, in the order of pa_plan.cuh: every full partition by
-// sequence, partition and KV head, then the partial last partitions in 16 size
+// The work list of one CTA, in the order of pa_plan.cuh: every partition but each
+// sequence's last by sequence, partition and KV head, then the last ones in 16 size
 // buckets, largest first, by sequence within a bucket; dealt in a snake. Warp w
 // takes the w-th quarter of the sequences, 32 at a time, so that one barrier
 // joins the warps' counts: the list is there 2.0 us into the launch at 128
@@ -106,10 +108,13 @@ __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commi
 constexpr int kListItems = 32;                 // of the CTA's items in shared memory
 constexpr int kItemShift = 10;
 static_assert(kItemRows == 1 << kItemShift && kPlanBuckets == 16 && kWarps == 4, "");
+// Partitions of a sequence that spans so many rows (> 0); the last one's bucket.
+__device__ __forceinline__ int parts4(int span) { return max(1, (span - kTailRows + kItemRows - 1) >> kItemShift); }
+__device__ __forceinline__ int bucket4(int rows) { return max(0, (kItemRows - rows) * kPlanBuckets >> kItemShift); }
 struct Plan4 {
     int4 list[kListItems];                     // the CTA's items; the rest in p.items
-    int full[kWarps];                          // full partitions of a warp's sequences
-    int hist[kWarps][kPlanBuckets];            // partial ones by bucket
+    int full[kWarps];                          // a warp's sequences' partitions but the last
+    int hist[kWarps][kPlanBuckets];            // and the last ones, by bucket
     alignas(8) float col_f[2][8];              // q columns' factors, two items' in turn; read in pairs
     int col_row[8];                            // column c's row beside column 0's
 };
@@ -132,9 +137,9 @@ __device__ int plan4(const DecodeParams& p, int c, int C, Plan4* sm) {
         const int n = s < end ? plan_len(p, s, mine) : -1;
         n_kept = n;
         const int span = n > 0 ? n - seq_row_base(n, p.window) : 0;
-        full += __reduce_add_sync(0xffffffffu, span >> kItemShift);
-        const int r = span & (kItemRows - 1);
-        if (r > 0) atomicAdd(&sm->hist[warp][(kItemRows - r) * kPlanBuckets >> kItemShift], 1);
+        const int nf = n > 0 ? parts4(span) - 1 : 0;
+        full += __reduce_add_sync(0xffffffffu, nf);
+        if (n > 0) atomicAdd(&sm->hist[warp][bucket4(span - nf * kItemRows)], 1);
         // The output rows of empty sequences are zeros.
         unsigned empty = __ballot_sync(0xffffffffu, mine && n == 0);
         while (empty != 0u) {
@@ -154,7 +159,7 @@ __device__ int plan4(const DecodeParams& p, int c, int C, Plan4* sm) {
         if (w < warp) full_at += sm->full[w];
         full_all += sm->full[w];
     }
-    // Lane b < 16: where this warp's partial partitions of bucket b start.
+    // Lane b < 16: where this warp's last partitions of bucket b start.
     int part_at = 0, part_all = 0;
     {
         int before = 0, count = 0;
@@ -193,7 +198,7 @@ __device__ int plan4(const DecodeParams& p, int c, int C, Plan4* sm) {
         const int s = s0 + lane;
         const int n = per_warp == 32 ? n_kept : s < end ? plan_len(p, s, false) : -1;
         const int span = n > 0 ? n - seq_row_base(n, p.window) : 0;
-        const int nf = span >> kItemShift, r = span & (kItemRows - 1);
+        const int nf = n > 0 ? parts4(span) - 1 : 0;
         int incl = nf;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -204,10 +209,10 @@ __device__ int plan4(const DecodeParams& p, int c, int C, Plan4* sm) {
         put(a, a + nf * Hkv, [&](int i) { return make_int4(s, i % Hkv, i / Hkv, n); });
         full_at += __shfl_sync(0xffffffffu, incl, 31);
 
-        const int b = r > 0 ? (kItemRows - r) * kPlanBuckets >> kItemShift : kPlanBuckets;
+        const int b = n > 0 ? bucket4(span - nf * kItemRows) : kPlanBuckets;
         const unsigned same = __match_any_sync(0xffffffffu, b);
         const int start = __shfl_sync(0xffffffffu, part_at, b & (kPlanBuckets - 1));
-        if (r > 0) {
+        if (n > 0) {
             const int f = (full_all + start + __popc(same & below)) * Hkv;
             put(f, f + Hkv, [&](int i) { return make_int4(s, i, nf, n); });
         }
@@ -284,8 +289,10 @@ __global__ void __launch_bounds__(kThreads4, MIN_CTAS) decode_int4_kernel(const 
     // The warp's units of item d, its first row, and the warp's tiles (the last
     // unit may have one).
     auto units_of = [&](const int4& d, int& lo, int& tiles) {
-        lo = seq_row_base(d.w, p.window) + d.z * kItemRows;
-        const int nt = (min(d.w, lo + kItemRows) - lo + kTileRows - 1) / kTileRows;
+        const int base = seq_row_base(d.w, p.window);
+        lo = base + d.z * kItemRows;
+        const int rows = d.z == parts4(d.w - base) - 1 ? d.w - lo : kItemRows;
+        const int nt = (rows + kTileRows - 1) / kTileRows;
         const int nu = (nt + 1) / 2;
         const int cnt = (nu - warp + kWarps - 1) / kWarps;
         // Only the item's very last unit can be half a one.
@@ -634,7 +641,7 @@ __global__ void __launch_bounds__(kThreads4, MIN_CTAS) decode_int4_kernel(const 
         // writes its next state here has passed the next item's barrier, which
         // every warp reaches only after this merge.
         __syncthreads();
-        const int nparts = (n - seq_row_base(n, p.window) + kItemRows - 1) / kItemRows;
+        const int nparts = parts4(n - seq_row_base(n, p.window));
         // Four dims of a column per thread.
         for (int idx = threadIdx.x; idx < ncols * (D / 4); idx += kThreads4) {
             const int g = idx / (D / 4), d = idx % (D / 4) * 4;

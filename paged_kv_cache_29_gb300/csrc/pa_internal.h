@@ -49,6 +49,7 @@ struct DecodeParams {
     int partition_size;            // rows per partition (seq_partition: of shorter sequences)
     int partition_long;            // rows per partition of sequences past partition_long_from
     int partition_long_from;       // span (rows from seq_row_base) above which partition_long applies
+    int partition_tail;            // a last partition of at most this many rows joins the one before (INT4; else 0)
     int max_parts;                 // ceil(max_context_len / partition_size), >= 1: the partials' row stride
     // Failure test only (-1 otherwise): the tile-ring kernels' CTA 0 announces
     // its stream tile withhold_tile without copying it or completing its
@@ -195,6 +196,10 @@ constexpr int kDefaultPartition8 = 1024;
 // An item's fixed work (q, the warps' merge, its partial) is that of four
 // 32-row units per warp: 8b_gqa 51.3 us at 1024 rows, 58.0 at 512.
 constexpr int kDefaultPartition4 = 1024;
+// Rows behind the last full partition that join it: one more unit of 32 rows for
+// a warp costs less than an item of its own (a sliding window of 1,024 rows spans
+// up to 1,040).
+constexpr int kPartitionTail4 = 128;
 constexpr int kNoLongPartitions = 0x7fffffff;   // partition_long_from: one size for all
 // Kernel of pa_decode_fp8 and pa_append_decode_fp8 when none is requested.
 constexpr pa_kernel kFp8DefaultKernel = PA_KERNEL_MMA;

@@ -78,6 +78,7 @@ class Batch:
 
 
 RAGGED = [1, 15, 16, 0, 17, 100, 511, 512, 513, 1030, 3000, 2]
+EDGES = [1023, 1024, 1025, 1040, 1151, 1152, 1153, 2047, 2048, 2175, 2176, 2177, 3200, 3201]   # of partitions and their tails
 
 
 @pytest.mark.parametrize("d", [64, 128])
@@ -87,6 +88,14 @@ def test_decode_ragged_groups(group, d):
     got = b.decode()
     assert int(b.err.item()) == 0
     b.check(got)
+
+
+@pytest.mark.parametrize("d,hq,Q", [(64, 4, 1), (128, 4, 1), (128, 4, 2)])
+def test_decode_partition_edges(d, hq, Q):
+    b = Batch(EDGES, hq=hq, hkv=1, d=d, Q=Q, seed=d).upload()
+    b.check(b.decode())
+    b.check(b.decode(1024), 1024)
+    assert int(b.err.item()) == 0
 
 
 @pytest.mark.parametrize("bs", [32, 48, 256])
