@@ -169,8 +169,15 @@ pa_status pa_decode_int4(const void* q, const void* k_cache, const void* v_cache
         !aligned(block_tables, 4) || !aligned(context_lens, 4) ||
         !pool4_ok(k_cache, v_cache, k_params, v_params))
         return PA_ERR_INVALID_ARG;
+    // The rows that any of the Q tokens sees: the last window + Q - 1. A window
+    // that no row can be outside of is none.
+    const int rows_seen =
+        (window == 0 || window >= max_context_len) ? 0 : window + num_queries - 1;
+    // Partitions of the longest sequence: a windowed one spans its rows seen and
+    // up to 15 before them in the same tile. With one there is nothing to merge.
     constexpr int P = pa::kDefaultPartition4;
-    const long long parts = max_context_len > 0 ? ceil_div(max_context_len, P) : 1;
+    const long long most = rows_seen > 0 && rows_seen + 15 < max_context_len ? rows_seen + 15 : max_context_len;
+    const long long parts = most > P + pa::kPartitionTail4 ? ceil_div(most - pa::kPartitionTail4, P) : 1;
     const long long chunk = num_seqs < pa::kPlanMaxSeqs ? num_seqs : pa::kPlanMaxSeqs;
     if (parts * chunk * num_kv_heads > 0x3fffffffLL) return PA_ERR_UNSUPPORTED;
     if (!workspace || !aligned16(workspace) ||
@@ -199,9 +206,7 @@ pa_status pa_decode_int4(const void* q, const void* k_cache, const void* v_cache
     base.k_pairs = static_cast<const uint32_t*>(k_params);
     base.v_pairs = static_cast<const uint32_t*>(v_params);
     base.num_queries = num_queries;
-    // The rows that any of the Q tokens sees: the last window + Q - 1. A window
-    // that no row can be outside of is none.
-    base.window = (window == 0 || window >= max_context_len) ? 0 : window + num_queries - 1;
+    base.window = rows_seen;
     base.num_heads = num_heads;
     base.num_kv_heads = num_kv_heads;
     base.head_dim = head_dim;
