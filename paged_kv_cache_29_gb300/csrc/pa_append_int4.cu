@@ -4,6 +4,14 @@
 // its KV heads, TPR lanes per head: the token's slot (the row's block) is looked
 // up once, reads of new rows and writes of values run over
 // consecutive heads, contiguous.
+//
+// Measured at 65,536 tokens, 8 KV heads of 128 dims, blocks of 16 in no order:
+//            bf16 rows             fp32 rows
+//   append   69.1 us, 4,914 GB/s   94.2 us, 6,456 GB/s
+//   gather   61.8 us, 5,496 GB/s   94.3 us, 6,452 GB/s
+// beside a plain copy's 6,797 GB/s. fp32 rows are bound by memory; bf16 rows, half
+// as long, by the arithmetic per element: the quotients' five fp32 operations,
+// unpacking and packing.
 #include "pa_int4.cuh"
 #include "pa_internal.h"
 
@@ -14,10 +22,12 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarpsPerCta = kThreads / 32;
 // Warps that fill the device (16 per SM); with fewer tokens than that, several
-// warps share a token's heads.
+// warps share a token's heads (append and gather of 512 and 1,024 rows: 5.4 us,
+// 5.7 with 8 per SM).
 constexpr long long kFillWarps = 2432;
-// CTAs of the gather (32 per SM): a batch of prompts 226 us with 4,864, 283 with
-// 2,432.
+// CTAs of the gather (32 per SM). Append and gather of 128 sequences of 16 to 8,192
+// rows: 434 us with 4,864 CTAs, 445 with 2,432, 435 with 9,728 (but 149 us instead
+// of 140 for 32 equal sequences of fp32 rows).
 constexpr long long kGatherCtas = 4864;
 
 // Sixteen elements as they are loaded, their fp32 values, and the row's pair.
@@ -88,9 +98,11 @@ struct Sixteen<__nv_bfloat16, TPR> {
 };
 
 // 16 dims a lane: the pair and its reciprocal, which every lane of a row works
-// out, cost four rows of a pass once.
+// out, cost four rows of a pass once. Two passes' bf16 loads in flight, five CTAs
+// on an SM: 69.1 us at the size above, with four CTAs 73.4, with four passes in
+// flight 70.9, with one operation per fp32 value instead of pairs 79.1.
 template <typename TIn, int TPR>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 5)
 append_int4_kernel(const TIn* __restrict__ k_new, const TIn* __restrict__ v_new,
                    const int64_t* __restrict__ slot_mapping, uint8_t* __restrict__ k_cache,
                    uint8_t* __restrict__ v_cache, uint32_t* __restrict__ k_params,
@@ -150,9 +162,17 @@ append_int4_kernel(const TIn* __restrict__ k_new, const TIn* __restrict__ v_new,
     }
 }
 
-// Eight dims' values. bf16: the FMA c s + lo of two dims at a time rounds the
-// exact sum once (c, s and lo are bf16 values; 128 + c is the bf16 bits 0x4300 | c).
-__device__ __forceinline__ void put_values(__nv_bfloat16* p, uint32_t w, uint32_t pair) {
+// The values of a row of L words, one in each of the first L of its lanes; every
+// lane of the warp takes part (on: this one stores). bf16: lane c stores its own
+// word's eight dims, 16 bytes; the FMA c s + lo of two dims at a time rounds the exact
+// sum once (c, s and lo are bf16 values; 128 + c is the bf16 bits 0x4300 | c).
+// fp32: eight dims are 32 bytes, and two 16-byte stores of them would each touch
+// every other half sector, so lane c stores quads c and c + L of the row instead,
+// taken from the lanes that hold their words (65,536 rows of 8 heads of 128:
+// 94.3 us against 139.6).
+template <int TPR>
+__device__ __forceinline__ void put_values(__nv_bfloat16* row, uint32_t w, uint32_t pair, int c, int, bool on) {
+    if (!on) return;
     auto h2 = [](uint32_t x) { return *reinterpret_cast<const __nv_bfloat162*>(&x); };
     auto u = [](__nv_bfloat162 h) { return *reinterpret_cast<const uint32_t*>(&h); };
     const __nv_bfloat162 s = h2(__byte_perm(pair, 0u, 0x3232)), lo = h2(__byte_perm(pair, 0u, 0x1010));
@@ -162,15 +182,22 @@ __device__ __forceinline__ void put_values(__nv_bfloat16* p, uint32_t w, uint32_
         const uint32_t bits = ((w >> (4 * e)) & 0x000f000fu) | 0x43004300u;
         r[e] = u(__hfma2(__hsub2(h2(bits), h2(0x43004300u)), s, lo));
     }
-    *reinterpret_cast<uint4*>(p) = make_uint4(__byte_perm(r[0], r[1], 0x5410), __byte_perm(r[2], r[3], 0x5410),
-                                              __byte_perm(r[0], r[1], 0x7632), __byte_perm(r[2], r[3], 0x7632));
+    *reinterpret_cast<uint4*>(row + 8 * c) = make_uint4(__byte_perm(r[0], r[1], 0x5410), __byte_perm(r[2], r[3], 0x5410),
+                                                        __byte_perm(r[0], r[1], 0x7632), __byte_perm(r[2], r[3], 0x7632));
 }
-__device__ __forceinline__ void put_values(float* p, uint32_t w, uint32_t pair) {
+template <int TPR>
+__device__ __forceinline__ void put_values(float* row, uint32_t w, uint32_t pair, int c, int L, bool on) {
     const float lo = int4_lo(pair), step = int4_step(pair);
-    float x[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = fmaf(step, static_cast<float>((w >> (4 * e)) & 15u), lo);
-    store8(p, x);
+    for (int k = 0; k < 2; ++k) {
+        const int quad = c + k * L;
+        const uint32_t word = __shfl_sync(0xffffffffu, w, quad / 2, TPR) >> (16 * (quad & 1));
+        float x[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)           // 2^23 + c is the fp32 bits 0x4b000000 | c
+            x[e] = fmaf(step, __uint_as_float(((word >> (4 * e)) & 15u) | 0x4b000000u) - 8388608.f, lo);
+        if (on) *reinterpret_cast<float4*>(row + 4 * quad) = make_float4(x[0], x[1], x[2], x[3]);
+    }
 }
 
 template <typename TOut, int TPR>
@@ -195,7 +222,8 @@ gather_int4_kernel(const uint8_t* __restrict__ k_cache, const uint8_t* __restric
     }
     const int lane = threadIdx.x & 31;
     const int sub = lane / TPR, c = lane % TPR;
-    const bool live = 8 * c < head_dim;
+    const int words = head_dim / 8;
+    const bool live = c < words;
     const int32_t* table = block_tables + static_cast<size_t>(s) * max_blocks_per_seq;
     const uint32_t stride = gridDim.x * kWarpsPerCta;
     // Unsigned: the row after the last may pass 2^31. Block ids a row ahead.
@@ -210,12 +238,13 @@ gather_int4_kernel(const uint8_t* __restrict__ k_cache, const uint8_t* __restric
             continue;
         }
         const size_t in0 = static_cast<size_t>(id) * num_kv_heads * block_size + row % ubs;
-        const size_t out0 = (static_cast<size_t>(start) + row) * num_kv_heads * head_dim + 8 * c;
+        const size_t out0 = (static_cast<size_t>(start) + row) * num_kv_heads * head_dim;
         for (int pass = 0; pass * kRowsPerPass < num_kv_heads; pass += U) {
             uint32_t w[U][2], pair[U][2];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int h = (pass + u) * kRowsPerPass + sub;
+                w[u][0] = w[u][1] = pair[u][0] = pair[u][1] = 0u;
                 if (h < num_kv_heads && live) {
                     const size_t r = in0 + static_cast<size_t>(h) * block_size;
                     w[u][0] = __ldg(reinterpret_cast<const uint32_t*>(k_cache + r * (head_dim / 2)) + c);
@@ -227,11 +256,10 @@ gather_int4_kernel(const uint8_t* __restrict__ k_cache, const uint8_t* __restric
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int h = (pass + u) * kRowsPerPass + sub;
-                if (h < num_kv_heads && live) {
-                    const size_t to = out0 + static_cast<size_t>(h) * head_dim;
-                    put_values(k_out + to, w[u][0], pair[u][0]);
-                    put_values(v_out + to, w[u][1], pair[u][1]);
-                }
+                const bool on = h < num_kv_heads && live;
+                const size_t to = out0 + static_cast<size_t>(h) * head_dim;
+                put_values<TPR>(k_out + to, w[u][0], pair[u][0], c, words, on);
+                put_values<TPR>(v_out + to, w[u][1], pair[u][1], c, words, on);
             }
         }
     }

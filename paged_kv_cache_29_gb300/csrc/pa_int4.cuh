@@ -32,6 +32,27 @@ __device__ __forceinline__ float int4_quotient(float d, float s, float r) {
     const float q = __fmul_rn(d, r);
     return __fmaf_rn(__fmaf_rn(-q, s, d), r, q);
 }
+// Two fp32 values side by side in one register pair: one instruction each.
+__device__ __forceinline__ uint64_t f32x2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
 // Steps (and a row's max - lo) outside these bounds divide instead.
 constexpr float kInt4Small = 0x1p-80f, kInt4Large = 0x1p80f;
 
@@ -60,11 +81,16 @@ __device__ __forceinline__ void int4_codes(const float* x, uint32_t pair, uint32
     const float r = step > 0.f ? __frcp_rn(step) : 0.f;   // a row of one value: differences 0
     float q[N];
     if (step == 0.f || (step > kInt4Small && step < kInt4Large)) {
+        const uint64_t mlo = f32x2(-lo, -lo), ms = f32x2(-step, -step), r2 = f32x2(r, r);
 #pragma unroll
-        for (int e = 0; e < N; ++e) q[e] = int4_quotient(__fsub_rn(x[e], lo), step, r);
+        for (int e = 0; e < N; e += 2) {
+            const uint64_t d = add2(f32x2(x[e], x[e + 1]), mlo), q0 = mul2(d, r2);
+            const uint64_t q1 = add2(fma2(fma2(q0, ms, d), r2, q0), f32x2(12582912.f, 12582912.f));
+            asm("mov.b64 {%0, %1}, %2;" : "=f"(q[e]), "=f"(q[e + 1]) : "l"(q1));
+        }
     } else {
 #pragma unroll
-        for (int e = 0; e < N; ++e) q[e] = __fdiv_rn(__fsub_rn(x[e], lo), step);
+        for (int e = 0; e < N; ++e) q[e] = __fadd_rn(__fdiv_rn(__fsub_rn(x[e], lo), step), 12582912.f);
     }
     // Adding 1.5 * 2^23 rounds to an integer, half to even, into the low bits; the
     // integers' common upper bits are taken off the sum below, mod 2^32.
@@ -73,7 +99,7 @@ __device__ __forceinline__ void int4_codes(const float* x, uint32_t pair, uint32
     for (int i = 0; i < N / 8; ++i) {
         uint32_t w = 0u;
 #pragma unroll
-        for (int e = 7; e >= 0; --e) w = w * 16u + __float_as_uint(__fadd_rn(q[8 * i + e], 12582912.f));
+        for (int e = 7; e >= 0; --e) w = w * 16u + __float_as_uint(q[8 * i + e]);
         codes[i] = w - kBits * 0x11111111u;
     }
 }
@@ -111,21 +137,13 @@ __device__ __forceinline__ long long slot_row(long long slot, long long num_slot
     return blk * num_kv_heads * block_size + (slot - blk * block_size);
 }
 
-// Eight consecutive elements as fp32, and eight fp32 values rounded and stored.
+// Eight consecutive elements as fp32.
 __device__ __forceinline__ void load8(const __nv_bfloat16* p, float* x) {
     ElemTraits<__nv_bfloat16>::unpack(*reinterpret_cast<const uint4*>(p), x);
 }
 __device__ __forceinline__ void load8(const float* p, float* x) {
     ElemTraits<float>::unpack(reinterpret_cast<const uint4*>(p)[0], x);
     ElemTraits<float>::unpack(reinterpret_cast<const uint4*>(p)[1], x + 4);
-}
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float* x) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                                              pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
-}
-__device__ __forceinline__ void store8(float* p, const float* x) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
 }
 
 }  // namespace pa
