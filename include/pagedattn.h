@@ -482,10 +482,11 @@ pa_status pa_test_withhold_tile(const void* q, const void* k_cache, const void* 
  * for the new K row x = k_new[t][h] (and V), every difference and quotient in
  * fp32 (IEEE); s = 0 (all x equal to lo) gives codes 0. The directed roundings
  * keep every x inside [lo, lo + 15 s], so a value is off by at most s / 2
- * (plus fp32 rounding). A zero lo is +0. Rows must be finite with a finite max - lo; a row that
- * is not gives unspecified codes and params for itself alone. new_dtype
- * PA_DTYPE_F32 or PA_DTYPE_BF16; head_dim a multiple of 32, at most 256. Slots
- * as in pa_reshape_and_cache.
+ * (plus fp32 rounding). A zero lo is +0. Rows must be finite with a finite
+ * max - lo; a row that is not gives unspecified codes and params for itself
+ * alone. new_dtype PA_DTYPE_F32 or PA_DTYPE_BF16; head_dim a multiple of 32, at
+ * most 256. Slots as in pa_reshape_and_cache; two tokens with the same slot
+ * may leave one's codes beside the other's pair.
  */
 pa_status pa_reshape_and_cache_int4(const void* k_new, const void* v_new, pa_dtype new_dtype,
                                     const int64_t* slot_mapping, void* k_cache, void* v_cache,
@@ -498,8 +499,8 @@ pa_status pa_reshape_and_cache_int4(const void* k_new, const void* v_new, pa_dty
  * The cached rows of every sequence as plain values, one after another:
  *   k_out[row_starts[s] + i][h][:] = lo + s * c of row i of sequence s, KV head h
  * (same for V) for i < context_lens[s], the exact sum rounded once to
- * out_dtype (PA_DTYPE_F32 or PA_DTYPE_BF16). Attention over a prompt that is processed in
- * chunks reads its earlier chunks this way. k_out, v_out: [num_rows]
+ * out_dtype (PA_DTYPE_F32 or PA_DTYPE_BF16). Attention over a prompt that is
+ * processed in chunks reads its earlier chunks this way. k_out, v_out: [num_rows]
  * [num_kv_heads][head_dim]; row_starts: int64 [num_seqs]. Output rows that no
  * sequence covers are left as they are. A context length outside
  * [0, max_context_len], or rows outside [0, num_rows), flag
@@ -527,8 +528,9 @@ pa_status pa_gather_int4(const void* k_cache, const void* v_cache, const void* k
  * rows; 0 < n < Q is flagged PA_DEVERR_CONTEXT (those rows are left as they
  * are). Scores, softmax and sums are fp32; q is held in f16 (exactly, but for
  * elements more than 2^20 below their head's largest), a probability times its
- * row's s is rounded to f16 once. Partitions of 1024 rows merged as in
- * pa_decode: a sequence's result does not depend on the rest of the batch.
+ * row's s is rounded to f16 once. Partitions of 1024 rows (a rest of at most
+ * 128 rows joins the last one) merged as in pa_decode: a sequence's result does
+ * not depend on the rest of the batch.
  * Workspace: pa_decode_workspace_size_multi(num_seqs, num_queries, num_heads,
  * head_dim, max_context_len) bytes, used as in pa_decode. Supported: head_dim
  * 64 or 128, block_size a multiple of 16, (num_heads / num_kv_heads) *

@@ -306,3 +306,43 @@ def test_steps_of_a_prompt_and_its_answer_over_a_4_bit_cache():
             np.testing.assert_array_equal(hp[3][b, :, o], pairs)
             want, tol = ref.attention4(fresh.read(q_out)[s][None], hp, tables[s], row[s] + 1, d ** -0.5, bs)
             assert (np.abs(fresh.read(out)[s] - want[0]) <= tol[0]).all()
+
+
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("lens", [[40] * 24, [40, 5000] * 12])
+def test_calls_back_to_back_wait_for_one_another(lens, captured):
+    """Attention and a rotation of its own q in place, in turn without a host
+    wait: each call starts while the one before it still runs (the merge of
+    sequences of one partition has nothing to do), and none may run ahead."""
+    hq, hkv, d, bs, B = 8, 2, 128, 16, len(lens)
+    width = 5000 // bs + 1
+    g = torch.Generator("cuda").manual_seed(3)
+    pool = [torch.randint(0, 256, (64, hkv, bs, d // 2), dtype=torch.uint8, device="cuda", generator=g) for _ in range(2)] + \
+        [torch.rand(64, hkv, bs, 2, device="cuda", generator=g).sub(0.4).to(torch.bfloat16) for _ in range(2)]
+    table = torch.randint(0, 64, (B, width), dtype=torch.int32, device="cuda", generator=g)
+    n, rows, steps = dev(np.array(lens, np.int32)), Rows(B, hq, hkv, d, seed=70), 6
+    pos, cs = rows.position_args()
+    start, k, _ = (t.clone() for t in rows.parts(rows.dqkv))
+    q, k_out = start.clone(), torch.empty_like(k)
+    ws = torch.empty(pa.pa_decode_workspace_size_multi(B, 1, hq, d, 5000), dtype=torch.uint8, device="cuda")
+
+    def run(outs, wait):
+        for out in outs:
+            pa.pa_decode_int4(q, *pool, table, n, d ** -0.5, out, 5000, workspace=ws)
+            wait()
+            pa.pa_norm_rope(q, k, pos, cs, q, k_out, rows.dw[0], rows.dw[1])
+            wait()
+
+    want = [torch.empty_like(q) for _ in range(steps)]
+    run(want, torch.cuda.synchronize)
+    got = [torch.empty_like(q) for _ in range(steps)]
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            run(got, lambda: None)
+    for _ in range(3):
+        q.copy_(start)
+        graph.replay() if captured else run(got, lambda: None)
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
