@@ -146,7 +146,8 @@ struct NormRopeParams {
     int num_tokens, num_heads, num_kv_heads, head_dim;
     int rot_dim, max_position, num_axes, interleaved;
     int block_size;
-    int splits;                    // warps per token
+    int splits;                    // warps per token: `part` takes passes part, part + splits, ... of q's rows,
+    int k_shift, v_shift;          //   then K's, then V's: from (part + shift) % splits of each
     alignas(4) uint8_t pair_axis[128];   // rot_dim / 2 <= 128; read four at a time
 };
 cudaError_t launch_norm_rope(const NormRopeParams& p, pa_dtype dtype, cudaStream_t stream);

@@ -13,14 +13,16 @@
 // turns pairs 4 c .. 4 c + 3, so four cosines and four sines, loaded once per
 // token, serve every row that the warp takes of it; nothing but the sum of
 // squares crosses lanes. A warp works on one token: passes part, part + splits,
-// ... of its q, K and V rows, U passes' loads in flight.
+// ... of its q, K and V rows, numbered through, U passes' loads in flight.
 //
 // Bound by memory once there are a few thousand tokens: 16,384 tokens of 32 q, K and
-// V heads of 128 dims (bf16, K and V into a pool) 130.5 us, 6,236 GB/s beside a
-// plain copy's 6,797; 4,099 tokens with 8 KV heads and three axes 18.0 us, 4,782
+// V heads of 128 dims (bf16, K and V into a pool) 129.1 us, 6,304 GB/s beside a
+// plain copy's 6,797; 4,099 tokens with 8 KV heads and three axes 17.9 us, 4,807
 // GB/s: all 4,099 warps are resident at once, so that the chain of each (positions,
 // table rows, first store) and the last warps' end are not hidden behind others.
-// 128 tokens 4.3 us, that chain alone.
+// 128 tokens 3.8 us, that chain alone.
+#include <atomic>
+
 #include "pa_int4.cuh"
 #include "pa_internal.h"
 
@@ -29,11 +31,6 @@ namespace pa {
 namespace {
 
 constexpr int kThreads = 128;
-// Warps that fill the device (16 per SM): more tokens than this take one warp
-// each. Prompt of 4,099 tokens, 40 rows of q and K each, three axes: 18.0 us with
-// one warp per token, 19.6 with two, 22.3 with three; 128 tokens of 32 heads: 4.3 us
-// with a warp for each of the 16 passes, 4.5 with ten warps.
-constexpr long long kNormRopeWarps = 2432;
 
 enum Dest { kOut, kPool, kPool4 };
 
@@ -105,7 +102,13 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
     };
     const T* const q = static_cast<const T*>(p.q) + t * p.q_stride;
     const T* const k = static_cast<const T*>(p.k) + t * p.k_stride;
-    load_batch(q, p.num_heads, part);
+    int k_part = part + p.k_shift, v_part = part + p.v_shift;
+    if (k_part >= p.splits) k_part -= p.splits;
+    if (v_part >= p.splits) v_part -= p.splits;
+    if (part * kRowsPerPass < p.num_heads)
+        load_batch(q, p.num_heads, part);
+    else
+        load_batch(k, p.num_kv_heads, k_part);
 
     float cs[4] = {1.f, 1.f, 1.f, 1.f}, sn[4] = {0.f, 0.f, 0.f, 0.f};
     if (p.rot_dim > 0) {
@@ -148,9 +151,9 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
         if (append) row0 = slot_row(slot, p.num_slots, p.num_kv_heads, p.block_size);
     }
 
-    // Normed and turned rows of q or K; raw holds the first batch, and the first
-    // batch of `then` (then_rows rows) at the end.
-    auto turn_rows = [&](const T* from, int rows, const void* weight, const T* then, int then_rows, auto&& put) {
+    // Normed and turned rows of q or K, passes start, start + splits, ...; raw holds
+    // the first batch, and that of K (then_k) at q's end.
+    auto turn_rows = [&](const T* from, int rows, int start, const void* weight, bool then_k, auto&& put) {
         float w[8];
         if (weight != nullptr && live) {
             if (p.weight_bf16) {
@@ -165,7 +168,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
 #pragma unroll
             for (int e = 0; e < 8; ++e) w[e] += p.weight_offset;
         }
-        for (int pass = part; pass * kRowsPerPass < rows; pass += U * p.splits) {
+        for (int pass = start; pass * kRowsPerPass < rows; pass += U * p.splits) {
             float in[U][8];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -174,8 +177,8 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
             }
             if ((pass + U * p.splits) * kRowsPerPass < rows)
                 load_batch(from, rows, pass + U * p.splits);
-            else if (then != nullptr)
-                load_batch(then, then_rows, part);
+            else if (then_k)
+                load_batch(k, p.num_kv_heads, k_part);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int first = (pass + u * p.splits) * kRowsPerPass;
@@ -230,22 +233,22 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
     };
 
     T* const q_out = static_cast<T*>(p.q_out) + t * p.q_out_stride;
-    turn_rows(q, p.num_heads, p.q_weight, DEST == kOut || append ? k : nullptr, p.num_kv_heads,
+    turn_rows(q, p.num_heads, part, p.q_weight, DEST == kOut || append,
               [&](int h, bool on, const float* x) { store_row(q_out + static_cast<long long>(h) * D, on, x); });
     if constexpr (DEST == kOut) {
         T* const k_out = static_cast<T*>(p.k_out) + t * p.k_out_stride;
-        turn_rows(k, p.num_kv_heads, p.k_weight, nullptr, 0,
+        turn_rows(k, p.num_kv_heads, k_part, p.k_weight, false,
                   [&](int h, bool on, const float* x) { store_row(k_out + static_cast<long long>(h) * D, on, x); });
     } else {
         if (!append) return;
         const T* const v = static_cast<const T*>(p.v) + t * p.v_stride;
         if constexpr (DEST == kPool) {
-            turn_rows(k, p.num_kv_heads, p.k_weight, nullptr, 0, [&](int h, bool on, const float* x) {
+            turn_rows(k, p.num_kv_heads, k_part, p.k_weight, false, [&](int h, bool on, const float* x) {
                 store_row(static_cast<T*>(p.k_cache) + (row0 + static_cast<long long>(h) * p.block_size) * D, on, x);
             });
             // V as it is, 16 bytes a lane.
             constexpr int kVecs = sizeof(T) / 2, UV = 4;
-            for (int pass = part; pass * kRowsPerPass < p.num_kv_heads; pass += UV * p.splits) {
+            for (int pass = v_part; pass * kRowsPerPass < p.num_kv_heads; pass += UV * p.splits) {
                 uint4 vec[UV][kVecs];
 #pragma unroll
                 for (int u = 0; u < UV; ++u) {
@@ -268,14 +271,14 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
                 }
             }
         } else {
-            turn_rows(k, p.num_kv_heads, p.k_weight, nullptr, 0, [&](int h, bool on, float* x) {
+            turn_rows(k, p.num_kv_heads, k_part, p.k_weight, false, [&](int h, bool on, float* x) {
                 // The codes are those of the row as pa_norm_rope would store it.
                 float y[8];
                 Q::unpack(Q::pack(x), y);
                 Q::unpack(Q::pack(x + 4), y + 4);
                 store_row4(false, row0 + static_cast<long long>(h) * p.block_size, on, y, d0, d1);
             });
-            for (int first = part * kRowsPerPass; first < p.num_kv_heads; first += p.splits * kRowsPerPass) {
+            for (int first = v_part * kRowsPerPass; first < p.num_kv_heads; first += p.splits * kRowsPerPass) {
                 const int h = first + sub;
                 const bool on = h < p.num_kv_heads && live;
                 float x[8];
@@ -288,14 +291,36 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
     }
 }
 
-template <typename T, Dest DEST>
+template <typename T, int TPR, Dest DEST>
 cudaError_t run(NormRopeParams p, cudaStream_t stream) {
-    const int tpr = p.head_dim <= 64 ? 8 : p.head_dim <= 128 ? 16 : 32;
-    // Warps per token: enough to fill the device when there are few tokens, one
-    // when there are many (a warp's table rows and weights then serve every row).
-    const int passes = (p.num_heads * tpr + 31) / 32;
-    const long long want = (kNormRopeWarps + p.num_tokens - 1) / p.num_tokens;
-    p.splits = static_cast<int>(want < passes ? want : passes);
+    auto kernel = norm_rope_kernel<T, TPR, DEST>;
+    // The warps that the device holds at once, once per device and instance.
+    static std::atomic<int> cached_warps[kMaxDevices];
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    int resident = dev < kMaxDevices ? cached_warps[dev].load(std::memory_order_relaxed) : 0;
+    if (resident == 0) {
+        int sms = 0, per_sm = 0;
+        err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+        if (err == cudaSuccess) err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kThreads, 0);
+        if (err != cudaSuccess) return err;
+        resident = sms * per_sm * (kThreads / 32);
+        if (dev < kMaxDevices) cached_warps[dev].store(resident, std::memory_order_relaxed);
+    }
+    // Warps per token: as many as are resident at once, with equal shares of the
+    // passes. 32 q heads and 8 KV heads of 128 dims (24 passes), bf16, into a pool,
+    // 4,256 warps: 300 tokens 4.5 us with 12 warps each (10.0 with one, 6.2 with
+    // 24), 1,000 tokens 7.6 with four (12.3; six 8.9), 2,000 tokens 12.5 with two
+    // (17.2; three 15.4). More tokens take one warp each, whose table rows and
+    // weights serve every row: 4,099 tokens 20.5 us (two 22.4), 16,384 tokens 70.9 (77.9).
+    const int q_passes = (p.num_heads * TPR + 31) / 32, kv_passes = (p.num_kv_heads * TPR + 31) / 32;
+    const int passes = q_passes + (DEST == kOut ? 1 : 2) * kv_passes;
+    const int most = max(1, min(passes, resident / p.num_tokens));
+    const int share = (passes + most - 1) / most;
+    p.splits = (passes + share - 1) / share;
+    p.k_shift = (p.splits - q_passes % p.splits) % p.splits;
+    p.v_shift = (p.splits - (q_passes + kv_passes) % p.splits) % p.splits;
     const long long warps = static_cast<long long>(p.num_tokens) * p.splits;
     const long long blocks = (warps * 32 + kThreads - 1) / kThreads;
     cudaLaunchConfig_t cfg = {};
@@ -307,13 +332,15 @@ cudaError_t run(NormRopeParams p, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    auto go = [&](auto kernel) {
-        const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, p);
-        return err != cudaSuccess ? err : cudaGetLastError();
-    };
-    return tpr == 8    ? go(norm_rope_kernel<T, 8, DEST>)
-           : tpr == 16 ? go(norm_rope_kernel<T, 16, DEST>)
-                       : go(norm_rope_kernel<T, 32, DEST>);
+    err = cudaLaunchKernelEx(&cfg, kernel, p);
+    return err != cudaSuccess ? err : cudaGetLastError();
+}
+
+template <typename T, Dest DEST>
+cudaError_t pick(const NormRopeParams& p, cudaStream_t stream) {
+    return p.head_dim <= 64    ? run<T, 8, DEST>(p, stream)
+           : p.head_dim <= 128 ? run<T, 16, DEST>(p, stream)
+                               : run<T, 32, DEST>(p, stream);
 }
 
 }  // namespace
@@ -321,10 +348,10 @@ cudaError_t run(NormRopeParams p, cudaStream_t stream) {
 cudaError_t launch_norm_rope(const NormRopeParams& p, pa_dtype dtype, cudaStream_t stream) {
     const bool bf = dtype == PA_DTYPE_BF16;
     if (p.k_params != nullptr)
-        return bf ? run<__nv_bfloat16, kPool4>(p, stream) : run<float, kPool4>(p, stream);
+        return bf ? pick<__nv_bfloat16, kPool4>(p, stream) : pick<float, kPool4>(p, stream);
     if (p.k_cache != nullptr)
-        return bf ? run<__nv_bfloat16, kPool>(p, stream) : run<float, kPool>(p, stream);
-    return bf ? run<__nv_bfloat16, kOut>(p, stream) : run<float, kOut>(p, stream);
+        return bf ? pick<__nv_bfloat16, kPool>(p, stream) : pick<float, kPool>(p, stream);
+    return bf ? pick<__nv_bfloat16, kOut>(p, stream) : pick<float, kOut>(p, stream);
 }
 
 }  // namespace pa
