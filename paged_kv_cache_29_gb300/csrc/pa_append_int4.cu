@@ -7,11 +7,11 @@
 //
 // Measured at 65,536 tokens, 8 KV heads of 128 dims, blocks of 16 in no order:
 //            bf16 rows             fp32 rows
-//   append   69.1 us, 4,914 GB/s   94.2 us, 6,456 GB/s
-//   gather   61.8 us, 5,496 GB/s   94.3 us, 6,452 GB/s
-// beside a plain copy's 6,797 GB/s. fp32 rows are bound by memory; bf16 rows, half
-// as long, by the arithmetic per element: the quotients' five fp32 operations,
-// unpacking and packing.
+//   append   62.1 us, 5,467 GB/s   89.3 us, 6,811 GB/s
+//   gather   54.6 us, 6,226 GB/s   93.7 us, 6,491 GB/s
+// beside a plain copy's 6,797 GB/s: memory bounds all but the append of bf16 rows, where
+// it is the arithmetic per element (ALU pipe 60 % busy, issue 64 %): unpacking, the
+// minimum and maximum, five fp32 operations for the quotient, packing.
 #include "pa_int4.cuh"
 #include "pa_internal.h"
 
@@ -19,16 +19,16 @@ namespace pa {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarpsPerCta = kThreads / 32;
 // Warps that fill the device (16 per SM); with fewer tokens than that, several
 // warps share a token's heads (append and gather of 512 and 1,024 rows: 5.4 us,
 // 5.7 with 8 per SM).
 constexpr long long kFillWarps = 2432;
-// CTAs of the gather (32 per SM). Append and gather of 128 sequences of 16 to 8,192
-// rows: 434 us with 4,864 CTAs, 445 with 2,432, 435 with 9,728 (but 149 us instead
-// of 140 for 32 equal sequences of fp32 rows).
-constexpr long long kGatherCtas = 4864;
+// CTAs of the gather (96 per SM, ten times what is resident), so that sequences
+// of 16 to 8,192 rows spread: append and gather of 128 of them 366 us, 370 with 9,728
+// CTAs, 385 with 4,864. 32 equal sequences: 54.6 us, 54.3 and 55.9.
+constexpr long long kGatherCtas = 14592;
 
 // Sixteen elements as they are loaded, their fp32 values, and the row's pair.
 template <typename T, int TPR>
@@ -98,11 +98,13 @@ struct Sixteen<__nv_bfloat16, TPR> {
 };
 
 // 16 dims a lane: the pair and its reciprocal, which every lane of a row works
-// out, cost four rows of a pass once. Two passes' bf16 loads in flight, five CTAs
-// on an SM: 69.1 us at the size above, with four CTAs 73.4, with four passes in
-// flight 70.9, with one operation per fp32 value instead of pairs 79.1.
+// out, cost four rows of a pass once. A pass takes K and V of the same heads, whose
+// offsets are the same: 62.1 us at the size above (five CTAs of twice the threads 63.7;
+// with K's and V's passes apart 69.1, and 79.1 with one fp32 value per instruction instead
+// of two). Ten CTAs on an SM (fp32 nine): with eight 66.1. Codes of four dims joined by
+// an exact fp32 FMA instead of shifted sums: 3 us more.
 template <typename TIn, int TPR>
-__global__ void __launch_bounds__(kThreads, 5)
+__global__ void __launch_bounds__(kThreads, sizeof(TIn) == 2 ? 10 : 9)
 append_int4_kernel(const TIn* __restrict__ k_new, const TIn* __restrict__ v_new,
                    const int64_t* __restrict__ slot_mapping, uint8_t* __restrict__ k_cache,
                    uint8_t* __restrict__ v_cache, uint32_t* __restrict__ k_params,
@@ -110,7 +112,6 @@ append_int4_kernel(const TIn* __restrict__ k_new, const TIn* __restrict__ v_new,
                    int num_kv_heads, int block_size, long long num_slots, int32_t* error_word) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     constexpr int kRowsPerPass = 32 / TPR;
-    constexpr int U = sizeof(TIn) == 2 ? 2 : 1;          // passes in flight
     const int lane = threadIdx.x & 31;
     const int sub = lane / TPR, c = lane % TPR;
     const bool live = 16 * c < head_dim;
@@ -126,37 +127,31 @@ append_int4_kernel(const TIn* __restrict__ k_new, const TIn* __restrict__ v_new,
         return;
     }
     const long long row0 = slot_row(slot, num_slots, num_kv_heads, block_size);
-    // Passes 0 .. n - 1 are the K heads', n .. 2 n - 1 the V heads'.
-    const int n = (num_kv_heads + kRowsPerPass - 1) / kRowsPerPass;
     const size_t from = static_cast<size_t>(t) * num_kv_heads * head_dim + 16 * c;
     const size_t codes0 = static_cast<size_t>(row0) * (head_dim / 2) + 8 * c;
     const size_t code_stride = static_cast<size_t>(block_size) * (head_dim / 2);   // between heads
-    for (int pass = part; pass < 2 * n; pass += U * splits) {
-        Sixteen<TIn, TPR> in[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int at = pass + u * splits;
-            const bool v = at >= n;
-            const int h = (v ? at - n : at) * kRowsPerPass + sub;
-            in[u].clear();
-            if (at < 2 * n && h < num_kv_heads && live) in[u].load((v ? v_new : k_new) + from + h * head_dim);
+    // A pass takes K and V of kRowsPerPass heads.
+    for (int h0 = part * kRowsPerPass; h0 < num_kv_heads; h0 += splits * kRowsPerPass) {
+        const size_t h = h0 + sub;
+        const bool on = h < num_kv_heads && live;
+        Sixteen<TIn, TPR> in[2];
+        in[0].clear();
+        in[1].clear();
+        if (on) {
+            in[0].load(k_new + from + h * head_dim);
+            in[1].load(v_new + from + h * head_dim);
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int at = pass + u * splits;
-            if (at >= 2 * n) break;                      // whole warps
-            const bool v = at >= n;
-            const int h = (v ? at - n : at) * kRowsPerPass + sub;
-            const bool on = h < num_kv_heads && live;
-            const uint32_t pair = in[u].pair(on);
+        for (int v = 0; v < 2; ++v) {
+            const uint32_t pair = in[v].pair(on);
             if (on) {
                 float x[16];
-                in[u].values(x);
+                in[v].values(x);
                 uint32_t codes[2];
                 int4_codes<16>(x, pair, codes);
                 *reinterpret_cast<uint2*>((v ? v_cache : k_cache) + codes0 + h * code_stride) =
                     make_uint2(codes[0], codes[1]);
-                if (c == 0) (v ? v_params : k_params)[row0 + static_cast<long long>(h) * block_size] = pair;
+                if (c == 0) (v ? v_params : k_params)[row0 + h * block_size] = pair;
             }
         }
     }
@@ -168,8 +163,8 @@ append_int4_kernel(const TIn* __restrict__ k_new, const TIn* __restrict__ v_new,
 // sum once (c, s and lo are bf16 values; 128 + c is the bf16 bits 0x4300 | c).
 // fp32: eight dims are 32 bytes, and two 16-byte stores of them would each touch
 // every other half sector, so lane c stores quads c and c + L of the row instead,
-// taken from the lanes that hold their words (65,536 rows of 8 heads of 128:
-// 94.3 us against 139.6).
+// taken from the lanes that hold their words (the 65,536 rows above: 94.3 us against
+// 139.6).
 template <int TPR>
 __device__ __forceinline__ void put_values(__nv_bfloat16* row, uint32_t w, uint32_t pair, int c, int, bool on) {
     if (!on) return;
@@ -201,7 +196,7 @@ __device__ __forceinline__ void put_values(float* row, uint32_t w, uint32_t pair
 }
 
 template <typename TOut, int TPR>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, 9)
 gather_int4_kernel(const uint8_t* __restrict__ k_cache, const uint8_t* __restrict__ v_cache,
                    const uint32_t* __restrict__ k_params, const uint32_t* __restrict__ v_params,
                    const int32_t* __restrict__ block_tables,
@@ -274,7 +269,7 @@ cudaError_t launch_append_int4(const void* k_new, const void* v_new, pa_dtype ne
                                cudaStream_t stream) {
     if (num_tokens == 0) return cudaSuccess;
     const int tpr = head_dim <= 64 ? 4 : head_dim <= 128 ? 8 : 16;
-    const long long passes = 2LL * ((static_cast<long long>(num_kv_heads) * tpr + 31) / 32);
+    const long long passes = (static_cast<long long>(num_kv_heads) * tpr + 31) / 32;
     const long long want = (kFillWarps + num_tokens - 1) / num_tokens;
     const int splits = static_cast<int>(want < passes ? want : passes);
     const long long blocks =
