@@ -16,7 +16,7 @@
 // ... of its q, K and V rows, numbered through, U passes' loads in flight.
 //
 // Bound by memory once there are a few thousand tokens: 16,384 tokens of 32 q, K and
-// V heads of 128 dims (bf16, K and V into a pool) 129.1 us, 6,304 GB/s beside a
+// V heads of 128 dims (bf16, K and V into a pool) 128.3 us, 6,345 GB/s beside a
 // plain copy's 6,797; 4,099 tokens with 8 KV heads and three axes 17.9 us, 4,807
 // GB/s: all 4,099 warps are resident at once, so that the chain of each (positions,
 // table rows, first store) and the last warps' end are not hidden behind others.
