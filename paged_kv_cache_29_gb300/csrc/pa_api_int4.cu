@@ -217,6 +217,7 @@ pa_status pa_decode_int4(const void* q, const void* k_cache, const void* v_cache
     base.partition_size = base.partition_long = P;
     base.partition_long_from = pa::kNoLongPartitions;
     base.partition_tail = pa::kPartitionTail4;
+    base.combine_chunk = pa::kCombineChunk4;
     base.max_parts = static_cast<int>(parts);
     // Batches above kPlanMaxSeqs sequences run as consecutive launches over
     // slices of the batch; they reuse the workspace in stream order.

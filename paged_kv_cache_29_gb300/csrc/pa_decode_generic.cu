@@ -151,7 +151,7 @@ decode_generic_kernel(const DecodeParams p, int group) {
     }
 }
 
-constexpr int kCombineChunk = 32;          // partitions per warp per pass (one per lane)
+constexpr int kCombineChunk = 32;          // partitions per warp per pass (one per lane), unless p.combine_chunk
 constexpr int kCombineMaxWarps = 16;
 constexpr int kCombineMaxElems = kMaxHeadDim / 32;   // output elements per lane
 constexpr int kCombineBatch = 8;           // partitions whose o rows are loaded before use
@@ -160,10 +160,13 @@ constexpr int kCombineBatch = 8;           // partitions whose o rows are loaded
 constexpr int kCombineHeadsPerCta = 4;
 
 // Warps used for a sequence of np partitions: warp w takes chunks w, w + nw,
-// ... of 32 consecutive partitions. Depends on np only, so a sequence's
-// summation order does not depend on the rest of the batch.
-__host__ __device__ __forceinline__ int combine_warps(int np) {
-    const int w = (np + kCombineChunk - 1) / kCombineChunk;
+// ... of `chunk` consecutive partitions (at most 32). Depends on np only, so a
+// sequence's summation order does not depend on the rest of the batch.
+__host__ __device__ __forceinline__ int combine_chunk(const DecodeParams& p) {
+    return p.combine_chunk > 0 ? p.combine_chunk : kCombineChunk;
+}
+__host__ __device__ __forceinline__ int combine_warps(int np, int chunk) {
+    const int w = (np + chunk - 1) / chunk;
     return w < kCombineMaxWarps ? w : kCombineMaxWarps;
 }
 
@@ -199,7 +202,8 @@ __global__ void __launch_bounds__(kCombineMaxWarps * 32) combine_kernel(const De
     asm volatile("griddepcontrol.wait;" ::: "memory");    // the partials are the decode kernel's output
     if (!merge) return;
     const int np = (span - p.partition_tail + P - 1) / P;
-    const int nw = HPB > 1 ? 1 : combine_warps(np);
+    const int chunk = combine_chunk(p);
+    const int nw = HPB > 1 ? 1 : combine_warps(np, chunk);
     const int D = p.head_dim;
     const size_t row = static_cast<size_t>(sq) * p.num_heads + qh;
     const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + row * p.max_parts;
@@ -210,8 +214,8 @@ __global__ void __launch_bounds__(kCombineMaxWarps * 32) combine_kernel(const De
         float acc[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] = 0.f;
-        for (int c0 = warp * kCombineChunk; c0 < np; c0 += nw * kCombineChunk) {
-            const int cnt = min(kCombineChunk, np - c0);
+        for (int c0 = warp * chunk; c0 < np; c0 += nw * chunk) {
+            const int cnt = min(chunk, np - c0);
             const float2 v = lane < cnt ? ml[c0 + lane] : make_float2(-INFINITY, 0.f);
             // The first o rows are loaded together with the maxima.
             float ov[kCombineBatch][E];
@@ -322,7 +326,7 @@ cudaError_t launch_decode_generic(const DecodeParams& p, pa_dtype dtype, cudaStr
 
 cudaError_t launch_combine(const DecodeParams& p, pa_dtype dtype, cudaStream_t stream) {
     if (p.max_parts <= 1 || p.num_seqs == 0) return cudaSuccess;
-    const int warps = combine_warps(p.max_parts);   // enough for the longest sequence
+    const int warps = combine_warps(p.max_parts, combine_chunk(p));   // enough for the longest sequence
     // One warp per head merges every partition: several heads per CTA.
     const bool packed = warps == 1 && kCombineHeadsPerCta > 1 &&
                         p.num_heads % kCombineHeadsPerCta == 0;

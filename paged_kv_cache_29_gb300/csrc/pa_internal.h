@@ -50,6 +50,7 @@ struct DecodeParams {
     int partition_long;            // rows per partition of sequences past partition_long_from
     int partition_long_from;       // span (rows from seq_row_base) above which partition_long applies
     int partition_tail;            // a last partition of at most this many rows joins the one before (INT4; else 0)
+    int combine_chunk;             // partitions that a warp of the merge takes at a time (0: 32)
     int max_parts;                 // ceil(max_context_len / partition_size), >= 1: the partials' row stride
     // Failure test only (-1 otherwise): the tile-ring kernels' CTA 0 announces
     // its stream tile withhold_tile without copying it or completing its
@@ -205,6 +206,10 @@ constexpr int kDefaultPartition4 = 1024;
 // 209,835-row batch 48.9 and 50.6; a tail of 512 rows takes 0.5 us more off that
 // batch but makes the longest item, which a small batch waits for, half as long again.
 constexpr int kPartitionTail4 = 128;
+// Partitions that a warp of the merge takes at a time (it loads 8 at once): one
+// sequence of 100,000 rows beside seven short ones takes 29.6 us, with 32 partitions 30.7,
+// with 8 30.5. Sequences of up to 16 partitions are still one warp's.
+constexpr int kCombineChunk4 = 16;
 constexpr int kNoLongPartitions = 0x7fffffff;   // partition_long_from: one size for all
 // Kernel of pa_decode_fp8 and pa_append_decode_fp8 when none is requested.
 constexpr pa_kernel kFp8DefaultKernel = PA_KERNEL_MMA;

@@ -252,6 +252,12 @@ def test_long_sequence_beside_short_ones():
     b.check(b.decode())
 
 
+def test_merges_of_many_partitions():
+    """One warp's 16 partitions, one more, and more than 16 warps take at once."""
+    b = Batch([128 + 16 * 1024, 129 + 16 * 1024, 300_000], hq=1, hkv=1, d=64, seed=15).upload()
+    b.check(b.decode())
+
+
 def test_more_sequences_than_one_launch_holds():
     rng = np.random.default_rng(15)
     b = Batch([int(n) for n in rng.integers(0, 40, 4400)], hq=2, hkv=1, d=64, seed=16).upload()
