@@ -42,18 +42,18 @@
 // warp to keep four consumers fed. At an item's end the warps' states are
 // merged through shared memory.
 //
-// Measured: 128 sequences, 32 heads over 8 KV heads of 128 dims, 209,835 rows: 48.8
-// us, 4,841 GB/s of 6,797 (a plain copy); 32 sequences of 32 KV heads 38.2 us, 4,321
+// Measured: 128 sequences, 32 heads over 8 KV heads of 128 dims, 209,835 rows: 48.0
+// us, 4,921 GB/s of 6,797 (a plain copy); 32 sequences of 32 KV heads 37.7 us, 4,388
 // GB/s. The kernel is bound on two sides at once: without its loads the first takes
-// 46.6 us (ALU 50 % busy with ANDs and permutes, tensor pipe 28 %, three warps per
-// scheduler issue 54 % of the cycles), without its arithmetic 45.7, of which about 6
-// pass before the first tile is there and 3 are the merge launch. No change there
-// (48.8): four interleaved chains of q . c MMAs, both tiles' weights before either's
+// 46.6 us (three warps per scheduler issue 54 % of the cycles, the ALU pipe's ANDs and
+// permutes 50 %, tensor pipe 28 %), without its arithmetic 45.7, of which about 6
+// pass before the first tile is there and 3 are the merge launch. No change there:
+// four interleaved chains of q . c MMAs, both tiles' weights before either's
 // products, two fp32 values per instruction. Slower: the next unit's q . c ahead of
-// this unit's softmax (51.2: the warps already fill each other's gaps), four CTAs
-// on an SM with 128 registers (51.9; 36.5 instead of 38.2 for the second batch,
-// whose reason was not found, so one rule for all), exponentials before the vote
-// (50.7).
+// this unit's softmax or among its products (49.8 to 51.2), four CTAs on an SM with 128
+// registers and two stages (51.6; 35.8 instead of 37.7 for the second batch, whose items
+// spread better over 608 CTAs, but less in flight everywhere else, so one rule for all),
+// exponentials before the vote (50.7).
 #include <atomic>
 
 #include "pa_int4.cuh"
@@ -239,7 +239,7 @@ __device__ int plan4(const DecodeParams& p, int c, int C, Plan4* sm) {
     return (full_all + part_all) * Hkv;
 }
 
-template <int D, int NC, int STAGES>
+template <int D, int STAGES>
 struct Smem4 {
     static constexpr int kCodes = kTileRows * D / 2;                 // K or V codes of a tile
     static constexpr int kTile = 2 * kCodes + 2 * kTileRows * 4;
@@ -248,24 +248,26 @@ struct Smem4 {
     // A warp's outputs of one column; four floats of padding spread the float2
     // stores of a half-warp (4 dim pairs x 4 column pairs) over all banks.
     static constexpr int kCol = D + 4;
-    static constexpr int kState = NC * (kCol + 2);                   // o, then m, l
+    static constexpr int kState = 8 * (kCol + 2);                    // o, then m, l
     static constexpr int kMerge = kWarps * kState * 4;
-    // Two merge areas in turn, where they leave room for three CTAs on an SM:
-    // one barrier per item instead of two.
-    static constexpr int kMerges = NC <= 4 ? 2 : 1;
     static constexpr int kQFrag = (D / 32) * 32 * 16;                // q fragments [D / 32][lane]
-    static constexpr int kQ = kRing + kMerges * kMerge;              // two items' in turn
+    static constexpr int kQ = kRing + kMerge;                        // two items' in turn
     static constexpr int kPlan = kQ + 2 * kQFrag;
     static constexpr int kBytes = kPlan + static_cast<int>(sizeof(Plan4));
     static_assert((kRing + kMerge) % 16 == 0, "16-byte fragments follow");
 };
 
-// D: head dim. NC: query columns the state holds (an item uses ncols <= NC).
-template <int D, int NC, int STAGES, int MIN_CTAS>
+// D: head dim. kShared: at most four query columns, and the two tiles of a unit
+// share the eight columns of the products: columns 0-3 are the first tile's, 4-7 the
+// second's, each with a state of its own, joined where the warps' are. A lane then has
+// four scores of a unit to work on instead of eight (128 sequences of 209,835 rows,
+// four columns: 48.8 -> 48.0 us; 32 sequences, one column: 38.3 -> 37.7).
+template <int D, bool kShared, int STAGES, int MIN_CTAS>
 __global__ void __launch_bounds__(kThreads4, MIN_CTAS) decode_int4_kernel(const DecodeParams p) {
-    using Smem = Smem4<D, NC, STAGES>;
+    using Smem = Smem4<D, STAGES>;
     constexpr int kKWords = D / 32;       // words of K codes per lane and row
     constexpr int kMt = D / 16;           // m-tiles of the output
+    constexpr int kSets = kShared ? 1 : 2;   // of 16 rows x 8 columns of scores in a unit
 
     extern __shared__ __align__(128) uint8_t smem_raw[];
     float* merge = reinterpret_cast<float*>(smem_raw + Smem::kRing);
@@ -274,6 +276,8 @@ __global__ void __launch_bounds__(kThreads4, MIN_CTAS) decode_int4_kernel(const 
     int* const col_row = plan->col_row;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int gid = lane >> 2, t4 = lane & 3;
+    const int own = t4 >> 1;              // kShared: the tile whose scores this lane has
+    const int c0 = kShared ? 2 * (t4 & 1) : 2 * t4, c1 = c0 + 1;   // its query columns
     const uint32_t ring = smem_addr(smem_raw) + warp * STAGES * Smem::kStage;
     const uint32_t ring_end = ring + STAGES * Smem::kStage;
 
@@ -433,18 +437,18 @@ __global__ void __launch_bounds__(kThreads4, MIN_CTAS) decode_int4_kernel(const 
         if (q_part == 0) plan->col_f[buf][q_col] = fmaxf(fabsf(p.scale_log2) * (inv * 16777216.f), 1e-30f);
     };
     uint32_t qb[kKWords][4];
-    float qf[2], qsum[2];                  // of columns 2 t4 and 2 t4 + 1
+    float qf[2], qsum[2];                  // of columns c0 and c1
     auto take_q = [&](int buf) {
         const uint4* q_frag = q_frags + buf * (Smem::kQFrag / 16);
         float ones[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < kKWords; ++i) {
-            const uint4 v = q_frag[i * 32 + lane];
+            const uint4 v = q_frag[i * 32 + (kShared ? lane & 15 : lane)];
             qb[i][0] = v.x; qb[i][1] = v.y; qb[i][2] = v.z; qb[i][3] = v.w;
             mma_16816_f16(ones, 0x00010001u, 0x00010001u, 0x00100010u, 0x00100010u, v.x, v.y);
             mma_16816_f16(ones, 0x00010001u, 0x00010001u, 0x00100010u, 0x00100010u, v.z, v.w);
         }
-        const float2 F = *reinterpret_cast<const float2*>(&plan->col_f[buf][2 * t4]);
+        const float2 F = *reinterpret_cast<const float2*>(&plan->col_f[buf][c0]);
         qf[0] = F.x; qf[1] = F.y;
         qsum[0] = ones[0]; qsum[1] = ones[1];
     };
@@ -465,7 +469,7 @@ __global__ void __launch_bounds__(kThreads4, MIN_CTAS) decode_int4_kernel(const 
     __syncthreads();
 
     uint32_t at = ring;                    // the stage of the next unit
-    const int j0 = (2 * t4) / grp, j1 = (2 * t4 + 1) / grp;   // the columns' query tokens
+    const int j0 = c0 / grp, j1 = c1 / grp;   // the columns' query tokens
     // This lane's offsets into a tile: K rows 2 gid and 2 gid + 1, the V row that
     // it points ldmatrix at (lanes 16-31: the next 16 bytes of the same rows).
     const int k_unit = D == 128 ? t4 ^ ((gid & 1) << 2) : (((gid & 1) << 2) | (t4 >> 1)) ^ (gid & 2);
@@ -500,12 +504,12 @@ __global__ void __launch_bounds__(kThreads4, MIN_CTAS) decode_int4_kernel(const 
             __syncwarp();
             const int row0 = lo + kUnitRows * (warp + kWarps * i);
 
-            // ---- S' of rows 2 gid, 2 gid + 1 of both tiles, columns 2 t4, 2 t4 + 1
-            float S[2][4];
-            uint2 vp[2];
+            // ---- S' of rows 2 gid, 2 gid + 1 of a tile (both tiles), columns c0, c1
+            float S[kSets][4];
+            uint2 vp[kSets];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const uint32_t kb = at + h * Smem::kTile + k_at, pb = at + h * Smem::kTile + 2 * Smem::kCodes;
+                const uint32_t kb = at + h * Smem::kTile + k_at;
                 uint32_t kw[2][kKWords];
                 if constexpr (D == 128) {
                     const uint4 a = lds128(kb + k_unit * 16), b = lds128(kb + (k_unit ^ 4) * 16);
@@ -525,12 +529,20 @@ __global__ void __launch_bounds__(kThreads4, MIN_CTAS) decode_int4_kernel(const 
                     mma_16816_f16(bcc, a8 & 0x000f000fu, b8 & 0x000f000fu, a8 & 0x00f000f0u,
                                   b8 & 0x00f000f0u, qb[u][2], qb[u][3]);
                 }
+                const int set = kShared ? 0 : h;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (!kShared || h == 0 || own == 1) S[set][e] = acc[e] + bcc[e];
+            }
+#pragma unroll
+            for (int h = 0; h < kSets; ++h) {
+                const uint32_t pb = at + (kShared ? own : h) * Smem::kTile + 2 * Smem::kCodes;
                 const uint2 kp = lds64(pb + 8 * gid);
                 vp[h] = lds64(pb + 64 + 8 * gid);
-                S[h][0] = fmaf(int4_step(kp.x), acc[0] + bcc[0], int4_lo(kp.x) * qsum[0]);
-                S[h][1] = fmaf(int4_step(kp.x), acc[1] + bcc[1], int4_lo(kp.x) * qsum[1]);
-                S[h][2] = fmaf(int4_step(kp.y), acc[2] + bcc[2], int4_lo(kp.y) * qsum[0]);
-                S[h][3] = fmaf(int4_step(kp.y), acc[3] + bcc[3], int4_lo(kp.y) * qsum[1]);
+                S[h][0] = fmaf(int4_step(kp.x), S[h][0], int4_lo(kp.x) * qsum[0]);
+                S[h][1] = fmaf(int4_step(kp.x), S[h][1], int4_lo(kp.x) * qsum[1]);
+                S[h][2] = fmaf(int4_step(kp.y), S[h][2], int4_lo(kp.y) * qsum[0]);
+                S[h][3] = fmaf(int4_step(kp.y), S[h][3], int4_lo(kp.y) * qsum[1]);
             }
             if (row0 + kUnitRows - 1 > n - Q || (window > 0 && row0 <= n - 1 - window)) {
                 // Some token does not see some row of the unit (whose second tile
@@ -538,8 +550,8 @@ __global__ void __launch_bounds__(kThreads4, MIN_CTAS) decode_int4_kernel(const 
                 const int top0 = n - Q + j0, top1 = n - Q + j1;
                 const int w = window > 0 ? window : INT_MAX;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int r = row0 + kTileRows * h + 2 * gid;
+                for (int h = 0; h < kSets; ++h) {
+                    const int r = row0 + kTileRows * (kShared ? own : h) + 2 * gid;
                     if (!(r <= top0 && top0 - r < w)) S[h][0] = -INFINITY;
                     if (!(r <= top1 && top1 - r < w)) S[h][1] = -INFINITY;
                     if (!(r + 1 <= top0 && top0 - r - 1 < w)) S[h][2] = -INFINITY;
@@ -549,10 +561,13 @@ __global__ void __launch_bounds__(kThreads4, MIN_CTAS) decode_int4_kernel(const 
                     if (r + 1 >= n || n - Q - r - 1 >= w) vp[h].y = 0u;
                 }
             }
-            const float smax = fmaxf(fmaxf(int4_step(vp[0].x), int4_step(vp[0].y)),
-                                     fmaxf(int4_step(vp[1].x), int4_step(vp[1].y)));
-            float mx0 = fmaxf(fmaxf(S[0][0], S[0][2]), fmaxf(S[1][0], S[1][2]));
-            float mx1 = fmaxf(fmaxf(S[0][1], S[0][3]), fmaxf(S[1][1], S[1][3]));
+            float smax = fmaxf(int4_step(vp[0].x), int4_step(vp[0].y));
+            float mx0 = fmaxf(S[0][0], S[0][2]), mx1 = fmaxf(S[0][1], S[0][3]);
+            if constexpr (!kShared) {
+                smax = fmaxf(smax, fmaxf(int4_step(vp[1].x), int4_step(vp[1].y)));
+                mx0 = fmaxf(mx0, fmaxf(S[1][0], S[1][2]));
+                mx1 = fmaxf(mx1, fmaxf(S[1][1], S[1][3]));
+            }
             if (__any_sync(0xffffffffu, fmaxf(fmaf(mx0, qf[0], r0), fmaf(mx1, qf[1], r1)) > kRaise || smax >= vtop)) {
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1) {
@@ -584,8 +599,8 @@ __global__ void __launch_bounds__(kThreads4, MIN_CTAS) decode_int4_kernel(const 
                 }
             }
             // ---- o += codes(V)^T . P, tile by tile
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
+            uint32_t b0[kSets], b1[kSets];
+            auto weights = [&](int h) {
                 const float E0 = fast_exp2(fmaf(S[h][0], qf[0], r0)), E1 = fast_exp2(fmaf(S[h][1], qf[1], r1));
                 const float E2 = fast_exp2(fmaf(S[h][2], qf[0], r0)), E3 = fast_exp2(fmaf(S[h][3], qf[1], r1));
                 const float u0 = int4_step(vp[h].x) * vinv, u1 = int4_step(vp[h].y) * vinv;
@@ -596,8 +611,15 @@ __global__ void __launch_bounds__(kThreads4, MIN_CTAS) decode_int4_kernel(const 
                 z1 = fmaf(E3, y1, fmaf(E1, y0, z1));
                 // B operand: lane (gid, t4) takes column gid, the rows of lane groups
                 // 2 t4 and 2 t4 + 1: rows 4 t4, 4 t4 + 2 (b0) and 4 t4 + 1, 4 t4 + 3 (b1)
-                const uint32_t b0 = transpose8x8(pack_f16x2(E0 * u0, E1 * u0));
-                const uint32_t b1 = transpose8x8(pack_f16x2(E2 * u1, E3 * u1));
+                b0[h] = transpose8x8(pack_f16x2(E0 * u0, E1 * u0));
+                b1[h] = transpose8x8(pack_f16x2(E2 * u1, E3 * u1));
+            };
+            if constexpr (kShared) weights(0);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if constexpr (!kShared) weights(h);
+                const bool mine = !kShared || (gid >> 2) == h;   // the other tile's columns weigh 0
+                const uint32_t p0 = mine ? b0[h % kSets] : 0u, p1 = mine ? b1[h % kSets] : 0u;
                 const uint32_t vb = at + h * Smem::kTile + Smem::kCodes + v_row;
 #pragma unroll
                 for (int u = 0; u < D / 64; ++u) {
@@ -607,7 +629,7 @@ __global__ void __launch_bounds__(kThreads4, MIN_CTAS) decode_int4_kernel(const 
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         const uint32_t x = w[q] & 0x00ff00ffu, y = prmt(w[q], 0u, 0x4341u);
-                        mma_16816_f16(o[4 * u + q], x & 0x000f000fu, x, y & 0x000f000fu, y, b0, b1);
+                        mma_16816_f16(o[4 * u + q], x & 0x000f000fu, x, y & 0x000f000fu, y, p0, p1);
                     }
                 }
             }
@@ -624,52 +646,48 @@ __global__ void __launch_bounds__(kThreads4, MIN_CTAS) decode_int4_kernel(const 
             z0 += __shfl_xor_sync(0xffffffffu, z0, off);
             z1 += __shfl_xor_sync(0xffffffffu, z1, off);
         }
-        float* const area = merge + (j & (Smem::kMerges - 1)) * (Smem::kMerge / 4);
-        float* st = area + warp * Smem::kState;
-        float* ml = st + NC * Smem::kCol;
-        const int c0 = 2 * t4, c1 = 2 * t4 + 1;
-        if (c0 < NC) {                     // NC is even: c1 < NC too
-            if (gid == 0) {
-                ml[c0] = m0 == -INFINITY ? -INFINITY : -r0;
-                ml[c1] = m1 == -INFINITY ? -INFINITY : -r1;
-                ml[NC + c0] = l0;
-                ml[NC + c1] = l1;
-            }
-            // even dims: o 2^e 2^24; odd ones: (o - even's) 2^e 2^20
-            const float ve2 = __uint_as_float(static_cast<uint32_t>(ve) << 23);
+        float* st = merge + warp * Smem::kState;
+        float* ml = st + 8 * Smem::kCol;
+        const int s0 = 2 * t4, s1 = s0 + 1;   // of the state's columns
+        if (gid == 0) {
+            ml[s0] = m0 == -INFINITY ? -INFINITY : -r0;
+            ml[s1] = m1 == -INFINITY ? -INFINITY : -r1;
+            ml[8 + s0] = l0;
+            ml[8 + s1] = l1;
+        }
+        // even dims: o 2^e 2^24; odd ones: (o - even's) 2^e 2^20
+        const float ve2 = __uint_as_float(static_cast<uint32_t>(ve) << 23);
 #pragma unroll
-            for (int mt = 0; mt < kMt; ++mt) {
-                const int d = 16 * mt + 2 * gid;   // dims d and d + 1
-                *reinterpret_cast<float2*>(st + c0 * Smem::kCol + d) =
-                    make_float2(fmaf(o[mt][0] * 16777216.f, ve2, z0),
-                                fmaf((o[mt][2] - o[mt][0]) * 1048576.f, ve2, z0));
-                *reinterpret_cast<float2*>(st + c1 * Smem::kCol + d) =
-                    make_float2(fmaf(o[mt][1] * 16777216.f, ve2, z1),
-                                fmaf((o[mt][3] - o[mt][1]) * 1048576.f, ve2, z1));
-            }
+        for (int mt = 0; mt < kMt; ++mt) {
+            const int d = 16 * mt + 2 * gid;   // dims d and d + 1
+            *reinterpret_cast<float2*>(st + s0 * Smem::kCol + d) =
+                make_float2(fmaf(o[mt][0] * 16777216.f, ve2, z0),
+                            fmaf((o[mt][2] - o[mt][0]) * 1048576.f, ve2, z0));
+            *reinterpret_cast<float2*>(st + s1 * Smem::kCol + d) =
+                make_float2(fmaf(o[mt][1] * 16777216.f, ve2, z1),
+                            fmaf((o[mt][3] - o[mt][1]) * 1048576.f, ve2, z1));
         }
         deal_q((j + 1) & 1);
-        // The states and the next q are complete. With two areas, a warp that
-        // writes its next state here has passed the next item's barrier, which
-        // every warp reaches only after this merge.
-        __syncthreads();
+        __syncthreads();                   // the states and the next q are complete
         const int nparts = parts4(n - seq_row_base(n, p.window));
         // Four dims of a column per thread.
         for (int idx = threadIdx.x; idx < ncols * (D / 4); idx += kThreads4) {
             const int g = idx / (D / 4), d = idx % (D / 4) * 4;
-            const float* col = area + g * Smem::kCol + d;
-            const float* mlg = area + NC * Smem::kCol + g;
-            float M = -INFINITY;
+            const float* col = merge + g * Smem::kCol + d;
+            const float* mlg = merge + 8 * Smem::kCol + g;
+            constexpr int kParts = kShared ? 2 * kWarps : kWarps;   // column g, and g + 4, of each warp
+            float M = -INFINITY, L = 0.f, O[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, mlg[w * Smem::kState]);
+            for (int w = 0; w < kParts; ++w) M = fmaxf(M, mlg[w % kWarps * Smem::kState + w / kWarps * 4]);
             const float ref = M == -INFINITY ? 0.f : M;
-            float L = 0.f, O[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float cw = fast_exp2(mlg[w * Smem::kState] - ref);
-                const float2 a = *reinterpret_cast<const float2*>(col + w * Smem::kState);
-                const float2 b = *reinterpret_cast<const float2*>(col + w * Smem::kState + 2);
-                L = fmaf(cw, mlg[w * Smem::kState + NC], L);
+            for (int w = 0; w < kParts; ++w) {
+                const float* cw4 = col + w % kWarps * Smem::kState + w / kWarps * 4 * Smem::kCol;
+                const float* ml4 = mlg + w % kWarps * Smem::kState + w / kWarps * 4;
+                const float cw = fast_exp2(ml4[0] - ref);
+                const float2 a = *reinterpret_cast<const float2*>(cw4);
+                const float2 b = *reinterpret_cast<const float2*>(cw4 + 2);
+                L = fmaf(cw, ml4[8], L);
                 O[0] = fmaf(cw, a.x, O[0]);
                 O[1] = fmaf(cw, a.y, O[1]);
                 O[2] = fmaf(cw, b.x, O[2]);
@@ -685,17 +703,17 @@ __global__ void __launch_bounds__(kThreads4, MIN_CTAS) decode_int4_kernel(const 
                 if (d == 0) *reinterpret_cast<float2*>(p.part_ml + 2 * slot) = make_float2(M, L);
             }
         }
-        if constexpr (Smem::kMerges == 1) __syncthreads();   // the next states overwrite the area
+        __syncthreads();                   // the next states overwrite these
         it = it_next;
         it_next = it_after;
     }
     cp_async_wait_group<0>();
 }
 
-template <int D, int NC, int STAGES, int MIN_CTAS>
+template <int D, bool SHARED, int STAGES, int MIN_CTAS>
 cudaError_t run(const DecodeParams& p, int sm_count, cudaStream_t stream) {
-    auto kernel = decode_int4_kernel<D, NC, STAGES, MIN_CTAS>;
-    constexpr int smem = Smem4<D, NC, STAGES>::kBytes;
+    auto kernel = decode_int4_kernel<D, SHARED, STAGES, MIN_CTAS>;
+    constexpr int smem = Smem4<D, STAGES>::kBytes;
     // The shared-memory attribute and the resulting CTAs per SM are set up
     // once per device and instance.
     static std::atomic<int> cached_per_sm[kMaxDevices];
@@ -741,8 +759,8 @@ cudaError_t launch_decode_int4(const DecodeParams& p, cudaStream_t stream) {
     }
     const int ncols = p.num_heads / p.num_kv_heads * p.num_queries;
     if (p.head_dim == 128)
-        return ncols <= 4 ? run<128, 4, 3, 3>(p, sms, stream) : run<128, 8, 3, 3>(p, sms, stream);
-    return ncols <= 4 ? run<64, 4, 4, 3>(p, sms, stream) : run<64, 8, 4, 3>(p, sms, stream);
+        return ncols <= 4 ? run<128, true, 3, 3>(p, sms, stream) : run<128, false, 3, 3>(p, sms, stream);
+    return ncols <= 4 ? run<64, true, 4, 3>(p, sms, stream) : run<64, false, 4, 3>(p, sms, stream);
 }
 
 }  // namespace pa
