@@ -21,10 +21,11 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kWarpsPerCta = kThreads / 32;
-// Warps that fill the device (16 per SM); with fewer tokens than that, several
-// warps share a token's heads (append and gather of 512 and 1,024 rows: 5.4 us,
-// 5.7 with 8 per SM).
-constexpr long long kFillWarps = 2432;
+// Warps of the append that the device holds at once (40 per SM): with few tokens,
+// as many warps as that share a token's heads in equal parts. 32 KV heads of bf16 (8
+// passes): 1,000 tokens 5.9 us with four warps each (two 6.9, six 6.5), 1,500 tokens 7.7
+// with four (two 8.9, one 12.7), 3,000 tokens 14.0 with two (one 16.6).
+constexpr int kAppendWarps = 6080;
 // CTAs of the gather (96 per SM, ten times what is resident), so that sequences
 // of 16 to 8,192 rows spread: append and gather of 128 of them 366 us, 370 with 9,728
 // CTAs, 385 with 4,864. 32 equal sequences: 54.6 us, 54.3 and 55.9.
@@ -269,9 +270,10 @@ cudaError_t launch_append_int4(const void* k_new, const void* v_new, pa_dtype ne
                                cudaStream_t stream) {
     if (num_tokens == 0) return cudaSuccess;
     const int tpr = head_dim <= 64 ? 4 : head_dim <= 128 ? 8 : 16;
-    const long long passes = (static_cast<long long>(num_kv_heads) * tpr + 31) / 32;
-    const long long want = (kFillWarps + num_tokens - 1) / num_tokens;
-    const int splits = static_cast<int>(want < passes ? want : passes);
+    const int passes = static_cast<int>((static_cast<long long>(num_kv_heads) * tpr + 31) / 32);
+    const int most = max(1, min(passes, kAppendWarps / num_tokens));
+    const int share = (passes + most - 1) / most;
+    const int splits = (passes + share - 1) / share;
     const long long blocks =
         (static_cast<long long>(num_tokens) * splits + kWarpsPerCta - 1) / kWarpsPerCta;
     auto run = [&](auto kernel, auto tag) {
