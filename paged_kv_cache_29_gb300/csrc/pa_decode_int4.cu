@@ -42,8 +42,8 @@
 // warp to keep four consumers fed. At an item's end the warps' states are
 // merged through shared memory.
 //
-// Measured: 128 sequences, 32 heads over 8 KV heads of 128 dims, 209,835 rows: 48.0
-// us, 4,921 GB/s of 6,797 (a plain copy); 32 sequences of 32 KV heads 37.7 us, 4,388
+// Measured: 128 sequences, 32 heads over 8 KV heads of 128 dims, 209,835 rows: 48.2
+// us, 4,896 GB/s of 6,797 (a plain copy); 32 sequences of 32 KV heads 37.8 us, 4,372
 // GB/s. The kernel is bound on two sides at once: without its loads the first takes
 // 46.6 us (three warps per scheduler issue 54 % of the cycles, the ALU pipe's ANDs and
 // permutes 50 %, tensor pipe 28 %), without its arithmetic 45.7, of which about 6
