@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
                         x[i] = fmaf(a, cs[i], -(b * sn[i]));
                         x[i + 4] = fmaf(b, cs[i], a * sn[i]);
                     }
-                } else {
+                } else if (turned) {                     // other dims pass through, infinities and zeros' signs too
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float a = x[2 * i], b = x[2 * i + 1];
