@@ -453,6 +453,16 @@ __global__ void __launch_bounds__(kThreads4, MIN_CTAS) decode_int4_kernel(const 
         qsum[0] = ones[0]; qsum[1] = ones[1];
     };
 
+    // Takes a pair with an infinity or NaN out of a row's products and puts NaN
+    // into the scores that are not masked.
+    auto confine = [](uint32_t& pair, float& a, float& b) {
+        if ((pair & 0x7f80u) == 0x7f80u || (pair & 0x7f800000u) == 0x7f800000u) {
+            pair = 0u;
+            if (a != -INFINITY) a = NAN;
+            if (b != -INFINITY) b = NAN;
+        }
+    };
+
     total = plan4(p, c, C, plan);
     __syncthreads();
     int4 it = own_item(0);
@@ -559,6 +569,11 @@ __global__ void __launch_bounds__(kThreads4, MIN_CTAS) decode_int4_kernel(const 
                     // Rows that no token sees may hold any pair.
                     if (r >= n || n - Q - r >= w) vp[h].x = 0u;
                     if (r + 1 >= n || n - Q - r - 1 >= w) vp[h].y = 0u;
+                    // A pair that is not finite reaches the tokens that see its row
+                    // through their scores: as a factor it would reach the others
+                    // too (0 * infinity).
+                    confine(vp[h].x, S[h][0], S[h][1]);
+                    confine(vp[h].y, S[h][2], S[h][3]);
                 }
             }
             float smax = fmaxf(int4_step(vp[0].x), int4_step(vp[0].y));
