@@ -527,8 +527,12 @@ pa_status pa_gather_int4(const void* k_cache, const void* v_cache, const void* k
  * q, out: [num_seqs][num_queries][num_heads][head_dim]. n == 0 gives zero
  * rows; 0 < n < Q is flagged PA_DEVERR_CONTEXT (those rows are left as they
  * are). Scores, softmax and sums are fp32; q is held in f16 (exactly, but for
- * elements more than 2^20 below their head's largest), a probability times its
- * row's s is rounded to f16 once. Partitions of 1024 rows (a rest of at most
+ * elements more than 2^20 below their head's largest). A probability times its
+ * row's s is rounded to f16 once, in a range set by the rows' own weights: it
+ * loses bits where it is 2^21 or more below the largest (|s| + 2^-12 |lo|) times
+ * probability, whatever the s of rows of little weight. |s| from 2^-102 to
+ * 2^100, or 0. A row of K or V that is not finite reaches the query tokens that
+ * attend to it and no other. Partitions of 1024 rows (a rest of at most
  * 128 rows joins the last one) merged as in pa_decode: a sequence's result does
  * not depend on the rest of the batch.
  * Workspace: pa_decode_workspace_size_multi(num_seqs, num_queries, num_heads,

@@ -25,12 +25,18 @@
 // q is scaled by a power of two per head to [2^12, 2^13) before it becomes f16
 // (exact: bf16 has fewer bits), whatever its size; sum q' is the product with a
 // row of ones.
-// A probability times its row's step is the V operand in f16: the steps are
-// taken relative to 2^e, e the largest step's exponent so far, and M is a
-// reference that the scores exceed by at most 8, so operands stay below 2^9
-// whatever the sizes of scores and steps. M and e are raised, and the output
-// rescaled, only when a row goes past them: most units need no cross-lane
-// maximum and no rescale. Sums, z = sum p lo, scores and outputs are fp32.
+// A probability times its row's step is the V operand in f16. Its range, 2^-14 to
+// 2^16, is spent on the rows that count: a column's reference M is taken over S +
+// log2 a, a = |s| + 2^-12 |lo| the size of the row's part in the output, so that
+// with E = 2^(S - M) the largest E a of the rows so far is 2^7 to 2^15 and a row of
+// large step but little weight pushes nobody below. (The part of lo keeps sum E lo
+// in range where s is 0, in rows of one value; a finite row's s is some 2^-12 |lo|
+// at least otherwise. Relative to the largest step alone, a row of no weight with a
+// step of 2^20 times the others' cost these all but 5 bits.) M is raised, and the sums
+// rescaled, only when a row goes past 2^15: most units need no cross-lane maximum
+// and no rescale. E is fp32 and not below 2^-126 for rows that count as long as
+// steps stay below 2^100; under 2^-102 a step loses bits. Sums, z = sum E lo, scores
+// and outputs are fp32.
 //
 // Work: items (sequence, KV head, partition) of kItemRows rows, a sequence's last
 // one of up to kTailRows more, dealt to persistent CTAs in the order of
@@ -70,7 +76,8 @@ constexpr int kItemRows = kDefaultPartition4;
 constexpr int kUnitRows = 2 * kTileRows;
 constexpr int kTailRows = kPartitionTail4;
 constexpr int kWarpUnits = (kItemRows + kTailRows + kUnitRows * kWarps - 1) / (kUnitRows * kWarps);   // of an item, at most
-constexpr float kRaise = 8.f;                                // M lags by at most this (base 2)
+constexpr float kRaise = 15.f, kPut = 7.f;                   // E a stays below 2^kRaise; a raise puts it at 2^kPut
+constexpr float kSizeBias = 65536.f + 127.f;                 // of row_size
 static_assert(2 * kWarpUnits <= 32, "a lane per tile holds its place in the pool");
 
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
@@ -91,6 +98,12 @@ __device__ __forceinline__ uint2 lds64(uint32_t addr) {
     uint2 v;
     asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
     return v;
+}
+// The size a = |s| + 2^-12 |lo| + 2^-102 of a V row's pair (above; the append's s are
+// not negative, others' may be): the upper 16 bits of a as the low bits of 2^23.
+__device__ __forceinline__ float row_size(uint32_t pair) {
+    const float a = fmaf(fabsf(int4_lo(pair)), 0x1p-12f, 0x1p-102f) + fabsf(int4_step(pair));
+    return __uint_as_float(__byte_perm(__float_as_uint(a), 0x4b000000u, 0x7432));
 }
 // An 8 x 8 matrix of 16-bit elements, two per lane, transposed.
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
@@ -501,12 +514,10 @@ __global__ void __launch_bounds__(kThreads4, MIN_CTAS) decode_int4_kernel(const 
         for (int mt = 0; mt < kMt; ++mt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[mt][e] = 0.f;
-        // References in units of S'; r = -F m (0 while a column has seen no row).
+        // References M; r = -M (0 while a column has seen no row).
         float m0 = -INFINITY, m1 = -INFINITY, r0 = 0.f, r1 = 0.f;
         float l0 = 0.f, l1 = 0.f, z0 = 0.f, z1 = 0.f;
-        int ve = 1;                        // e + 127
-        float vinv = 0.f;                  // 2^-e
-        float vtop = -1.f;                 // 2^(e + 1); -1: raise at the next unit
+        float raise_at = -INFINITY;        // until every column has seen a row
 
         for (int i = 0; i < cnt; ++i) {
             issue();
@@ -576,37 +587,55 @@ __global__ void __launch_bounds__(kThreads4, MIN_CTAS) decode_int4_kernel(const 
                     confine(vp[h].y, S[h][2], S[h][3]);
                 }
             }
-            float smax = fmaxf(int4_step(vp[0].x), int4_step(vp[0].y));
-            float mx0 = fmaxf(S[0][0], S[0][2]), mx1 = fmaxf(S[0][1], S[0][3]);
-            if constexpr (!kShared) {
-                smax = fmaxf(smax, fmaxf(int4_step(vp[1].x), int4_step(vp[1].y)));
-                mx0 = fmaxf(mx0, fmaxf(S[1][0], S[1][2]));
-                mx1 = fmaxf(mx1, fmaxf(S[1][1], S[1][3]));
+            // X = F S' - M, and beside it log2 of the row's a (see above): the upper
+            // half of a's bits b stands for b / 128 - 127, at most 0.1 too low. As the
+            // low bits of 2^23 and in units of 1 / 128 it reads 65536 + b / 128.
+            float X[kSets][4], ab[kSets][2];
+            float top = -INFINITY;
+#pragma unroll
+            for (int h = 0; h < kSets; ++h) {
+                X[h][0] = fmaf(S[h][0], qf[0], r0); X[h][1] = fmaf(S[h][1], qf[1], r1);
+                X[h][2] = fmaf(S[h][2], qf[0], r0); X[h][3] = fmaf(S[h][3], qf[1], r1);
+                ab[h][0] = row_size(vp[h].x);
+                ab[h][1] = row_size(vp[h].y);
+                top = fmaxf(top, fmaxf(fmaf(ab[h][0], 0x1p-7f, fmaxf(X[h][0], X[h][1])),
+                                       fmaf(ab[h][1], 0x1p-7f, fmaxf(X[h][2], X[h][3]))));
             }
-            if (__any_sync(0xffffffffu, fmaxf(fmaf(mx0, qf[0], r0), fmaf(mx1, qf[1], r1)) > kRaise || smax >= vtop)) {
+            if (__any_sync(0xffffffffu, top > raise_at)) {
+                float n0 = -INFINITY, n1 = -INFINITY;
+#pragma unroll
+                for (int h = 0; h < kSets; ++h) {
+                    const float x = fmaf(ab[h][0], 0x1p-7f, -kSizeBias), y = fmaf(ab[h][1], 0x1p-7f, -kSizeBias);
+                    n0 = fmaxf(n0, fmaxf(fmaf(S[h][0], qf[0], x), fmaf(S[h][2], qf[0], y)));
+                    n1 = fmaxf(n1, fmaxf(fmaf(S[h][1], qf[1], x), fmaf(S[h][3], qf[1], y)));
+                }
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1) {
-                    mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, off));
-                    mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
+                    n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, off));
+                    n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, off));
                 }
-                const float n0 = fmaxf(m0, mx0), n1 = fmaxf(m1, mx1);
-                const float q0 = n0 == -INFINITY ? 0.f : -(n0 * qf[0]);
-                const float q1 = n1 == -INFINITY ? 0.f : -(n1 * qf[1]);
-                const float a0 = m0 == -INFINITY ? 0.f : fast_exp2(q0 - r0);
-                const float a1 = m1 == -INFINITY ? 0.f : fast_exp2(q1 - r1);
-                m0 = n0; m1 = n1; r0 = q0; r1 = q1;
-                const int ne = max(ve, min(253, static_cast<int>(__reduce_max_sync(0xffffffffu,
-                                                                  __float_as_uint(smax)) >> 23)));
-                const float ae = __uint_as_float(static_cast<uint32_t>(max(0, 127 + ve - ne)) << 23);
-                ve = ne;
-                vinv = __uint_as_float(static_cast<uint32_t>(254 - ne) << 23);
+                n0 = fmaxf(m0, n0 - kPut);
+                n1 = fmaxf(m1, n1 - kPut);
+                // Square roots of the sums' factors, applied twice: a factor may be
+                // below fp32's range where the sum is large.
+                const float a0 = m0 == -INFINITY ? 0.f : fast_exp2(0.5f * (m0 - n0));
+                const float a1 = m1 == -INFINITY ? 0.f : fast_exp2(0.5f * (m1 - n1));
+                m0 = n0; m1 = n1;
+                r0 = m0 == -INFINITY ? 0.f : -m0;
+                r1 = m1 == -INFINITY ? 0.f : -m1;
                 // A column that has seen no row yet takes its first reference
                 // from the next unit.
-                vtop = __any_sync(0xffffffffu, m0 == -INFINITY || m1 == -INFINITY)
-                           ? -1.f : __uint_as_float(static_cast<uint32_t>(ne + 1) << 23);
+                raise_at = __any_sync(0xffffffffu, m0 == -INFINITY || m1 == -INFINITY) ? -INFINITY
+                                                                                       : kSizeBias + kRaise;
+#pragma unroll
+                for (int h = 0; h < kSets; ++h) {
+                    X[h][0] = fmaf(S[h][0], qf[0], r0); X[h][1] = fmaf(S[h][1], qf[1], r1);
+                    X[h][2] = fmaf(S[h][2], qf[0], r0); X[h][3] = fmaf(S[h][3], qf[1], r1);
+                }
                 if (i > 0) {               // else every sum is 0
-                    l0 *= a0; z0 *= a0; l1 *= a1; z1 *= a1;
-                    const float b0 = a0 * ae, b1 = a1 * ae;
+                    l0 = l0 * a0 * a0; z0 = z0 * a0 * a0;
+                    l1 = l1 * a1 * a1; z1 = z1 * a1 * a1;
+                    const float b0 = a0 * a0, b1 = a1 * a1;
 #pragma unroll
                     for (int mt = 0; mt < kMt; ++mt) {
                         o[mt][0] *= b0; o[mt][1] *= b1; o[mt][2] *= b0; o[mt][3] *= b1;
@@ -616,9 +645,9 @@ __global__ void __launch_bounds__(kThreads4, MIN_CTAS) decode_int4_kernel(const 
             // ---- o += codes(V)^T . P, tile by tile
             uint32_t b0[kSets], b1[kSets];
             auto weights = [&](int h) {
-                const float E0 = fast_exp2(fmaf(S[h][0], qf[0], r0)), E1 = fast_exp2(fmaf(S[h][1], qf[1], r1));
-                const float E2 = fast_exp2(fmaf(S[h][2], qf[0], r0)), E3 = fast_exp2(fmaf(S[h][3], qf[1], r1));
-                const float u0 = int4_step(vp[h].x) * vinv, u1 = int4_step(vp[h].y) * vinv;
+                const float E0 = fast_exp2(X[h][0]), E1 = fast_exp2(X[h][1]);
+                const float E2 = fast_exp2(X[h][2]), E3 = fast_exp2(X[h][3]);
+                const float u0 = int4_step(vp[h].x), u1 = int4_step(vp[h].y);
                 const float y0 = int4_lo(vp[h].x), y1 = int4_lo(vp[h].y);
                 l0 += E0 + E2;
                 l1 += E1 + E3;
@@ -664,23 +693,30 @@ __global__ void __launch_bounds__(kThreads4, MIN_CTAS) decode_int4_kernel(const 
         float* st = merge + warp * Smem::kState;
         float* ml = st + 8 * Smem::kCol;
         const int s0 = 2 * t4, s1 = s0 + 1;   // of the state's columns
+        // With its sum brought to [1, 2) by a power of two, a state's outputs are of the
+        // size of V, whatever M: states join by what they weigh.
+        const int x0 = min(253, static_cast<int>(__float_as_uint(l0) >> 23 & 255u));
+        const int x1 = min(253, static_cast<int>(__float_as_uint(l1) >> 23 & 255u));
+        const float f0 = __uint_as_float(static_cast<uint32_t>(254 - x0) << 23);
+        const float f1 = __uint_as_float(static_cast<uint32_t>(254 - x1) << 23);
         if (gid == 0) {
-            ml[s0] = m0 == -INFINITY ? -INFINITY : -r0;
-            ml[s1] = m1 == -INFINITY ? -INFINITY : -r1;
-            ml[8 + s0] = l0;
-            ml[8 + s1] = l1;
+            ml[s0] = m0 + static_cast<float>(x0 - 127);
+            ml[s1] = m1 + static_cast<float>(x1 - 127);
+            ml[8 + s0] = l0 * f0;
+            ml[8 + s1] = l1 * f1;
         }
-        // even dims: o 2^e 2^24; odd ones: (o - even's) 2^e 2^20
-        const float ve2 = __uint_as_float(static_cast<uint32_t>(ve) << 23);
+        z0 *= f0;
+        z1 *= f1;
+        // even dims: o 2^24; odd ones: (o - even's) 2^20
 #pragma unroll
         for (int mt = 0; mt < kMt; ++mt) {
             const int d = 16 * mt + 2 * gid;   // dims d and d + 1
             *reinterpret_cast<float2*>(st + s0 * Smem::kCol + d) =
-                make_float2(fmaf(o[mt][0] * 16777216.f, ve2, z0),
-                            fmaf((o[mt][2] - o[mt][0]) * 1048576.f, ve2, z0));
+                make_float2(fmaf(o[mt][0] * 16777216.f, f0, z0),
+                            fmaf((o[mt][2] - o[mt][0]) * 1048576.f, f0, z0));
             *reinterpret_cast<float2*>(st + s1 * Smem::kCol + d) =
-                make_float2(fmaf(o[mt][1] * 16777216.f, ve2, z1),
-                            fmaf((o[mt][3] - o[mt][1]) * 1048576.f, ve2, z1));
+                make_float2(fmaf(o[mt][1] * 16777216.f, f1, z1),
+                            fmaf((o[mt][3] - o[mt][1]) * 1048576.f, f1, z1));
         }
         deal_q((j + 1) & 1);
         __syncthreads();                   // the states and the next q are complete

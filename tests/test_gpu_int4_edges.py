@@ -1,10 +1,11 @@
 """4-bit decode at the edges of its values, against 64 bits: rows that are not
-finite and are masked for some of the query tokens."""
+finite and are masked for some of the query tokens, value rows whose steps lie
+far apart."""
 import numpy as np
 import pytest
 
 import rows_reference as ref
-from test_gpu_int4 import Batch, value
+from test_gpu_int4 import Batch, bf16, value
 
 pytestmark = pytest.mark.gpu
 
@@ -52,3 +53,156 @@ def test_a_bad_row_that_has_left_the_later_tokens_windows(Q, window):
         for s, n in enumerate(lens):
             want, tol = ref.attention4(value(b.q[s]), b.pools, b.table[s], n, b.scale, b.bs, window)
             assert (np.abs(got[s] - want) <= tol)[1:].all(), s
+
+
+# --------------------------------------- steps of value rows that lie far apart
+
+
+def attention4_weighted(q, pools, table, n, scale, block_size):
+    """rows_reference.attention4 for one query token with a bound in which every row
+    counts by its weight w:
+      2^-8 |o|                      the rounding to bf16
+      2^-11 sum w |s| c             each weight times s rounded to f16
+      2^-25 max(w a) sum c          half of f16's smallest step, 2^-24, for products
+                                    below f16's normal range: they are taken relative
+                                    to the largest w a, a = |s| + 2^-12 |lo| of a row
+      2 d sum w (|lo| + |s| c)      d as in attention4: errors of the weights themselves
+    """
+    _, hq, D = q.shape
+    kc, vc, kp, vp = pools
+    hkv = kc.shape[1]
+    i = np.arange(n)
+    blk, off = np.asarray(table)[i // block_size], i % block_size
+    out, tol = np.zeros((hq, D)), np.zeros((hq, D))
+    for qh in range(hq):
+        h = qh // (hq // hkv)
+        k = ref.values4(kc[blk, h, off], kp[blk, h, off])
+        klo, ks = (ref.bf16_value(kp[blk, h, off][:, e]).astype(np.float64) for e in (0, 1))
+        vlo, vs = (ref.bf16_value(vp[blk, h, off][:, e]).astype(np.float64) for e in (0, 1))
+        code = ref.codes4(vc[blk, h, off]).astype(np.float64)
+        x = q[0, qh]
+        s = scale * (k @ x)
+        w = np.exp(s - s.max())
+        w /= w.sum()
+        o = w @ (vlo[:, None] + vs[:, None] * code)
+        size = abs(scale) * (np.abs(ks) * (ref.codes4(kc[blk, h, off]) @ np.abs(x)) + np.abs(klo) * np.abs(x).sum())
+        d = size.max() * 2.0 ** -18 + 2.0 ** -20
+        out[qh] = o
+        tol[qh] = (2.0 ** -8 * np.abs(o) + 2.0 ** -11 * ((w * np.abs(vs)) @ code)
+                   + 2.0 ** -25 * (w * (np.abs(vs) + 2.0 ** -12 * np.abs(vlo))).max() * code.sum(0)
+                   + 2 * d * (w @ (np.abs(vlo)[:, None] + np.abs(vs)[:, None] * code)))
+    return out, tol
+
+
+def _row_weights(b, s, h):
+    """Weights of sequence s's rows for the query heads of KV head h: [G][n]."""
+    i = np.arange(b.lens[s])
+    blk, off = b.table[s, i // b.bs], i % b.bs
+    G = b.hq // b.hkv
+    z = b.scale * value(b.q[s, 0, h * G:(h + 1) * G]) @ ref.values4(b.pools[0][blk, h, off], b.pools[2][blk, h, off]).T
+    w = np.exp(z - z.max(-1, keepdims=True))
+    return w / w.sum(-1, keepdims=True)
+
+
+def _set_value_row(b, s, h, i, x):
+    codes, pair = ref.quantise4(np.asarray(x, np.float32)[None])
+    at = b.table[s, i // b.bs], h, i % b.bs
+    b.pools[1][at], b.pools[3][at] = codes[0], pair[0]
+
+
+def _check(b):
+    got = b.upload().decode()[:, 0]
+    assert int(b.err.item()) == 0
+    for s, n in enumerate(b.lens):
+        want, tol = attention4_weighted(value(b.q[s]), b.pools, b.table[s], n, b.scale, b.bs)
+        worst = (np.abs(got[s] - want) - tol).max()
+        assert worst <= 0, f"sequence {s} of {n} rows: {worst:.3g} over its bound"
+
+
+SPREAD = [40, 100, 290, 700, 1500, 2300]
+
+
+@pytest.mark.parametrize("group", [1, 4, 8])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("ratio", [16, 20, 24, 40, 60])
+def test_a_row_of_no_weight_with_a_large_step(ratio, d, group):
+    """The row of least weight has a step 2^ratio times the others': its share of
+    the output is nothing, and the others keep their bits."""
+    b = Batch(SPREAD, hq=2 * group, hkv=2, d=d, seed=ratio + group)
+    b.scale *= 12
+    rng = np.random.default_rng(ratio)
+    for s in range(len(SPREAD)):
+        for h in range(2):
+            i = int(_row_weights(b, s, h).max(0).argmin())
+            _set_value_row(b, s, h, i, rng.standard_normal(d) * 2.0 ** ratio)
+    _check(b)
+
+
+@pytest.mark.parametrize("ratio", [20, 40, 60])
+def test_a_large_step_among_ordinary_weights(ratio):
+    """Some rows with large steps and their ordinary share of the weight."""
+    b = Batch(SPREAD, hq=8, hkv=2, seed=ratio)
+    b.scale *= 4
+    rng = np.random.default_rng(ratio)
+    for s, n in enumerate(SPREAD):
+        for i in rng.integers(0, n, 3):
+            _set_value_row(b, s, 0, int(i), rng.standard_normal(128) * 2.0 ** ratio)
+    _check(b)
+
+
+@pytest.mark.parametrize("where", ["first", "middle", "last"])
+@pytest.mark.parametrize("content", [0.0, 2.0 ** -30, 3.0, 1e6, 1e20])
+def test_a_row_of_nearly_all_weight_and_one_value(content, where):
+    """A row that takes nearly all the weight holds one value (a step of zero);
+    where that is 0, the output is the others' small share."""
+    b = Batch(SPREAD, hq=8, hkv=2, seed=77)
+    G = b.hq // b.hkv
+    for s, n in enumerate(SPREAD):
+        i = {"first": 0, "middle": n // 2, "last": n - 1}[where]
+        for h in range(2):
+            b.q[s, 0, h * G:(h + 1) * G] = b.q[s, 0, h * G]
+            x = value(b.q[s, 0, h * G])
+            codes, pair = ref.quantise4((x * 2.2).astype(np.float32)[None])
+            at = b.table[s, i // b.bs], h, i % b.bs
+            b.pools[0][at], b.pools[2][at] = codes[0], pair[0]
+            _set_value_row(b, s, h, i, np.full(128, content))
+    _check(b)
+
+
+@pytest.mark.parametrize("big", [12, 60])
+@pytest.mark.parametrize("lead", [0, 10, 25, 37, 60])
+def test_partitions_of_zero_rows_beside_one_of_large_steps(lead, big):
+    """Zero value rows whose scores lead by `lead` (base 2) over those of a partition
+    of large steps: parts of a sequence whose ranges differ by far join soundly."""
+    b = Batch([2300, 700], hq=4, hkv=1, seed=lead + big)
+    b.scale *= 0.01                                       # scores near 0
+    b.q[:, :, :, 0] = bf16(np.float32(4.0))
+    rng = np.random.default_rng(lead)
+    for s, n in enumerate(b.lens):
+        for i in range(n):
+            at = b.table[s, i // b.bs], 0, i % b.bs
+            large = i >= n - 60
+            x = rng.standard_normal(128) * 0.01
+            x[0] = 0.0 if large else lead * np.log(2.0) / (4.0 * b.scale)
+            codes, pair = ref.quantise4(x.astype(np.float32)[None])
+            b.pools[0][at], b.pools[2][at] = codes[0], pair[0]
+            _set_value_row(b, s, 0, i, rng.standard_normal(128) * 2.0 ** big if large else np.zeros(128))
+    _check(b)
+
+
+@pytest.mark.parametrize("v_gain", [2.0 ** -98, 2.0 ** -60, 2.0 ** 60, 2.0 ** 98])
+def test_steps_at_the_ends_of_the_range(v_gain):
+    b = Batch(SPREAD, hq=8, hkv=2, seed=3, v_gain=v_gain)
+    b.scale *= 4
+    _check(b)
+
+
+@pytest.mark.parametrize("group", [1, 8])
+def test_steps_of_either_sign(group):
+    """A row's value is lo + s c whatever the sign of s (the append writes none below 0)."""
+    b = Batch(SPREAD, hq=2 * group, hkv=2, seed=61)
+    b.scale *= 4
+    flip = np.random.default_rng(62).random(b.pools[3].shape[:3])
+    for pairs, below in ((b.pools[2], 0.3), (b.pools[3], 0.6)):
+        pairs[..., 1] ^= np.where(flip < below, 0x8000, 0).astype(np.uint16)
+    _check(b)
