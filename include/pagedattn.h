@@ -527,7 +527,8 @@ pa_status pa_gather_int4(const void* k_cache, const void* v_cache, const void* k
  * q, out: [num_seqs][num_queries][num_heads][head_dim]. n == 0 gives zero
  * rows; 0 < n < Q is flagged PA_DEVERR_CONTEXT (those rows are left as they
  * are). Scores, softmax and sums are fp32; q is held in f16 (exactly, but for
- * elements more than 2^20 below their head's largest). A probability times its
+ * elements more than 2^20 below their head's largest; |scale| times that largest
+ * below 2^115). A probability times its
  * row's s is rounded to f16 once, in a range set by the rows' own weights: it
  * loses bits where it is 2^21 or more below the largest (|s| + 2^-12 |lo|) times
  * probability, whatever the s of rows of little weight. |s| from 2^-102 to

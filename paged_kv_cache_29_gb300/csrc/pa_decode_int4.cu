@@ -23,7 +23,7 @@
 // converts its operands to f16 itself: the batch below took 66 us with it.)
 //
 // q is scaled by a power of two per head to [2^12, 2^13) before it becomes f16
-// (exact: bf16 has fewer bits), whatever its size; sum q' is the product with a
+// (exact: bf16 has fewer bits), up to |scale| max |q| of 2^115; sum q' is the product with a
 // row of ones.
 // A probability times its row's step is the V operand in f16. Its range, 2^-14 to
 // 2^16, is spent on the rows that count: a column's reference M is taken over S +
@@ -435,19 +435,25 @@ __global__ void __launch_bounds__(kThreads4, MIN_CTAS) decode_int4_kernel(const 
         }
 #pragma unroll
         for (int off = 8; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-        // f = 2^k with mx * f in [2^12, 2^13); 1 / f = 2^-k. A negative scale
-        // turns q, so that the factor F below is positive.
+        // f = 2^(139 - ex) with mx * f in [2^12, 2^13). A negative scale turns q, so
+        // that the factor F below is positive.
         const int ex = max(13, min(253, static_cast<int>(__float_as_uint(mx) >> 23)));
         const float f = copysignf(__uint_as_float(static_cast<uint32_t>(266 - ex) << 23), p.scale_log2);
-        const float inv = __uint_as_float(static_cast<uint32_t>(ex - 12) << 23);
         const float g = f * 0.0625f;
         if (q_col < 8 && q_part < kQLanes)
             q_frag[q_part % kKWords * 32 + q_col * 4 + q_part / kKWords] =
                 make_uint4(pack_f16x2(x[0] * f, x[4] * f), pack_f16x2(x[1] * g, x[5] * g),
                            pack_f16x2(x[2] * f, x[6] * f), pack_f16x2(x[3] * g, x[7] * g));
         // S = F S', S' = s acc + lo qsum, acc = f 2^-24 q . c, qsum = f 2^-24 q . 1,
-        // F = |scale| 2^24 / f (kept above 0: scale 0 gives equal weights).
-        if (q_part == 0) plan->col_f[buf][q_col] = fmaxf(fabsf(p.scale_log2) * (inv * 16777216.f), 1e-30f);
+        // F = |scale| 2^24 / f, kept above 0 (scale 0 gives equal weights). 2^24 / f is
+        // multiplied on in two halves: its range is wider than F's, and F below 2^128 is
+        // |scale| mx below 2^115.
+        if (q_part == 0) {
+            const int k = ex - 115, k0 = k >> 1;
+            const float F = fabsf(p.scale_log2) * __uint_as_float(static_cast<uint32_t>(127 + k0) << 23) *
+                            __uint_as_float(static_cast<uint32_t>(127 + k - k0) << 23);
+            plan->col_f[buf][q_col] = fmaxf(F, __uint_as_float(1u));
+        }
     };
     uint32_t qb[kKWords][4];
     float qf[2], qsum[2];                  // of columns c0 and c1

@@ -1,6 +1,6 @@
 """4-bit decode at the edges of its values, against 64 bits: rows that are not
 finite and are masked for some of the query tokens, value rows whose steps lie
-far apart."""
+far apart, queries and keys near the ends of bf16's range."""
 import numpy as np
 import pytest
 
@@ -206,3 +206,28 @@ def test_steps_of_either_sign(group):
     for pairs, below in ((b.pools[2], 0.3), (b.pools[3], 0.6)):
         pairs[..., 1] ^= np.where(flip < below, 0x8000, 0).astype(np.uint16)
     _check(b)
+
+
+# ----------------------------------- queries and keys at the ends of the range
+
+
+@pytest.mark.parametrize("gain", [-125, -110, 100, 112, 115, 120, 123])
+def test_queries_of_any_size_with_ordinary_scores(gain):
+    b = Batch([5, 600, 1500], hq=8, hkv=2, seed=9)
+    b.q = bf16(np.clip(value(b.q), -3.9, 3.9) * 2.0 ** gain)
+    b.scale *= 2.0 ** -gain
+    b.upload()
+    b.check(b.decode())
+
+
+@pytest.mark.parametrize("gain", [1e-33, 1e33, 3e36])
+def test_keys_of_any_size_with_ordinary_scores(gain):
+    b = Batch([5, 600, 1500], hq=8, hkv=2, seed=19, k_gain=gain).upload()
+    b.check(b.decode())
+
+
+def test_zero_scale_weighs_rows_equally_whatever_the_keys():
+    b = Batch([5, 600, 1500], hq=8, hkv=2, seed=20, k_gain=3e36)
+    b.scale = 0.0
+    b.upload()
+    b.check(b.decode())
