@@ -225,6 +225,22 @@ def _stream(stream) -> int | None:
     return stream.cuda_stream or None
 
 
+def _scratch(nbytes, stream, device):
+    """Workspace of one call that brings none, from torch's caching allocator. It
+    is taken as the launch stream's own: the allocator then hands its bytes out
+    again, and takes them from, work in that stream's order only. Taken on
+    torch's current stream and dropped while a call on another one runs, it could go
+    to the next tensor there under the running kernel."""
+    import torch
+    if stream is None:
+        return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+    _check_device(stream)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    with torch.cuda.stream(stream):
+        return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+
+
 def _check_cuda(name, t, dtype=None, ndim=None):
     if t is None:
         raise ValueError(f"{name} is required")
@@ -332,7 +348,7 @@ def pa_decode_fp8(q, k_cache, v_cache, block_tables, context_lens, scale, out, m
                   workspace)
     if workspace is None:
         need = pa_decode_workspace_size(B, hq, d, int(max_context_len))
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        workspace = _scratch(need, stream, q.device)
     _check_cuda("workspace", workspace)
     opts = _Options(KERNELS[kernel], 0, 0, 0)
     rc = lib().pa_decode_fp8_ex(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
@@ -371,7 +387,7 @@ def pa_test_withhold_tile(q, k_cache, v_cache, block_tables, context_lens, scale
                   workspace)
     if workspace is None:
         need = pa_decode_workspace_size(B, hq, d, int(max_context_len))
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        workspace = _scratch(need, stream, q.device)
     _check_cuda("workspace", workspace)
     rc = lib().pa_test_withhold_tile(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
                                      _ptr(context_lens), float(scale), _ptr(out), B, hq, hkv, d,
@@ -411,7 +427,7 @@ def pa_decode_multi(q, k_cache, v_cache, block_tables, context_lens, scale, out,
                   workspace)
     if workspace is None:
         need = pa_decode_workspace_size_multi(B, Q, hq, d, int(max_context_len))
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        workspace = _scratch(need, stream, q.device)
     _check_cuda("workspace", workspace)
     rc = lib().pa_decode_multi(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
                                _ptr(context_lens), float(scale), _ptr(out), B, Q, hq, hkv, d, bs,
@@ -444,7 +460,7 @@ def pa_decode_window(q, k_cache, v_cache, block_tables, context_lens, scale, win
                   workspace)
     if workspace is None:
         need = pa_decode_workspace_size(B, hq, d, int(max_context_len))
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        workspace = _scratch(need, stream, q.device)
     _check_cuda("workspace", workspace)
     rc = lib().pa_decode_window(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
                                 _ptr(context_lens), float(scale), int(window), _ptr(out), B, hq,
@@ -512,7 +528,7 @@ def pa_decode_int8(q, k_cache, v_cache, k_scales, v_scales, block_tables, contex
                   context_lens, error_word, workspace)
     if workspace is None:
         need = pa_decode_workspace_size(B, hq, d, int(max_context_len))
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        workspace = _scratch(need, stream, q.device)
     _check_cuda("workspace", workspace)
     rc = lib().pa_decode_int8(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scales),
                               _ptr(v_scales), _ptr(block_tables), _ptr(context_lens),
@@ -561,8 +577,8 @@ def pa_decode(q, k_cache, v_cache, block_tables, context_lens, scale, out, max_c
 
     max_context_len bounds context_lens (host value; sizes the work list and
     the workspace). workspace: a CUDA tensor of at least
-    pa_decode_workspace_size(...) bytes; when None, one is allocated from
-    torch's caching allocator for this call. long_partition_size /
+    pa_decode_workspace_size(...) bytes; when None, one is taken from torch's
+    caching allocator for this call, on its stream. long_partition_size /
     long_partition_from: partitions of that many rows for sequences longer
     than long_partition_from rows (0 = one size for all)."""
     import torch
@@ -585,7 +601,7 @@ def pa_decode(q, k_cache, v_cache, block_tables, context_lens, scale, out, max_c
         # The C library allocates nothing; the binding takes the scratch from
         # torch's allocator for callers that do not manage their own.
         need = pa_decode_workspace_size(B, hq, d, int(max_context_len), int(partition_size))
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        workspace = _scratch(need, stream, q.device)
     _check_cuda("workspace", workspace)
     ws_bytes = workspace.numel() * workspace.element_size()
     opts = _Options(KERNELS[kernel], int(partition_size), int(long_partition_size),
@@ -628,7 +644,7 @@ def pa_append_decode(k_new, v_new, slot_mapping, k_cache, v_cache, q, block_tabl
                   context_lens, error_word, workspace)
     if workspace is None:
         need = pa_decode_workspace_size(B, hq, d, int(max_context_len))
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        workspace = _scratch(need, stream, q.device)
     _check_cuda("workspace", workspace)
     ws_bytes = workspace.numel() * workspace.element_size()
     rc = lib().pa_append_decode(_ptr(k_new), _ptr(v_new), _ptr(slot_mapping), _ptr(k_cache),
@@ -676,7 +692,7 @@ def pa_append_decode_fp8(k_new, v_new, slot_mapping, k_cache, v_cache, q, block_
                   context_lens, error_word, workspace)
     if workspace is None:
         need = pa_decode_workspace_size(B, hq, d, int(max_context_len))
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        workspace = _scratch(need, stream, q.device)
     _check_cuda("workspace", workspace)
     rc = lib().pa_append_decode_fp8(_ptr(k_new), _ptr(v_new), _ptr(slot_mapping), _ptr(k_cache),
                                     _ptr(v_cache), float(k_scale), float(v_scale), _ptr(q),
@@ -704,7 +720,7 @@ def pa_append_decode_int8(k_new, v_new, slot_mapping, k_cache, v_cache, k_scales
                   v_scales, block_tables, context_lens, error_word, workspace)
     if workspace is None:
         need = pa_decode_workspace_size(B, hq, d, int(max_context_len))
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        workspace = _scratch(need, stream, q.device)
     _check_cuda("workspace", workspace)
     rc = lib().pa_append_decode_int8(_ptr(k_new), _ptr(v_new), _ptr(slot_mapping), _ptr(k_cache),
                                      _ptr(v_cache), _ptr(k_scales), _ptr(v_scales), _ptr(q),
@@ -899,7 +915,7 @@ def pa_decode_int4(q, k_cache, v_cache, k_params, v_params, block_tables, contex
     rows 0 .. n - Q + j). window > 0: each token attends to its last `window`
     rows only. workspace: a CUDA tensor of at least
     pa_decode_workspace_size_multi(B, Q, Hq, D, max_context_len) bytes; when
-    None, one is allocated from torch's caching allocator for this call."""
+    None, one is taken from torch's caching allocator for this call, on its stream."""
     import torch
     dev = torch.cuda.current_device()
     (nb, hkv, bs, d), (kc, vc, kp, vp) = _int4_pool(k_cache, v_cache, k_params, v_params, dev)
@@ -919,7 +935,7 @@ def pa_decode_int4(q, k_cache, v_cache, k_params, v_params, block_tables, contex
         raise ValueError("shape mismatch between q/out/block_tables/context_lens and the caches")
     if workspace is None:
         need = pa_decode_workspace_size_multi(B, Q, hq, d, int(max_context_len))
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        workspace = _scratch(need, stream, q.device)
     ws = _arg("workspace", workspace, dev)
     rc = lib().pa_decode_int4(qp, kc, vc, kp, vp, bt, cl, float(scale), int(window), op, B, Q, hq, hkv,
                               d, bs, nb, mb, int(max_context_len), ws,
