@@ -306,7 +306,7 @@ cudaError_t launch_gather_int4(const void* k_cache, const void* v_cache, const v
     const int tpr = head_dim <= 64 ? 8 : head_dim <= 128 ? 16 : 32;
     // Rows beyond a sequence's length cost nothing but a CTA's look at it, so the
     // sequences share a bounded number of CTAs, at most one warp per row.
-    long long bx = (max_context_len + kWarpsPerCta - 1) / kWarpsPerCta;
+    long long bx = (static_cast<long long>(max_context_len) + kWarpsPerCta - 1) / kWarpsPerCta;
     const long long share = (kGatherCtas + num_seqs - 1) / num_seqs;
     if (bx > share) bx = share;
     if (bx < 1) bx = 1;
