@@ -474,7 +474,8 @@ pa_status pa_test_withhold_tile(const void* q, const void* k_cache, const void* 
  *   codes   uint8 [num_blocks][num_kv_heads][block_size][head_dim / 2]
  *   params  bf16  [num_blocks][num_kv_heads][block_size][2], (lo, s)
  * head_dim / 2 + 4 bytes a row: 0.27 of a bf16 cache's at head_dim 128.
- * Codes and params are 16-byte aligned.
+ * Codes and params are 16-byte aligned. These calls and pa_norm_rope* take at most
+ * 2^20 heads (else PA_ERR_UNSUPPORTED).
  *
  * pa_reshape_and_cache_int4 -- quantising append:
  *   lo = min_d x[d] rounded down to bf16, s = (max_d x[d] - lo) / 15 rounded

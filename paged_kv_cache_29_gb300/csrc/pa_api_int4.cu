@@ -10,6 +10,9 @@
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
+// Heads of a token that these calls take: products of heads, lanes per row, query
+// tokens and dims stay below 2^31 in the launches and kernels.
+constexpr int kMaxHeads = 1 << 20;
 
 bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 bool aligned16(const void* p) { return aligned(p, 16); }
@@ -33,7 +36,8 @@ pa_status norm_rope_params(const pa_norm_rope_args* a, pa::NormRopeParams* p) {
         a->eps == INFINITY || !std::isfinite(a->weight_offset) || a->rot_dim < 0 ||
         a->rot_dim > a->head_dim)
         return PA_ERR_INVALID_ARG;
-    if (a->head_dim % 16 != 0 || a->head_dim > pa::kMaxHeadDim || a->rot_dim % 16 != 0)
+    if (a->head_dim % 16 != 0 || a->head_dim > pa::kMaxHeadDim || a->rot_dim % 16 != 0 ||
+        a->num_heads > kMaxHeads || a->num_kv_heads > kMaxHeads)
         return PA_ERR_UNSUPPORTED;
     if (a->rot_dim > 0) {
         if (a->num_axes < 1 || a->num_axes > 4 || a->max_position <= 0) return PA_ERR_INVALID_ARG;
@@ -107,7 +111,8 @@ pa_status pa_reshape_and_cache_int4(const void* k_new, const void* v_new, pa_dty
     if (num_tokens < 0 || num_kv_heads <= 0 || head_dim <= 0 || block_size <= 0 ||
         num_blocks <= 0 || !plain_dtype(new_dtype))
         return PA_ERR_INVALID_ARG;
-    if (head_dim % 32 != 0 || head_dim > pa::kMaxHeadDim) return PA_ERR_UNSUPPORTED;
+    if (head_dim % 32 != 0 || head_dim > pa::kMaxHeadDim || num_kv_heads > kMaxHeads)
+        return PA_ERR_UNSUPPORTED;
     if (num_tokens == 0) return PA_OK;
     if (!k_new || !v_new || !slot_mapping || !aligned16(k_new) || !aligned16(v_new) ||
         !aligned(slot_mapping, 8) || !pool4_ok(k_cache, v_cache, k_params, v_params))
@@ -130,7 +135,8 @@ pa_status pa_gather_int4(const void* k_cache, const void* v_cache, const void* k
         return PA_ERR_INVALID_ARG;
     if (static_cast<long long>(max_context_len) > static_cast<long long>(max_blocks_per_seq) * block_size)
         return PA_ERR_INVALID_ARG;
-    if (head_dim % 32 != 0 || head_dim > pa::kMaxHeadDim) return PA_ERR_UNSUPPORTED;
+    if (head_dim % 32 != 0 || head_dim > pa::kMaxHeadDim || num_kv_heads > kMaxHeads)
+        return PA_ERR_UNSUPPORTED;
     if (num_seqs == 0) return PA_OK;
     // With no rows to write the outputs may be null; lengths are still checked.
     if (!block_tables || !context_lens || !row_starts || (num_rows > 0 && (!k_out || !v_out)) ||
@@ -161,7 +167,7 @@ pa_status pa_decode_int4(const void* q, const void* k_cache, const void* v_cache
     // pool below 2^32.
     if ((head_dim != 64 && head_dim != 128) || block_size % 16 != 0 ||
         static_cast<long long>(num_heads / num_kv_heads) * num_queries > 8 ||
-        max_context_len > INT_MAX - 4096 ||
+        max_context_len > INT_MAX - 4096 || num_heads > kMaxHeads ||
         static_cast<double>(num_blocks) * num_kv_heads * (block_size / 16) >= 4294967296.0)
         return PA_ERR_UNSUPPORTED;
     if (num_seqs == 0) return PA_OK;
