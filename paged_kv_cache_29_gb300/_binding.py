@@ -818,6 +818,14 @@ def _heads_arg(name, t, dev, dtype=None):
     return t.data_ptr(), (st if T > 1 else H * D)
 
 
+def _int32(name, v):
+    """A number as the C int that it is passed as (ctypes would cut it to 32 bits)."""
+    v = int(v)
+    if not -2 ** 31 <= v < 2 ** 31:
+        raise ValueError(f"{name} must fit 32 bits, got {v}")
+    return v
+
+
 _raw_stream_of = None
 
 
@@ -899,8 +907,9 @@ def pa_gather_int4(k_cache, v_cache, k_params, v_params, block_tables, context_l
     if context_lens.shape[0] != B or row_starts.shape[0] != B or v_out.shape != k_out.shape \
             or h != hkv or do != d:
         raise ValueError("shape mismatch between the outputs, the tables and the caches")
+    bound = _int32("max_context_len", max_context_len)
     rc = lib().pa_gather_int4(kc, vc, kp, vp, bt, cl, rs, ko, vo, _plain_dtype_code(k_out), rows, B, hkv, d,
-                              bs, nb, mb, int(max_context_len),
+                              bs, nb, mb, bound,
                               _opt_arg("error_word", error_word, dev, torch.int32),
                               _stream_on(stream, dev))
     if rc != PA_OK:
@@ -933,12 +942,13 @@ def pa_decode_int4(q, k_cache, v_cache, k_params, v_params, block_tables, contex
     rows, mb = block_tables.shape
     if dq != d or out.shape != shape or rows != B or context_lens.shape[0] != B:
         raise ValueError("shape mismatch between q/out/block_tables/context_lens and the caches")
+    bound, window = _int32("max_context_len", max_context_len), _int32("window", window)
     if workspace is None:
-        need = pa_decode_workspace_size_multi(B, Q, hq, d, int(max_context_len))
+        need = pa_decode_workspace_size_multi(B, Q, hq, d, bound)
         workspace = _scratch(need, stream, q.device)
     ws = _arg("workspace", workspace, dev)
-    rc = lib().pa_decode_int4(qp, kc, vc, kp, vp, bt, cl, float(scale), int(window), op, B, Q, hq, hkv,
-                              d, bs, nb, mb, int(max_context_len), ws,
+    rc = lib().pa_decode_int4(qp, kc, vc, kp, vp, bt, cl, float(scale), window, op, B, Q, hq, hkv,
+                              d, bs, nb, mb, bound, ws,
                               workspace.numel() * workspace.element_size(),
                               _opt_arg("error_word", error_word, dev, torch.int32),
                               _stream_on(stream, dev))
