@@ -12,6 +12,9 @@
 // beside a plain copy's 6,797 GB/s: memory bounds all but the append of bf16 rows, where
 // it is the arithmetic per element (ALU pipe 60 % busy, issue 64 %): unpacking, the
 // minimum and maximum, five fp32 operations for the quotient, packing.
+#include <algorithm>
+#include <atomic>
+
 #include "pa_int4.cuh"
 #include "pa_internal.h"
 
@@ -21,15 +24,11 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kWarpsPerCta = kThreads / 32;
-// Warps of the append that the device holds at once (40 per SM): with few tokens,
-// as many warps as that share a token's heads in equal parts. 32 KV heads of bf16 (8
-// passes): 1,000 tokens 5.9 us with four warps each (two 6.9, six 6.5), 1,500 tokens 7.7
-// with four (two 8.9, one 12.7), 3,000 tokens 14.0 with two (one 16.6).
-constexpr int kAppendWarps = 6080;
-// CTAs of the gather (96 per SM, ten times what is resident), so that sequences
-// of 16 to 8,192 rows spread: append and gather of 128 of them 366 us, 370 with 9,728
-// CTAs, 385 with 4,864. 32 equal sequences: 54.6 us, 54.3 and 55.9.
-constexpr long long kGatherCtas = 14592;
+// CTAs of the gather, in times what is resident (nine per SM of the bf16 kernel), so
+// that sequences of 16 to 8,192 rows spread: append and gather of 128 of them 365.1
+// us, 365.5 with eleven, 366.2 with ten, 385 with three and a half, 363.4 with sixteen.
+// The gather of 32 equal sequences: 54.3 us, 54.8, 54.7, 55.9 and 54.5.
+constexpr int kGatherWaves = 12;
 
 // Sixteen elements as they are loaded, their fp32 values, and the row's pair.
 template <typename T, int TPR>
@@ -263,34 +262,77 @@ gather_int4_kernel(const uint8_t* __restrict__ k_cache, const uint8_t* __restric
 
 }  // namespace
 
+namespace {
+
+template <typename TIn, int TPR>
+cudaError_t run_append(const TIn* k_new, const TIn* v_new, const int64_t* slot_mapping, uint8_t* k_cache,
+                       uint8_t* v_cache, uint32_t* k_params, uint32_t* v_params, int num_tokens,
+                       int num_kv_heads, int head_dim, int block_size, int num_blocks, int32_t* error_word,
+                       cudaStream_t stream) {
+    auto kernel = append_int4_kernel<TIn, TPR>;
+    static std::atomic<int> cached_ctas[kMaxDevices];
+    int resident = 0;
+    const cudaError_t err = resident_ctas(kernel, kThreads, cached_ctas, &resident);
+    if (err != cudaSuccess) return err;
+    // With few tokens, as many warps as the device holds at once share a token's heads in
+    // equal parts. 32 KV heads of bf16 (8 passes), 40 warps on an SM: 1,000 tokens 5.9 us
+    // with four warps each (two 6.9, six 6.5), 1,500 tokens 7.7 with four (two 8.9, one
+    // 12.7), 3,000 tokens 14.0 with two (one 16.6). fp32, 36 warps on an SM: 2,000 tokens
+    // 15.1 us with two; three, the count for 40 warps on an SM, 17.6.
+    const int passes = static_cast<int>((static_cast<long long>(num_kv_heads) * TPR + 31) / 32);
+    const int most = max(1, min(passes, resident * kWarpsPerCta / num_tokens));
+    const int share = (passes + most - 1) / most;
+    const int splits = (passes + share - 1) / share;
+    const long long blocks = (static_cast<long long>(num_tokens) * splits + kWarpsPerCta - 1) / kWarpsPerCta;
+    kernel<<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(
+        k_new, v_new, slot_mapping, k_cache, v_cache, k_params, v_params, num_tokens, splits, head_dim,
+        num_kv_heads, block_size, static_cast<long long>(num_blocks) * block_size, error_word);
+    return cudaGetLastError();
+}
+
+template <typename TOut, int TPR>
+cudaError_t run_gather(const uint8_t* k_cache, const uint8_t* v_cache, const uint32_t* k_params,
+                       const uint32_t* v_params, const int32_t* block_tables, const int32_t* context_lens,
+                       const int64_t* row_starts, TOut* k_out, TOut* v_out, long long num_rows, int num_seqs,
+                       int num_kv_heads, int head_dim, int block_size, int num_blocks, int max_blocks_per_seq,
+                       int max_context_len, int32_t* error_word, cudaStream_t stream) {
+    auto kernel = gather_int4_kernel<TOut, TPR>;
+    static std::atomic<int> cached_ctas[kMaxDevices];
+    int resident = 0;
+    cudaError_t err = resident_ctas(kernel, kThreads, cached_ctas, &resident);
+    if (err != cudaSuccess) return err;
+    // Rows beyond a sequence's length cost nothing but a CTA's look at it, so the
+    // sequences share a bounded number of CTAs, at most one warp per row.
+    const long long rows = (static_cast<long long>(max_context_len) + kWarpsPerCta - 1) / kWarpsPerCta;
+    const long long share = (static_cast<long long>(kGatherWaves) * resident + num_seqs - 1) / num_seqs;
+    const long long bx = std::max(1LL, std::min(rows, share));
+    for (int s0 = 0; s0 < num_seqs; s0 += 65535) {   // grid.y holds 65,535 sequences
+        const int m = num_seqs - s0 < 65535 ? num_seqs - s0 : 65535;
+        kernel<<<dim3(static_cast<unsigned>(bx), static_cast<unsigned>(m)), kThreads, 0, stream>>>(
+            k_cache, v_cache, k_params, v_params, block_tables + static_cast<size_t>(s0) * max_blocks_per_seq,
+            context_lens + s0, row_starts + s0, k_out, v_out, num_rows, num_kv_heads, head_dim, block_size,
+            num_blocks, max_blocks_per_seq, max_context_len, error_word);
+        err = cudaGetLastError();
+        if (err != cudaSuccess) return err;
+    }
+    return cudaSuccess;
+}
+
+}  // namespace
+
 cudaError_t launch_append_int4(const void* k_new, const void* v_new, pa_dtype new_dtype,
                                const int64_t* slot_mapping, void* k_cache, void* v_cache,
                                void* k_params, void* v_params, int num_tokens, int num_kv_heads,
                                int head_dim, int block_size, int num_blocks, int32_t* error_word,
                                cudaStream_t stream) {
     if (num_tokens == 0) return cudaSuccess;
-    const int tpr = head_dim <= 64 ? 4 : head_dim <= 128 ? 8 : 16;
-    const int passes = static_cast<int>((static_cast<long long>(num_kv_heads) * tpr + 31) / 32);
-    const int most = max(1, min(passes, kAppendWarps / num_tokens));
-    const int share = (passes + most - 1) / most;
-    const int splits = (passes + share - 1) / share;
-    const long long blocks =
-        (static_cast<long long>(num_tokens) * splits + kWarpsPerCta - 1) / kWarpsPerCta;
-    auto run = [&](auto kernel, auto tag) {
-        using TIn = decltype(tag);
-        kernel<<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(
-            static_cast<const TIn*>(k_new), static_cast<const TIn*>(v_new), slot_mapping,
-            static_cast<uint8_t*>(k_cache), static_cast<uint8_t*>(v_cache),
-            static_cast<uint32_t*>(k_params), static_cast<uint32_t*>(v_params), num_tokens, splits,
-            head_dim, num_kv_heads, block_size, static_cast<long long>(num_blocks) * block_size,
-            error_word);
-        return cudaGetLastError();
-    };
     auto pick = [&](auto tag) {
         using TIn = decltype(tag);
-        return tpr == 4   ? run(append_int4_kernel<TIn, 4>, tag)
-               : tpr == 8 ? run(append_int4_kernel<TIn, 8>, tag)
-                          : run(append_int4_kernel<TIn, 16>, tag);
+        auto run = head_dim <= 64 ? run_append<TIn, 4> : head_dim <= 128 ? run_append<TIn, 8> : run_append<TIn, 16>;
+        return run(static_cast<const TIn*>(k_new), static_cast<const TIn*>(v_new), slot_mapping,
+                   static_cast<uint8_t*>(k_cache), static_cast<uint8_t*>(v_cache), static_cast<uint32_t*>(k_params),
+                   static_cast<uint32_t*>(v_params), num_tokens, num_kv_heads, head_dim, block_size, num_blocks,
+                   error_word, stream);
     };
     return new_dtype == PA_DTYPE_BF16 ? pick(__nv_bfloat16{}) : pick(float{});
 }
@@ -303,34 +345,14 @@ cudaError_t launch_gather_int4(const void* k_cache, const void* v_cache, const v
                                int num_blocks, int max_blocks_per_seq, int max_context_len,
                                int32_t* error_word, cudaStream_t stream) {
     if (num_seqs == 0) return cudaSuccess;
-    const int tpr = head_dim <= 64 ? 8 : head_dim <= 128 ? 16 : 32;
-    // Rows beyond a sequence's length cost nothing but a CTA's look at it, so the
-    // sequences share a bounded number of CTAs, at most one warp per row.
-    long long bx = (static_cast<long long>(max_context_len) + kWarpsPerCta - 1) / kWarpsPerCta;
-    const long long share = (kGatherCtas + num_seqs - 1) / num_seqs;
-    if (bx > share) bx = share;
-    if (bx < 1) bx = 1;
-    auto run = [&](auto kernel, auto tag) {
-        using TOut = decltype(tag);
-        for (int s0 = 0; s0 < num_seqs; s0 += 65535) {   // grid.y holds 65,535 sequences
-            const int m = num_seqs - s0 < 65535 ? num_seqs - s0 : 65535;
-            kernel<<<dim3(static_cast<unsigned>(bx), static_cast<unsigned>(m)), kThreads, 0, stream>>>(
-                static_cast<const uint8_t*>(k_cache), static_cast<const uint8_t*>(v_cache),
-                static_cast<const uint32_t*>(k_params), static_cast<const uint32_t*>(v_params),
-                block_tables + static_cast<size_t>(s0) * max_blocks_per_seq, context_lens + s0,
-                row_starts + s0, static_cast<TOut*>(k_out), static_cast<TOut*>(v_out), num_rows,
-                num_kv_heads, head_dim, block_size, num_blocks, max_blocks_per_seq,
-                max_context_len, error_word);
-            const cudaError_t err = cudaGetLastError();
-            if (err != cudaSuccess) return err;
-        }
-        return cudaSuccess;
-    };
     auto pick = [&](auto tag) {
         using TOut = decltype(tag);
-        return tpr == 8    ? run(gather_int4_kernel<TOut, 8>, tag)
-               : tpr == 16 ? run(gather_int4_kernel<TOut, 16>, tag)
-                           : run(gather_int4_kernel<TOut, 32>, tag);
+        auto run = head_dim <= 64 ? run_gather<TOut, 8> : head_dim <= 128 ? run_gather<TOut, 16> : run_gather<TOut, 32>;
+        return run(static_cast<const uint8_t*>(k_cache), static_cast<const uint8_t*>(v_cache),
+                   static_cast<const uint32_t*>(k_params), static_cast<const uint32_t*>(v_params), block_tables,
+                   context_lens, row_starts, static_cast<TOut*>(k_out), static_cast<TOut*>(v_out), num_rows, num_seqs,
+                   num_kv_heads, head_dim, block_size, num_blocks, max_blocks_per_seq, max_context_len, error_word,
+                   stream);
     };
     return out_dtype == PA_DTYPE_BF16 ? pick(__nv_bfloat16{}) : pick(float{});
 }

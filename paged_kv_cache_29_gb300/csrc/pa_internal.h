@@ -2,6 +2,7 @@
 // the kernel translation units. Not part of the public ABI.
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda.h>
@@ -210,6 +211,23 @@ constexpr int kPartitionTail4 = 128;
 // sequence of 100,000 rows beside seven short ones takes 29.6 us, with 32 partitions 30.7,
 // with 8 30.5. Sequences of up to 16 partitions are still one warp's.
 constexpr int kCombineChunk4 = 16;
+// CTAs of a kernel (no dynamic shared memory) that the current device holds at
+// once, asked for once per device; `cached` is the kernel's own.
+template <typename Kernel>
+cudaError_t resident_ctas(Kernel kernel, int threads, std::atomic<int> (&cached)[kMaxDevices], int* ctas) {
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    *ctas = dev < kMaxDevices ? cached[dev].load(std::memory_order_relaxed) : 0;
+    if (*ctas > 0) return cudaSuccess;
+    int sms = 0, per_sm = 0;
+    err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (err == cudaSuccess) err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, 0);
+    if (err != cudaSuccess) return err;
+    *ctas = sms * per_sm;
+    if (dev < kMaxDevices) cached[dev].store(*ctas, std::memory_order_relaxed);
+    return cudaSuccess;
+}
 constexpr int kNoLongPartitions = 0x7fffffff;   // partition_long_from: one size for all
 // Kernel of pa_decode_fp8 and pa_append_decode_fp8 when none is requested.
 constexpr pa_kernel kFp8DefaultKernel = PA_KERNEL_MMA;

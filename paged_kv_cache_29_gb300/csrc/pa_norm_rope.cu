@@ -294,20 +294,11 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
 template <typename T, int TPR, Dest DEST>
 cudaError_t run(NormRopeParams p, cudaStream_t stream) {
     auto kernel = norm_rope_kernel<T, TPR, DEST>;
-    // The warps that the device holds at once, once per device and instance.
-    static std::atomic<int> cached_warps[kMaxDevices];
-    int dev = 0;
-    cudaError_t err = cudaGetDevice(&dev);
+    static std::atomic<int> cached_ctas[kMaxDevices];
+    int resident = 0;
+    cudaError_t err = resident_ctas(kernel, kThreads, cached_ctas, &resident);
     if (err != cudaSuccess) return err;
-    int resident = dev < kMaxDevices ? cached_warps[dev].load(std::memory_order_relaxed) : 0;
-    if (resident == 0) {
-        int sms = 0, per_sm = 0;
-        err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-        if (err == cudaSuccess) err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kThreads, 0);
-        if (err != cudaSuccess) return err;
-        resident = sms * per_sm * (kThreads / 32);
-        if (dev < kMaxDevices) cached_warps[dev].store(resident, std::memory_order_relaxed);
-    }
+    resident *= kThreads / 32;
     // Warps per token: as many as are resident at once, with equal shares of the
     // passes. 32 q heads and 8 KV heads of 128 dims (24 passes), bf16, into a pool,
     // 4,256 warps: 300 tokens 4.5 us with 12 warps each (10.0 with one, 6.2 with
