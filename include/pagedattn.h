@@ -483,7 +483,10 @@ pa_status pa_test_withhold_tile(const void* q, const void* k_cache, const void* 
  * for the new K row x = k_new[t][h] (and V), every difference and quotient in
  * fp32 (IEEE); s = 0 (all x equal to lo) gives codes 0. The directed roundings
  * keep every x inside [lo, lo + 15 s], so a value is off by at most s / 2
- * (plus fp32 rounding). A zero lo is +0. Rows must be finite with a finite
+ * (plus fp32 rounding). s is (max - min) / 15 widened by up to 2^-7 of itself for
+ * bf16 rows, whose lo is exact; for fp32 rows rounding lo adds up to 2^-7 |lo| / 15,
+ * so that a row whose offset is some 2^7 times its spread or more loses its
+ * detail. A zero lo is +0. Rows must be finite with a finite
  * max - lo; a row that is not gives unspecified codes and params for itself
  * alone. new_dtype PA_DTYPE_F32 or PA_DTYPE_BF16; head_dim a multiple of 32, at
  * most 256. Slots as in pa_reshape_and_cache; two tokens with the same slot
@@ -529,7 +532,7 @@ pa_status pa_gather_int4(const void* k_cache, const void* v_cache, const void* k
  * rows; 0 < n < Q is flagged PA_DEVERR_CONTEXT (those rows are left as they
  * are). Scores, softmax and sums are fp32; q is held in f16 (exactly, but for
  * elements more than 2^20 below their head's largest; |scale| times that largest
- * below 2^115). A probability times its
+ * below 2^115, scores below 2^27). A probability times its
  * row's s is rounded to f16 once, in a range set by the rows' own weights: it
  * loses bits where it is 2^21 or more below the largest (|s| + 2^-12 |lo|) times
  * probability, whatever the s of rows of little weight. |s| from 2^-102 to

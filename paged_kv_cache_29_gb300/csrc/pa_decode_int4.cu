@@ -34,7 +34,9 @@
 // at least otherwise. Relative to the largest step alone, a row of no weight with a
 // step of 2^20 times the others' cost these all but 5 bits.) M is raised, and the sums
 // rescaled, only when a row goes past 2^15: most units need no cross-lane maximum
-// and no rescale. E is fp32 and not below 2^-126 for rows that count as long as
+// and no rescale. M is rounded to fp32, S - M once from the exact product: scores
+// below 2^27 (2^28 in base 2, where M is off by at most 8) keep E a below 2^15.2 and
+// the largest above 2^-1. E is fp32 and not below 2^-126 for rows that count as long as
 // steps stay below 2^100; under 2^-102 a step loses bits. Sums, z = sum E lo, scores
 // and outputs are fp32.
 //

@@ -8,9 +8,11 @@
 // Differences and quotients are IEEE fp32, so every caller gives the same
 // bits. The pair costs 4 bytes a row where fp32 would cost 8 (11 % of a row at
 // head dim 128); rounding lo down and s up keeps every x inside the codes'
-// range, so the coarser pair widens the step by at most 2^-7 of itself and
-// adds no error of its own: codes are computed against the pair that is kept.
-// bf16 and not f16, so that any finite bf16 row has a finite pair.
+// range, and codes are computed against the pair that is kept. For a bf16 row lo
+// is exact and the step at most 2^-7 of itself wider than (max - min) / 15; for an
+// fp32 row rounding lo widens the range by up to 2^-7 |lo|, whatever the row's
+// spread: values from 1003.90 to 1003.99 get lo 1000 and a step of 0.27. bf16 and
+// not f16, so that any bf16 row with a finite max - min has a finite pair.
 #pragma once
 
 #include "pa_common.cuh"

@@ -231,3 +231,33 @@ def test_zero_scale_weighs_rows_equally_whatever_the_keys():
     b.scale = 0.0
     b.upload()
     b.check(b.decode())
+
+
+@pytest.mark.parametrize("group", [1, 8])
+@pytest.mark.parametrize("power", [16, 20, 24])
+def test_scores_up_to_2_to_the_27(power, group):
+    """Scores of some 2^power to 5 * 2^power: where one row leads by more than the scores'
+    error (2^-18 of their terms) it is the output. Below 2^27, 2^28 in base 2, the
+    reference is off by half of fp32's step of 16 there at most, so that the f16
+    operands, put at 2^7, stay between 2^-1 and 2^15.2."""
+    b = Batch([5, 600, 1500], hq=2 * group, hkv=2, seed=power)
+    b.scale *= 2.0 ** power
+    got = b.upload().decode()[:, 0]
+    assert np.isfinite(got).all()
+    led = 0
+    for s, n in enumerate(b.lens):
+        i = np.arange(n)
+        blk, off = b.table[s, i // b.bs], i % b.bs
+        for qh in range(b.hq):
+            h = qh // group
+            x = value(b.q[s, 0, qh])
+            z = b.scale * (ref.values4(b.pools[0][blk, h, off], b.pools[2][blk, h, off]) @ x)
+            pair = ref.bf16_value(b.pools[2][blk, h, off]).astype(np.float64)
+            size = b.scale * ((np.abs(pair[:, 0]) + 15 * pair[:, 1]) * np.abs(x).sum()).max()
+            assert size < 2.0 ** 32 and np.abs(z).max() < 2.0 ** 27
+            first, second = np.sort(z)[-1:-3:-1]
+            if first - second > 2.0 ** -17 * size + 32:
+                led += 1
+                v = ref.values4(b.pools[1][blk, h, off], b.pools[3][blk, h, off])[z.argmax()]
+                assert (np.abs(got[s, qh] - v) <= (2.0 ** -8 + 2.0 ** -10) * np.abs(v) + 2.0 ** -10 * np.abs(v).max()).all()
+    assert led > b.hq
