@@ -7,10 +7,10 @@
 //
 // Measured at 65,536 tokens, 8 KV heads of 128 dims, blocks of 16 in no order:
 //            bf16 rows             fp32 rows
-//   append   62.1 us, 5,467 GB/s   89.3 us, 6,811 GB/s
-//   gather   54.6 us, 6,226 GB/s   93.7 us, 6,491 GB/s
+//   append   62.2 us, 5,461 GB/s   89.3 us, 6,809 GB/s
+//   gather   54.2 us, 6,271 GB/s   92.4 us, 6,579 GB/s
 // beside a plain copy's 6,797 GB/s: memory bounds all but the append of bf16 rows, where
-// it is the arithmetic per element (ALU pipe 60 % busy, issue 64 %): unpacking, the
+// it is the arithmetic per element (ALU pipe 60 % busy, issue 68 %): unpacking, the
 // minimum and maximum, five fp32 operations for the quotient, packing.
 #include <algorithm>
 #include <atomic>

@@ -50,18 +50,19 @@
 // warp to keep four consumers fed. At an item's end the warps' states are
 // merged through shared memory.
 //
-// Measured: 128 sequences, 32 heads over 8 KV heads of 128 dims, 209,835 rows: 48.2
-// us, 4,896 GB/s of 6,797 (a plain copy); 32 sequences of 32 KV heads 37.8 us, 4,372
-// GB/s. The kernel is bound on two sides at once: without its loads the first takes
-// 46.6 us (three warps per scheduler issue 54 % of the cycles, the ALU pipe's ANDs and
-// permutes 50 %, tensor pipe 28 %), without its arithmetic 45.7, of which about 6
-// pass before the first tile is there and 3 are the merge launch. No change there:
-// four interleaved chains of q . c MMAs, both tiles' weights before either's
-// products, two fp32 values per instruction. Slower: the next unit's q . c ahead of
-// this unit's softmax or among its products (49.8 to 51.2), four CTAs on an SM with 128
-// registers and two stages (51.6; 35.8 instead of 37.7 for the second batch, whose items
-// spread better over 608 CTAs, but less in flight everywhere else, so one rule for all),
-// exponentials before the vote (50.7).
+// Measured: 128 sequences, 32 heads over 8 KV heads of 128 dims, 209,835 rows: 48.9
+// us, 4,830 GB/s of 6,797 (a plain copy); 32 sequences of 32 KV heads 38.3 us, 4,320
+// GB/s. The kernel is bound on two sides at once: three warps per scheduler issue 52 %
+// of the cycles (the ALU pipe's ANDs and permutes 50 %, tensor pipe 28 %); when it took
+// 48.2 us, it took 46.6 without its loads and 45.7 without its arithmetic, of which about
+// 6 pass before the first tile is there and 3 are the merge launch (48.2: with references
+// over the scores alone and one step exponent for all rows, which lost bits, see above).
+// Measured on that build and earlier ones, no change: four interleaved chains of q . c
+// MMAs, both tiles' weights before either's products, two fp32 values per instruction.
+// Slower: the next unit's q . c ahead of this unit's softmax or among its products (49.8 to
+// 51.2), four CTAs on an SM with 128 registers and two stages (51.6; 35.8 instead of 37.7
+// for the second batch, whose items spread better over 608 CTAs, but less in flight
+// everywhere else, so one rule for all), exponentials before the vote (50.7).
 #include <atomic>
 
 #include "pa_int4.cuh"
@@ -276,7 +277,7 @@ struct Smem4 {
 // share the eight columns of the products: columns 0-3 are the first tile's, 4-7 the
 // second's, each with a state of its own, joined where the warps' are. A lane then has
 // four scores of a unit to work on instead of eight (128 sequences of 209,835 rows,
-// four columns: 48.8 -> 48.0 us; 32 sequences, one column: 38.3 -> 37.7).
+// four columns: 48.8 -> 48.0 us; 32 sequences, one column: 38.3 -> 37.7, both as built then).
 template <int D, bool kShared, int STAGES, int MIN_CTAS>
 __global__ void __launch_bounds__(kThreads4, MIN_CTAS) decode_int4_kernel(const DecodeParams p) {
     using Smem = Smem4<D, STAGES>;

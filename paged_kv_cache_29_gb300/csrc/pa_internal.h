@@ -198,18 +198,18 @@ constexpr int kDefaultPartition8 = 1024;
 // INT4 caches: about the bytes of 512 bf16 rows again (139 KB at head dim 128).
 // An item's fixed work (q, the warps' merge, its partial) is that of four
 // 32-row units per warp: 128 sequences of 32 heads over 8 KV heads of 128 dims,
-// 209,835 rows, take 48.8 us at 1024 rows, 56.7 at 512; 32 sequences of 32 heads,
-// 512 to 2,048 rows, 38.2 and 41.1.
+// 209,835 rows, took 48.8 us at 1024 rows, 56.7 at 512, when this was chosen; 32
+// sequences of 32 heads, 512 to 2,048 rows, 38.2 and 41.1.
 constexpr int kDefaultPartition4 = 1024;
 // Rows behind the last full partition that join it: one more unit of 32 rows for
 // a warp costs less than an item of its own (a sliding window of 1,024 rows spans
-// up to 1,040). That window's batch takes 29.2 us with the tail, 35.7 without, the
-// 209,835-row batch 48.9 and 50.6; a tail of 512 rows takes 0.5 us more off that
+// up to 1,040). That window's batch takes 29.5 us with the tail, 36.2 without, the
+// 209,835-row batch 48.9 and 50.6; a tail of 512 rows took 0.5 us more off that
 // batch but makes the longest item, which a small batch waits for, half as long again.
 constexpr int kPartitionTail4 = 128;
 // Partitions that a warp of the merge takes at a time (it loads 8 at once): one
-// sequence of 100,000 rows beside seven short ones takes 29.6 us, with 32 partitions 30.7,
-// with 8 30.5. Sequences of up to 16 partitions are still one warp's.
+// sequence of 100,000 rows beside seven short ones takes 30.0 us, with 32 partitions 31.1,
+// with 8 30.7. Sequences of up to 16 partitions are still one warp's.
 constexpr int kCombineChunk4 = 16;
 // CTAs of a kernel (no dynamic shared memory) that the current device holds at
 // once, asked for once per device; `cached` is the kernel's own.

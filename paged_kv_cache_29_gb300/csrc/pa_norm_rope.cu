@@ -17,7 +17,7 @@
 //
 // Bound by memory once there are a few thousand tokens: 16,384 tokens of 32 q, K and
 // V heads of 128 dims (bf16, K and V into a pool) 128.3 us, 6,345 GB/s beside a
-// plain copy's 6,797; 4,099 tokens with 8 KV heads and three axes 17.9 us, 4,807
+// plain copy's 6,797; 4,099 tokens with 8 KV heads and three axes 18.0 us, 4,780
 // GB/s: all 4,099 warps are resident at once, so that the chain of each (positions,
 // table rows, first store) and the last warps' end are not hidden behind others.
 // 128 tokens 3.8 us, that chain alone.
