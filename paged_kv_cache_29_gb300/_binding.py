@@ -235,8 +235,9 @@ def _scratch(nbytes, stream, device):
     if stream is None:
         return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
     _check_device(stream)
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    if not isinstance(stream, torch.cuda.Stream):     # a raw handle, or another library's stream
+        handle = _stream(stream)
+        stream = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
     with torch.cuda.stream(stream):
         return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
 

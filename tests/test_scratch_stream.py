@@ -14,8 +14,17 @@ BF, U8, I32, I64, F32 = torch.bfloat16, torch.uint8, torch.int32, torch.int64, t
 
 
 class _Stream:
+    """Stands for torch.cuda.Stream."""
+
     def __init__(self, handle, index=0):
         self.cuda_stream, self.device = handle, torch.device("cuda", index)
+
+
+class _OtherStream:
+    """Another library's stream: a handle and nothing else."""
+
+    def __init__(self, handle):
+        self.cuda_stream = handle
 
 
 def _t(shape, dtype=BF):
@@ -59,6 +68,7 @@ def taken(monkeypatch):
 
     @contextlib.contextmanager
     def stream(st):
+        assert isinstance(st, torch.cuda.Stream)      # torch.cuda.stream takes no other
         before, under[0] = under[0], st.cuda_stream
         yield
         under[0] = before
@@ -70,6 +80,7 @@ def taken(monkeypatch):
     monkeypatch.setattr(pa, "lib", Library)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     monkeypatch.setattr(torch.cuda, "stream", stream)
+    monkeypatch.setattr(torch.cuda, "Stream", _Stream)
     monkeypatch.setattr(torch.cuda, "ExternalStream", _Stream)
     monkeypatch.setattr(torch.cuda, "default_stream", lambda: _Stream(0))
     monkeypatch.setattr(pa, "_raw_stream", lambda: 7)
@@ -93,6 +104,12 @@ def test_a_given_stream_owns_the_scratch(taken, name):
 @pytest.mark.parametrize("name", NAMES)
 def test_a_raw_handle_owns_the_scratch(taken, name):
     assert taken(name, 55) == [(55, 4096)]
+
+
+@pytest.mark.parametrize("handle", [77, 0])
+@pytest.mark.parametrize("name", NAMES)
+def test_another_library_s_stream_owns_the_scratch(taken, name, handle):
+    assert taken(name, _OtherStream(handle)) == [(handle, 4096)]
 
 
 @pytest.mark.parametrize("name", NAMES)
