@@ -87,6 +87,8 @@ typedef enum pa_dtype {
 #define PA_DEVERR_CONTEXT 0x4   /* context_len < 0, or > max_context_len, or past the table */
 #define PA_DEVERR_TIMEOUT 0x8   /* a shared-memory barrier wait gave up after its limit */
 #define PA_DEVERR_POSITION 0x10 /* a position outside [0, max_position) (pa_norm_rope*) */
+#define PA_DEVERR_TOKEN 0x20    /* a drafted token, a number of drafts or a row of probabilities
+                                   that pa_verify_draft cannot use */
 
 /*
  * Append one K and one V row per token into the paged pool:
@@ -621,6 +623,147 @@ pa_status pa_norm_rope_append_int4(const pa_norm_rope_args* args, const void* v,
                                    void* v_cache, void* k_params, void* v_params, int block_size,
                                    int num_blocks, int32_t* error_word,
                                    struct CUstream_st* stream);
+
+/*
+ * Which rows of a cache count: attention to a window and the first rows, the
+ * rows' accumulated attention weights, eviction by them, and the verification of
+ * drafted tokens, whose rejected rows leave again. These calls take at most 2^20
+ * heads (else PA_ERR_UNSUPPORTED).
+ *
+ * pa_decode_sinks -- decode attention to the last `window` rows and the first
+ * num_sinks rows, which stay visible as a sequence grows. num_queries (Q) new
+ * tokens per sequence, the last Q of its n = context_lens[s] rows (1: plain
+ * decode); query token j sits at row r = n - Q + j and attends to the rows i <= r
+ * with i < num_sinks or i > r - window, each once:
+ *   out[s][j][qh][:] = sum_i softmax_i(scale * <q[s][j][qh], K_i>) * V_i[:]
+ * q, out: dtype [num_seqs][num_queries][num_heads][head_dim], fp32 or bf16.
+ * n == 0 gives zero rows; 0 < n < Q is flagged PA_DEVERR_CONTEXT. Only the rows
+ * of the 16-row tiles that hold a visible row are read. A row that is not finite
+ * reaches the query tokens that attend to it and no other. Partitions of 512
+ * rows, counted without the rows between the first ones and the window, are merged as
+ * in pa_decode: a sequence's result does not depend on the rest of the batch.
+ * window >= 1, num_sinks >= 0, 1 <= num_queries <= 8. Workspace:
+ * pa_decode_workspace_size_multi. head_dim up to 256, any block_size >= 1, at most
+ * 1024 heads per KV head * num_queries. The fast kernels need block_size a multiple of 16, head_dim 64 or
+ * 128, and over bf16 heads per KV head * num_queries <= 8, over fp32 1, 2, 4 or
+ * 8 heads per KV head and one query token; other shapes run a plain kernel.
+ */
+pa_status pa_decode_sinks(const void* q, const void* k_cache, const void* v_cache,
+                          const int32_t* block_tables, const int32_t* context_lens, float scale,
+                          int window, int num_sinks, void* out, int num_seqs, int num_queries,
+                          int num_heads, int num_kv_heads, int head_dim, int block_size,
+                          int num_blocks, int max_blocks_per_seq, int max_context_len,
+                          pa_dtype dtype, void* workspace, size_t workspace_bytes,
+                          int32_t* error_word, struct CUstream_st* stream);
+
+/*
+ * pa_decode_weights -- decode attention (pa_decode, or with num_queries > 1
+ * pa_decode_multi) that also accumulates what each cached row was attended with:
+ * for row i of sequence s and KV head h
+ *   w = sum over the query tokens j with n - Q + j >= i and the heads qh of h of
+ *       softmax_i(scale * <q[s][j][qh], K_i>),
+ *   row_weights[slot of row i][h] = w                         for i >= n - Q,
+ *                                   row_weights[...] + w      else:
+ * the rows of this step's tokens begin their sums, whatever their slots held.
+ * row_weights: fp32 [num_blocks][num_kv_heads][block_size]; the rows of a prompt
+ * begin with what the caller puts there. A row in a block that several sequences of
+ * the batch share gets the weights of all of them (in any order of addition). All
+ * weights are fp32, from fp32 scores and the sequence's final maximum and sum.
+ * A sequence that is flagged leaves its row weights as they are; other
+ * arguments, shapes and errors as pa_decode_sinks without the window. Workspace:
+ * pa_decode_workspace_size_weights bytes (4 bytes of it per row of
+ * max_context_len, query token and head of each sequence hold the scores).
+ */
+pa_status pa_decode_weights(const void* q, const void* k_cache, const void* v_cache,
+                            const int32_t* block_tables, const int32_t* context_lens, float scale,
+                            void* out, float* row_weights, int num_seqs, int num_queries,
+                            int num_heads, int num_kv_heads, int head_dim, int block_size,
+                            int num_blocks, int max_blocks_per_seq, int max_context_len,
+                            pa_dtype dtype, void* workspace, size_t workspace_bytes,
+                            int32_t* error_word, struct CUstream_st* stream);
+
+size_t pa_decode_workspace_size_weights(int num_seqs, int num_queries, int num_heads,
+                                        int head_dim, int max_context_len);
+
+/*
+ * pa_evict -- cuts sequences to a number of rows, for each KV head the rows that were
+ * attended to most. Of the n = context_lens[s] rows of sequence s
+ * k = min(n, keep_lens[s]) stay under each KV head: the first num_sinks and the
+ * last num_recent rows, and of the others those with the largest row_weights (of
+ * equal ones those with the lowest index; NaN counts as -infinity). The rows
+ * that stay move, in their order, to rows 0 .. k - 1 of out_tables, with their
+ * row_weights and, for INT8 and INT4 caches, their scales or pairs; bit copies.
+ * lens_out[s] = k. Rows of the pool that no kept row moves to are left as they are.
+ *
+ * out_tables: int32 [num_seqs][max_blocks_per_seq]. block_tables itself (or equal
+ *   entries): in place. Else each entry is that of block_tables at the same place,
+ *   or a block that holds no row of the batch's sequences and stands nowhere else in
+ *   out_tables: sequences that share blocks with others move into blocks of their
+ *   own. Entries past ceil(k / block_size) are not read.
+ * lens_out: int32 [num_seqs], may be context_lens itself.
+ * k_cache, v_cache: pools of dtype as the decode calls take them; k_params,
+ *   v_params: 4 bytes per row and KV head [num_blocks][num_kv_heads][block_size]
+ *   (the fp32 scales of an INT8 cache, the bf16 pairs of an INT4 cache), null for the
+ *   other types. row_weights as in pa_decode_weights.
+ * max_context_len: an upper bound on every context_lens[s], at most
+ *   max_blocks_per_seq * block_size.
+ * A context length outside [0, max_context_len], keep_lens[s] < 0 or
+ * keep_lens[s] < min(n, num_sinks + num_recent) flags PA_DEVERR_CONTEXT, a block
+ * outside the pool PA_DEVERR_BLOCK_ID: lens_out[s] = context_lens[s] then, and
+ * nothing of the sequence moves.
+ * Row bytes (head_dim * element, head_dim / 2 for INT4) a multiple of 16, pools
+ * 16-byte aligned, num_blocks * num_kv_heads * block_size < 2^32 (else
+ * PA_ERR_UNSUPPORTED, alignment PA_ERR_INVALID_ARG). workspace: 16-byte aligned,
+ * pa_evict_workspace_size bytes; as for the decode calls.
+ */
+pa_status pa_evict(void* k_cache, void* v_cache, void* k_params, void* v_params,
+                   float* row_weights, const int32_t* block_tables, const int32_t* context_lens,
+                   const int32_t* keep_lens, const int32_t* out_tables, int32_t* lens_out,
+                   int num_sinks, int num_recent, int num_seqs, int num_kv_heads, int head_dim,
+                   int block_size, int num_blocks, int max_blocks_per_seq, int max_context_len,
+                   pa_dtype dtype, void* workspace, size_t workspace_bytes, int32_t* error_word,
+                   struct CUstream_st* stream);
+
+size_t pa_evict_workspace_size(int num_seqs, int num_kv_heads, int max_context_len);
+
+/*
+ * pa_verify_draft -- verification of drafted tokens against the target's
+ * probabilities, from given random numbers, so that the tokens are distributed as
+ * the target's. Sequence s has d = num_drafts[s] drafted tokens x_0 .. x_{d-1}
+ * (num_drafts null: d = max_drafts); p_i = target_probs[s][i] is the target's
+ * distribution of token i, q_i = draft_probs[s][i] the one that x_i was drawn from.
+ *   Tokens are accepted in turn while u_i * q_i(x_i) < p_i(x_i), u = uniforms[s];
+ *   a = the number accepted = num_accepted[s].
+ *   One more token is drawn: the smallest v with
+ *     r(0) + .. + r(v) > u_{max_drafts} * (r(0) + .. + r(V - 1)),
+ *   r = max(p_a - q_a, 0) where x_a was rejected, p_d where all were accepted (p_a
+ *   too where the difference leaves nothing).
+ *   out_tokens[s] = x_0 .. x_{a-1}, the drawn token, then -1.
+ *   lens_out[s] = context_lens[s] - (d - a): the rows of rejected tokens leave the
+ *   cache (context_lens counts the rows of all d; both null: no such output).
+ * draft_probs null: the drafts were not drawn (a lookup), q_i is 1 at x_i and 0
+ * elsewhere. Products, differences and sums keep at least the bits of 64-bit ones:
+ * the fp32 inputs decide, not the order of summation. A NaN or negative r counts as 0.
+ *
+ * target_probs: fp32 [num_seqs][max_drafts + 1][vocab_size], draft_probs: fp32
+ * [num_seqs][max_drafts][vocab_size], with any strides (elements) between
+ * sequences and rows; draft_tokens: int32 [num_seqs][max_drafts]; uniforms: fp32
+ * [num_seqs][max_drafts + 1] in [0, 1); out_tokens: int32
+ * [num_seqs][max_drafts + 1]; num_accepted, num_drafts, context_lens, lens_out:
+ * int32 [num_seqs], lens_out may be context_lens. 0 <= max_drafts <= 64.
+ * A drafted token outside [0, vocab_size) among the first d, d outside
+ * [0, max_drafts], or a row p_a without a positive value flags PA_DEVERR_TOKEN,
+ * context_lens[s] < d - a PA_DEVERR_CONTEXT; nothing of that sequence is written.
+ * No workspace.
+ */
+pa_status pa_verify_draft(const float* target_probs, int64_t target_seq_stride,
+                          int64_t target_row_stride, const float* draft_probs,
+                          int64_t draft_seq_stride, int64_t draft_row_stride,
+                          const int32_t* draft_tokens, const int32_t* num_drafts,
+                          const float* uniforms, int32_t* out_tokens, int32_t* num_accepted,
+                          const int32_t* context_lens, int32_t* lens_out, int num_seqs,
+                          int max_drafts, int vocab_size, int32_t* error_word,
+                          struct CUstream_st* stream);
 
 /* Human-readable name of a status. Never NULL. */
 const char* pa_status_string(pa_status status);

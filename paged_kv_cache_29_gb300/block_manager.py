@@ -73,6 +73,7 @@ class BlockManager:
         self._cached: dict[bytes, int] = {}         # key of a full block -> block id
         self._tables: dict[str, list[int]] = {}
         self._salts: dict[str, str] = {}
+        self._evicted: set[str] = set()             # sequences whose rows are no longer their tokens' in order
 
     # ---- queries -------------------------------------------------------
     @property
@@ -104,12 +105,9 @@ class BlockManager:
         if not self._free:
             raise OutOfBlocks("out of KV blocks: preempt a sequence")
         block, _ = self._free.popitem(last=False)
-        key = self._key[block]
-        if key is not None and self._cached.get(key) == block:
-            del self._cached[key]          # reuse evicts the prefix the block held
+        self._forget_key(block)            # reuse evicts the prefix the block held
         self._refs[block] = 1
         self._tokens[block] = list(tokens)
-        self._key[block] = None
         return block
 
     def _seal_if_full(self, block: int, parent: Optional[bytes], salt: str) -> None:
@@ -117,6 +115,12 @@ class BlockManager:
             key = _chain_key(parent, self._tokens[block], salt)
             self._key[block] = key
             self._cached.setdefault(key, block)
+
+    def _forget_key(self, block: int) -> None:
+        key = self._key[block]
+        if key is not None and self._cached.get(key) == block:
+            del self._cached[key]
+        self._key[block] = None
 
     def _parent_key(self, table: list[int], index: int) -> Optional[bytes]:
         return self._key[table[index - 1]] if index > 0 else None
@@ -172,7 +176,8 @@ class BlockManager:
             cow = (shared, private)
         last = table[-1]
         self._tokens[last].append(int(token))
-        self._seal_if_full(last, self._parent_key(table, len(table) - 1), salt)
+        if seq not in self._evicted:
+            self._seal_if_full(last, self._parent_key(table, len(table) - 1), salt)
         return AppendResult(last * self.block_size + len(self._tokens[last]) - 1, cow)
 
     def fork(self, seq: str, child: str) -> None:
@@ -184,12 +189,71 @@ class BlockManager:
             self._refs[b] += 1
         self._tables[child] = list(table)
         self._salts[child] = self._salts[seq]
+        if seq in self._evicted:
+            self._evicted.add(child)
 
     def release(self, seq: str) -> None:
         """Drop a finished sequence; blocks whose count reaches zero join the
         free queue's tail, last block first, and stay reusable by key."""
         self._drop(self._tables.pop(seq))
         self._salts.pop(seq, None)
+        self._evicted.discard(seq)
+
+    def truncate(self, seq: str, num_tokens: int) -> Optional[tuple[int, int]]:
+        """Take back the last tokens of ``seq`` (rejected drafts: pa_verify_draft's
+        lens_out) so that ``num_tokens`` are left. A block that is cut loses its key;
+        where other sequences share it, it is replaced by a private copy, and the
+        (source, destination) pair to copy before the next append is returned."""
+        table = self._tables[seq]
+        if not 0 <= num_tokens <= self.num_tokens(seq):
+            raise ValueError(f"sequence {seq!r} holds {self.num_tokens(seq)} tokens, not {num_tokens} or more")
+        keep = -(-num_tokens // self.block_size)
+        left = num_tokens - (keep - 1) * self.block_size       # tokens in the last block
+        last = table[keep - 1] if keep else -1
+        cut = keep > 0 and left < len(self._tokens[last])
+        gone = table[keep:]
+        if cut and self._refs[last] > 1 and not self._free and all(self._refs[b] > 1 for b in gone):
+            raise OutOfBlocks("out of KV blocks: preempt a sequence")
+        del table[keep:]
+        self._drop(gone)
+        if not cut:
+            return None
+        if self._refs[last] > 1:
+            private = self._allocate(self._tokens[last][:left])
+            self._refs[last] -= 1
+            table[-1] = private
+            return (last, private)
+        del self._tokens[last][left:]
+        self._forget_key(last)
+        return None
+
+    def evict(self, rows: dict[str, int]) -> dict[str, list[int]]:
+        """Cut each sequence to ``rows[seq]`` rows whose places pa_evict chooses:
+        returns the block tables to give it as out_tables, and takes them as the
+        sequences' own. A block that a sequence has to itself stays its place; a shared
+        one is replaced by a fresh one, which is no block that any of them held. Which
+        tokens the rows hold is known to the device alone, so the blocks lose their
+        keys and the sequences no longer enter the prefix cache."""
+        for seq, n in rows.items():
+            if not 0 <= n <= self.num_tokens(seq):
+                raise ValueError(f"sequence {seq!r} holds {self.num_tokens(seq)} rows, not {n} or more")
+        bs = self.block_size
+        keep = {seq: -(-n // bs) for seq, n in rows.items()}
+        fresh = sum(self._refs[b] > 1 for seq in rows for b in self._tables[seq][:keep[seq]])
+        if fresh > len(self._free):
+            raise OutOfBlocks("out of KV blocks: preempt a sequence")
+        # Decided before a reference changes: a block that two of them share is fresh for both.
+        out = {seq: [self._allocate([]) if self._refs[b] > 1 else b for b in self._tables[seq][:keep[seq]]]
+               for seq in rows}
+        for seq, n in rows.items():
+            own = set(out[seq])
+            self._drop([b for b in self._tables[seq] if b not in own])
+            for i, b in enumerate(out[seq]):
+                self._tokens[b] = [None] * min(bs, n - i * bs)
+                self._forget_key(b)
+            self._tables[seq] = list(out[seq])
+            self._evicted.add(seq)
+        return out
 
     def _drop(self, table: list[int]) -> None:
         for b in reversed(table):

@@ -13,7 +13,7 @@ namespace {
 
 using pa::DecodeParams;
 
-constexpr int kVersion = 10200;   // 1.2.0
+constexpr int kVersion = 10300;   // 1.3.0
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr size_t kMaxDynamicSmem = 227 * 1024;
 
@@ -44,33 +44,6 @@ bool valid_dtype(pa_dtype d) { return d == PA_DTYPE_F32 || d == PA_DTYPE_BF16; }
 // plain row copies leave it out).
 bool valid_cache_dtype(pa_dtype d) { return valid_dtype(d) || d == PA_DTYPE_FP8_E4M3; }
 bool valid_decode_cache_dtype(pa_dtype d) { return valid_cache_dtype(d) || d == PA_DTYPE_INT8; }
-
-// The pool viewed as a 3D tensor for TMA: x = element within a 128-byte
-// column half of a row, y = row (rows = blocks * kv_heads * block_size, stride
-// one row), z = which 128-byte half (stride 128 bytes). One box {128 B, 16
-// rows, all halves} is one 16-row tile of one (block, KV head), landing in
-// shared memory as [half][row][128 B] with the 128-byte swizzle.
-pa_status make_pool_map(CUtensorMap* map, const void* base, pa_dtype dtype, int head_dim,
-                        long long rows) {
-    EncodeTiledFn fn = encode_tiled();
-    if (fn == nullptr) return PA_ERR_CUDA;
-    const int es = elem_bytes(dtype);
-    const int row_bytes = head_dim * es;
-    const int halves = row_bytes / 128;
-    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(128 / es), static_cast<cuuint64_t>(rows),
-                                static_cast<cuuint64_t>(halves)};
-    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(row_bytes), 128};
-    const cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / es), 16u, static_cast<cuuint32_t>(halves)};
-    const cuuint32_t estr[3] = {1u, 1u, 1u};
-    const CUresult r = fn(map,
-                          dtype == PA_DTYPE_BF16   ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                          : dtype == PA_DTYPE_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
-                                                  : CU_TENSOR_MAP_DATA_TYPE_UINT8,
-                          3, const_cast<void*>(base), dims, strides, box, estr,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? PA_OK : PA_ERR_CUDA;
-}
 
 long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 
@@ -255,19 +228,11 @@ pa_status decode_call(const void* q, const void* k_cache, const void* v_cache,
     CUtensorMap tk, tv;
     int sm_count = 0;
     if (kernel != PA_KERNEL_GENERIC) {
-        pa_status ps = make_pool_map(&tk, k_cache, dtype, head_dim, rows);
-        if (ps == PA_OK) ps = make_pool_map(&tv, v_cache, dtype, head_dim, rows);
+        pa_status ps = pa::make_pool_map(&tk, k_cache, dtype, head_dim, rows);
+        if (ps == PA_OK) ps = pa::make_pool_map(&tv, v_cache, dtype, head_dim, rows);
         if (ps != PA_OK) return ps;
-        static std::atomic<int> cached_sms[pa::kMaxDevices];
-        int dev = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess) return PA_ERR_CUDA;
-        sm_count = dev < pa::kMaxDevices ? cached_sms[dev].load(std::memory_order_relaxed) : 0;
-        if (sm_count <= 0) {
-            if (cudaDeviceGetAttribute(&sm_count, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-                sm_count <= 0)
-                return PA_ERR_CUDA;
-            if (dev < pa::kMaxDevices) cached_sms[dev].store(sm_count, std::memory_order_relaxed);
-        }
+        sm_count = pa::device_sms();
+        if (sm_count <= 0) return PA_ERR_CUDA;
     }
     const size_t es = static_cast<size_t>(elem_bytes(act_dtype));   // q, out and new rows
     // Batches above kPlanMaxSeqs sequences run as consecutive launches over
@@ -309,6 +274,44 @@ pa_status decode_call(const void* q, const void* k_cache, const void* v_cache,
 }
 
 }  // namespace
+
+// The pool viewed as a 3D tensor for TMA: x = element within a 128-byte
+// column half of a row, y = row (rows = blocks * kv_heads * block_size, stride
+// one row), z = which 128-byte half (stride 128 bytes). One box {128 B, 16
+// rows, all halves} is one 16-row tile of one (block, KV head), landing in
+// shared memory as [half][row][128 B] with the 128-byte swizzle.
+pa_status pa::make_pool_map(CUtensorMap* map, const void* base, pa_dtype dtype, int head_dim,
+                            long long rows) {
+    EncodeTiledFn fn = encode_tiled();
+    if (fn == nullptr) return PA_ERR_CUDA;
+    const int es = elem_bytes(dtype);
+    const int row_bytes = head_dim * es;
+    const int halves = row_bytes / 128;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(128 / es), static_cast<cuuint64_t>(rows),
+                                static_cast<cuuint64_t>(halves)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(row_bytes), 128};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / es), 16u, static_cast<cuuint32_t>(halves)};
+    const cuuint32_t estr[3] = {1u, 1u, 1u};
+    const CUresult r = fn(map,
+                          dtype == PA_DTYPE_BF16   ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                          : dtype == PA_DTYPE_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                                  : CU_TENSOR_MAP_DATA_TYPE_UINT8,
+                          3, const_cast<void*>(base), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? PA_OK : PA_ERR_CUDA;
+}
+
+int pa::device_sms() {
+    static std::atomic<int> cached[kMaxDevices];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    int sms = dev < kMaxDevices ? cached[dev].load(std::memory_order_relaxed) : 0;
+    if (sms > 0) return sms;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) return 0;
+    if (dev < kMaxDevices) cached[dev].store(sms, std::memory_order_relaxed);
+    return sms;
+}
 
 extern "C" {
 

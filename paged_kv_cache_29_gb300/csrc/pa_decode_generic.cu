@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(kCombineMaxWarps * 32) combine_kernel(const De
     // (0, 0) always waits, so that this grid never completes before the
     // decode kernel does.
     const int n = __ldg(p.context_lens + s);
-    const int span = n - seq_row_base(n, p.window);       // rows of the partitions
+    const int span = n - seq_gap(p, n);                   // rows of the partitions
     const int P = seq_partition(p, span);
     const bool merge = n <= p.context_cap && n >= p.num_queries &&
                        span > P + p.partition_tail;           // else flagged or one partition

@@ -1,0 +1,251 @@
+// pa_decode_rows.cu -- pa_decode_sinks and pa_decode_weights beside the tile
+// ring: the plain decode kernel for the shapes that the ring has no instance
+// for, and the kernel that turns the scores of pa_decode_weights into row weights.
+//
+// A query token j of a sequence of n rows sits at row r = n - Q + j. With a window it
+// sees the rows i <= r with i < num_sinks or i > r - window (p.window counts the
+// rows of all Q tokens, window + Q - 1). Partitions cover the rows that some token
+// may see: the first rows, then those from the window's tile on, without the rows
+// between them (seq_gap).
+#include "pa_common.cuh"
+#include "pa_internal.h"
+
+namespace pa {
+
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kCols = 8;              // query columns that the plain kernel takes at a time
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    return v;
+}
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+    return v;
+}
+
+// The plain kernel: one CTA per (sequence, KV head, partition), the scores of up
+// to kCols query columns (a query token's head of the group each) at a time in shared
+// memory. Rows that a column does not see are left out of its sums, whatever they hold.
+// Not tuned.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) decode_rows_kernel(const DecodeParams p) {
+    using E = ElemTraits<T>;
+    extern __shared__ float sm[];
+    const int D = p.head_dim, PS = p.partition_size;
+    float* qf = sm;                           // [kCols][D]
+    float* sc = qf + kCols * D;               // [kCols][PS]; -1 in place of the weight of an unseen row
+    float* red = sc + kCols * PS;             // [kCols][2]: max, sum
+    long long* rows = reinterpret_cast<long long*>(red + 2 * kCols);   // [PS] pool row of each row
+    __shared__ int bad;
+
+    const int bh = p.num_seqs * p.num_kv_heads;
+    const int part = blockIdx.x / bh;
+    const int rem = blockIdx.x - part * bh;
+    const int s = rem / p.num_kv_heads;
+    const int h = rem - s * p.num_kv_heads;
+    const int Q = p.num_queries;
+    const int grp = p.num_heads / p.num_kv_heads;
+    const int n = __ldg(p.context_lens + s);
+    if (n < 0 || n > p.context_cap || (n > 0 && n < Q)) {
+        if (threadIdx.x == 0 && part == 0 && h == 0) raise_error(p.error_word, PA_DEVERR_CONTEXT);
+        return;
+    }
+    // Query column c: token c / grp, head h * grp + c % grp.
+    const int cols = grp * Q;
+    auto out_row = [&](int c) {
+        return (static_cast<size_t>(s) * Q + c / grp) * p.num_heads + h * grp + c % grp;
+    };
+    if (n == 0) {
+        if (part == 0)
+            for (int i = threadIdx.x; i < cols * D; i += kThreads)
+                E::store(static_cast<T*>(p.out) + out_row(i / D) * D + i % D, 0.f);
+        return;
+    }
+    const int gap = seq_gap(p, n), head = sink_rows(p);
+    const int span = n - gap;
+    const int lo = part * PS;
+    if (lo >= span) return;
+    const int len = min(span - lo, PS);
+    const int nparts = (span + PS - 1) / PS;
+    const int bs = p.block_size;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    auto row_at = [&](int i) {                // the sequence's row of the partition's row i
+        const int v = lo + i;
+        return gap > 0 && v >= head ? v + gap : v;
+    };
+
+    if (threadIdx.x == 0) bad = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < len; i += kThreads) {
+        const int r = row_at(i);
+        const int id = __ldg(p.block_tables + static_cast<size_t>(s) * p.max_blocks_per_seq + r / bs);
+        if (id < 0 || id >= p.num_blocks) bad = 1;
+        rows[i] = (static_cast<long long>(id) * p.num_kv_heads + h) * bs + r % bs;
+    }
+    __syncthreads();
+    if (bad) {
+        if (threadIdx.x == 0) raise_error(p.error_word, PA_DEVERR_BLOCK_ID);
+        return;
+    }
+    const T* kc = static_cast<const T*>(p.k_cache);
+    const T* vc = static_cast<const T*>(p.v_cache);
+    const int window = p.window > 0 ? p.window - Q + 1 : 0;   // of one token
+    auto sees = [&](int c, int r) {
+        const int last = n - Q + c / grp;
+        return r <= last && (window == 0 || r < p.num_sinks || r > last - window);
+    };
+    for (int c0 = 0; c0 < cols; c0 += kCols) {
+        const int nc = min(kCols, cols - c0);
+        for (int i = threadIdx.x; i < nc * D; i += kThreads)
+            qf[i] = E::load(static_cast<const T*>(p.q) + out_row(c0 + i / D) * D + i % D) * p.scale_log2;
+        __syncthreads();
+        for (int i = warp; i < len; i += kThreads / 32) {
+            const T* krow = kc + rows[i] * D;
+            const int r = row_at(i);
+            for (int c = 0; c < nc; ++c) {
+                float acc = 0.f;
+                for (int d = lane; d < D; d += 32) acc = fmaf(qf[c * D + d], E::load(krow + d), acc);
+                acc = warp_sum(acc);
+                if (!sees(c0 + c, r)) acc = -INFINITY;
+                if (lane == 0) {
+                    sc[c * PS + i] = acc;
+                    if (p.scores != nullptr)
+                        p.scores[((static_cast<size_t>(s) * p.num_kv_heads + h) * p.score_rows + r) * cols + c0 + c] = acc;
+                }
+            }
+        }
+        __syncthreads();
+        for (int c = warp; c < nc; c += kThreads / 32) {
+            float mx = -INFINITY;
+            for (int i = lane; i < len; i += 32) mx = fmaxf(mx, sc[c * PS + i]);
+            mx = warp_max(mx);
+            const float ref = mx == -INFINITY ? 0.f : mx;
+            float sum = 0.f;
+            for (int i = lane; i < len; i += 32) {
+                const bool see = sees(c0 + c, row_at(i));
+                const float e = see ? fast_exp2(sc[c * PS + i] - ref) : 0.f;
+                sc[c * PS + i] = see ? e : -1.f;
+                sum += e;
+            }
+            sum = warp_sum(sum);
+            if (lane == 0) {
+                red[2 * c] = mx;
+                red[2 * c + 1] = sum;
+            }
+        }
+        __syncthreads();
+        for (int idx = threadIdx.x; idx < nc * D; idx += kThreads) {
+            const int c = idx / D, d = idx - c * D;
+            float acc = 0.f;
+            for (int i = 0; i < len; ++i) {
+                const float w = sc[c * PS + i];
+                if (!(w < 0.f)) acc = fmaf(w, E::load(vc + rows[i] * D + d), acc);
+            }
+            const size_t row = out_row(c0 + c);
+            const size_t slot = row * p.max_parts + part;
+            if (nparts == 1)
+                E::store(static_cast<T*>(p.out) + row * D + d, acc / red[2 * c + 1]);
+            else
+                p.part_o[slot * D + d] = acc;
+            if (d == 0 && (nparts > 1 || p.scores != nullptr)) {
+                p.part_ml[2 * slot] = red[2 * c];
+                p.part_ml[2 * slot + 1] = red[2 * c + 1];
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// Row weights: a CTA per (sequence, KV head, kChunk rows) takes the final maximum and
+// sum of every query column from the partitions' states, then for each row
+//   w = sum_c 2^(score_c - M_c) / L_c,
+// stored for the rows of this call's tokens, added for the others (atomically:
+// sequences may share a block).
+constexpr int kWeightThreads = 256;
+constexpr int kChunk = 1024;
+
+__global__ void __launch_bounds__(kWeightThreads) row_weights_kernel(const DecodeParams p) {
+    extern __shared__ float ml[];             // [cols][2]: M, 1 / L
+    __shared__ int bad;
+    const int chunk = blockIdx.x / (p.num_seqs * p.num_kv_heads);
+    const int sh = blockIdx.x - chunk * (p.num_seqs * p.num_kv_heads);
+    const int s = sh / p.num_kv_heads;
+    const int h = sh - s * p.num_kv_heads;
+    const int Q = p.num_queries;
+    const int n = __ldg(p.context_lens + s);
+    const int i0 = chunk * kChunk;
+    if (n > p.context_cap || n < Q || i0 >= n) return;         // empty, flagged, or past its rows
+    const int grp = p.num_heads / p.num_kv_heads;
+    const int cols = grp * Q;
+    const int P = p.partition_size, nparts = (n + P - 1) / P;
+    const int bs = p.block_size;
+    const int32_t* table = p.block_tables + static_cast<size_t>(s) * p.max_blocks_per_seq;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // A sequence with a block outside the pool (flagged by the decode kernel) keeps its weights.
+    if (threadIdx.x == 0) bad = 0;
+    __syncthreads();
+    for (int b = threadIdx.x; b < (n + bs - 1) / bs; b += kWeightThreads) {
+        const int id = __ldg(table + b);
+        if (id < 0 || id >= p.num_blocks) bad = 1;
+    }
+    for (int c = warp; c < cols; c += kWeightThreads / 32) {
+        const size_t row = (static_cast<size_t>(s) * Q + c / grp) * p.num_heads + h * grp + c % grp;
+        const float* st = p.part_ml + 2 * row * p.max_parts;
+        float M = -INFINITY;
+        for (int i = lane; i < nparts; i += 32) M = fmaxf(M, st[2 * i]);
+        M = warp_max(M);
+        const float ref = M == -INFINITY ? 0.f : M;
+        float L = 0.f;
+        for (int i = lane; i < nparts; i += 32) L += fast_exp2(st[2 * i] - ref) * st[2 * i + 1];
+        L = warp_sum(L);
+        if (lane == 0) {
+            ml[2 * c] = ref;
+            ml[2 * c + 1] = 1.f / L;
+        }
+    }
+    __syncthreads();
+    if (bad) return;
+    const float* sc = p.scores + (static_cast<size_t>(s) * p.num_kv_heads + h) * p.score_rows * cols;
+    for (int i = i0 + threadIdx.x; i < min(n, i0 + kChunk); i += kWeightThreads) {
+        float w = 0.f;
+        for (int c = 0; c < cols; ++c)
+            w = fmaf(fast_exp2(sc[static_cast<size_t>(i) * cols + c] - ml[2 * c]), ml[2 * c + 1], w);
+        float* at = p.row_weights + (static_cast<size_t>(__ldg(table + i / bs)) * p.num_kv_heads + h) * bs + i % bs;
+        if (i >= n - Q)
+            *at = w;
+        else
+            atomicAdd(at, w);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_decode_rows(const DecodeParams& p, pa_dtype dtype, cudaStream_t stream) {
+    const size_t smem = 4 * (static_cast<size_t>(kCols) * (p.head_dim + p.partition_size + 2)) + 8 * static_cast<size_t>(p.partition_size);
+    const long long grid = static_cast<long long>(p.max_parts) * p.num_seqs * p.num_kv_heads;
+    if (grid <= 0) return cudaSuccess;
+    if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    // At most 8 x (256 + 512 + 2) floats and 512 row numbers: within the default limit.
+    if (dtype == PA_DTYPE_BF16)
+        decode_rows_kernel<__nv_bfloat16><<<static_cast<unsigned>(grid), kThreads, smem, stream>>>(p);
+    else
+        decode_rows_kernel<float><<<static_cast<unsigned>(grid), kThreads, smem, stream>>>(p);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_row_weights(const DecodeParams& p, cudaStream_t stream) {
+    if (p.num_seqs == 0 || p.context_cap == 0) return cudaSuccess;
+    const int cols = p.num_heads / p.num_kv_heads * p.num_queries;
+    const long long grid = (static_cast<long long>(p.context_cap) + kChunk - 1) / kChunk * p.num_seqs * p.num_kv_heads;
+    if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    row_weights_kernel<<<static_cast<unsigned>(grid), kWeightThreads, 8 * static_cast<size_t>(cols), stream>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace pa

@@ -40,6 +40,11 @@ struct DecodeParams {
     int num_seqs;
     int num_queries;               // query tokens per sequence, the last rows of each (>= 1)
     int window;                    // sliding window: attend to the last `window` rows (0 = all)
+    int num_sinks;                 // pa_decode_sinks: first rows that stay visible (else 0); `window` then
+                                   //   counts the rows that any of the num_queries tokens' windows holds
+    float* row_weights;            // pa_decode_weights: [num_blocks][num_kv_heads][block_size] (else null),
+    float* scores;                 //   scores [B][Hkv][score_rows][columns], base 2, of every row
+    int score_rows;
     int num_heads;
     int num_kv_heads;
     int head_dim;
@@ -154,6 +159,52 @@ struct NormRopeParams {
 };
 cudaError_t launch_norm_rope(const NormRopeParams& p, pa_dtype dtype, cudaStream_t stream);
 
+// Eviction (pa_evict in the header). moves: for each (sequence, KV head)
+// context_cap pairs of pool rows (from, to), counts how many; new_lens: what
+// lens_out gets.
+struct EvictParams {
+    void* k_cache;
+    void* v_cache;
+    uint32_t* k_params;            // null: no parameters beside the rows
+    uint32_t* v_params;
+    float* row_weights;
+    const int32_t* block_tables;
+    const int32_t* out_tables;
+    const int32_t* context_lens;
+    const int32_t* keep_lens;
+    int32_t* lens_out;
+    uint2* moves;                  // [B][Hkv][context_cap]
+    int32_t* counts;               // [B][Hkv]
+    int32_t* new_lens;             // [B]
+    int32_t* error_word;
+    int num_sinks, num_recent;
+    int num_seqs, num_kv_heads, row_bytes;
+    int block_size, num_blocks, max_blocks_per_seq, context_cap;
+};
+cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream);
+
+// Verification of drafted tokens (pa_verify_draft in the header).
+struct VerifyParams {
+    const float* target;
+    const float* draft;            // null: q_i is 1 at x_i
+    long long target_seq, target_row, draft_seq, draft_row;   // strides, elements
+    const int32_t* tokens;
+    const int32_t* num_drafts;     // null: max_drafts each
+    const float* uniforms;
+    int32_t* out_tokens;
+    int32_t* num_accepted;
+    const int32_t* context_lens;   // null: no lens_out
+    int32_t* lens_out;
+    int32_t* error_word;
+    int num_seqs, max_drafts, vocab;
+};
+cudaError_t launch_verify(const VerifyParams& p, cudaStream_t stream);
+
+// The pool as the tile-ring kernels' TMA copies see it (pa_api.cu).
+pa_status make_pool_map(CUtensorMap* map, const void* base, pa_dtype dtype, int head_dim, long long rows);
+// SMs of the current device, asked for once per device; 0: a CUDA error.
+int device_sms();
+
 // Quantising append into an FP8 cache (new rows fp32 or bf16).
 cudaError_t launch_append_fp8(const void* k_new, const void* v_new, pa_dtype new_dtype,
                               const int64_t* slot_mapping, void* k_cache, void* v_cache,
@@ -166,6 +217,14 @@ constexpr int kPlanMaxSeqs = 4096;   // sequences per persistent decode launch
 // Direct-load kernel for any block size and head dim <= 256.
 cudaError_t launch_decode_generic(const DecodeParams& p, pa_dtype dtype, cudaStream_t stream);
 size_t generic_smem_bytes(int group, int head_dim, int partition_size, int block_size);
+
+// pa_decode_sinks and pa_decode_weights for any block size, group and number of
+// query tokens (head dim <= 256).
+cudaError_t launch_decode_rows(const DecodeParams& p, pa_dtype dtype, cudaStream_t stream);
+
+// Accumulates the row weights of pa_decode_weights from the scores and the
+// partitions' maxima and sums.
+cudaError_t launch_row_weights(const DecodeParams& p, cudaStream_t stream);
 
 // Merge of partition partials for sequences longer than one partition.
 cudaError_t launch_combine(const DecodeParams& p, pa_dtype dtype, cudaStream_t stream);
@@ -184,6 +243,16 @@ __host__ __device__ inline int seq_partition(const DecodeParams& p, int span) {
 // rows base + p * partition_size ..). Depends only on n and W.
 __host__ __device__ inline int seq_row_base(int n, int window) {
     return (window > 0 && n > window) ? ((n - window) / 16) * 16 : 0;
+}
+
+// Rows between the first rows that stay visible (rounded up to whole tiles) and
+// the tile that the window begins in: no partition covers them. The partitions of a
+// sequence count its other rows, n - seq_gap(p, n) of them: row v of those is row v
+// of the sequence below sink_rows(p), else row v + seq_gap(p, n).
+__host__ __device__ inline int sink_rows(const DecodeParams& p) { return (p.num_sinks + 15) / 16 * 16; }
+__host__ __device__ inline int seq_gap(const DecodeParams& p, int n) {
+    const int gap = seq_row_base(n, p.window) - sink_rows(p);
+    return gap > 0 ? gap : 0;
 }
 
 constexpr int kMaxHeadDim = 256;
