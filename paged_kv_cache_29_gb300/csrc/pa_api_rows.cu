@@ -118,6 +118,18 @@ pa_status rows_call(const void* q, const void* k_cache, const void* v_cache, con
     base.partition_long_from = pa::kNoLongPartitions;
     base.max_parts = static_cast<int>(parts);
     const size_t es = dtype == PA_DTYPE_F32 ? 4 : 2;
+    const long long pool_rows = static_cast<long long>(num_blocks) * num_kv_heads * block_size;
+    const bool ring = block_size % 16 == 0 && pool_rows < INT_MAX &&
+                      pa::has_rows_instance(dtype, head_dim, group, num_queries);
+    CUtensorMap tk, tv;
+    int sms = 0;
+    if (ring) {
+        pa_status ps = pa::make_pool_map(&tk, k_cache, dtype, head_dim, pool_rows);
+        if (ps == PA_OK) ps = pa::make_pool_map(&tv, v_cache, dtype, head_dim, pool_rows);
+        if (ps != PA_OK) return ps;
+        sms = pa::device_sms();
+        if (sms <= 0) return PA_ERR_CUDA;
+    }
     // Batches above kPlanMaxSeqs sequences run as consecutive launches over
     // slices of the batch; they reuse the workspace in stream order.
     for (int s0 = 0; s0 < num_seqs; s0 += pa::kPlanMaxSeqs) {
@@ -128,7 +140,10 @@ pa_status rows_call(const void* q, const void* k_cache, const void* v_cache, con
         p.block_tables = block_tables + static_cast<size_t>(s0) * max_blocks_per_seq;
         p.context_lens = context_lens + s0;
         p.num_seqs = num_seqs - s0 < pa::kPlanMaxSeqs ? num_seqs - s0 : pa::kPlanMaxSeqs;
-        if (pa::launch_decode_rows(p, dtype, stream_of(stream)) != cudaSuccess) return PA_ERR_CUDA;
+        const cudaError_t err = !ring     ? pa::launch_decode_rows(p, dtype, stream_of(stream))
+                                : weights ? pa::launch_decode_weights(tk, tv, p, dtype, sms, stream_of(stream))
+                                          : pa::launch_decode_sinks(tk, tv, p, dtype, sms, stream_of(stream));
+        if (err != cudaSuccess) return PA_ERR_CUDA;
         if (parts > 1 && pa::launch_combine(p, dtype, stream_of(stream)) != cudaSuccess) return PA_ERR_CUDA;
         if (weights && pa::launch_row_weights(p, stream_of(stream)) != cudaSuccess) return PA_ERR_CUDA;
     }

@@ -1,0 +1,52 @@
+// pa_decode_rows_ring.cuh -- choice of the tile-ring instance for pa_decode_sinks and
+// pa_decode_weights by head dim and query columns.
+#pragma once
+
+#include "pa_decode_stream.cuh"
+#include "pa_tile_math_rows.cuh"
+
+namespace pa {
+
+namespace {
+constexpr int kWarps = 4;            // consumer warps, ring stages and CTAs per SM as the plain
+constexpr int kStages = 4;           // decode kernels have them (pa_decode_mma.cu, pa_decode_simt.cu)
+constexpr int kMinCtasPerSm = 4;
+
+template <int D, int G, bool SCORES>
+cudaError_t run_mma(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeParams& p, int sm_count,
+                    cudaStream_t stream) {
+    return launch_stream_instance<RowsMmaMath<D, G, SCORES>, D, G, kWarps, kStages, kMinCtasPerSm, false>(
+        tk, tv, p, sm_count, stream);
+}
+
+template <int D, int G, bool SCORES>
+cudaError_t run_simt(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeParams& p, int sm_count,
+                     cudaStream_t stream) {
+    return launch_stream_instance<RowsSimtMath<D, G, SCORES>, D, G, kWarps, kWarps, 1, false>(tk, tv, p, sm_count,
+                                                                                              stream);
+}
+
+template <int D, bool SCORES>
+cudaError_t by_columns(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeParams& p, pa_dtype dtype,
+                       int sm_count, cudaStream_t stream) {
+    const int cols = (p.num_heads / p.num_kv_heads) * p.num_queries;
+    const bool bf16 = dtype == PA_DTYPE_BF16;
+    if (cols <= 1) return bf16 ? run_mma<D, 1, SCORES>(tk, tv, p, sm_count, stream)
+                               : run_simt<D, 1, SCORES>(tk, tv, p, sm_count, stream);
+    if (cols <= 2) return bf16 ? run_mma<D, 2, SCORES>(tk, tv, p, sm_count, stream)
+                               : run_simt<D, 2, SCORES>(tk, tv, p, sm_count, stream);
+    if (cols <= 4) return bf16 ? run_mma<D, 4, SCORES>(tk, tv, p, sm_count, stream)
+                               : run_simt<D, 4, SCORES>(tk, tv, p, sm_count, stream);
+    return bf16 ? run_mma<D, 8, SCORES>(tk, tv, p, sm_count, stream)
+                : run_simt<D, 8, SCORES>(tk, tv, p, sm_count, stream);
+}
+
+template <bool SCORES>
+cudaError_t launch_rows_ring(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeParams& p, pa_dtype dtype,
+                             int sm_count, cudaStream_t stream) {
+    return p.head_dim == 64 ? by_columns<64, SCORES>(tk, tv, p, dtype, sm_count, stream)
+                            : by_columns<128, SCORES>(tk, tv, p, dtype, sm_count, stream);
+}
+}  // namespace
+
+}  // namespace pa

@@ -91,6 +91,7 @@ __device__ __forceinline__ void cp_async_wait_all() {
 // order the plan gives its full partitions. A warp-wide scan of the
 // full-partition counts over the context lengths finds its sequence; a
 // flagged length counts no partition, as in the plan.
+template <bool ROWS>
 __device__ __forceinline__ int4 first_item_by_warp(const DecodeParams& p, int c, int lane) {
     if (p.partition_long != p.partition_size) return make_int4(-1, 0, 0, 0);
     const int Hkv = p.num_kv_heads;
@@ -99,7 +100,7 @@ __device__ __forceinline__ int4 first_item_by_warp(const DecodeParams& p, int c,
     for (int s0 = 0; s0 < p.num_seqs; s0 += 32) {
         const int s = s0 + lane;
         const int n = s < p.num_seqs ? plan_len(p, s, false) : -1;
-        const int nf = n > 0 ? (n - seq_row_base(n, p.window)) / p.partition_size : 0;
+        const int nf = n > 0 ? plan_span<ROWS>(p, n) / p.partition_size : 0;
         int incl = nf;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -215,7 +216,7 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap tmap_k,
     // after the plan barrier completes.
     int total = 0;
     if (warp < W) {
-        total = plan_cta<T, W * 32, 1>(p, c, C, reinterpret_cast<int*>(merge), first_items);
+        total = plan_cta<T, W * 32, 1, Math::kRows>(p, c, C, reinterpret_cast<int*>(merge), first_items);
         named_barrier(1, W * 32);       // every consumer's item writes precede the arrival
         if (threadIdx.x == 0) {
             total_sm[0] = total;
@@ -231,6 +232,20 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap tmap_k,
     const int bs = p.block_size;
     // Rows per partition of the sequence an item belongs to (n rows).
     auto part_rows = [&](int n) { return seq_partition(p, n - seq_row_base(n, p.window)); };
+    // The rows of an item: [lo, hi), numbered within its sequence, or with
+    // Math::kRows within the rows that its partitions cover (seq_gap), of which row v
+    // is row v + gap_from(n, v) of the sequence.
+    auto item_rows = [&](const int4& it, int& lo, int& hi) {
+        if constexpr (Math::kRows) {
+            lo = it.z * p.partition_size;
+            hi = min(it.w - seq_gap(p, it.w), lo + p.partition_size);
+        } else {
+            const int P = part_rows(it.w);
+            lo = seq_row_base(it.w, p.window) + it.z * P;
+            hi = min(it.w, lo + P);
+        }
+    };
+    auto gap_from = [&](int n, int v) { return Math::kRows && v >= sink_rows(p) ? seq_gap(p, n) : 0; };
     const uint32_t ring_addr = smem_addr(ring);
 
     if (warp == W) {
@@ -240,7 +255,7 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap tmap_k,
         // once (they take it from there if the plan gives them the same item,
         // after the completion of every lane's copies and lane 0's note of
         // which item it is).
-        const int4 first = first_item_by_warp(p, c, lane);
+        const int4 first = first_item_by_warp<Math::kRows>(p, c, lane);
         if constexpr (Math::kQInSmem) {
             if (first.x >= 0) {
                 const int grp0 = Math::kCausal ? p.num_heads / p.num_kv_heads : G;
@@ -533,13 +548,22 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap tmap_k,
             // with cp.async one item ahead of their use.
             auto prefetch_ids = [&](const int4& it, int32_t* buf) {
                 if (it.x >= 0) {
-                    const int P = part_rows(it.w);
-                    const int lo = seq_row_base(it.w, p.window) + it.z * P;
-                    const int hi = min(it.w, lo + P);
-                    const int b0 = lo / bs;
-                    const int nblk = (hi - 1) / bs - b0 + 1;
-                    const int32_t* bt = p.block_tables + static_cast<size_t>(it.x) * p.max_blocks_per_seq + b0;
-                    for (int i = lane; i < nblk; i += 32) cp_async_4(smem_addr(buf + i), bt + i);
+                    int lo, hi;
+                    item_rows(it, lo, hi);
+                    const int32_t* bt = p.block_tables + static_cast<size_t>(it.x) * p.max_blocks_per_seq;
+                    if constexpr (Math::kRows) {
+                        // An id per tile (an item's rows may be two runs of the sequence's).
+                        const int ntiles = (hi - lo + kTileRows - 1) / kTileRows;
+                        for (int i = lane; i < ntiles; i += 32) {
+                            const int v = lo + kTileRows * i;
+                            cp_async_4(smem_addr(buf + i), bt + (v + gap_from(it.w, v)) / bs);
+                        }
+                    } else {
+                        const int b0 = lo / bs;
+                        const int nblk = (hi - 1) / bs - b0 + 1;
+                        bt += b0;
+                        for (int i = lane; i < nblk; i += 32) cp_async_4(smem_addr(buf + i), bt + i);
+                    }
                 }
                 cp_async_commit();
             };
@@ -581,21 +605,20 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     cp_async_wait_all();                // the first item's ids, the only group
                 }
                 __syncwarp();
-                const int P = part_rows(cur.w);
-                const int lo = seq_row_base(cur.w, p.window) + cur.z * P;
-                const int hi = min(cur.w, lo + P);
+                int lo, hi;
+                item_rows(cur, lo, hi);
                 const int b0 = lo / bs;
-                const int nblk = (hi - 1) / bs - b0 + 1;
-                bool bad_lane = false;
-                for (int i = lane; i < nblk; i += 32) bad_lane |= (ids[i] < 0) | (ids[i] >= p.num_blocks);
-                const int cur_bad = __any_sync(0xffffffffu, bad_lane) ? 1 : 0;
                 const int ntiles = (hi - lo + kTileRows - 1) / kTileRows;
+                const int nids = Math::kRows ? ntiles : (hi - 1) / bs - b0 + 1;
+                bool bad_lane = false;
+                for (int i = lane; i < nids; i += 32) bad_lane |= (ids[i] < 0) | (ids[i] >= p.num_blocks);
+                const int cur_bad = __any_sync(0xffffffffu, bad_lane) ? 1 : 0;
                 if (cur_bad && lane == 0) raise_error(p.error_word, PA_DEVERR_BLOCK_ID);
                 // Fused append: the item holding the sequence's last row writes
                 // this KV head's new K and V rows into their slot before the
                 // tile that holds them is loaded (the slot must be that row's).
                 const long long new_slot =
-                    (p.k_new != nullptr && hi == cur.w) ? __ldg(p.slot_mapping + cur.x) : -1;
+                    (!Math::kRows && p.k_new != nullptr && hi == cur.w) ? __ldg(p.slot_mapping + cur.x) : -1;
                 const int new_tile = (cur.w - 1 - lo) / kTileRows;
                 // The new rows, 16-byte chunks dealt over the lanes (K, then V),
                 // loaded now and stored when their tile comes up.
@@ -670,8 +693,8 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     // (all 128-byte column halves of 16 rows), issued after lane
                     // 0's expect_tx (ordered by the shuffle above).
                     if (data && lane < 2) {
-                        const int id = ids[tok / bs - b0];
-                        const int row = (id * p.num_kv_heads + cur.y) * bs + (tok % bs);
+                        const int id = ids[Math::kRows ? tt : tok / bs - b0];
+                        const int row = (id * p.num_kv_heads + cur.y) * bs + (tok + gap_from(cur.w, tok)) % bs;
                         const uint32_t dst = ring_addr + stage * Geom::kStageBytes +
                                              (lane ? Geom::kTileBytes : 0);
                         tma_load_3d(dst, lane ? static_cast<const void*>(&tmap_v)
@@ -767,10 +790,8 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap tmap_k,
     int t0 = 0;                 // stream index of the current item's first tile (a multiple of W)
     for (int j = 0; it.x >= 0; ++j) {
         const int s = it.x, h = it.y, part = it.z, n = it.w;
-        const int base = seq_row_base(n, p.window);
-        const int P = seq_partition(p, n - base);
-        const int lo = base + part * P;
-        const int hi = min(n, lo + P);
+        int lo, hi;
+        item_rows(it, lo, hi);
         const int ntiles = (hi - lo + kTileRows - 1) / kTileRows;
         const int4 it_after = item_at(j + 2);
         if constexpr (Math::kQInSmem) {
@@ -784,6 +805,7 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap tmap_k,
             math.begin(p, q_next);
             if (it_next.x >= 0) math.load_q(p, it_next.x, it_next.y, q_next);
         }
+        if constexpr (Math::kRows) math.begin_rows(p, s, h, ncols);
         const int span = ((ntiles + W - 1) / W) * W;   // padded as the producer pads
         const int limit0 = n - Qn;                      // the last row query token 0 sees
         bool bad = false;
@@ -798,8 +820,9 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 if (stage_bad[stage]) {
                     bad = true;
                 } else if (t - t0 < ntiles) {
-                    const int row0 = lo + kTileRows * (t - t0);
+                    int row0 = lo + kTileRows * (t - t0);
                     const int valid = min(kTileRows, hi - row0);
+                    row0 += gap_from(n, row0);
                     const uint32_t kb = ring_addr + stage * Geom::kStageBytes;
                     // Rows of the tile before a sliding window (<= 0: none).
                     const int skip = p.window > 0 ? n - p.window - row0 : 0;
@@ -831,7 +854,8 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap tmap_k,
 #pragma unroll
         for (int w = 0; w < W; ++w) any_bad |= warp_bad[(j & 1) * W + w] != 0;
         // any_bad: flagged by the producer; output left unspecified
-        const int nparts = (n - base + P - 1) / P;
+        const int P = Math::kRows ? p.partition_size : part_rows(n);
+        const int nparts = (plan_span<Math::kRows>(p, n) + P - 1) / P;
         for (int idx = any_bad ? ncols * D : threadIdx.x; idx < ncols * D; idx += W * 32) {
             const int g = idx / D;            // query column
             const int d = idx - g * D;
@@ -852,15 +876,15 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap tmap_k,
             const size_t row = Math::kCausal
                                    ? query_row(p, s, h, g, grp)
                                    : static_cast<size_t>(s) * p.num_heads + h * G + g;
-            if (nparts == 1) {
+            const size_t slot = row * p.max_parts + part;
+            if (nparts == 1)
                 ElemTraits<T>::store(static_cast<T*>(p.out) + row * D + d, O / L);
-            } else {
-                const size_t slot = row * p.max_parts + part;
+            else
                 p.part_o[slot * D + d] = O;
-                if (d == 0) {
-                    p.part_ml[2 * slot] = M;
-                    p.part_ml[2 * slot + 1] = L;
-                }
+            // (pa_decode_weights takes the state of a single partition too.)
+            if (d == 0 && (nparts > 1 || (Math::kRows && p.scores != nullptr))) {
+                p.part_ml[2 * slot] = M;
+                p.part_ml[2 * slot + 1] = L;
             }
         }
         // The next item's warp states overwrite the merge area.

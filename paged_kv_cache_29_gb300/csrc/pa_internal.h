@@ -222,6 +222,13 @@ size_t generic_smem_bytes(int group, int head_dim, int partition_size, int block
 // query tokens (head dim <= 256).
 cudaError_t launch_decode_rows(const DecodeParams& p, pa_dtype dtype, cudaStream_t stream);
 
+// Their tile-ring instances (head dim 64 or 128, block size a multiple of 16).
+cudaError_t launch_decode_sinks(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeParams& p,
+                                pa_dtype dtype, int sm_count, cudaStream_t stream);
+cudaError_t launch_decode_weights(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeParams& p,
+                                  pa_dtype dtype, int sm_count, cudaStream_t stream);
+bool has_rows_instance(pa_dtype dtype, int head_dim, int group, int num_queries);
+
 // Accumulates the row weights of pa_decode_weights from the scores and the
 // partitions' maxima and sums.
 cudaError_t launch_row_weights(const DecodeParams& p, cudaStream_t stream);

@@ -60,6 +60,14 @@ __device__ __forceinline__ void for_own_items(int a, int e, int c, int C, F&& f)
     }
 }
 
+// Rows of the partitions of a sequence of n rows: those from seq_row_base on, or
+// with ROWS (pa_decode_sinks, pa_decode_weights) the first rows too.
+template <bool ROWS>
+__device__ __forceinline__ int plan_span(const DecodeParams& p, int n) {
+    if constexpr (ROWS) return n - seq_gap(p, n);
+    return n - seq_row_base(n, p.window);
+}
+
 // Context length of sequence s, or -1 (flagged) when it is out of range
 // (negative, past max_context_len, or shorter than the query tokens it holds).
 __device__ __forceinline__ int plan_len(const DecodeParams& p, int s, bool flag) {
@@ -121,7 +129,7 @@ __device__ __forceinline__ int block_scan(int v, int* wsum, int* carry) {
 // call it (all of them with BAR = 0, else they meet on named barrier BAR);
 // `sm` holds plan_scratch_ints(NT) ints. Row bytes of the output (num_heads *
 // head_dim * sizeof(T)) are a multiple of 16.
-template <typename T, int NT, int BAR = 0>
+template <typename T, int NT, int BAR = 0, bool ROWS = false>
 __device__ int plan_cta(const DecodeParams& p, int c, int C, int* sm, int4* first) {
     constexpr int NW = NT / 32;
     int* wsum = sm;                          // [NW]
@@ -152,7 +160,7 @@ __device__ int plan_cta(const DecodeParams& p, int c, int C, int* sm, int4* firs
     for (int s0 = 0; s0 < B; s0 += NT) {
         const int s = s0 + tid;
         const int n = s < B ? plan_len(p, s, s % C == c) : -1;
-        const int span = n > 0 ? n - seq_row_base(n, p.window) : 0;   // rows of its partitions
+        const int span = n > 0 ? plan_span<ROWS>(p, n) : 0;   // rows of its partitions
         const int P = seq_partition(p, span);
         const bool lng = P != Pb;
         const int nf = span / P;
@@ -201,7 +209,7 @@ __device__ int plan_cta(const DecodeParams& p, int c, int C, int* sm, int4* firs
     for (int s0 = 0; s0 < B; s0 += NT) {
         const int s = s0 + tid;
         const int n = s < B ? plan_len(p, s, false) : -1;
-        const int span = n > 0 ? n - seq_row_base(n, p.window) : 0;
+        const int span = n > 0 ? plan_span<ROWS>(p, n) : 0;
         const int P = seq_partition(p, span);
         const bool lng = P != Pb;
         const int nf = span / P;

@@ -127,6 +127,7 @@ struct MmaMath {
     using T = __nv_bfloat16;
     static constexpr bool kCausal = CAUSAL;
     static constexpr bool kQuantAppend = false;   // a fused append copies rows as they are
+    static constexpr bool kRows = false;           // items count every row from seq_row_base on
     static constexpr int kExtraStageBytes = 0;
     using Geom = TileGeom<T, D>;
     static constexpr int kSteps = D / 16;
@@ -176,51 +177,27 @@ struct MmaMath {
         l[0] = l[1] = 0.f;
     }
 
-    // valid: rows of the tile before the end of the sequence (V rows past it
-    // are zeroed). Row row0 + i is visible to query column c when row0 + i <=
-    // limit0 + c / grp (limit0: the last row query token 0 sees) and i >= skip
-    // (rows before a sliding window; skip <= 0 without one). A tile always
-    // holds a visible row for one query per sequence.
-    __device__ __forceinline__ void tile(uint32_t kbase, uint32_t vbase, int valid,
-                                         float scale_log2, int lane, int row0, int limit0,
-                                         int grp, int skip, uint32_t /*xb: none*/) {
+    // Scores of the tile's rows, base 2: c0, c1 = (row gid, columns 2t4, 2t4 + 1),
+    // c2, c3 = (row gid + 8, the same columns).
+    __device__ __forceinline__ void qk(uint32_t kbase, float scale_log2, int lane, float (&c)[4]) const {
         const int mi = lane >> 3;
-        const int lr = lane & 7;
-        float c[4] = {0.f, 0.f, 0.f, 0.f};
-        {
-            const int r = lr + ((mi & 1) << 3);
+        const int r = (lane & 7) + ((mi & 1) << 3);
 #pragma unroll
-            for (int kk = 0; kk < kSteps; ++kk) {
-                uint32_t a0, a1, a2, a3;
-                ldsm_x4(swizzled(kbase + (kk >> 2) * kBoxBytes, r, 2 * (kk & 3) + (mi >> 1)),
-                        a0, a1, a2, a3);
-                mma_16816(c, a0, a1, a2, a3, qb[kk][0], qb[kk][1]);
-            }
+        for (int i = 0; i < 4; ++i) c[i] = 0.f;
+#pragma unroll
+        for (int kk = 0; kk < kSteps; ++kk) {
+            uint32_t a0, a1, a2, a3;
+            ldsm_x4(swizzled(kbase + (kk >> 2) * kBoxBytes, r, 2 * (kk & 3) + (mi >> 1)), a0, a1,
+                    a2, a3);
+            mma_16816(c, a0, a1, a2, a3, qb[kk][0], qb[kk][1]);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) c[i] *= scale_log2;
-        if constexpr (CAUSAL) {
-            if (row0 + kTileRows - 1 > limit0) {
-                // Rows past the query token's own row.
-                const int j0 = (2 * t4) / grp, j1 = (2 * t4 + 1) / grp;
-                const int r = row0 + gid;
-                if (r > limit0 + j0) c[0] = -INFINITY;
-                if (r > limit0 + j1) c[1] = -INFINITY;
-                if (r + 8 > limit0 + j0) c[2] = -INFINITY;
-                if (r + 8 > limit0 + j1) c[3] = -INFINITY;
-            }
-        } else {
-            if (valid < kTileRows) {
-                // Rows past the sequence.
-                if (gid >= valid) c[0] = c[1] = -INFINITY;
-                if (gid + 8 >= valid) c[2] = c[3] = -INFINITY;
-            }
-            if (skip > 0) {
-                // Rows before a sliding window.
-                if (gid < skip) c[0] = c[1] = -INFINITY;
-                if (gid + 8 < skip) c[2] = c[3] = -INFINITY;
-            }
-        }
+    }
+
+    // Folds masked scores into the running max and sum (rescaling o), and leaves
+    // the tile's weights P^T as the B operand of the products with V.
+    __device__ __forceinline__ void softmax(const float (&c)[4], uint32_t& b0, uint32_t& b1) {
         float mx0 = fmaxf(c[0], c[2]);
         float mx1 = fmaxf(c[1], c[3]);
 #pragma unroll
@@ -268,33 +245,88 @@ struct MmaMath {
         const uint32_t w0 = __shfl_sync(0xffffffffu, p23, src_a);
         const uint32_t w1 = __shfl_sync(0xffffffffu, p23, src_a + 4);
         const uint32_t sel = (gid & 1) ? 0x7632u : 0x5410u;
-        const uint32_t b0 = prmt(v0, v1, sel);
-        const uint32_t b1 = prmt(w0, w1, sel);
-        const int r = lr + ((mi >> 1) << 3);
-        if (valid == kTileRows) {
+        b0 = prmt(v0, v1, sel);
+        b1 = prmt(w0, w1, sel);
+    }
+
+    // o += P . V of the tile, every row.
+    __device__ __forceinline__ void pv(uint32_t vbase, int lane, uint32_t b0, uint32_t b1) {
+        const int mi = lane >> 3;
+        const int r = (lane & 7) + ((mi >> 1) << 3);
 #pragma unroll
-            for (int mt = 0; mt < kSteps; ++mt) {
-                uint32_t a0, a1, a2, a3;
-                ldsm_x4_trans(
-                    swizzled(vbase + (mt >> 2) * kBoxBytes, r, 2 * (mt & 3) + (mi & 1)), a0, a1,
-                    a2, a3);
-                mma_16816(o[mt], a0, a1, a2, a3, b0, b1);
-            }
-        } else {
-            // Rows past the sequence hold whatever the pool holds (possibly NaN
-            // bit patterns): zero their V values so that 0 * V stays 0.
-            const int tk = 2 * t4;
-            const uint32_t mlo = (tk < valid ? 0x0000ffffu : 0u) | (tk + 1 < valid ? 0xffff0000u : 0u);
-            const uint32_t mhi = (tk + 8 < valid ? 0x0000ffffu : 0u) | (tk + 9 < valid ? 0xffff0000u : 0u);
+        for (int mt = 0; mt < kSteps; ++mt) {
+            uint32_t a0, a1, a2, a3;
+            ldsm_x4_trans(swizzled(vbase + (mt >> 2) * kBoxBytes, r, 2 * (mt & 3) + (mi & 1)), a0,
+                          a1, a2, a3);
+            mma_16816(o[mt], a0, a1, a2, a3, b0, b1);
+        }
+    }
+
+    // The same with V zero outside the rows of `rows` (a bit each), so that 0 * V
+    // stays 0 whatever those hold (possibly NaN bit patterns). SOME: only the lane's
+    // first (own0) and second (own1) column take the sums.
+    template <bool SOME = false>
+    __device__ __forceinline__ void pv_rows(uint32_t vbase, int lane, uint32_t b0, uint32_t b1, uint32_t rows,
+                                            bool own0 = true, bool own1 = true) {
+        const int mi = lane >> 3;
+        const int r = (lane & 7) + ((mi >> 1) << 3);
+        const uint32_t own = rows >> (2 * t4);
+        const uint32_t mlo = (own & 1u ? 0x0000ffffu : 0u) | (own & 2u ? 0xffff0000u : 0u);
+        const uint32_t mhi = (own & 256u ? 0x0000ffffu : 0u) | (own & 512u ? 0xffff0000u : 0u);
 #pragma unroll
-            for (int mt = 0; mt < kSteps; ++mt) {
-                uint32_t a0, a1, a2, a3;
-                ldsm_x4_trans(
-                    swizzled(vbase + (mt >> 2) * kBoxBytes, r, 2 * (mt & 3) + (mi & 1)), a0, a1,
-                    a2, a3);
+        for (int mt = 0; mt < kSteps; ++mt) {
+            uint32_t a0, a1, a2, a3;
+            ldsm_x4_trans(swizzled(vbase + (mt >> 2) * kBoxBytes, r, 2 * (mt & 3) + (mi & 1)), a0,
+                          a1, a2, a3);
+            if constexpr (SOME) {
+                float t[4] = {o[mt][0], o[mt][1], o[mt][2], o[mt][3]};
+                mma_16816(t, a0 & mlo, a1 & mlo, a2 & mhi, a3 & mhi, b0, b1);
+                if (own0) { o[mt][0] = t[0]; o[mt][2] = t[2]; }
+                if (own1) { o[mt][1] = t[1]; o[mt][3] = t[3]; }
+            } else {
                 mma_16816(o[mt], a0 & mlo, a1 & mlo, a2 & mhi, a3 & mhi, b0, b1);
             }
         }
+    }
+
+    // valid: rows of the tile before the end of the sequence (V rows past it
+    // are zeroed). Row row0 + i is visible to query column c when row0 + i <=
+    // limit0 + c / grp (limit0: the last row query token 0 sees) and i >= skip
+    // (rows before a sliding window; skip <= 0 without one). A tile always
+    // holds a visible row for one query per sequence.
+    __device__ __forceinline__ void tile(uint32_t kbase, uint32_t vbase, int valid,
+                                         float scale_log2, int lane, int row0, int limit0,
+                                         int grp, int skip, uint32_t /*xb: none*/) {
+        float c[4];
+        qk(kbase, scale_log2, lane, c);
+        if constexpr (CAUSAL) {
+            if (row0 + kTileRows - 1 > limit0) {
+                // Rows past the query token's own row.
+                const int j0 = (2 * t4) / grp, j1 = (2 * t4 + 1) / grp;
+                const int r = row0 + gid;
+                if (r > limit0 + j0) c[0] = -INFINITY;
+                if (r > limit0 + j1) c[1] = -INFINITY;
+                if (r + 8 > limit0 + j0) c[2] = -INFINITY;
+                if (r + 8 > limit0 + j1) c[3] = -INFINITY;
+            }
+        } else {
+            if (valid < kTileRows) {
+                // Rows past the sequence.
+                if (gid >= valid) c[0] = c[1] = -INFINITY;
+                if (gid + 8 >= valid) c[2] = c[3] = -INFINITY;
+            }
+            if (skip > 0) {
+                // Rows before a sliding window.
+                if (gid < skip) c[0] = c[1] = -INFINITY;
+                if (gid + 8 < skip) c[2] = c[3] = -INFINITY;
+            }
+        }
+        uint32_t b0, b1;
+        softmax(c, b0, b1);
+        if (valid == kTileRows)
+            pv(vbase, lane, b0, b1);
+        else
+            pv_rows(vbase, lane, b0, b1, (1u << valid) - 1u);
     }
 
     // State layout: m[G], l[G], o[G][D] (fp32, base-2 max); columns < ncols.
@@ -332,6 +364,7 @@ struct SimtMath {
     using T = TT;
     static constexpr bool kCausal = false;
     static constexpr bool kQuantAppend = false;   // a fused append copies rows as they are
+    static constexpr bool kRows = false;           // items count every row from seq_row_base on
     static constexpr int kExtraStageBytes = 0;
     using Geom = TileGeom<T, D>;
     using E = ElemTraits<T>;
@@ -408,6 +441,22 @@ struct SimtMath {
                                          float /*scale_log2*/, int /*lane*/, int /*row0*/,
                                          int /*limit0*/, int /*grp*/, int skip,
                                          uint32_t /*xb: none*/) {
+        fold_rows(kbase, vbase, [&](int row) { return row < valid && row >= skip; },
+                  [&](int row) { return row < valid; }, valid < kTileRows || skip > 0, [](int, const float (&)[G]) {});
+    }
+
+    // One query per sequence: the rows of `seen` (a bit each); on_scores(row, the
+    // row's masked scores) in every lane of the row.
+    template <class OnScores>
+    __device__ __forceinline__ void fold(uint32_t kbase, uint32_t vbase, uint32_t seen, OnScores&& on_scores) {
+        auto sees = [&](int row) { return ((seen >> row) & 1u) != 0u; };
+        fold_rows(kbase, vbase, sees, sees, seen != 0xffffu, on_scores);
+    }
+
+    // sees(row): its score counts; reads(row): its V row is read; masked: some are not.
+    template <class Sees, class Reads, class OnScores>
+    __device__ __forceinline__ void fold_rows(uint32_t kbase, uint32_t vbase, Sees&& sees, Reads&& reads, bool masked,
+                                              OnScores&& on_scores) {
         const uint32_t kbox = kbase + (ch >> 3) * kBoxBytes;
         const uint32_t vbox = vbase + (ch >> 3) * kBoxBytes;
         const int cc = ch & 7;
@@ -434,15 +483,17 @@ struct SimtMath {
 #pragma unroll
                     for (int off = 1; off < kLpr; off <<= 1)
                         sc[j][g] += __shfl_xor_sync(0xffffffffu, sc[j][g], off);
-            if (valid < kTileRows || skip > 0) {
+            if (masked) {
 #pragma unroll
                 for (int j = 0; j < kSub; ++j) {
                     const int row = (sub * kSub + j) * kRpp + rr;
-                    if (row >= valid || row < skip)
+                    if (!sees(row))
 #pragma unroll
                         for (int g = 0; g < G; ++g) sc[j][g] = -INFINITY;
                 }
             }
+#pragma unroll
+            for (int j = 0; j < kSub; ++j) on_scores((sub * kSub + j) * kRpp + rr, sc[j]);
 #pragma unroll
             for (int g = 0; g < G; ++g) {
                 float mx = sc[0][g];
@@ -469,7 +520,7 @@ struct SimtMath {
 #pragma unroll
             for (int j = 0; j < kSub; ++j) {
                 const int row = (sub * kSub + j) * kRpp + rr;
-                if (row < valid) {
+                if (reads(row)) {
                     float vv[kEpc];
                     E::unpack(lds128(swizzled(vbox, row, cc)), vv);
 #pragma unroll

@@ -164,6 +164,7 @@ struct QuantMmaMath {
     static constexpr bool kCausal = false;
     // The fused append quantises new rows with Codes::append_row.
     static constexpr bool kQuantAppend = true;
+    static constexpr bool kRows = false;           // items count every row from seq_row_base on
     static_assert(D == 128, "one 128-byte row of codes per token");
     static_assert(G >= 1 && G <= 8, "the MMA N dimension holds at most 8 query heads");
     static constexpr int kSteps = D / 16;
