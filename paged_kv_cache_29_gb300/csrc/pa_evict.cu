@@ -4,23 +4,41 @@
 // the `more` with the largest weights stay under each KV head. Weights become 32-bit
 // keys in their order; a radix selection, eight bits a pass from the top, finds the
 // more-th largest key and how many of the rows that hold just that key stay: the
-// first ones. A walk over the rows in order then numbers the rows that stay, and
-// lists each that changes its place as a pair of pool rows (from, to).
+// first ones. A walk over the rows in order then numbers the rows that stay: the
+// j-th of them moves to row j, and is listed as a pair of pool rows (from, to).
+//
+// A cluster of CTAs shares the rows under one KV head of a sequence. A CTA holds the
+// keys of a run of rows in shared memory, so that the weights are read once; counts by
+// digit, and of rows that stay, are added up through the cluster's shared memory.
 //
 // The list is in the rows' order, to <= from within a sequence: a stretch of the list
 // that was read whole may be written whatever of it stands in its way, and no
 // later stretch reads a row that an earlier one wrote. So rows can move in place, a
-// stretch at a time, as long as all of a stretch's reads come before its writes. Bytes of a
-// row at different offsets never meet: each warp moves one slice of the row under one
-// KV head through the whole list on its own, with no barrier beyond its own.
+// stretch at a time, as long as all of a stretch's reads come before its writes; the reads
+// of later stretches may come before them too. Bytes of a row at different offsets
+// never meet: CTAs move slices of the rows under one KV head through the whole list, with
+// no barrier between them.
+#include <climits>
+
+#include <cooperative_groups.h>
+
 #include "pa_common.cuh"
 #include "pa_internal.h"
+
+namespace cg = cooperative_groups;
 
 namespace pa {
 
 namespace {
 
-constexpr int kSelectThreads = 256;
+constexpr int kSelectThreads = 512;
+constexpr int kSelectWarps = kSelectThreads / 32;
+constexpr int kMaxCluster = 8;
+constexpr int kCopies = 8;                    // of the digit counts: at most 4 lanes meet in one
+constexpr uint32_t kStays = 0xffffffffu;      // key of a row that stays in any case; no weight has it
+// Keys that a CTA holds. Sequences of more rows than a cluster holds read their weights
+// again in every pass.
+constexpr int kMaxKeys = 48 * 1024;
 
 // 32 bits in the order of the weights: NaN as -infinity, -0 as +0.
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -29,14 +47,22 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// One CTA per (sequence, KV head): the list of its rows' moves.
-__global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const EvictParams p) {
-    __shared__ uint32_t hist[256];
-    __shared__ uint32_t warp_sums[kSelectThreads / 32];
+// One cluster per (sequence, KV head): the list of its rows' moves, and from where on rows
+// change their place.
+__global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const EvictParams p, int max_keys) {
+    extern __shared__ uint32_t keys[];        // [max_keys]
+    __shared__ uint32_t hist[256 * kCopies];
+    __shared__ uint32_t digits[2][256];       // this CTA's counts by digit, of two passes
+    __shared__ uint32_t scan_sums[8];
     __shared__ uint32_t found[2];             // digit, rows of larger digits
-    __shared__ int bad;
-    const int s = blockIdx.x / p.num_kv_heads;
-    const int h = blockIdx.x - s * p.num_kv_heads;
+    __shared__ uint2 warp_counts[kSelectWarps];
+    __shared__ uint2 cta_counts;              // rows of the CTA above the border, at it
+    __shared__ int bad, first_move;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int ranks = cluster.num_blocks(), rank = cluster.block_rank();
+    const int sh = blockIdx.x / ranks;
+    const int s = sh / p.num_kv_heads;
+    const int h = sh - s * p.num_kv_heads;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int bs = p.block_size;
     const int n = __ldg(p.context_lens + s);
@@ -46,198 +72,291 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
     const int first = odd ? 0 : min(n, p.num_sinks);             // rows [first, last) may leave
     const int last = odd ? 0 : max(first, n - min(n, p.num_recent));
     const int more = keep - first - (n - last);                  // rows of them that stay
-    const int32_t* from = p.block_tables + static_cast<size_t>(s) * p.max_blocks_per_seq;
-    const int32_t* to = p.out_tables + static_cast<size_t>(s) * p.max_blocks_per_seq;
-    if (tid == 0) bad = 0;
-    __syncthreads();
-    if (!odd && more >= 0) {
-        bool outside = false;
-        for (int b = tid; b < (n + bs - 1) / bs; b += kSelectThreads) {
-            const int id = __ldg(from + b);
-            outside |= id < 0 || id >= p.num_blocks;
-        }
-        for (int b = tid; b < (keep + bs - 1) / bs; b += kSelectThreads) {
-            const int id = __ldg(to + b);
-            outside |= id < 0 || id >= p.num_blocks;
-        }
-        if (outside) bad = 1;
-    }
-    __syncthreads();
-    if (odd || more < 0 || bad) {
-        if (tid == 0) {
+    if (odd || more < 0) {                    // the same in every CTA of the cluster
+        if (tid == 0 && rank == 0) {
             if (h == 0) {
-                raise_error(p.error_word, odd || more < 0 ? PA_DEVERR_CONTEXT : PA_DEVERR_BLOCK_ID);
+                raise_error(p.error_word, PA_DEVERR_CONTEXT);
                 p.new_lens[s] = n;
             }
-            p.counts[blockIdx.x] = 0;
+            p.starts[sh] = INT_MAX;
         }
         return;
     }
-    if (tid == 0 && h == 0) p.new_lens[s] = keep;
-    auto from_row = [&](int i) {
-        return (static_cast<uint32_t>(__ldg(from + i / bs)) * p.num_kv_heads + h) * bs + i % bs;
+    const int32_t* from = p.block_tables + static_cast<size_t>(s) * p.max_blocks_per_seq;
+    const int32_t* to = p.out_tables + static_cast<size_t>(s) * p.max_blocks_per_seq;
+    // This CTA's rows, and this warp's: runs of whole 32s.
+    const int share = ((n + ranks - 1) / ranks + 31) / 32 * 32;
+    const int row0 = min(n, rank * share), row1 = min(n, row0 + share);
+    const int warp_share = ((row1 - row0 + kSelectWarps - 1) / kSelectWarps + 31) / 32 * 32;
+    const int w0 = min(row1, row0 + warp * warp_share), w1 = min(row1, w0 + warp_share);
+    const bool held = share <= max_keys;
+    if (tid == 0) {
+        bad = 0;
+        first_move = INT_MAX;
+    }
+    for (int i = tid; i < 256 * kCopies; i += kSelectThreads) hist[i] = 0;
+    __syncthreads();
+    auto pool_row = [&](int id, int i) { return (static_cast<uint32_t>(id) * p.num_kv_heads + h) * bs + i % bs; };
+    auto load_key = [&](int i) -> uint32_t {  // a row of a block outside the pool: any key
+        const int id = __ldg(from + i / bs);
+        if (id < 0 || id >= p.num_blocks) {
+            bad = 1;
+            return 0u;
+        }
+        return i < first || i >= last ? kStays : weight_key(p.row_weights[pool_row(id, i)]);
     };
-    auto to_row = [&](int i) {
-        return (static_cast<uint32_t>(__ldg(to + i / bs)) * p.num_kv_heads + h) * bs + i % bs;
-    };
-
-    // The more-th largest key, and how many rows that hold it stay.
-    uint32_t border = 0, level = 0;
-    const int m = last - first;
-    if (more == 0) {
-        border = 0xffffffffu;                // no key is that large
-    } else if (more < m) {
-        uint32_t want = more;
-        for (int shift = 24; shift >= 0; shift -= 8) {
-            const uint32_t mask = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
-            hist[tid] = 0;
-            __syncthreads();
-            for (int i = first + tid; i < last; i += kSelectThreads) {
-                const uint32_t key = weight_key(p.row_weights[from_row(i)]);
-                if ((key & mask) == border) atomicAdd(&hist[(key >> shift) & 255u], 1u);
-            }
-            __syncthreads();
-            // Rows of larger digits: an inclusive scan from the top; thread t has digit 255 - t.
-            const uint32_t own = hist[255 - tid];
-            uint32_t incl = own;
+    bool outside = false;
+    for (int b = rank * kSelectThreads + tid; b < (keep + bs - 1) / bs; b += ranks * kSelectThreads) {
+        const int id = __ldg(to + b);
+        outside |= id < 0 || id >= p.num_blocks;
+    }
+    if (outside) bad = 1;
+    if (held) {
+        constexpr int kAhead = 4;             // loads of a thread before their use
+        for (int i0 = row0 + tid; i0 < row1; i0 += kAhead * kSelectThreads) {
+            uint32_t k[kAhead];
 #pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const uint32_t u = __shfl_up_sync(0xffffffffu, incl, off);
-                if (lane >= off) incl += u;
+            for (int u = 0; u < kAhead; ++u) k[u] = i0 + u * kSelectThreads < row1 ? load_key(i0 + u * kSelectThreads) : 0u;
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u)
+                if (i0 + u * kSelectThreads < row1) keys[i0 + u * kSelectThreads - row0] = k[u];
+        }
+    } else {
+        for (int i = row0 + tid; i < row1; i += kSelectThreads) (void)load_key(i);
+    }
+    cluster.sync();
+    bool any_bad = false;
+    for (int r = 0; r < ranks; ++r) any_bad |= *cluster.map_shared_rank(&bad, r) != 0;
+    if (any_bad) {
+        if (tid == 0 && rank == 0) {
+            if (h == 0) {
+                raise_error(p.error_word, PA_DEVERR_BLOCK_ID);
+                p.new_lens[s] = n;
             }
-            if (lane == 31) warp_sums[warp] = incl;
+            p.starts[sh] = INT_MAX;
+        }
+        cluster.sync();                       // every CTA has read the others' flags
+        return;
+    }
+    auto key_at = [&](int i) { return held ? keys[i - row0] : load_key(i); };
+
+    // The more-th largest key of [first, last), and how many rows that hold it stay.
+    uint32_t border = 0, level = 0;
+    if (more == 0) {
+        border = kStays - 1;                  // no weight's key is that large
+    } else if (more < last - first) {
+        uint32_t want = more;
+        for (int pass = 0; pass < 4; ++pass) {
+            const int shift = 24 - 8 * pass;
+            const uint32_t mask = pass == 0 ? 0u : 0xffffffffu << (shift + 8);
+            for (int i = row0 + tid; i < row1; i += kSelectThreads) {
+                const uint32_t key = key_at(i);
+                if (key != kStays && (key & mask) == border)
+                    atomicAdd(&hist[((key >> shift) & 255u) * kCopies + (lane & (kCopies - 1))], 1u);
+            }
             __syncthreads();
-            for (int w = 0; w < warp; ++w) incl += warp_sums[w];
-            if (incl >= want && incl - own < want) {
-                found[0] = 255 - tid;
-                found[1] = incl - own;
+            if (tid < 256) {
+                uint32_t sum = 0;
+#pragma unroll
+                for (int c = 0; c < kCopies; ++c) {
+                    sum += hist[tid * kCopies + c];
+                    hist[tid * kCopies + c] = 0;
+                }
+                digits[pass & 1][tid] = sum;
+            }
+            // (The other CTAs read digits[pass & 1]; it is written again two passes on,
+            // behind the next pass's barrier.)
+            cluster.sync();
+            uint32_t own = 0, incl = 0;
+            if (tid < 256) {
+                // Rows of larger digits: an inclusive scan from the top; thread t has digit 255 - t.
+                for (int r = 0; r < ranks; ++r) own += cluster.map_shared_rank(&digits[pass & 1][0], r)[255 - tid];
+                incl = own;
+#pragma unroll
+                for (int off = 1; off < 32; off <<= 1) {
+                    const uint32_t u = __shfl_up_sync(0xffffffffu, incl, off);
+                    if (lane >= off) incl += u;
+                }
+                if (lane == 31) scan_sums[warp] = incl;
+            }
+            __syncthreads();
+            if (tid < 256) {
+                for (int w = 0; w < warp; ++w) incl += scan_sums[w];
+                if (incl >= want && incl - own < want) {
+                    found[0] = 255 - tid;
+                    found[1] = incl - own;
+                }
             }
             __syncthreads();
             border |= found[0] << shift;
             want -= found[1];
         }
         level = want;
-    }                                        // else all stay: every key is above 0
+    }                                         // else all stay: every key is above 0
 
-    // Number the rows that stay, in order, and list those that change their place.
-    uint2* list = p.moves + static_cast<size_t>(blockIdx.x) * p.context_cap;
-    uint32_t above0 = 0, equal0 = 0, listed0 = 0;   // rows before this stretch: larger, equal, listed
-    for (int i0 = 0; i0 < n; i0 += kSelectThreads) {
-        const int i = i0 + tid;
-        bool above = false, equal = false;
-        if (i < n) {
-            if (i < first || i >= last) {
-                above = true;
-            } else {
-                const uint32_t key = weight_key(p.row_weights[from_row(i)]);
-                above = key > border;
-                equal = key == border;
-            }
-        }
-        const uint32_t below = (1u << lane) - 1u;
-        const uint32_t va = __ballot_sync(0xffffffffu, above), ve = __ballot_sync(0xffffffffu, equal);
-        __syncthreads();
-        if (lane == 0) warp_sums[warp] = __popc(va) | (__popc(ve) << 16);
-        __syncthreads();
-        uint32_t a = above0 + __popc(va & below), e = equal0 + __popc(ve & below);
-        uint32_t ta = 0, te = 0;
-        for (int w = 0; w < kSelectThreads / 32; ++w) {
-            const uint32_t v = warp_sums[w];
-            if (w < warp) {
-                a += v & 0xffffu;
-                e += v >> 16;
-            }
-            ta += v & 0xffffu;
-            te += v >> 16;
-        }
-        const bool stays = above || (equal && e < level);
-        uint32_t src = 0, dst = 0;
-        if (stays) {
-            src = from_row(i);
-            dst = to_row(a + min(e, level));
-        }
-        const bool moves = stays && src != dst;
-        const uint32_t vm = __ballot_sync(0xffffffffu, moves);
-        __syncthreads();
-        if (lane == 0) warp_sums[warp] = __popc(vm);
-        __syncthreads();
-        uint32_t at = listed0 + __popc(vm & below), tm = 0;
-        for (int w = 0; w < kSelectThreads / 32; ++w) {
-            if (w < warp) at += warp_sums[w];
-            tm += warp_sums[w];
-        }
-        if (moves) list[at] = make_uint2(src, dst);
-        above0 += ta;
-        equal0 += te;
-        listed0 += tm;
+    // Rows above the border and at it, by warp, CTA and cluster.
+    uint32_t above = 0, equal = 0;
+    for (int i = w0 + lane; i - lane < w1; i += 32) {
+        const uint32_t key = i < w1 ? key_at(i) : 0u;
+        above += __popc(__ballot_sync(0xffffffffu, i < w1 && key > border));
+        equal += __popc(__ballot_sync(0xffffffffu, i < w1 && key == border));
     }
-    if (tid == 0) p.counts[blockIdx.x] = listed0;
+    if (lane == 0) warp_counts[warp] = make_uint2(above, equal);
+    __syncthreads();
+    above = equal = 0;                        // now: before this warp's rows
+    uint2 all = make_uint2(0, 0);
+    for (int w = 0; w < kSelectWarps; ++w) {
+        const uint2 c = warp_counts[w];
+        if (w < warp) {
+            above += c.x;
+            equal += c.y;
+        }
+        all.x += c.x;
+        all.y += c.y;
+    }
+    if (tid == 0) cta_counts = all;
+    cluster.sync();
+    for (int r = 0; r < rank; ++r) {
+        const uint2 c = *cluster.map_shared_rank(&cta_counts, r);
+        above += c.x;
+        equal += c.y;
+    }
+    uint2* list = p.moves + static_cast<size_t>(sh) * p.context_cap;
+    int moved = INT_MAX;
+    for (int i = w0 + lane; i - lane < w1; i += 32) {
+        const uint32_t key = i < w1 ? key_at(i) : 0u;
+        const uint32_t va = __ballot_sync(0xffffffffu, i < w1 && key > border);
+        const uint32_t ve = __ballot_sync(0xffffffffu, i < w1 && key == border);
+        const uint32_t before = (1u << lane) - 1u;
+        const uint32_t e = equal + __popc(ve & before);
+        if (i < w1 && (key > border || (key == border && e < level))) {
+            const int j = above + __popc(va & before) + min(e, level);
+            const uint32_t src = pool_row(__ldg(from + i / bs), i), dst = pool_row(__ldg(to + j / bs), j);
+            list[j] = make_uint2(src, dst);
+            if (src != dst) moved = min(moved, j);
+        }
+        above += __popc(va);
+        equal += __popc(ve);
+    }
+    moved = __reduce_min_sync(0xffffffffu, moved);
+    if (lane == 0 && moved != INT_MAX) atomicMin(&first_move, moved);
+    cluster.sync();
+    if (rank == 0 && tid == 0) {
+        int start = INT_MAX;
+        for (int r = 0; r < ranks; ++r) start = min(start, *cluster.map_shared_rank(&first_move, r));
+        p.starts[sh] = start;
+        if (h == 0) p.new_lens[s] = keep;
+    }
+    cluster.sync();                           // no CTA ends before rank 0 has read it
 }
 
-// Moves. A warp per (sequence, KV head, slice): slices 0 .. 2 kSlices - 1 are parts of
-// the K and V rows, the ones after them the 4-byte values beside the rows.
-constexpr int kMoveThreads = 128;
-constexpr int kBatch = 8;                     // loads of a lane before their stores
+// Moves: a CTA of WARPS warps per (sequence, KV head, slice). Slices 0 .. 2 slices - 1 are
+// parts of the K and V rows, of `lanes` 16-byte pieces, the ones after them the 4-byte
+// values beside the rows.
+constexpr int kBatch = 8;                     // rows of a lane per stretch
 
-template <typename T>
-__device__ __forceinline__ void move_values(T* base, const uint2* list, int count, int lanes, int lane, size_t pitch) {
-    // `lanes` lanes share a row, 32 / lanes rows at a time; pitch: elements of T per row.
-    const int sub = lane % lanes, per = 32 / lanes;
-    for (int j0 = 0; j0 < count; j0 += per * kBatch) {
-        T v[kBatch];
-        uint32_t dst[kBatch];
+// lanes: lanes that share a row (a power of two), pitch: elements of T from row to row.
+template <typename T, int WARPS>
+__device__ __forceinline__ void move_rows(T* base, const uint2* list, int start, int count, int lanes, size_t pitch) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int per = 32 / lanes;               // rows of a warp at a time
+    const int own = warp * per + lane / lanes;
+    T* at = base + lane % lanes;
+    const int step = WARPS * per;
+    uint2 mv[kBatch], mv_next[kBatch];
+    T v[kBatch], v_next[kBatch];
+    auto look = [&](uint2 (&m)[kBatch], int j0) {
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
-            const int j = j0 + u * per + lane / lanes;
-            if (j < count) {
-                const uint2 mv = list[j];
-                dst[u] = mv.y;
-                v[u] = base[mv.x * pitch + sub];
-            }
+            const int j = j0 + u * step + own;
+            if (j < count) m[u] = list[j];
         }
-        __syncwarp();
+    };
+    auto read = [&](T (&x)[kBatch], const uint2 (&m)[kBatch], int j0) {
 #pragma unroll
         for (int u = 0; u < kBatch; ++u)
-            if (j0 + u * per + lane / lanes < count) base[dst[u] * pitch + sub] = v[u];
-        __syncwarp();
+            if (j0 + u * step + own < count) x[u] = at[m[u].x * pitch];
+    };
+    look(mv, start);
+    read(v, mv, start);
+    look(mv_next, start + kBatch * step);
+    for (int j0 = start; j0 < count; j0 += kBatch * step) {
+        // The next stretch is read before this one is written; every thread's reads of this
+        // one are before the barrier, the writes behind it.
+        read(v_next, mv_next, j0 + kBatch * step);
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u)
+            if (j0 + u * step + own < count) at[mv[u].y * pitch] = v[u];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            mv[u] = mv_next[u];
+            v[u] = v_next[u];
+        }
+        look(mv_next, j0 + 2 * kBatch * step);
     }
 }
 
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictParams p, int slices, int units) {
-    const long long unit = static_cast<long long>(blockIdx.x) * (kMoveThreads / 32) + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    const long long sh = unit / units;
-    const int part = static_cast<int>(unit - sh * units);
-    if (sh >= static_cast<long long>(p.num_seqs) * p.num_kv_heads) return;
-    if (part == 0 && sh % p.num_kv_heads == 0 && lane == 0)
-        p.lens_out[sh / p.num_kv_heads] = p.new_lens[sh / p.num_kv_heads];
-    const int count = p.counts[sh];
-    const uint2* list = p.moves + sh * p.context_cap;
+template <int WARPS>
+__global__ void __launch_bounds__(WARPS * 32) evict_move_kernel(const EvictParams p, int slices, int lanes, int units) {
+    const int sh = blockIdx.x / units;
+    const int part = blockIdx.x - sh * units;
+    const int s = sh / p.num_kv_heads;
+    const int count = p.new_lens[s];
+    // Nothing reads the lengths any more: lens_out may be the array they are in.
+    if (part == 0 && sh == s * p.num_kv_heads && threadIdx.x == 0) p.lens_out[s] = count;
+    const int start = p.starts[sh];
+    if (start >= count) return;
+    const uint2* list = p.moves + static_cast<size_t>(sh) * p.context_cap;
     if (part < 2 * slices) {
         const int which = part / slices, slice = part - which * slices;
-        const int lanes = p.row_bytes / 16 / slices;
         uint4* base = static_cast<uint4*>(which ? p.v_cache : p.k_cache) + slice * lanes;
-        if (lanes <= 32) move_values(base, list, count, lanes, lane, p.row_bytes / 16);
+        move_rows<uint4, WARPS>(base, list, start, count, lanes, p.row_bytes / 16);
     } else {
         const int which = part - 2 * slices;
         uint32_t* base = which == 0 ? reinterpret_cast<uint32_t*>(p.row_weights) : which == 1 ? p.k_params : p.v_params;
-        move_values(base, list, count, 1, lane, 1);
+        move_rows<uint32_t, WARPS>(base, list, start, count, 1, 1);
     }
 }
 
 }  // namespace
 
 cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream) {
-    const long long heads = static_cast<long long>(p.num_seqs) * p.num_kv_heads;
+    const int heads = p.num_seqs * p.num_kv_heads;
     if (heads == 0) return cudaSuccess;
-    evict_select_kernel<<<static_cast<unsigned>(heads), kSelectThreads, 0, stream>>>(p);
-    cudaError_t err = cudaGetLastError();
+    const int sms = device_sms();
+    if (sms <= 0) return cudaErrorInvalidDevice;
+    int ranks = 1;
+    while (ranks < kMaxCluster && static_cast<long long>(heads) * ranks < 2 * sms && p.context_cap / ranks > 2048) ranks *= 2;
+    const int share = ((p.context_cap + ranks - 1) / ranks + 31) / 32 * 32;
+    const int max_keys = share < kMaxKeys ? share : kMaxKeys;
+    cudaError_t err = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * kMaxKeys);
     if (err != cudaSuccess) return err;
-    const int slices = p.row_bytes / 16;     // 16 bytes each
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(heads) * ranks);
+    cfg.blockDim = dim3(kSelectThreads);
+    cfg.dynamicSmemBytes = 4 * static_cast<size_t>(max_keys);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = ranks;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    err = cudaLaunchKernelEx(&cfg, evict_select_kernel, p, max_keys);
+    if (err != cudaSuccess) return err;
+    // Slices of 32 bytes (a sector), or what divides the row.
+    const int pieces = p.row_bytes / 16;
+    const int lanes = pieces % 2 == 0 ? 2 : 1;
+    const int slices = pieces / lanes;
     const int units = 2 * slices + (p.k_params ? 3 : 1);
-    const long long ctas = (heads * units + kMoveThreads / 32 - 1) / (kMoveThreads / 32);
-    if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    evict_move_kernel<<<static_cast<unsigned>(ctas), kMoveThreads, 0, stream>>>(p, slices, units);
+    const unsigned ctas = static_cast<unsigned>(heads) * units;
+    if (static_cast<long long>(heads) * units > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    // Few units: more rows of each on the way at once.
+    if (ctas < 16u * sms)
+        evict_move_kernel<8><<<ctas, 256, 0, stream>>>(p, slices, lanes, units);
+    else
+        evict_move_kernel<1><<<ctas, 32, 0, stream>>>(p, slices, lanes, units);
     return cudaGetLastError();
 }
 

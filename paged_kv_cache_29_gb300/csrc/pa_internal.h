@@ -160,8 +160,8 @@ struct NormRopeParams {
 cudaError_t launch_norm_rope(const NormRopeParams& p, pa_dtype dtype, cudaStream_t stream);
 
 // Eviction (pa_evict in the header). moves: for each (sequence, KV head)
-// context_cap pairs of pool rows (from, to), counts how many; new_lens: what
-// lens_out gets.
+// context_cap pairs of pool rows (from, to), one per row that stays; starts: the first
+// of them that changes its place; new_lens: what lens_out gets.
 struct EvictParams {
     void* k_cache;
     void* v_cache;
@@ -174,7 +174,7 @@ struct EvictParams {
     const int32_t* keep_lens;
     int32_t* lens_out;
     uint2* moves;                  // [B][Hkv][context_cap]
-    int32_t* counts;               // [B][Hkv]
+    int32_t* starts;               // [B][Hkv]
     int32_t* new_lens;             // [B]
     int32_t* error_word;
     int num_sinks, num_recent;

@@ -5,13 +5,15 @@
 // r = max(p - q, 0) (or p) by its running sum: the smallest v with
 // r(0) + .. + r(v) > u S, S the sum of all. Only that one row of p (and of q) is read.
 //
-// A cluster of CTAs shares a sequence's row, a CTA a run of its segments of 1,024
-// values. A warp sums a segment: each lane its 32 values as an fp32 value and the
+// A cluster of CTAs shares a sequence's row, a CTA a run of its segments of 512
+// values. A warp sums a segment: each lane its 16 values as an fp32 value and the
 // running error of it (the difference p - q and every addition leave an exact error
 // term; fp64 adds and conversions are slow here), the lanes in 64 bits. Running sums over
 // the CTA's segments, then over the cluster's CTAs through their shared memory, find
-// the one segment that u S falls into, which is walked through in 64 bits. Every order of
-// addition is fixed by the row's length and the cluster's size.
+// the one segment that u S falls into; the CTA scans that in 64 bits, a value a thread.
+// Every order of addition is fixed by the row's length and the cluster's size.
+#include <climits>
+
 #include <cooperative_groups.h>
 
 #include "pa_common.cuh"
@@ -24,8 +26,10 @@ namespace pa {
 namespace {
 
 constexpr int kVerifyThreads = 512;
-constexpr int kSegment = 1024;
+constexpr int kSegment = 512;                 // a value a thread, in the last step
+constexpr int kWarps = kVerifyThreads / 32;
 constexpr int kMaxCluster = 8;
+constexpr int kMaxSegments = 4096;            // of a CTA: their running sums fit the default shared memory
 
 // value and error term of a sum of fp32 values
 struct Sum {
@@ -47,10 +51,36 @@ __device__ __forceinline__ double warp_scan(double v, int lane) {
     return v;
 }
 
+// A lane's part of the segment's sum that begins at v0 - lane: r = max(p - q, 0) or, without q, p
+// but for value `out`. All loads go out before their use.
+template <bool HAS_Q>
+__device__ __forceinline__ double sum_part(const float* pr, const float* qr, int v0, int V, int out) {
+    constexpr int N = kSegment / 32;
+    float x[N], y[HAS_Q ? N : 1];
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        const int v = v0 + 32 * k;
+        x[k] = v < V && (HAS_Q || v != out) ? __ldg(pr + v) : 0.f;
+        if constexpr (HAS_Q) y[k] = v < V ? __ldg(qr + v) : 0.f;
+    }
+    Sum sum;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        if constexpr (HAS_Q) {
+            const float diff = x[k] - y[k];
+            const float b = x[k] - diff;     // x - y is diff + (x - (diff + b)) + (b - y) exactly
+            if (diff > 0.f) sum.add(diff, (x[k] - (diff + b)) + (b - y[k]));
+        } else if (x[k] > 0.f) {
+            sum.add(x[k], 0.f);
+        }
+    }
+    return static_cast<double>(sum.hi) + static_cast<double>(sum.lo);
+}
+
 __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyParams p, int segs_per_cta) {
     extern __shared__ double seg_sum[];       // [segs_per_cta], then their running sums
-    __shared__ double cta_total;
-    __shared__ int first_rejected, bad;
+    __shared__ double cta_total, warp_total[kWarps];
+    __shared__ int first_rejected, bad, chosen;
     cg::cluster_group cluster = cg::this_cluster();
     const int ranks = cluster.num_blocks(), rank = cluster.block_rank();
     const int s = blockIdx.x / ranks;
@@ -93,28 +123,22 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
     const float* qr = rejected && draft != nullptr ? draft + a * p.draft_row : nullptr;
     const int looked_up = rejected && draft == nullptr ? __ldg(tokens + a) : -1;
     bool plain = false;                       // from p itself, where the difference leaves nothing
-    auto q_at = [&](int v) { return plain ? 0.f : qr != nullptr ? __ldg(qr + v) : v == looked_up ? 1.f : 0.f; };
+    // r(v) in 64 bits
+    auto value = [&](int v) -> double {
+        const double x = __ldg(pr + v);
+        const double r = plain ? x : qr != nullptr ? x - static_cast<double>(__ldg(qr + v)) : v == looked_up ? 0.0 : x;
+        return r > 0.0 ? r : 0.0;
+    };
 
     const int seg0 = rank * segs_per_cta;
     const int segs = max(0, min((V + kSegment - 1) / kSegment - seg0, segs_per_cta));
     double base = 0.0, total = 0.0, own_end = 0.0;
     for (int pass = 0; pass < 2; ++pass) {
         plain = pass == 1;
-        for (int g = warp; g < segs; g += kVerifyThreads / 32) {
+        for (int g = warp; g < segs; g += kWarps) {
             const int v0 = (seg0 + g) * kSegment + lane;
-            Sum sum;
-#pragma unroll 8
-            for (int k = 0; k < kSegment / 32; ++k) {
-                const int v = v0 + 32 * k;
-                if (v < V) {
-                    const float x = __ldg(pr + v), y = q_at(v);
-                    const float diff = x - y;
-                    const float b = x - diff;            // diff + (b - y) + ((x - diff) - b) is x - y exactly
-                    const float err = (x - (diff + b)) + (b - y);
-                    if (diff > 0.f) sum.add(diff, err);
-                }
-            }
-            double v = static_cast<double>(sum.hi) + static_cast<double>(sum.lo);
+            double v = !plain && qr != nullptr ? sum_part<true>(pr, qr, v0, V, -1)
+                                               : sum_part<false>(pr, nullptr, v0, V, plain ? -1 : looked_up);
 #pragma unroll
             for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
             if (lane == 0) seg_sum[g] = v;
@@ -147,37 +171,48 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
     const float u = fminf(fmaxf(__ldg(uniforms + Q), 0.f), 0.99999994f);   // [0, 1)
     const double border = static_cast<double>(u) * total;
     if (!(base <= border && border < own_end)) return;   // one CTA of the cluster goes on
-    if (warp != 0) return;
-    // The segment: the first whose running sum passes the border.
-    int seg = 0;
-    for (int g0 = 0; g0 < segs; g0 += 32) {
-        const unsigned hit = __ballot_sync(0xffffffffu, g0 + lane < segs && base + seg_sum[g0 + lane] > border);
-        if (hit != 0u) {
-            seg = g0 + __ffs(hit) - 1;
-            break;
-        }
-    }
+    // The segment: the first whose running sum passes the border. (Where the two ways to
+    // sum part by a rounding the walk may go on to the next, or end behind the last.)
+    if (tid == 0) chosen = INT_MAX;
+    __syncthreads();
+    for (int g = tid; g < segs; g += kVerifyThreads)
+        if (base + seg_sum[g] > border) atomicMin(&chosen, g);
+    __syncthreads();
+    const int seg = chosen;                   // there is one: the last running sum is the CTA's end
     double upto = base + (seg > 0 ? seg_sum[seg - 1] : 0.0);
-    // Its values in turn; beyond it only where roundings of the two ways to sum part.
-    const int end = min(V, (seg0 + segs) * kSegment);
-    int token = -1;
-    for (int v0 = (seg0 + seg) * kSegment; v0 < end && token < 0; v0 += 32) {
-        double r = 0.0;
-        if (v0 + lane < end) {
-            r = static_cast<double>(__ldg(pr + v0 + lane)) - static_cast<double>(q_at(v0 + lane));
-            if (!(r > 0.0)) r = 0.0;
+    __syncthreads();
+    if (tid == 0) chosen = INT_MAX;
+    int token = INT_MAX, last_positive = -1;
+    for (int g = seg; g < segs && token == INT_MAX; ++g) {
+        const int v = (seg0 + g) * kSegment + tid;
+        const double r = v < V ? value(v) : 0.0;
+        double run = warp_scan(r, lane);
+        if (lane == 31) warp_total[warp] = run;
+        __syncthreads();
+        run += upto;
+        double end = upto;
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) run += warp_total[w];
+            end += warp_total[w];
         }
-        const double incl = warp_scan(r, lane) + upto;
-        const unsigned hit = __ballot_sync(0xffffffffu, r > 0.0 && incl > border);
-        if (hit != 0u) token = v0 + __ffs(hit) - 1;
-        upto = __shfl_sync(0xffffffffu, incl, 31);
+        if (r > 0.0 && run > border) atomicMin(&chosen, v);
+        if (r > 0.0) last_positive = v;
+        __syncthreads();
+        token = chosen;
+        upto = end;
     }
-    for (int v0 = end - 32; token < 0; v0 -= 32) {       // the last value that can be drawn
-        const int v = v0 + lane;
-        const unsigned some = __ballot_sync(0xffffffffu, v >= 0 && __ldg(pr + max(v, 0)) > q_at(max(v, 0)));
-        if (some != 0u) token = v0 + 31 - __clz(some);
-        if (v0 <= 0) break;
+    if (token == INT_MAX) {
+        // The last value that can be drawn: of the segments walked, else before them.
+        __syncthreads();                      // every thread has read `chosen`
+        if (tid == 0) chosen = -1;
+        __syncthreads();
+        for (int v = seg0 * kSegment + tid; last_positive < 0 && v < min(V, (seg0 + seg) * kSegment); v += kVerifyThreads)
+            if (value(v) > 0.0) atomicMax(&chosen, v);
+        if (last_positive >= 0) atomicMax(&chosen, last_positive);
+        __syncthreads();
+        token = chosen;
     }
+    if (warp != 0) return;
     for (int i = lane; i <= Q; i += 32)
         p.out_tokens[static_cast<size_t>(s) * (Q + 1) + i] = i < a ? __ldg(tokens + i) : i == a ? token : -1;
     if (lane == 0) {
@@ -194,12 +229,14 @@ cudaError_t launch_verify(const VerifyParams& p, cudaStream_t stream) {
     if (sms <= 0) return cudaErrorInvalidDevice;
     const int segs = (p.vocab + kSegment - 1) / kSegment;
     int ranks = 1;
-    while (ranks < kMaxCluster && ranks < segs && static_cast<long long>(p.num_seqs) * ranks < sms) ranks *= 2;
+    while (ranks < kMaxCluster && ranks < segs &&
+           (static_cast<long long>(p.num_seqs) * ranks < sms || segs > kMaxSegments * ranks))
+        ranks *= 2;
     const int per_cta = (segs + ranks - 1) / ranks;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(p.num_seqs) * ranks);
     cfg.blockDim = dim3(kVerifyThreads);
-    cfg.dynamicSmemBytes = 8 * static_cast<size_t>(per_cta);   // at most 4,096 segments: 32 KB
+    cfg.dynamicSmemBytes = 8 * static_cast<size_t>(per_cta);   // 32 KB at most
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -68,7 +68,7 @@ class Verify:
 
 @pytest.mark.parametrize("lookup", [False, True])
 @pytest.mark.parametrize("B,Q,V", [(1, 4, 32000), (7, 1, 1), (5, 3, 2), (64, 5, 31), (33, 4, 1000), (16, 7, 1024), (9, 2, 1025), (3, 16, 50021),
-                                   (150, 3, 4099), (400, 2, 777), (2, 64, 333), (20, 4, 131072), (6, 0, 5000), (1, 1, 1 << 20)])
+                                   (150, 3, 4099), (400, 2, 777), (2, 64, 333), (20, 4, 131072), (6, 0, 5000), (1, 1, 1 << 20), (160, 1, 20011)])
 def test_tokens(B, Q, V, lookup):
     Verify(B, Q, V, lookup, seed=B + Q + V).check()
 
@@ -164,3 +164,18 @@ def test_drawn_tokens_are_distributed_as_the_targets():
     pa.pa_verify_draft(target, torch.from_numpy(q).cuda().expand(B, 1, V), tokens, u, out, acc)
     counts = np.bincount(out[:, 0].cpu().numpy(), minlength=V)
     assert (np.abs(counts - B * p) <= 5 * np.sqrt(B * p * (1 - p))).all(), counts
+
+
+@pytest.mark.parametrize("B", [1, 160])
+def test_the_largest_vocabulary(B):
+    """No drafts: draws from one row of 2^22 values, each sequence with its own number."""
+    V = 1 << 22
+    r = np.random.default_rng(9)
+    p = softmax(2 * r.standard_normal(V))
+    u = r.random((B, 1), dtype=np.float32)
+    out, acc = torch.zeros(B, 1, dtype=torch.int32, device="cuda"), torch.ones(B, dtype=torch.int32, device="cuda")
+    pa.pa_verify_draft(torch.from_numpy(p).cuda().expand(B, 1, V), None, torch.zeros(B, 0, dtype=torch.int32, device="cuda"), torch.from_numpy(u).cuda(),
+                       out, acc)
+    run = np.cumsum(p.astype(np.float64))
+    want = np.searchsorted(run, u[:, 0].astype(np.float64) * run[-1], side="right")
+    assert np.array_equal(out[:, 0].cpu().numpy(), want) and not acc.any()
