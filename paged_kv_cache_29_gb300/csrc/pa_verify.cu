@@ -5,14 +5,18 @@
 // r = max(p - q, 0) (or p) by its running sum: the smallest v with
 // r(0) + .. + r(v) > u S, S the sum of all. Only that one row of p (and of q) is read.
 //
+// Sums are pairs of fp32 values, a sum and its error: the difference p - q and each
+// addition leave an exact error term, and what is lost is below 2^-44 of a sum. (An fp64
+// instruction holds the SM's fp64 pipe for 16 cycles a warp: with fp64 lanes the
+// additions took as long as the loads.) Borders are compared in 64 bits, or pair to pair.
+//
 // A cluster of CTAs shares a sequence's row, a CTA a run of its segments of 512
-// values. A warp sums a segment: each lane its 16 values as an fp32 value and the
-// running error of it (the difference p - q and every addition leave an exact error
-// term; fp64 adds and conversions are slow here), the lanes in 64 bits. Running sums over
-// the CTA's segments, then over the cluster's CTAs through their shared memory, find
-// the one segment that u S falls into; the CTA scans that in 64 bits, a value a thread.
-// Every order of addition is fixed by the row's length and the cluster's size.
+// values, a warp a segment at a time. Running sums over the CTA's segments, then over
+// the cluster's CTAs through their shared memory, find the one segment that u S falls
+// into; its CTA scans that, a value a thread. Every order of addition is fixed by the
+// row's length and the cluster's size.
 #include <climits>
+#include <utility>
 
 #include <cooperative_groups.h>
 
@@ -31,16 +35,41 @@ constexpr int kWarps = kVerifyThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxSegments = 4096;            // of a CTA: their running sums fit the default shared memory
 
-// value and error term of a sum of fp32 values
+// A sum of fp32 values as hi + lo, |lo| at most half a step of hi.
 struct Sum {
-    float hi = 0.f, lo = 0.f;
+    float hi, lo;
+    // + x + err; lo is left to grow (take() or plus() bring the pair to order)
     __device__ __forceinline__ void add(float x, float err) {
         const float s = hi + x;
         const float b = s - hi;
         lo += ((hi - (s - b)) + (x - b)) + err;
         hi = s;
     }
+    __device__ __forceinline__ Sum plus(const Sum& o) const {
+        const float s = hi + o.hi;
+        const float b = s - hi;
+        const float e = ((hi - (s - b)) + (o.hi - b)) + (lo + o.lo);
+        Sum r;
+        r.hi = s + e;
+        r.lo = e - (r.hi - s);
+        return r;
+    }
+    __device__ __forceinline__ Sum order() const {
+        Sum r;
+        r.hi = hi + lo;
+        r.lo = lo - (r.hi - hi);
+        return r;
+    }
+    __device__ __forceinline__ bool above(const Sum& o) const { return hi > o.hi || (hi == o.hi && lo > o.lo); }
+    __device__ __forceinline__ double value() const { return static_cast<double>(hi) + static_cast<double>(lo); }
 };
+
+// x - y for x > y, else nothing; NaN counts as nothing.
+__device__ __forceinline__ void add_excess(Sum& sum, float x, float y) {
+    const float diff = x - y;
+    const float b = x - diff;                 // x - y is diff + (x - (diff + b)) + (b - y) exactly
+    if (diff > 0.f) sum.add(diff, (x - (diff + b)) + (b - y));
+}
 
 __device__ __forceinline__ double warp_scan(double v, int lane) {
 #pragma unroll
@@ -51,10 +80,21 @@ __device__ __forceinline__ double warp_scan(double v, int lane) {
     return v;
 }
 
+__device__ __forceinline__ Sum warp_scan(Sum v, int lane) {
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        Sum u;
+        u.hi = __shfl_up_sync(0xffffffffu, v.hi, off);
+        u.lo = __shfl_up_sync(0xffffffffu, v.lo, off);
+        if (lane >= off) v = u.plus(v);
+    }
+    return v;
+}
+
 // A lane's part of the segment's sum that begins at v0 - lane: r = max(p - q, 0) or, without q, p
 // but for value `out`. All loads go out before their use.
 template <bool HAS_Q>
-__device__ __forceinline__ double sum_part(const float* pr, const float* qr, int v0, int V, int out) {
+__device__ __forceinline__ Sum sum_part(const float* pr, const float* qr, int v0, int V, int out) {
     constexpr int N = kSegment / 32;
     float x[N], y[HAS_Q ? N : 1];
 #pragma unroll
@@ -63,51 +103,46 @@ __device__ __forceinline__ double sum_part(const float* pr, const float* qr, int
         x[k] = v < V && (HAS_Q || v != out) ? __ldg(pr + v) : 0.f;
         if constexpr (HAS_Q) y[k] = v < V ? __ldg(qr + v) : 0.f;
     }
-    Sum sum;
+    Sum sum{0.f, 0.f};
 #pragma unroll
-    for (int k = 0; k < N; ++k) {
-        if constexpr (HAS_Q) {
-            const float diff = x[k] - y[k];
-            const float b = x[k] - diff;     // x - y is diff + (x - (diff + b)) + (b - y) exactly
-            if (diff > 0.f) sum.add(diff, (x[k] - (diff + b)) + (b - y[k]));
-        } else if (x[k] > 0.f) {
-            sum.add(x[k], 0.f);
-        }
-    }
-    return static_cast<double>(sum.hi) + static_cast<double>(sum.lo);
+    for (int k = 0; k < N; ++k) add_excess(sum, x[k], HAS_Q ? y[k] : 0.f);
+    return sum.order();
 }
 
 __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyParams p, int segs_per_cta) {
-    extern __shared__ double seg_sum[];       // [segs_per_cta], then their running sums
-    __shared__ double cta_total, warp_total[kWarps];
-    __shared__ int first_rejected, bad, chosen;
+    extern __shared__ double seg_sum[];       // [segs_per_cta]: first each segment's Sum (its bits), then running sums
+    __shared__ double cta_total;
+    __shared__ Sum warp_total[kWarps], border_left;
+    __shared__ int first_rejected, bad, chosen, owner;
     cg::cluster_group cluster = cg::this_cluster();
     const int ranks = cluster.num_blocks(), rank = cluster.block_rank();
     const int s = blockIdx.x / ranks;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int Q = p.max_drafts, V = p.vocab;
-    const int d = p.num_drafts != nullptr ? __ldg(p.num_drafts + s) : Q;
-    const bool bad_count = d < 0 || d > Q;
     const float* target = p.target + s * p.target_seq;
     const float* draft = p.draft == nullptr ? nullptr : p.draft + s * p.draft_seq;
     const int32_t* tokens = p.tokens + static_cast<size_t>(s) * Q;
     const float* uniforms = p.uniforms + static_cast<size_t>(s) * (Q + 1);
-    // Read by every CTA before the cluster's barrier; lens_out (it may be the
-    // same array) is written behind it.
+    // Independent loads first. (lens_out may be context_lens: it is written behind the
+    // cluster's barrier, which every CTA reaches after this read.)
+    const int d = p.num_drafts != nullptr ? __ldg(p.num_drafts + s) : Q;
     const int rows = p.context_lens != nullptr ? p.context_lens[s] : 0;
+    const int x = tid < Q ? __ldg(tokens + tid) : 0;
+    const float ux = tid < Q ? __ldg(uniforms + tid) : 0.f;
+    const float u_last = __ldg(uniforms + Q);
+    const bool bad_count = d < 0 || d > Q;
     if (tid == 0) {
         first_rejected = bad_count ? 0 : d;
         bad = bad_count ? PA_DEVERR_TOKEN : 0;
     }
     __syncthreads();
     if (!bad_count && tid < d) {
-        const int x = __ldg(tokens + tid);
         if (x < 0 || x >= V) {
             atomicOr(&bad, PA_DEVERR_TOKEN);
         } else {
             const double px = __ldg(target + tid * p.target_row + x);
             const double qx = draft != nullptr ? __ldg(draft + tid * p.draft_row + x) : 1.0f;
-            if (!(static_cast<double>(__ldg(uniforms + tid)) * qx < px)) atomicMin(&first_rejected, tid);
+            if (!(static_cast<double>(ux) * qx < px)) atomicMin(&first_rejected, tid);
         }
     }
     __syncthreads();
@@ -121,104 +156,126 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
     const bool rejected = a < d;
     const float* pr = target + a * p.target_row;
     const float* qr = rejected && draft != nullptr ? draft + a * p.draft_row : nullptr;
-    const int looked_up = rejected && draft == nullptr ? __ldg(tokens + a) : -1;
-    bool plain = false;                       // from p itself, where the difference leaves nothing
-    // r(v) in 64 bits
-    auto value = [&](int v) -> double {
-        const double x = __ldg(pr + v);
-        const double r = plain ? x : qr != nullptr ? x - static_cast<double>(__ldg(qr + v)) : v == looked_up ? 0.0 : x;
-        return r > 0.0 ? r : 0.0;
-    };
+    int left_out = rejected && draft == nullptr ? __ldg(tokens + a) : -1;   // looked up: q is 1 there
 
     const int seg0 = rank * segs_per_cta;
     const int segs = max(0, min((V + kSegment - 1) / kSegment - seg0, segs_per_cta));
-    double base = 0.0, total = 0.0, own_end = 0.0;
+    bool some = false;
     for (int pass = 0; pass < 2; ++pass) {
-        plain = pass == 1;
+        if (pass == 1) {                      // the difference leaves nothing: from p itself
+            qr = nullptr;
+            left_out = -1;
+        }
         for (int g = warp; g < segs; g += kWarps) {
             const int v0 = (seg0 + g) * kSegment + lane;
-            double v = !plain && qr != nullptr ? sum_part<true>(pr, qr, v0, V, -1)
-                                               : sum_part<false>(pr, nullptr, v0, V, plain ? -1 : looked_up);
+            Sum v = qr != nullptr ? sum_part<true>(pr, qr, v0, V, -1) : sum_part<false>(pr, nullptr, v0, V, left_out);
 #pragma unroll
-            for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-            if (lane == 0) seg_sum[g] = v;
+            for (int off = 16; off > 0; off >>= 1) {
+                Sum o;
+                o.hi = __shfl_xor_sync(0xffffffffu, v.hi, off);
+                o.lo = __shfl_xor_sync(0xffffffffu, v.lo, off);
+                v = v.plus(o);
+            }
+            if (lane == 0) seg_sum[g] = __hiloint2double(__float_as_int(v.hi), __float_as_int(v.lo));
         }
         __syncthreads();
         if (warp == 0) {
             double carry = 0.0;
             for (int g0 = 0; g0 < segs; g0 += 32) {
-                const double v = warp_scan(g0 + lane < segs ? seg_sum[g0 + lane] : 0.0, lane) + carry;
-                if (g0 + lane < segs) seg_sum[g0 + lane] = v;
+                const bool in = g0 + lane < segs;
+                const double bits = in ? seg_sum[g0 + lane] : 0.0;   // (a Sum of zeros, too)
+                const Sum own{__int_as_float(__double2hiint(bits)), __int_as_float(__double2loint(bits))};
+                const double v = warp_scan(own.value(), lane) + carry;
+                if (in) seg_sum[g0 + lane] = v;
                 carry = __shfl_sync(0xffffffffu, v, min(31, segs - g0 - 1));
             }
             if (lane == 0) cta_total = carry;        // the last running sum itself
         }
         cluster.sync();
-        total = 0.0;
-        for (int r = 0; r < ranks; ++r) {
-            if (r == rank) base = total;
-            total += *cluster.map_shared_rank(&cta_total, r);
-            if (r == rank) own_end = total;
+        if (warp == 0) {
+            // Where u S falls: in this CTA's part, and in which of its segments?
+            const double mine = lane < ranks ? *cluster.map_shared_rank(&cta_total, lane) : 0.0;
+            double total = 0.0, base = 0.0, end = 0.0;
+            for (int r = 0; r < ranks; ++r) {
+                if (r == rank) base = total;
+                total += __shfl_sync(0xffffffffu, mine, r);
+                if (r == rank) end = total;
+            }
+            const double u = fminf(fmaxf(u_last, 0.f), 0.99999994f);   // [0, 1)
+            const double border = u * total;
+            const bool here = base <= border && border < end;
+            int seg = segs - 1;
+            if (here) {
+                for (int g0 = 0; g0 < segs; g0 += 32) {
+                    const unsigned hit = __ballot_sync(0xffffffffu, g0 + lane < segs && base + seg_sum[g0 + lane] > border);
+                    if (hit != 0u) {
+                        seg = g0 + __ffs(hit) - 1;
+                        break;
+                    }
+                }
+            }
+            if (lane == 0) {
+                const double left = border - (base + (here && seg > 0 ? seg_sum[seg - 1] : 0.0));
+                border_left.hi = static_cast<float>(left);
+                border_left.lo = static_cast<float>(left - static_cast<double>(border_left.hi));
+                owner = !(total > 0.0) ? -2 : here ? seg : -1;
+                chosen = INT_MAX;
+            }
         }
-        // Every CTA has read the totals: another pass may write them, or a CTA end.
-        cluster.sync();
-        if (total > 0.0) break;
-    }
-    if (!(total > 0.0)) {
-        if (rank == 0 && tid == 0) raise_error(p.error_word, PA_DEVERR_TOKEN);
-        return;
-    }
-    const float u = fminf(fmaxf(__ldg(uniforms + Q), 0.f), 0.99999994f);   // [0, 1)
-    const double border = static_cast<double>(u) * total;
-    if (!(base <= border && border < own_end)) return;   // one CTA of the cluster goes on
-    // The segment: the first whose running sum passes the border. (Where the two ways to
-    // sum part by a rounding the walk may go on to the next, or end behind the last.)
-    if (tid == 0) chosen = INT_MAX;
-    __syncthreads();
-    for (int g = tid; g < segs; g += kVerifyThreads)
-        if (base + seg_sum[g] > border) atomicMin(&chosen, g);
-    __syncthreads();
-    const int seg = chosen;                   // there is one: the last running sum is the CTA's end
-    double upto = base + (seg > 0 ? seg_sum[seg - 1] : 0.0);
-    __syncthreads();
-    if (tid == 0) chosen = INT_MAX;
-    int token = INT_MAX, last_positive = -1;
-    for (int g = seg; g < segs && token == INT_MAX; ++g) {
-        const int v = (seg0 + g) * kSegment + tid;
-        const double r = v < V ? value(v) : 0.0;
-        double run = warp_scan(r, lane);
-        if (lane == 31) warp_total[warp] = run;
         __syncthreads();
-        run += upto;
-        double end = upto;
-        for (int w = 0; w < kWarps; ++w) {
-            if (w < warp) run += warp_total[w];
-            end += warp_total[w];
+        some = owner != -2;
+        if (some) break;
+        cluster.sync();                       // every CTA has read the totals: the second pass writes them
+    }
+    // The totals are read; no CTA ends before all have said so.
+    auto arrived = cluster.barrier_arrive();
+    const int seg = owner;
+    if (!some && rank == 0 && tid == 0) raise_error(p.error_word, PA_DEVERR_TOKEN);
+    if (seg >= 0) {
+        // The first value whose running sum passes the border. (Where the two ways to sum part
+        // by a rounding the walk may go on to the next segment, or end behind the last.)
+        Sum upto{0.f, 0.f};
+        const Sum border = border_left;
+        int token = INT_MAX, last_positive = -1;
+        for (int g = seg; g < segs && token == INT_MAX; ++g) {
+            const int v = (seg0 + g) * kSegment + tid;
+            Sum r{0.f, 0.f};
+            if (v < V && v != left_out) add_excess(r, __ldg(pr + v), qr != nullptr ? __ldg(qr + v) : 0.f);
+            Sum run = warp_scan(r, lane);
+            if (lane == 31) warp_total[warp] = run;
+            __syncthreads();
+            Sum before = upto;
+            for (int w = 0; w < kWarps; ++w) {
+                if (w == warp) run = before.plus(run);
+                before = before.plus(warp_total[w]);
+            }
+            upto = before;
+            if (r.hi > 0.f) {
+                last_positive = v;
+                if (run.above(border)) atomicMin(&chosen, v);
+            }
+            __syncthreads();
+            token = chosen;
         }
-        if (r > 0.0 && run > border) atomicMin(&chosen, v);
-        if (r > 0.0) last_positive = v;
-        __syncthreads();
-        token = chosen;
-        upto = end;
+        if (token == INT_MAX) {
+            // The last value that can be drawn: of the segments walked, else before them.
+            __syncthreads();                  // every thread has read `chosen`
+            if (tid == 0) chosen = -1;
+            __syncthreads();
+            for (int v = seg0 * kSegment + tid; last_positive < 0 && v < min(V, (seg0 + seg) * kSegment); v += kVerifyThreads)
+                if (v != left_out && __ldg(pr + v) > (qr != nullptr ? __ldg(qr + v) : 0.f)) atomicMax(&chosen, v);
+            if (last_positive >= 0) atomicMax(&chosen, last_positive);
+            __syncthreads();
+            token = chosen;
+        }
+        for (int i = tid; i <= Q; i += kVerifyThreads)
+            p.out_tokens[static_cast<size_t>(s) * (Q + 1) + i] = i < a ? __ldg(tokens + i) : i == a ? token : -1;
+        if (tid == 0) {
+            p.num_accepted[s] = a;
+            if (p.lens_out != nullptr) p.lens_out[s] = rows - (d - a);
+        }
     }
-    if (token == INT_MAX) {
-        // The last value that can be drawn: of the segments walked, else before them.
-        __syncthreads();                      // every thread has read `chosen`
-        if (tid == 0) chosen = -1;
-        __syncthreads();
-        for (int v = seg0 * kSegment + tid; last_positive < 0 && v < min(V, (seg0 + seg) * kSegment); v += kVerifyThreads)
-            if (value(v) > 0.0) atomicMax(&chosen, v);
-        if (last_positive >= 0) atomicMax(&chosen, last_positive);
-        __syncthreads();
-        token = chosen;
-    }
-    if (warp != 0) return;
-    for (int i = lane; i <= Q; i += 32)
-        p.out_tokens[static_cast<size_t>(s) * (Q + 1) + i] = i < a ? __ldg(tokens + i) : i == a ? token : -1;
-    if (lane == 0) {
-        p.num_accepted[s] = a;
-        if (p.lens_out != nullptr) p.lens_out[s] = rows - (d - a);
-    }
+    cluster.barrier_wait(std::move(arrived));
 }
 
 }  // namespace
