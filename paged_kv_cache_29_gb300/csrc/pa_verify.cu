@@ -11,7 +11,7 @@
 // additions took as long as the loads.) Borders are compared in 64 bits, or pair to pair.
 //
 // A cluster of CTAs shares a sequence's row, a CTA a run of its segments of 512
-// values, a warp a segment at a time. Running sums over the CTA's segments, then over
+// (or 256) values, a warp a segment at a time. Running sums over the CTA's segments, then over
 // the cluster's CTAs through their shared memory, find the one segment that u S falls
 // into; its CTA scans that, a value a thread. Every order of addition is fixed by the
 // row's length and the cluster's size.
@@ -29,11 +29,10 @@ namespace pa {
 
 namespace {
 
-constexpr int kVerifyThreads = 512;
-constexpr int kSegment = 512;                 // a value a thread, in the last step
-constexpr int kWarps = kVerifyThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kMaxSegments = 4096;            // of a CTA: their running sums fit the default shared memory
+// Segments of a CTA: their running sums fit the default shared memory, and 2^22 values
+// (2^14 segments of 256) fit a cluster.
+constexpr int kMaxSegments = 4096;
 
 // A sum of fp32 values as hi + lo, |lo| at most half a step of hi.
 struct Sum {
@@ -91,25 +90,99 @@ __device__ __forceinline__ Sum warp_scan(Sum v, int lane) {
     return v;
 }
 
-// A lane's part of the segment's sum that begins at v0 - lane: r = max(p - q, 0) or, without q, p
-// but for value `out`. All loads go out before their use.
+// Two values of a lane side by side.
+__device__ __forceinline__ uint64_t two(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void apart(uint64_t v, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t plus2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t minus2(uint64_t a, uint64_t b) {   // b * -1 + a, one rounding
+    constexpr uint64_t kMinusOnes = 0xbf800000bf800000ull;
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(b), "l"(kMinusOnes), "l"(a));
+    return r;
+}
+
+// add_excess of two values into two sums, two values an instruction.
 template <bool HAS_Q>
-__device__ __forceinline__ Sum sum_part(const float* pr, const float* qr, int v0, int V, int out) {
-    constexpr int N = kSegment / 32;
-    float x[N], y[HAS_Q ? N : 1];
+__device__ __forceinline__ void add_excess2(uint64_t& hi, uint64_t& lo, float x0, float x1, float y0, float y1) {
+    float d0 = x0, d1 = x1;
+    uint64_t err = 0;
+    if constexpr (HAS_Q) {
+        const uint64_t x = two(x0, x1), y = two(y0, y1);
+        const uint64_t diff = minus2(x, y);
+        const uint64_t b = minus2(x, diff);
+        err = plus2(minus2(x, plus2(diff, b)), minus2(b, y));
+        float e0, e1;
+        apart(diff, d0, d1);
+        apart(err, e0, e1);
+        err = two(d0 > 0.f ? e0 : 0.f, d1 > 0.f ? e1 : 0.f);
+    }
+    const uint64_t d = two(fmaxf(d0, 0.f), fmaxf(d1, 0.f));   // NaN: 0
+    const uint64_t s = plus2(hi, d);
+    const uint64_t b = minus2(s, hi);
+    const uint64_t lost = plus2(minus2(hi, minus2(s, b)), minus2(d, b));
+    lo = plus2(lo, HAS_Q ? plus2(lost, err) : lost);
+    hi = s;
+}
+
+// A lane's part of the sum of the segment of 32 N values at v0: r = max(p - q, 0) or,
+// without q, max(p, 0). Whole segments: VEC with 16-byte loads, or by single values. All
+// loads go out before their use.
+template <int N, bool HAS_Q, bool VEC>
+__device__ __forceinline__ Sum sum_part(const float* pr, const float* qr, int v0, int lane) {
+    float x[N], y[N];
+    if constexpr (VEC) {
+#pragma unroll
+        for (int k = 0; k < N / 4; ++k) {
+            *reinterpret_cast<float4*>(x + 4 * k) = __ldg(reinterpret_cast<const float4*>(pr + v0) + lane + 32 * k);
+            if constexpr (HAS_Q)
+                *reinterpret_cast<float4*>(y + 4 * k) = __ldg(reinterpret_cast<const float4*>(qr + v0) + lane + 32 * k);
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            x[k] = __ldg(pr + v0 + lane + 32 * k);
+            if constexpr (HAS_Q) y[k] = __ldg(qr + v0 + lane + 32 * k);
+        }
+    }
+    uint64_t hi = 0, lo = 0;
+#pragma unroll
+    for (int k = 0; k < N; k += 2) add_excess2<HAS_Q>(hi, lo, x[k], x[k + 1], HAS_Q ? y[k] : 0.f, HAS_Q ? y[k + 1] : 0.f);
+    Sum a, b;
+    apart(hi, a.hi, b.hi);
+    apart(lo, a.lo, b.lo);
+    return a.plus(b);
+}
+
+// The same for a segment that ends behind the row, or holds the value `out` that is left out.
+template <int N>
+__device__ __forceinline__ Sum sum_some(const float* pr, const float* qr, int v0, int lane, int V, int out) {
+    float x[N], y[N];
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-        const int v = v0 + 32 * k;
-        x[k] = v < V && (HAS_Q || v != out) ? __ldg(pr + v) : 0.f;
-        if constexpr (HAS_Q) y[k] = v < V ? __ldg(qr + v) : 0.f;
+        const int v = v0 + lane + 32 * k;
+        x[k] = v < V && v != out ? __ldg(pr + v) : 0.f;
+        y[k] = v < V && qr != nullptr ? __ldg(qr + v) : 0.f;
     }
     Sum sum{0.f, 0.f};
 #pragma unroll
-    for (int k = 0; k < N; ++k) add_excess(sum, x[k], HAS_Q ? y[k] : 0.f);
+    for (int k = 0; k < N; ++k) add_excess(sum, x[k], y[k]);
     return sum.order();
 }
 
-__global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyParams p, int segs_per_cta) {
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) verify_kernel(const VerifyParams p, int segs_per_cta) {
+    constexpr int kSegment = THREADS;         // a value a thread, in the last step
+    constexpr int kWarps = THREADS / 32;
     extern __shared__ double seg_sum[];       // [segs_per_cta]: first each segment's Sum (its bits), then running sums
     __shared__ double cta_total;
     __shared__ Sum warp_total[kWarps], border_left;
@@ -166,9 +239,17 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
             qr = nullptr;
             left_out = -1;
         }
+        constexpr int N = kSegment / 32;
+        const bool vec = ((reinterpret_cast<uintptr_t>(pr) | reinterpret_cast<uintptr_t>(qr)) & 15u) == 0;
         for (int g = warp; g < segs; g += kWarps) {
-            const int v0 = (seg0 + g) * kSegment + lane;
-            Sum v = qr != nullptr ? sum_part<true>(pr, qr, v0, V, -1) : sum_part<false>(pr, nullptr, v0, V, left_out);
+            const int v0 = (seg0 + g) * kSegment;
+            Sum v;
+            if (v0 + kSegment > V || (left_out >= v0 && left_out < v0 + kSegment))
+                v = sum_some<N>(pr, qr, v0, lane, V, left_out);
+            else if (qr != nullptr)
+                v = vec ? sum_part<N, true, true>(pr, qr, v0, lane) : sum_part<N, true, false>(pr, qr, v0, lane);
+            else
+                v = vec ? sum_part<N, false, true>(pr, nullptr, v0, lane) : sum_part<N, false, false>(pr, nullptr, v0, lane);
 #pragma unroll
             for (int off = 16; off > 0; off >>= 1) {
                 Sum o;
@@ -180,16 +261,18 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
         }
         __syncthreads();
         if (warp == 0) {
-            double carry = 0.0;
-            for (int g0 = 0; g0 < segs; g0 += 32) {
-                const bool in = g0 + lane < segs;
-                const double bits = in ? seg_sum[g0 + lane] : 0.0;   // (a Sum of zeros, too)
-                const Sum own{__int_as_float(__double2hiint(bits)), __int_as_float(__double2loint(bits))};
-                const double v = warp_scan(own.value(), lane) + carry;
-                if (in) seg_sum[g0 + lane] = v;
-                carry = __shfl_sync(0xffffffffu, v, min(31, segs - g0 - 1));
+            // Running sums: each lane's run of segments, then the lanes'.
+            const int run = (segs + 31) / 32, g0 = min(segs, lane * run), g1 = min(segs, g0 + run);
+            double own = 0.0;
+            for (int g = g0; g < g1; ++g) {
+                const double bits = seg_sum[g];
+                own += Sum{__int_as_float(__double2hiint(bits)), __int_as_float(__double2loint(bits))}.value();
+                seg_sum[g] = own;
             }
-            if (lane == 0) cta_total = carry;        // the last running sum itself
+            const double before = warp_scan(own, lane) - own;
+            for (int g = g0; g < g1; ++g) seg_sum[g] += before;
+            __syncwarp();
+            if (lane == 0) cta_total = segs > 0 ? seg_sum[segs - 1] : 0.0;
         }
         cluster.sync();
         if (warp == 0) {
@@ -262,13 +345,13 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
             __syncthreads();                  // every thread has read `chosen`
             if (tid == 0) chosen = -1;
             __syncthreads();
-            for (int v = seg0 * kSegment + tid; last_positive < 0 && v < min(V, (seg0 + seg) * kSegment); v += kVerifyThreads)
+            for (int v = seg0 * kSegment + tid; last_positive < 0 && v < min(V, (seg0 + seg) * kSegment); v += THREADS)
                 if (v != left_out && __ldg(pr + v) > (qr != nullptr ? __ldg(qr + v) : 0.f)) atomicMax(&chosen, v);
             if (last_positive >= 0) atomicMax(&chosen, last_positive);
             __syncthreads();
             token = chosen;
         }
-        for (int i = tid; i <= Q; i += kVerifyThreads)
+        for (int i = tid; i <= Q; i += THREADS)
             p.out_tokens[static_cast<size_t>(s) * (Q + 1) + i] = i < a ? __ldg(tokens + i) : i == a ? token : -1;
         if (tid == 0) {
             p.num_accepted[s] = a;
@@ -278,21 +361,17 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
     cluster.barrier_wait(std::move(arrived));
 }
 
-}  // namespace
-
-cudaError_t launch_verify(const VerifyParams& p, cudaStream_t stream) {
-    if (p.num_seqs == 0) return cudaSuccess;
-    const int sms = device_sms();
-    if (sms <= 0) return cudaErrorInvalidDevice;
-    const int segs = (p.vocab + kSegment - 1) / kSegment;
+template <int THREADS>
+cudaError_t launch(const VerifyParams& p, long long ctas, cudaStream_t stream) {
+    const int segs = (p.vocab + THREADS - 1) / THREADS;
     int ranks = 1;
     while (ranks < kMaxCluster && ranks < segs &&
-           (static_cast<long long>(p.num_seqs) * ranks < sms || segs > kMaxSegments * ranks))
+           (static_cast<long long>(p.num_seqs) * ranks < ctas || segs > kMaxSegments * ranks))
         ranks *= 2;
     const int per_cta = (segs + ranks - 1) / ranks;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(p.num_seqs) * ranks);
-    cfg.blockDim = dim3(kVerifyThreads);
+    cfg.blockDim = dim3(THREADS);
     cfg.dynamicSmemBytes = 8 * static_cast<size_t>(per_cta);   // 32 KB at most
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -301,9 +380,21 @@ cudaError_t launch_verify(const VerifyParams& p, cudaStream_t stream) {
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cudaError_t err = cudaLaunchKernelEx(&cfg, verify_kernel, p, per_cta);
+    cudaError_t err = cudaLaunchKernelEx(&cfg, verify_kernel<THREADS>, p, per_cta);
     if (err != cudaSuccess) return err;
     return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_verify(const VerifyParams& p, cudaStream_t stream) {
+    if (p.num_seqs == 0) return cudaSuccess;
+    const int sms = device_sms();
+    if (sms <= 0) return cudaErrorInvalidDevice;
+    // Few sequences: the CTAs of a largest cluster do not fill the device, so that each has
+    // more loads on the way. Many: smaller CTAs, several to an SM, spread evenly.
+    return static_cast<long long>(p.num_seqs) * kMaxCluster <= sms ? launch<512>(p, sms, stream)
+                                                                   : launch<256>(p, 2LL * sms, stream);
 }
 
 }  // namespace pa
