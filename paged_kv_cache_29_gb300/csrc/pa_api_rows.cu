@@ -253,6 +253,7 @@ pa_status pa_evict(void* k_cache, void* v_cache, void* k_params, void* v_params,
     p.num_blocks = num_blocks;
     p.max_blocks_per_seq = max_blocks_per_seq;
     p.context_cap = max_context_len;
+    p.by_block = pa::Divisor(static_cast<uint32_t>(block_size));
     return pa::launch_evict(p, stream_of(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 

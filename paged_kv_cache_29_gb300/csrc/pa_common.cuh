@@ -16,6 +16,17 @@ __device__ __forceinline__ void raise_error(int32_t* error_word, uint32_t bits) 
     if (error_word != nullptr) atomicOr(reinterpret_cast<unsigned int*>(error_word), bits);
 }
 
+// ---- programmatic dependent launch ----------------------------------------------
+// A kernel launched as a programmatic dependent reads and writes global memory
+// behind the wait only: every kernel before it on the stream has completed then.
+__device__ __forceinline__ void grid_dependency_wait() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+__device__ __forceinline__ void grid_launch_dependents() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // ---- shared-memory addresses ------------------------------------------------
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));

@@ -59,14 +59,6 @@
 
 namespace pa {
 
-__device__ __forceinline__ void grid_dependency_wait() {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
-__device__ __forceinline__ void grid_launch_dependents() {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-
 // Block ids of one item: partitions of up to 4096 rows span at most
 // 4096 / 16 + 1 = 257 blocks when block_size is a multiple of 16.
 constexpr int kMaxItemBlocks = 260;

@@ -31,9 +31,8 @@ namespace pa {
 
 namespace {
 
-constexpr int kSelectThreads = 512;
-constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kMaxCluster = 8;
+constexpr int kFew = 256;                     // candidates that are ranked against one another
 constexpr int kCopies = 8;                    // of the digit counts: at most 4 lanes meet in one
 constexpr uint32_t kStays = 0xffffffffu;      // key of a row that stays in any case; no weight has it
 // Keys that a CTA holds. Sequences of more rows than a cluster holds read their weights
@@ -49,17 +48,31 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 
 // One cluster per (sequence, KV head): the list of its rows' moves, and from where on rows
 // change their place.
-__global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const EvictParams p, int max_keys) {
+template <int kSelectThreads>
+__global__ void __launch_bounds__(kSelectThreads, kSelectThreads == 256 ? 5 : 2) evict_select_kernel(const EvictParams p, int max_keys) {
+    constexpr int kSelectWarps = kSelectThreads / 32;
+    static_assert(kSelectThreads >= 256, "a thread per digit, a warp per CTA of the cluster");
     extern __shared__ uint32_t keys[];        // [max_keys]
     __shared__ uint32_t hist[256 * kCopies];
     __shared__ uint32_t digits[2][256];       // this CTA's counts by digit, of two passes
+    __shared__ uint32_t few[2][kFew];         // candidates: this CTA's, the cluster's
+    __shared__ uint32_t few_count[2];
     __shared__ uint32_t scan_sums[8];
-    __shared__ uint32_t found[2];             // digit, rows of larger digits
+    __shared__ uint32_t found[3];             // digit, rows of larger digits, rows of this digit
     __shared__ uint2 warp_counts[kSelectWarps];
     __shared__ uint2 cta_counts;              // rows of the CTA above the border, at it
-    __shared__ int bad, first_move;
+    __shared__ uint2 cluster_counts;          // of the CTAs before it
+    __shared__ int bad, any_bad, first_move;
     cg::cluster_group cluster = cg::this_cluster();
     const int ranks = cluster.num_blocks(), rank = cluster.block_rank();
+    auto meet = [&] {                         // (a barrier of one CTA is the cheaper one)
+        if (ranks > 1)
+            cluster.sync();
+        else
+            __syncthreads();
+    };
+    grid_dependency_wait();
+    grid_launch_dependents();
     const int sh = blockIdx.x / ranks;
     const int s = sh / p.num_kv_heads;
     const int h = sh - s * p.num_kv_heads;
@@ -93,41 +106,52 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
     if (tid == 0) {
         bad = 0;
         first_move = INT_MAX;
+        few_count[0] = few_count[1] = 0;
     }
     for (int i = tid; i < 256 * kCopies; i += kSelectThreads) hist[i] = 0;
     __syncthreads();
-    auto pool_row = [&](int id, int i) { return (static_cast<uint32_t>(id) * p.num_kv_heads + h) * bs + i % bs; };
-    auto load_key = [&](int i) -> uint32_t {  // a row of a block outside the pool: any key
-        const int id = __ldg(from + i / bs);
-        if (id < 0 || id >= p.num_blocks) {
-            bad = 1;
-            return 0u;
-        }
-        return i < first || i >= last ? kStays : weight_key(p.row_weights[pool_row(id, i)]);
+    auto block_index = [&](int i) { return p.by_block.quotient(i); };
+    auto pool_row = [&](int id, int i) {
+        return (static_cast<uint32_t>(id) * p.num_kv_heads + h) * bs + p.by_block.rest(i, block_index(i));
+    };
+    auto key_of = [&](int i, int id) {
+        const uint32_t key = weight_key(p.row_weights[pool_row(id, i)]);
+        return i < first || i >= last ? kStays : key;
     };
     bool outside = false;
     for (int b = rank * kSelectThreads + tid; b < (keep + bs - 1) / bs; b += ranks * kSelectThreads) {
         const int id = __ldg(to + b);
         outside |= id < 0 || id >= p.num_blocks;
     }
-    if (outside) bad = 1;
-    if (held) {
-        constexpr int kAhead = 4;             // loads of a thread before their use
-        for (int i0 = row0 + tid; i0 < row1; i0 += kAhead * kSelectThreads) {
-            uint32_t k[kAhead];
+    constexpr int kRows = 8;                  // rows of a thread whose loads are on the way together
+    for (int i0 = row0 + tid; i0 < row1; i0 += kRows * kSelectThreads) {
+        int id[kRows];
+        uint32_t k[kRows];
 #pragma unroll
-            for (int u = 0; u < kAhead; ++u) k[u] = i0 + u * kSelectThreads < row1 ? load_key(i0 + u * kSelectThreads) : 0u;
+        for (int u = 0; u < kRows; ++u) id[u] = __ldg(from + block_index(min(i0 + u * kSelectThreads, row1 - 1)));
 #pragma unroll
-            for (int u = 0; u < kAhead; ++u)
-                if (i0 + u * kSelectThreads < row1) keys[i0 + u * kSelectThreads - row0] = k[u];
+        for (int u = 0; u < kRows; ++u) {
+            const bool in = id[u] >= 0 && id[u] < p.num_blocks;
+            outside |= !in;
+            if (!in) id[u] = 0;               // (its key is not used)
         }
-    } else {
-        for (int i = row0 + tid; i < row1; i += kSelectThreads) (void)load_key(i);
+        if (!held) continue;
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) k[u] = key_of(min(i0 + u * kSelectThreads, row1 - 1), id[u]);
+#pragma unroll
+        for (int u = 0; u < kRows; ++u)
+            if (i0 + u * kSelectThreads < row1) keys[i0 + u * kSelectThreads - row0] = k[u];
     }
-    cluster.sync();
-    bool any_bad = false;
-    for (int r = 0; r < ranks; ++r) any_bad |= *cluster.map_shared_rank(&bad, r) != 0;
-    if (any_bad) {
+    if (outside) bad = 1;
+    meet();
+    if (ranks > 1) {
+        if (warp == 0) {
+            const bool theirs = __any_sync(0xffffffffu, lane < ranks && *cluster.map_shared_rank(&bad, lane) != 0);
+            if (lane == 0) any_bad = theirs;
+        }
+        __syncthreads();
+    }
+    if (ranks > 1 ? any_bad : bad) {
         if (tid == 0 && rank == 0) {
             if (h == 0) {
                 raise_error(p.error_word, PA_DEVERR_BLOCK_ID);
@@ -135,10 +159,10 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
             }
             p.starts[sh] = INT_MAX;
         }
-        cluster.sync();                       // every CTA has read the others' flags
+        meet();                       // every CTA has read the others' flags
         return;
     }
-    auto key_at = [&](int i) { return held ? keys[i - row0] : load_key(i); };
+    auto key_at = [&](int i) { return held ? keys[i - row0] : key_of(i, __ldg(from + block_index(i))); };
 
     // The more-th largest key of [first, last), and how many rows that hold it stay.
     uint32_t border = 0, level = 0;
@@ -166,11 +190,12 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
             }
             // (The other CTAs read digits[pass & 1]; it is written again two passes on,
             // behind the next pass's barrier.)
-            cluster.sync();
+            meet();
             uint32_t own = 0, incl = 0;
             if (tid < 256) {
                 // Rows of larger digits: an inclusive scan from the top; thread t has digit 255 - t.
-                for (int r = 0; r < ranks; ++r) own += cluster.map_shared_rank(&digits[pass & 1][0], r)[255 - tid];
+                for (int r = 0; r < ranks; ++r)
+                    own += ranks > 1 ? cluster.map_shared_rank(&digits[pass & 1][0], r)[255 - tid] : digits[pass & 1][255 - tid];
                 incl = own;
 #pragma unroll
                 for (int off = 1; off < 32; off <<= 1) {
@@ -185,11 +210,45 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
                 if (incl >= want && incl - own < want) {
                     found[0] = 255 - tid;
                     found[1] = incl - own;
+                    found[2] = own;
                 }
             }
             __syncthreads();
             border |= found[0] << shift;
             want -= found[1];
+            if (shift > 0 && found[2] <= kFew) {
+                // Few rows share the digits so far: the border is the one of them that fewer
+                // than `want` are above, and with its equals at least `want`.
+                const uint32_t digits_so_far = 0xffffffffu << shift;
+                for (int i = row0 + tid; i < row1; i += kSelectThreads) {
+                    const uint32_t key = key_at(i);
+                    if (key != kStays && (key & digits_so_far) == border) few[0][atomicAdd(&few_count[0], 1u)] = key;
+                }
+                meet();
+                if (warp < ranks) {           // a warp takes another CTA's
+                    const uint32_t c = *cluster.map_shared_rank(&few_count[0], warp);
+                    const uint32_t* theirs = cluster.map_shared_rank(&few[0][0], warp);
+                    for (uint32_t i = lane; i < c; i += 32) few[1][atomicAdd(&few_count[1], 1u)] = theirs[i];
+                }
+                __syncthreads();
+                const uint32_t count = few_count[1];
+                for (uint32_t i = tid; i < count; i += kSelectThreads) {
+                    const uint32_t key = few[1][i];
+                    uint32_t larger = 0, same = 0;
+                    for (uint32_t k = 0; k < count; ++k) {
+                        larger += few[1][k] > key;
+                        same += few[1][k] == key;
+                    }
+                    if (larger < want && larger + same >= want) {   // (each of its equals writes the same)
+                        found[0] = key;
+                        found[1] = larger;
+                    }
+                }
+                __syncthreads();
+                border = found[0];
+                want -= found[1];
+                break;                        // (the cluster meets again before a CTA can end)
+            }
         }
         level = want;
     }                                         // else all stay: every key is above 0
@@ -214,40 +273,58 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
         all.x += c.x;
         all.y += c.y;
     }
-    if (tid == 0) cta_counts = all;
-    cluster.sync();
-    for (int r = 0; r < rank; ++r) {
-        const uint2 c = *cluster.map_shared_rank(&cta_counts, r);
-        above += c.x;
-        equal += c.y;
+    if (ranks > 1) {
+        if (tid == 0) cta_counts = all;
+        cluster.sync();
+        if (warp == 0) {
+            const uint2 c = lane < rank ? *cluster.map_shared_rank(&cta_counts, lane) : make_uint2(0, 0);
+            const uint32_t x = __reduce_add_sync(0xffffffffu, c.x), y = __reduce_add_sync(0xffffffffu, c.y);
+            if (lane == 0) cluster_counts = make_uint2(x, y);
+        }
+        __syncthreads();
+        above += cluster_counts.x;
+        equal += cluster_counts.y;
     }
     uint2* list = p.moves + static_cast<size_t>(sh) * p.context_cap;
     int moved = INT_MAX;
-    for (int i = w0 + lane; i - lane < w1; i += 32) {
-        const uint32_t key = i < w1 ? key_at(i) : 0u;
-        const uint32_t va = __ballot_sync(0xffffffffu, i < w1 && key > border);
-        const uint32_t ve = __ballot_sync(0xffffffffu, i < w1 && key == border);
-        const uint32_t before = (1u << lane) - 1u;
-        const uint32_t e = equal + __popc(ve & before);
-        if (i < w1 && (key > border || (key == border && e < level))) {
-            const int j = above + __popc(va & before) + min(e, level);
-            const uint32_t src = pool_row(__ldg(from + i / bs), i), dst = pool_row(__ldg(to + j / bs), j);
-            list[j] = make_uint2(src, dst);
-            if (src != dst) moved = min(moved, j);
+    constexpr int kAhead = 4;                 // rows of a lane whose table entries are on the way together
+    for (int i0 = w0 + lane; i0 - lane < w1; i0 += 32 * kAhead) {
+        int to_row[kAhead], from_id[kAhead], to_id[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int i = i0 + 32 * u;
+            const uint32_t key = i < w1 ? key_at(i) : 0u;
+            const uint32_t va = __ballot_sync(0xffffffffu, i < w1 && key > border);
+            const uint32_t ve = __ballot_sync(0xffffffffu, i < w1 && key == border);
+            const uint32_t before = (1u << lane) - 1u;
+            const uint32_t e = equal + __popc(ve & before);
+            const bool stays = i < w1 && (key > border || (key == border && e < level));
+            to_row[u] = stays ? static_cast<int>(above + __popc(va & before) + min(e, level)) : -1;
+            if (stays) {
+                from_id[u] = __ldg(from + block_index(i));
+                to_id[u] = __ldg(to + block_index(to_row[u]));
+            }
+            above += __popc(va);
+            equal += __popc(ve);
         }
-        above += __popc(va);
-        equal += __popc(ve);
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            if (to_row[u] < 0) continue;
+            const uint32_t src = pool_row(from_id[u], i0 + 32 * u), dst = pool_row(to_id[u], to_row[u]);
+            list[to_row[u]] = make_uint2(src, dst);
+            if (src != dst) moved = min(moved, to_row[u]);
+        }
     }
     moved = __reduce_min_sync(0xffffffffu, moved);
     if (lane == 0 && moved != INT_MAX) atomicMin(&first_move, moved);
-    cluster.sync();
+    meet();
     if (rank == 0 && tid == 0) {
         int start = INT_MAX;
         for (int r = 0; r < ranks; ++r) start = min(start, *cluster.map_shared_rank(&first_move, r));
         p.starts[sh] = start;
         if (h == 0) p.new_lens[s] = keep;
     }
-    cluster.sync();                           // no CTA ends before rank 0 has read it
+    meet();                           // no CTA ends before rank 0 has read it
 }
 
 // Moves: a CTA of WARPS warps per (sequence, KV head, slice). Slices 0 .. 2 slices - 1 are
@@ -299,6 +376,8 @@ __device__ __forceinline__ void move_rows(T* base, const uint2* list, int start,
 
 template <int WARPS>
 __global__ void __launch_bounds__(WARPS * 32) evict_move_kernel(const EvictParams p, int slices, int lanes, int units) {
+    grid_dependency_wait();
+    grid_launch_dependents();
     const int sh = blockIdx.x / units;
     const int part = blockIdx.x - sh * units;
     const int s = sh / p.num_kv_heads;
@@ -330,33 +409,48 @@ cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream) {
     while (ranks < kMaxCluster && static_cast<long long>(heads) * ranks < 2 * sms && p.context_cap / ranks > 2048) ranks *= 2;
     const int share = ((p.context_cap + ranks - 1) / ranks + 31) / 32 * 32;
     const int max_keys = share < kMaxKeys ? share : kMaxKeys;
-    cudaError_t err = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * kMaxKeys);
-    if (err != cudaSuccess) return err;
+    // More threads where a CTA has many rows; else smaller CTAs, more of them to an SM.
+    auto* select = share > 8192 ? evict_select_kernel<512> : evict_select_kernel<256>;
+    cudaError_t err = cudaSuccess;
+    if (max_keys > 8192) {                    // beyond the shared memory that needs no asking
+        err = cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * kMaxKeys);
+        if (err != cudaSuccess) return err;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(heads) * ranks);
-    cfg.blockDim = dim3(kSelectThreads);
+    cfg.blockDim = dim3(share > 8192 ? 512 : 256);
     cfg.dynamicSmemBytes = 4 * static_cast<size_t>(max_keys);
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = ranks;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    // Programmatic dependents where the keys take little shared memory. Where they take
+    // much, moving CTAs beside selecting ones have little of the SM's memory left for loads
+    // on their way: 128 sequences of 1,640 rows then take 350 us, and 226 without.
+    const bool early = max_keys <= 2048;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    err = cudaLaunchKernelEx(&cfg, evict_select_kernel, p, max_keys);
+    cfg.numAttrs = early ? 2 : 1;
+    err = cudaLaunchKernelEx(&cfg, select, p, max_keys);
     if (err != cudaSuccess) return err;
     // Slices of 32 bytes (a sector), or what divides the row.
     const int pieces = p.row_bytes / 16;
     const int lanes = pieces % 2 == 0 ? 2 : 1;
     const int slices = pieces / lanes;
     const int units = 2 * slices + (p.k_params ? 3 : 1);
-    const unsigned ctas = static_cast<unsigned>(heads) * units;
-    if (static_cast<long long>(heads) * units > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    const long long ctas = static_cast<long long>(heads) * units;
+    if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     // Few units: more rows of each on the way at once.
-    if (ctas < 16u * sms)
-        evict_move_kernel<8><<<ctas, 256, 0, stream>>>(p, slices, lanes, units);
-    else
-        evict_move_kernel<1><<<ctas, 32, 0, stream>>>(p, slices, lanes, units);
+    const bool wide = ctas < 16LL * sms;
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+    cfg.blockDim = dim3(wide ? 256 : 32);
+    cfg.dynamicSmemBytes = 0;
+    cfg.attrs = attr + 1;
+    cfg.numAttrs = early ? 1 : 0;
+    err = cudaLaunchKernelEx(&cfg, wide ? evict_move_kernel<8> : evict_move_kernel<1>, p, slices, lanes, units);
+    if (err != cudaSuccess) return err;
     return cudaGetLastError();
 }
 

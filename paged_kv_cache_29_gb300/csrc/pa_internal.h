@@ -159,6 +159,25 @@ struct NormRopeParams {
 };
 cudaError_t launch_norm_rope(const NormRopeParams& p, pa_dtype dtype, cudaStream_t stream);
 
+// Division of numbers below 2^31 by a divisor that a launch knows: n / d =
+// (hi32(n * mul) + n) >> shift with shift = ceil(log2 d), mul = floor(2^32 (2^shift - d) / d) + 1
+// (a kernel's own division by a number that it learns at run time takes some 20 instructions;
+// with it the walks over a sequence's rows in pa_evict took three times as long).
+struct Divisor {
+    uint32_t d, mul, shift;
+    Divisor() = default;
+    explicit Divisor(uint32_t by) : d(by), mul(1), shift(0) {
+        while ((1ull << shift) < by) ++shift;
+        mul = static_cast<uint32_t>((((1ull << shift) - by) << 32) / by + 1);
+    }
+#ifdef __CUDACC__
+    __device__ __forceinline__ int quotient(int n) const {
+        return static_cast<int>((__umulhi(static_cast<uint32_t>(n), mul) + static_cast<uint32_t>(n)) >> shift);
+    }
+    __device__ __forceinline__ int rest(int n, int quotient) const { return n - quotient * static_cast<int>(d); }
+#endif
+};
+
 // Eviction (pa_evict in the header). moves: for each (sequence, KV head)
 // context_cap pairs of pool rows (from, to), one per row that stays; starts: the first
 // of them that changes its place; new_lens: what lens_out gets.
@@ -180,6 +199,7 @@ struct EvictParams {
     int num_sinks, num_recent;
     int num_seqs, num_kv_heads, row_bytes;
     int block_size, num_blocks, max_blocks_per_seq, context_cap;
+    Divisor by_block;              // block_size
 };
 cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream);
 

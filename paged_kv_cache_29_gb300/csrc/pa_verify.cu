@@ -189,6 +189,8 @@ __global__ void __launch_bounds__(THREADS) verify_kernel(const VerifyParams p, i
     __shared__ int first_rejected, bad, chosen, owner;
     cg::cluster_group cluster = cg::this_cluster();
     const int ranks = cluster.num_blocks(), rank = cluster.block_rank();
+    grid_dependency_wait();
+    grid_launch_dependents();
     const int s = blockIdx.x / ranks;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int Q = p.max_drafts, V = p.vocab;
@@ -374,12 +376,14 @@ cudaError_t launch(const VerifyParams& p, long long ctas, cudaStream_t stream) {
     cfg.blockDim = dim3(THREADS);
     cfg.dynamicSmemBytes = 8 * static_cast<size_t>(per_cta);   // 32 KB at most
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = ranks;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ranks;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     cudaError_t err = cudaLaunchKernelEx(&cfg, verify_kernel<THREADS>, p, per_cta);
     if (err != cudaSuccess) return err;
     return cudaGetLastError();
