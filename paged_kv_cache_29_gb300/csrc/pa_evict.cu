@@ -2,14 +2,15 @@
 //
 // Of the m rows between the first num_sinks and the last num_recent of a sequence,
 // the `more` with the largest weights stay under each KV head. Weights become 32-bit
-// keys in their order; a radix selection, eight bits a pass from the top, finds the
-// more-th largest key and how many of the rows that hold just that key stay: the
-// first ones. A walk over the rows in order then numbers the rows that stay: the
+// keys in their order; passes that count the keys in 256 equal parts of a range, from that
+// of all keys on, find the part with the more-th largest, until few enough are left to be
+// ranked against one another (mostly after one pass): that key, and how many of the
+// rows that hold just that key stay, the first ones. A walk over the rows in order then numbers the rows that stay: the
 // j-th of them moves to row j, and is listed as a pair of pool rows (from, to).
 //
 // A cluster of CTAs shares the rows under one KV head of a sequence. A CTA holds the
 // keys of a run of rows in shared memory, so that the weights are read once; counts by
-// digit, and of rows that stay, are added up through the cluster's shared memory.
+// part, and of rows that stay, are added up through the cluster's shared memory.
 //
 // The list is in the rows' order, to <= from within a sequence: a stretch of the list
 // that was read whole may be written whatever of it stands in its way, and no
@@ -33,7 +34,8 @@ namespace {
 
 constexpr int kMaxCluster = 8;
 constexpr int kFew = 256;                     // candidates that are ranked against one another
-constexpr int kCopies = 8;                    // of the digit counts: at most 4 lanes meet in one
+constexpr int kCopies = 2;                    // of the counts: 16 lanes at most meet in one
+constexpr int kApart = -1;                    // in place of a first move: no block is moved from and to
 constexpr uint32_t kStays = 0xffffffffu;      // key of a row that stays in any case; no weight has it
 // Keys that a CTA holds. Sequences of more rows than a cluster holds read their weights
 // again in every pass.
@@ -49,20 +51,22 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 // One cluster per (sequence, KV head): the list of its rows' moves, and from where on rows
 // change their place.
 template <int kSelectThreads>
-__global__ void __launch_bounds__(kSelectThreads, kSelectThreads == 256 ? 5 : 2) evict_select_kernel(const EvictParams p, int max_keys) {
+__global__ void __launch_bounds__(kSelectThreads, kSelectThreads == 256 ? 4 : 2) evict_select_kernel(const EvictParams p, int max_keys) {
     constexpr int kSelectWarps = kSelectThreads / 32;
-    static_assert(kSelectThreads >= 256, "a thread per digit, a warp per CTA of the cluster");
+    static_assert(kSelectThreads >= 256, "a thread per part, a warp per CTA of the cluster");
     extern __shared__ uint32_t keys[];        // [max_keys]
     __shared__ uint32_t hist[256 * kCopies];
-    __shared__ uint32_t digits[2][256];       // this CTA's counts by digit, of two passes
+    __shared__ uint32_t parts[2][256];       // this CTA's counts by part, of two passes
     __shared__ uint32_t few[2][kFew];         // candidates: this CTA's, the cluster's
     __shared__ uint32_t few_count[2];
+    __shared__ uint32_t range[2], all_range[2];   // least and largest key of a weight
     __shared__ uint32_t scan_sums[8];
-    __shared__ uint32_t found[3];             // digit, rows of larger digits, rows of this digit
+    __shared__ uint32_t found[3];             // part, rows of larger parts, rows of this part
     __shared__ uint2 warp_counts[kSelectWarps];
     __shared__ uint2 cta_counts;              // rows of the CTA above the border, at it
     __shared__ uint2 cluster_counts;          // of the CTAs before it
-    __shared__ int bad, any_bad, first_move;
+    __shared__ int flags, all_flags, first_move;
+    constexpr int kBad = 1, kSame = 2;        // a block outside the pool; one that rows stay in
     cg::cluster_group cluster = cg::this_cluster();
     const int ranks = cluster.num_blocks(), rank = cluster.block_rank();
     auto meet = [&] {                         // (a barrier of one CTA is the cheaper one)
@@ -104,9 +108,11 @@ __global__ void __launch_bounds__(kSelectThreads, kSelectThreads == 256 ? 5 : 2)
     const int w0 = min(row1, row0 + warp * warp_share), w1 = min(row1, w0 + warp_share);
     const bool held = share <= max_keys;
     if (tid == 0) {
-        bad = 0;
+        flags = 0;
         first_move = INT_MAX;
         few_count[0] = few_count[1] = 0;
+        range[0] = kStays;
+        range[1] = 0;
     }
     for (int i = tid; i < 256 * kCopies; i += kSelectThreads) hist[i] = 0;
     __syncthreads();
@@ -118,10 +124,12 @@ __global__ void __launch_bounds__(kSelectThreads, kSelectThreads == 256 ? 5 : 2)
         const uint32_t key = weight_key(p.row_weights[pool_row(id, i)]);
         return i < first || i >= last ? kStays : key;
     };
-    bool outside = false;
+    bool outside = false, same = false;
+    uint32_t least = kStays, most = 0;        // of the weights' keys
     for (int b = rank * kSelectThreads + tid; b < (keep + bs - 1) / bs; b += ranks * kSelectThreads) {
         const int id = __ldg(to + b);
         outside |= id < 0 || id >= p.num_blocks;
+        same |= id == __ldg(from + b);
     }
     constexpr int kRows = 8;                  // rows of a thread whose loads are on the way together
     for (int i0 = row0 + tid; i0 < row1; i0 += kRows * kSelectThreads) {
@@ -135,23 +143,42 @@ __global__ void __launch_bounds__(kSelectThreads, kSelectThreads == 256 ? 5 : 2)
             outside |= !in;
             if (!in) id[u] = 0;               // (its key is not used)
         }
-        if (!held) continue;
 #pragma unroll
         for (int u = 0; u < kRows; ++u) k[u] = key_of(min(i0 + u * kSelectThreads, row1 - 1), id[u]);
 #pragma unroll
         for (int u = 0; u < kRows; ++u)
-            if (i0 + u * kSelectThreads < row1) keys[i0 + u * kSelectThreads - row0] = k[u];
+            if (i0 + u * kSelectThreads < row1) {
+                if (held) keys[i0 + u * kSelectThreads - row0] = k[u];
+                if (k[u] != kStays) {
+                    least = min(least, k[u]);
+                    most = max(most, k[u]);
+                }
+            }
     }
-    if (outside) bad = 1;
+    if (outside) atomicOr(&flags, kBad);
+    if (same) atomicOr(&flags, kSame);
+    least = __reduce_min_sync(0xffffffffu, least);
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 0) {
+        atomicMin(&range[0], least);
+        atomicMax(&range[1], most);
+    }
     meet();
-    if (ranks > 1) {
-        if (warp == 0) {
-            const bool theirs = __any_sync(0xffffffffu, lane < ranks && *cluster.map_shared_rank(&bad, lane) != 0);
-            if (lane == 0) any_bad = theirs;
+    if (warp == 0) {
+        const int theirs = lane >= ranks ? 0 : ranks > 1 ? *cluster.map_shared_rank(&flags, lane) : flags;
+        const uint32_t all = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(theirs));
+        least = lane >= ranks ? kStays : ranks > 1 ? cluster.map_shared_rank(&range[0], lane)[0] : range[0];
+        most = lane >= ranks ? 0u : ranks > 1 ? cluster.map_shared_rank(&range[0], lane)[1] : range[1];
+        least = __reduce_min_sync(0xffffffffu, least);
+        most = __reduce_max_sync(0xffffffffu, most);
+        if (lane == 0) {
+            all_flags = static_cast<int>(all);
+            all_range[0] = least;
+            all_range[1] = most;
         }
-        __syncthreads();
     }
-    if (ranks > 1 ? any_bad : bad) {
+    __syncthreads();
+    if (all_flags & kBad) {
         if (tid == 0 && rank == 0) {
             if (h == 0) {
                 raise_error(p.error_word, PA_DEVERR_BLOCK_ID);
@@ -159,7 +186,7 @@ __global__ void __launch_bounds__(kSelectThreads, kSelectThreads == 256 ? 5 : 2)
             }
             p.starts[sh] = INT_MAX;
         }
-        meet();                       // every CTA has read the others' flags
+        meet();                               // every CTA has read the others' flags
         return;
     }
     auto key_at = [&](int i) { return held ? keys[i - row0] : key_of(i, __ldg(from + block_index(i))); };
@@ -170,13 +197,15 @@ __global__ void __launch_bounds__(kSelectThreads, kSelectThreads == 256 ? 5 : 2)
         border = kStays - 1;                  // no weight's key is that large
     } else if (more < last - first) {
         uint32_t want = more;
-        for (int pass = 0; pass < 4; ++pass) {
-            const int shift = 24 - 8 * pass;
-            const uint32_t mask = pass == 0 ? 0u : 0xffffffffu << (shift + 8);
+        border = all_range[0];                // least key of the range, 256 parts of 2^shift
+        int shift = max(0, 24 - __clz(all_range[1] - border));
+        uint32_t in_range = 256;              // parts that the range has
+        auto part_of = [&](uint32_t key) { return (key - border) >> shift; };
+        for (int pass = 0;; ++pass) {
             for (int i = row0 + tid; i < row1; i += kSelectThreads) {
                 const uint32_t key = key_at(i);
-                if (key != kStays && (key & mask) == border)
-                    atomicAdd(&hist[((key >> shift) & 255u) * kCopies + (lane & (kCopies - 1))], 1u);
+                if (key != kStays && part_of(key) < in_range)   // (below the range: it wraps beyond)
+                    atomicAdd(&hist[part_of(key) * kCopies + (lane & (kCopies - 1))], 1u);
             }
             __syncthreads();
             if (tid < 256) {
@@ -186,16 +215,16 @@ __global__ void __launch_bounds__(kSelectThreads, kSelectThreads == 256 ? 5 : 2)
                     sum += hist[tid * kCopies + c];
                     hist[tid * kCopies + c] = 0;
                 }
-                digits[pass & 1][tid] = sum;
+                parts[pass & 1][tid] = sum;
             }
-            // (The other CTAs read digits[pass & 1]; it is written again two passes on,
+            // (The other CTAs read parts[pass & 1]; it is written again two passes on,
             // behind the next pass's barrier.)
             meet();
             uint32_t own = 0, incl = 0;
             if (tid < 256) {
-                // Rows of larger digits: an inclusive scan from the top; thread t has digit 255 - t.
+                // Rows of larger parts: an inclusive scan from the top; thread t has part 255 - t.
                 for (int r = 0; r < ranks; ++r)
-                    own += ranks > 1 ? cluster.map_shared_rank(&digits[pass & 1][0], r)[255 - tid] : digits[pass & 1][255 - tid];
+                    own += ranks > 1 ? cluster.map_shared_rank(&parts[pass & 1][0], r)[255 - tid] : parts[pass & 1][255 - tid];
                 incl = own;
 #pragma unroll
                 for (int off = 1; off < 32; off <<= 1) {
@@ -214,15 +243,15 @@ __global__ void __launch_bounds__(kSelectThreads, kSelectThreads == 256 ? 5 : 2)
                 }
             }
             __syncthreads();
-            border |= found[0] << shift;
+            border += found[0] << shift;
             want -= found[1];
-            if (shift > 0 && found[2] <= kFew) {
-                // Few rows share the digits so far: the border is the one of them that fewer
-                // than `want` are above, and with its equals at least `want`.
-                const uint32_t digits_so_far = 0xffffffffu << shift;
+            if (shift == 0) break;
+            if (found[2] <= kFew) {
+                // Few rows are in that part: the border is the key of the one that fewer than
+                // `want` are above, and with its equals at least `want`.
                 for (int i = row0 + tid; i < row1; i += kSelectThreads) {
                     const uint32_t key = key_at(i);
-                    if (key != kStays && (key & digits_so_far) == border) few[0][atomicAdd(&few_count[0], 1u)] = key;
+                    if (key != kStays && part_of(key) == 0u) few[0][atomicAdd(&few_count[0], 1u)] = key;
                 }
                 meet();
                 if (warp < ranks) {           // a warp takes another CTA's
@@ -249,6 +278,8 @@ __global__ void __launch_bounds__(kSelectThreads, kSelectThreads == 256 ? 5 : 2)
                 want -= found[1];
                 break;                        // (the cluster meets again before a CTA can end)
             }
+            in_range = shift >= 8 ? 256u : 1u << shift;
+            shift = max(0, shift - 8);
         }
         level = want;
     }                                         // else all stay: every key is above 0
@@ -321,24 +352,25 @@ __global__ void __launch_bounds__(kSelectThreads, kSelectThreads == 256 ? 5 : 2)
     if (rank == 0 && tid == 0) {
         int start = INT_MAX;
         for (int r = 0; r < ranks; ++r) start = min(start, *cluster.map_shared_rank(&first_move, r));
-        p.starts[sh] = start;
+        p.starts[sh] = all_flags & kSame ? start : kApart;
         if (h == 0) p.new_lens[s] = keep;
     }
     meet();                           // no CTA ends before rank 0 has read it
 }
 
-// Moves: a CTA of WARPS warps per (sequence, KV head, slice). Slices 0 .. 2 slices - 1 are
-// parts of the K and V rows, of `lanes` 16-byte pieces, the ones after them the 4-byte
-// values beside the rows.
-constexpr int kBatch = 8;                     // rows of a lane per stretch
+// Moves: `ctas` CTAs of WARPS warps per (sequence, KV head). The 16-byte pieces of a K and a V
+// row side by side, and the 4-byte values beside them, are a row. Where no block is moved from
+// and to, each CTA takes a run of whole rows; else each takes slices (of `lanes` pieces) of
+// every row, and the last one the values.
 
-// lanes: lanes that share a row (a power of two), pitch: elements of T from row to row.
-template <typename T, int WARPS>
-__device__ __forceinline__ void move_rows(T* base, const uint2* list, int start, int count, int lanes, size_t pitch) {
+// List entries [start, count): a lane moves the element at `at` of its rows (none if null),
+// `lanes` lanes (a power of two) share a row, pitch: elements from row to row.
+// kBatch: rows of a lane per stretch.
+template <typename T, int WARPS, int kBatch>
+__device__ __forceinline__ void move_rows(T* at, const uint2* list, int start, int count, int lanes, size_t pitch) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int per = 32 / lanes;               // rows of a warp at a time
     const int own = warp * per + lane / lanes;
-    T* at = base + lane % lanes;
     const int step = WARPS * per;
     uint2 mv[kBatch], mv_next[kBatch];
     T v[kBatch], v_next[kBatch];
@@ -352,7 +384,7 @@ __device__ __forceinline__ void move_rows(T* base, const uint2* list, int start,
     auto read = [&](T (&x)[kBatch], const uint2 (&m)[kBatch], int j0) {
 #pragma unroll
         for (int u = 0; u < kBatch; ++u)
-            if (j0 + u * step + own < count) x[u] = at[m[u].x * pitch];
+            if (at != nullptr && j0 + u * step + own < count) x[u] = at[m[u].x * pitch];
     };
     look(mv, start);
     read(v, mv, start);
@@ -364,7 +396,7 @@ __device__ __forceinline__ void move_rows(T* base, const uint2* list, int start,
         __syncthreads();
 #pragma unroll
         for (int u = 0; u < kBatch; ++u)
-            if (j0 + u * step + own < count) at[mv[u].y * pitch] = v[u];
+            if (at != nullptr && j0 + u * step + own < count) at[mv[u].y * pitch] = v[u];
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
             mv[u] = mv_next[u];
@@ -374,27 +406,49 @@ __device__ __forceinline__ void move_rows(T* base, const uint2* list, int start,
     }
 }
 
-template <int WARPS>
-__global__ void __launch_bounds__(WARPS * 32) evict_move_kernel(const EvictParams p, int slices, int lanes, int units) {
+template <int WARPS, int kBatch>
+__global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? 3 : 4) evict_move_kernel(const EvictParams p, int lanes, int ctas) {
     grid_dependency_wait();
     grid_launch_dependents();
-    const int sh = blockIdx.x / units;
-    const int part = blockIdx.x - sh * units;
+    const int sh = blockIdx.x / ctas;
+    const int part = blockIdx.x - sh * ctas;
     const int s = sh / p.num_kv_heads;
-    const int count = p.new_lens[s];
+    int count = p.new_lens[s];
+    int start = p.starts[sh];
     // Nothing reads the lengths any more: lens_out may be the array they are in.
     if (part == 0 && sh == s * p.num_kv_heads && threadIdx.x == 0) p.lens_out[s] = count;
-    const int start = p.starts[sh];
+    const int pieces = 2 * (p.row_bytes / 16);
+    int slice = part, step = ctas - 1;
+    bool values = part == ctas - 1;
+    if (start == kApart) {
+        lanes = min(32, pieces & -pieces);
+        const int run = max((count + ctas - 1) / ctas, WARPS * kBatch * 32 / lanes);   // a stretch at least
+        start = min(count, part * run);
+        count = min(count, start + run);
+        slice = 0;
+        step = 1;
+        values = true;
+    }
     if (start >= count) return;
     const uint2* list = p.moves + static_cast<size_t>(sh) * p.context_cap;
-    if (part < 2 * slices) {
-        const int which = part / slices, slice = part - which * slices;
-        uint4* base = static_cast<uint4*>(which ? p.v_cache : p.k_cache) + slice * lanes;
-        move_rows<uint4, WARPS>(base, list, start, count, lanes, p.row_bytes / 16);
-    } else {
-        const int which = part - 2 * slices;
-        uint32_t* base = which == 0 ? reinterpret_cast<uint32_t*>(p.row_weights) : which == 1 ? p.k_params : p.v_params;
-        move_rows<uint32_t, WARPS>(base, list, start, count, 1, 1);
+    const int lane = threadIdx.x & 31;
+    if (slice < step)
+        for (; slice < pieces / lanes; slice += step) {
+            const int piece = slice * lanes + lane % lanes;
+            uint4* at = piece < pieces / 2 ? static_cast<uint4*>(p.k_cache) + piece
+                                           : static_cast<uint4*>(p.v_cache) + (piece - pieces / 2);
+            move_rows<uint4, WARPS, kBatch>(at, list, start, count, lanes, p.row_bytes / 16);
+        }
+    if (values) {
+        if (p.k_params == nullptr) {
+            move_rows<uint32_t, WARPS, kBatch>(reinterpret_cast<uint32_t*>(p.row_weights), list, start, count, 1, 1);
+        } else {                              // three values in a group of four lanes
+            uint32_t* at = lane % 4 == 0   ? reinterpret_cast<uint32_t*>(p.row_weights)
+                           : lane % 4 == 1 ? p.k_params
+                           : lane % 4 == 2 ? p.v_params
+                                           : nullptr;
+            move_rows<uint32_t, WARPS, kBatch>(at, list, start, count, 4, 1);
+        }
     }
 }
 
@@ -435,21 +489,23 @@ cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream) {
     cfg.numAttrs = early ? 2 : 1;
     err = cudaLaunchKernelEx(&cfg, select, p, max_keys);
     if (err != cudaSuccess) return err;
-    // Slices of 32 bytes (a sector), or what divides the row.
-    const int pieces = p.row_bytes / 16;
-    const int lanes = pieces % 2 == 0 ? 2 : 1;
+    // Slices of 128 bytes, or what divides the rows. Few sequences: of 32 bytes (a sector), larger
+    // CTAs and more of them.
+    const int pieces = 2 * (p.row_bytes / 16);
+    const bool wide = heads < sms;
+    const int most_ctas = wide ? 32 : 64;
+    int lanes = 1;
+    while (lanes < (wide ? 2 : 8) && pieces % (2 * lanes) == 0) lanes *= 2;
+    while (lanes < 32 && pieces / lanes >= most_ctas && pieces % (2 * lanes) == 0) lanes *= 2;
     const int slices = pieces / lanes;
-    const int units = 2 * slices + (p.k_params ? 3 : 1);
-    const long long ctas = static_cast<long long>(heads) * units;
-    if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    // Few units: more rows of each on the way at once.
-    const bool wide = ctas < 16LL * sms;
-    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-    cfg.blockDim = dim3(wide ? 256 : 32);
+    const int ctas = wide || slices >= most_ctas ? most_ctas : slices + 1;
+    if (static_cast<long long>(heads) * ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    cfg.gridDim = dim3(static_cast<unsigned>(heads) * ctas);
+    cfg.blockDim = dim3(wide ? 256 : 128);
     cfg.dynamicSmemBytes = 0;
     cfg.attrs = attr + 1;
     cfg.numAttrs = early ? 1 : 0;
-    err = cudaLaunchKernelEx(&cfg, wide ? evict_move_kernel<8> : evict_move_kernel<1>, p, slices, lanes, units);
+    err = cudaLaunchKernelEx(&cfg, wide ? evict_move_kernel<8, 4> : evict_move_kernel<4, 8>, p, lanes, ctas);
     if (err != cudaSuccess) return err;
     return cudaGetLastError();
 }

@@ -200,3 +200,22 @@ def test_captured_and_replayed_in_place():
     graph.replay()
     torch.cuda.synchronize()
     assert np.array_equal(raw(e.k), first) and list(out.cpu()) == [120, 64]
+
+
+def narrow(kind, r, shape):
+    """Weights in ranges where counting passes end in parts of less than a byte's width, or of one key."""
+    base = np.float32(1.0).view(np.uint32)
+    spread = {"300 keys": 300, "2^12 keys": 1 << 12, "2^19 keys": 1 << 19, "one key": 1}[kind]
+    bits = base + r.integers(0, spread, shape).astype(np.uint32)
+    w = bits.view(np.float32)
+    w[r.random(shape) < 0.05] = 0.0                    # far below the others
+    return w
+
+
+@pytest.mark.parametrize("kind", ["300 keys", "2^12 keys", "2^19 keys", "one key"])
+@pytest.mark.parametrize("n", [600, 5000, 40000])
+@pytest.mark.parametrize("place", ["same", "other"])
+def test_weights_that_are_close_together(kind, n, place):
+    e = Evict([n, n // 2, 3], [n // 3, n // 2 - 1, 1], 1, 0, "bf16", hkv=2, D=8, place=place, seed=n, weights="equal")
+    e.w = narrow(kind, np.random.default_rng(n), e.w.shape)
+    e.check()
