@@ -24,10 +24,11 @@ long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 cudaStream_t stream_of(struct CUstream_st* s) { return reinterpret_cast<cudaStream_t>(s); }
 
 // Workspace of one launch of at most kPlanMaxSeqs sequences, as pa_decode lays it
-// out: 256 bytes, the work items, the partitions' maxima and sums, their outputs;
-// pa_decode_weights has the maxima and sums of single partitions too, and the scores.
+// out: 256 bytes (the number of work items first), the work items, the partitions' maxima and sums, their outputs;
+// pa_decode_weights has the maxima and sums of single partitions too, those of whole
+// sequences, and the scores.
 struct Layout {
-    size_t items, ml, o, scores, total;
+    size_t items, ml, o, final_ml, scores, total;
 };
 
 Layout layout_for(long long num_seqs, long long num_heads, int head_dim, int max_context_len, long long parts,
@@ -39,8 +40,9 @@ Layout layout_for(long long num_seqs, long long num_heads, int head_dim, int max
     w.items = 256;
     w.ml = w.items + 16 * units;
     w.o = w.ml + (weights || parts > 1 ? 8 * prows : 0);
-    w.scores = w.o + (parts > 1 ? 4 * prows * static_cast<size_t>(head_dim) : 0);
-    w.scores = (w.scores + 15) / 16 * 16;
+    w.final_ml = w.o + (parts > 1 ? 4 * prows * static_cast<size_t>(head_dim) : 0);
+    if (weights) w.final_ml = (w.final_ml + 15) / 16 * 16;
+    w.scores = w.final_ml + (weights ? (8 * static_cast<size_t>(seqs) * num_heads * num_queries + 15) / 16 * 16 : 0);
     w.total = w.scores + (weights ? 4 * static_cast<size_t>(seqs) * num_heads * num_queries *
                                         ((static_cast<size_t>(max_context_len) + 15) / 16 * 16)
                                   : 0);
@@ -77,9 +79,18 @@ pa_status rows_call(const void* q, const void* k_cache, const void* v_cache, con
     const int sinks = all ? 0 : (num_sinks < max_context_len ? num_sinks : max_context_len);
     // Rows of the longest sequence's partitions: its first rows in whole tiles,
     // its windows' and up to 15 before them in the same tile.
-    constexpr int P = pa::kDefaultPartition;
-    const long long seen = static_cast<long long>(rows_seen) + 15 + (sinks + 15) / 16 * 16;
+    const long long seen = (static_cast<long long>(rows_seen) + 30) / 16 * 16 + (static_cast<long long>(sinks) + 15) / 16 * 16;
     const long long most = all || seen > max_context_len ? max_context_len : seen;
+    // A windowed sequence in equal partitions of 512 rows or more: 128 sequences with a window
+    // of 1,024 rows and 4 first ones, 1,056 with their tiles, take 87 us in two partitions, 91
+    // in 512 + 512 + 32. By the window alone, so that a sequence's partitions do not depend on
+    // the batch.
+    int P = pa::kDefaultPartition;
+    if (!all) {
+        const long long equal = (seen + P / 2) / P;
+        const long long rows = equal > 0 ? ceil_div(ceil_div(seen, equal), 16) * 16 : 0;
+        if (rows > P) P = static_cast<int>(rows);
+    }
     const long long parts = most > 0 ? ceil_div(most, P) : 1;
     const long long chunk = num_seqs < pa::kPlanMaxSeqs ? num_seqs : pa::kPlanMaxSeqs;
     if (parts * chunk * num_kv_heads > 0x3fffffffLL) return PA_ERR_UNSUPPORTED;
@@ -98,8 +109,10 @@ pa_status rows_call(const void* q, const void* k_cache, const void* v_cache, con
     if (parts > 1) base.part_o = reinterpret_cast<float*>(ws + lay.o);
     if (weights) {
         base.row_weights = row_weights;
+        base.final_ml = reinterpret_cast<float2*>(ws + lay.final_ml);
         base.scores = reinterpret_cast<float*>(ws + lay.scores);
         base.score_rows = (max_context_len + 15) / 16 * 16;
+        base.item_count = reinterpret_cast<int32_t*>(ws);
     }
     base.error_word = error_word;
     base.scale_log2 = scale * kLog2e;
@@ -145,7 +158,8 @@ pa_status rows_call(const void* q, const void* k_cache, const void* v_cache, con
                                           : pa::launch_decode_sinks(tk, tv, p, dtype, sms, stream_of(stream));
         if (err != cudaSuccess) return PA_ERR_CUDA;
         if (parts > 1 && pa::launch_combine(p, dtype, stream_of(stream)) != cudaSuccess) return PA_ERR_CUDA;
-        if (weights && pa::launch_row_weights(p, stream_of(stream)) != cudaSuccess) return PA_ERR_CUDA;
+        if (weights && pa::launch_row_weights(p, ring ? p.item_count : nullptr, stream_of(stream)) != cudaSuccess)
+            return PA_ERR_CUDA;
     }
     return PA_OK;
 }

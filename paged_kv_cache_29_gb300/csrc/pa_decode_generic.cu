@@ -264,6 +264,7 @@ __global__ void __launch_bounds__(kCombineMaxWarps * 32) combine_kernel(const De
                 const int d = lane + 32 * e;
                 if (d < D) ElemTraits<T>::store(out + d, acc[e] / L);
             }
+            if (p.final_ml != nullptr && lane == 0) p.final_ml[row] = make_float2(M, L);
         } else {
             float* st = sm + warp * (D + 2);
             if (lane == 0) {
@@ -283,6 +284,7 @@ __global__ void __launch_bounds__(kCombineMaxWarps * 32) combine_kernel(const De
     for (int w = 0; w < nw; ++w) M = fmaxf(M, sm[w * (D + 2)]);
     float L = 0.f;
     for (int w = 0; w < nw; ++w) L = fmaf(fast_exp2(sm[w * (D + 2)] - M), sm[w * (D + 2) + 1], L);
+    if (p.final_ml != nullptr && threadIdx.x == 0) p.final_ml[row] = make_float2(M, L);
     T* out = static_cast<T*>(p.out) + row * D;
     for (int d = threadIdx.x; d < D; d += blockDim.x) {
         float a = 0.f;

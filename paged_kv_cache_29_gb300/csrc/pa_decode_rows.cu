@@ -91,6 +91,8 @@ __global__ void __launch_bounds__(kThreads) decode_rows_kernel(const DecodeParam
     __syncthreads();
     if (bad) {
         if (threadIdx.x == 0) raise_error(p.error_word, PA_DEVERR_BLOCK_ID);
+        if (p.scores != nullptr)
+            for (int c = threadIdx.x; c < cols; c += kThreads) p.part_ml[2 * (out_row(c) * p.max_parts + part) + 1] = kNoSum;
         return;
     }
     const T* kc = static_cast<const T*>(p.k_cache);
@@ -162,65 +164,121 @@ __global__ void __launch_bounds__(kThreads) decode_rows_kernel(const DecodeParam
     }
 }
 
-// Row weights: a CTA per (sequence, KV head, kChunk rows) takes the final maximum and
-// sum of every query column from the partitions' states, then for each row
-//   w = sum_c 2^(score_c - M_c) / L_c,
-// stored for the rows of this call's tokens, added for the others (atomically:
-// sequences may share a block).
+// Row weights: with the final maximum and sum of every query column (of a merged sequence
+// the merge's, else its only partition's)
+//   w = sum_c 2^(score_c - M_c) / L_c
+// for every row, stored for the rows of this call's tokens, added for the others
+// (atomically: sequences may share a block). A partition with a block outside the pool, flagged
+// by the decode kernel, has the sum kNoSum: its sequence keeps its weights.
+//
+// A warp takes 128 rows of a partition under one KV head, four a lane; all that it loads
+// (states, scores, block ids) is on the way together, so that the time is some three
+// latencies of memory, in 1.5 rounds of warps for 128 sequences of 1,640 rows (a CTA
+// per partition, which found its columns' states from all partitions first, took
+// three times as long).
 constexpr int kWeightThreads = 256;
-constexpr int kChunk = 1024;
+constexpr int kWeightRows = 4;                // of a lane
+constexpr int kWeightUnit = 32 * kWeightRows;
+constexpr int kWeightSplit = kDefaultPartition / kWeightUnit;   // warps of a partition
+constexpr int kWeightItems = kWeightThreads / 32 / kWeightSplit;   // partitions of a CTA at a time
+static_assert(kDefaultPartition % kWeightUnit == 0 && kWeightThreads / 32 % kWeightSplit == 0, "whole warps");
 
-__global__ void __launch_bounds__(kWeightThreads) row_weights_kernel(const DecodeParams p) {
-    extern __shared__ float ml[];             // [cols][2]: M, 1 / L
-    __shared__ int bad;
-    const int chunk = blockIdx.x / (p.num_seqs * p.num_kv_heads);
-    const int sh = blockIdx.x - chunk * (p.num_seqs * p.num_kv_heads);
-    const int s = sh / p.num_kv_heads;
-    const int h = sh - s * p.num_kv_heads;
-    const int Q = p.num_queries;
-    const int n = __ldg(p.context_lens + s);
-    const int i0 = chunk * kChunk;
-    if (n > p.context_cap || n < Q || i0 >= n) return;         // empty, flagged, or past its rows
-    const int grp = p.num_heads / p.num_kv_heads;
+// LISTED: the partitions are those of the tile ring's work list, item_count[0] of them; else
+// (the plain kernel has no list) all that there may be.
+template <bool LISTED>
+__global__ void __launch_bounds__(kWeightThreads) row_weights_kernel(const DecodeParams p, const int32_t* item_count,
+                                                                     int most_items) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int lane = threadIdx.x & 31;
+    const int grp = p.num_heads / p.num_kv_heads, Q = p.num_queries;
     const int cols = grp * Q;
-    const int P = p.partition_size, nparts = (n + P - 1) / P;
     const int bs = p.block_size;
-    const int32_t* table = p.block_tables + static_cast<size_t>(s) * p.max_blocks_per_seq;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // A sequence with a block outside the pool (flagged by the decode kernel) keeps its weights.
-    if (threadIdx.x == 0) bad = 0;
-    __syncthreads();
-    for (int b = threadIdx.x; b < (n + bs - 1) / bs; b += kWeightThreads) {
-        const int id = __ldg(table + b);
-        if (id < 0 || id >= p.num_blocks) bad = 1;
-    }
-    for (int c = warp; c < cols; c += kWeightThreads / 32) {
-        const size_t row = (static_cast<size_t>(s) * Q + c / grp) * p.num_heads + h * grp + c % grp;
-        const float* st = p.part_ml + 2 * row * p.max_parts;
-        float M = -INFINITY;
-        for (int i = lane; i < nparts; i += 32) M = fmaxf(M, st[2 * i]);
-        M = warp_max(M);
-        const float ref = M == -INFINITY ? 0.f : M;
-        float L = 0.f;
-        for (int i = lane; i < nparts; i += 32) L += fast_exp2(st[2 * i] - ref) * st[2 * i + 1];
-        L = warp_sum(L);
-        if (lane == 0) {
-            ml[2 * c] = ref;
-            ml[2 * c + 1] = 1.f / L;
+    const int warp = threadIdx.x >> 5, sub = warp % kWeightSplit;
+    const int items = LISTED ? item_count[0] : most_items;
+    for (int k = blockIdx.x * kWeightItems + warp / kWeightSplit; k < items; k += gridDim.x * kWeightItems) {
+        int s, h, part, n;
+        if constexpr (LISTED) {
+            const int4 it = p.items[k];
+            s = it.x;
+            h = it.y;
+            part = it.z;
+            n = it.w;
+        } else {
+            const int bh = p.num_seqs * p.num_kv_heads;
+            part = k / bh;
+            s = (k - part * bh) / p.num_kv_heads;
+            h = k - part * bh - s * p.num_kv_heads;
+            n = __ldg(p.context_lens + s);
+            if (n > p.context_cap || n < Q) continue;                        // flagged or empty
         }
-    }
-    __syncthreads();
-    if (bad) return;
-    const float* sc = p.scores + (static_cast<size_t>(s) * p.num_kv_heads + h) * p.score_rows * cols;
-    for (int i = i0 + threadIdx.x; i < min(n, i0 + kChunk); i += kWeightThreads) {
-        float w = 0.f;
-        for (int c = 0; c < cols; ++c)
-            w = fmaf(fast_exp2(sc[static_cast<size_t>(i) * cols + c] - ml[2 * c]), ml[2 * c + 1], w);
-        float* at = p.row_weights + (static_cast<size_t>(__ldg(table + i / bs)) * p.num_kv_heads + h) * bs + i % bs;
-        if (i >= n - Q)
-            *at = w;
-        else
-            atomicAdd(at, w);
+        const int i0 = part * kDefaultPartition + sub * kWeightUnit + lane;
+        const int end = min(n, (part + 1) * kDefaultPartition);
+        if (i0 - lane >= end) continue;
+        const int nparts = (n + kDefaultPartition - 1) / kDefaultPartition;
+        const size_t row0 = static_cast<size_t>(s) * Q * p.num_heads + h * grp;   // of column 0
+        const float2* states = reinterpret_cast<const float2*>(p.part_ml);
+        bool no_sum = false;
+        for (int i = lane; i < nparts; i += 32) no_sum |= states[row0 * p.max_parts + i].y == kNoSum;
+        const int32_t* table = p.block_tables + static_cast<size_t>(s) * p.max_blocks_per_seq;
+        int id[kWeightRows];
+        float w[kWeightRows];
+#pragma unroll
+        for (int u = 0; u < kWeightRows; ++u) {
+            const int i = min(i0 + 32 * u, end - 1);
+            id[u] = __ldg(table + i / bs);
+            w[u] = 0.f;
+        }
+        const float* sc = p.scores + (static_cast<size_t>(s) * p.num_kv_heads + h) * p.score_rows * cols;
+        for (int c0 = 0; c0 < cols; c0 += 32) {
+            float2 own = make_float2(0.f, 1.f);
+            if (c0 + lane < cols) {
+                const int c = c0 + lane, j = c / grp;
+                const size_t row = row0 + static_cast<size_t>(j) * p.num_heads + (c - j * grp);
+                own = nparts > 1 ? p.final_ml[row] : states[row * p.max_parts];
+            }
+            own.x = own.x == -INFINITY ? 0.f : own.x;
+            own.y = 1.f / own.y;
+            auto take = [&](int u, float score, int c) {
+                const float m = __shfl_sync(0xffffffffu, own.x, c - c0), r = __shfl_sync(0xffffffffu, own.y, c - c0);
+                w[u] = fmaf(fast_exp2(score - m), r, w[u]);
+            };
+            const int ce = min(cols, c0 + 32);
+            if (cols % 4 == 0) {
+                for (int c = c0; c < ce; c += 4) {
+                    float4 v[kWeightRows];
+#pragma unroll
+                    for (int u = 0; u < kWeightRows; ++u)
+                        v[u] = *reinterpret_cast<const float4*>(sc + static_cast<size_t>(min(i0 + 32 * u, end - 1)) * cols + c);
+#pragma unroll
+                    for (int u = 0; u < kWeightRows; ++u) {
+                        take(u, v[u].x, c);
+                        take(u, v[u].y, c + 1);
+                        take(u, v[u].z, c + 2);
+                        take(u, v[u].w, c + 3);
+                    }
+                }
+            } else {
+                for (int c = c0; c < ce; ++c) {
+                    float v[kWeightRows];
+#pragma unroll
+                    for (int u = 0; u < kWeightRows; ++u) v[u] = sc[static_cast<size_t>(min(i0 + 32 * u, end - 1)) * cols + c];
+#pragma unroll
+                    for (int u = 0; u < kWeightRows; ++u) take(u, v[u], c);
+                }
+            }
+        }
+        if (__any_sync(0xffffffffu, no_sum)) continue;
+#pragma unroll
+        for (int u = 0; u < kWeightRows; ++u) {
+            const int i = i0 + 32 * u;
+            if (i >= end) continue;
+            float* at = p.row_weights + (static_cast<size_t>(id[u]) * p.num_kv_heads + h) * bs + i % bs;
+            if (i >= n - Q)
+                *at = w[u];
+            else
+                atomicAdd(at, w[u]);
+        }
     }
 }
 
@@ -239,12 +297,26 @@ cudaError_t launch_decode_rows(const DecodeParams& p, pa_dtype dtype, cudaStream
     return cudaGetLastError();
 }
 
-cudaError_t launch_row_weights(const DecodeParams& p, cudaStream_t stream) {
-    if (p.num_seqs == 0 || p.context_cap == 0) return cudaSuccess;
-    const int cols = p.num_heads / p.num_kv_heads * p.num_queries;
-    const long long grid = (static_cast<long long>(p.context_cap) + kChunk - 1) / kChunk * p.num_seqs * p.num_kv_heads;
-    if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    row_weights_kernel<<<static_cast<unsigned>(grid), kWeightThreads, 8 * static_cast<size_t>(cols), stream>>>(p);
+cudaError_t launch_row_weights(const DecodeParams& p, const int32_t* item_count, cudaStream_t stream) {
+    const long long most = static_cast<long long>(p.max_parts) * p.num_seqs * p.num_kv_heads;
+    if (most == 0 || p.context_cap == 0) return cudaSuccess;
+    if (most > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    const int sms = device_sms();
+    if (sms <= 0) return cudaErrorInvalidDevice;
+    if (p.partition_size != kDefaultPartition) return cudaErrorInvalidValue;
+    const long long ctas = (most + kWeightItems - 1) / kWeightItems;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas < 8LL * sms ? ctas : 8LL * sms));
+    cfg.blockDim = dim3(kWeightThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, item_count != nullptr ? row_weights_kernel<true> : row_weights_kernel<false>,
+                                               p, item_count, static_cast<int>(most));
+    if (err != cudaSuccess) return err;
     return cudaGetLastError();
 }
 

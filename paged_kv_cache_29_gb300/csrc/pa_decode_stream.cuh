@@ -213,6 +213,9 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap tmap_k,
         if (threadIdx.x == 0) {
             total_sm[0] = total;
             mbar_arrive(smem_addr(plan_bar));
+            if constexpr (Math::kRows) {
+                if (c == 0 && p.item_count != nullptr) p.item_count[0] = total;
+            }
         }
     }
     // The CTA's j-th item (x = -1: none): the first two from shared memory.
@@ -846,6 +849,10 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap tmap_k,
 #pragma unroll
         for (int w = 0; w < W; ++w) any_bad |= warp_bad[(j & 1) * W + w] != 0;
         // any_bad: flagged by the producer; output left unspecified
+        if constexpr (Math::kRows) {
+            if (any_bad && p.scores != nullptr && threadIdx.x < ncols)
+                p.part_ml[2 * (query_row(p, s, h, threadIdx.x, grp) * p.max_parts + part) + 1] = kNoSum;
+        }
         const int P = Math::kRows ? p.partition_size : part_rows(n);
         const int nparts = (plan_span<Math::kRows>(p, n) + P - 1) / P;
         for (int idx = any_bad ? ncols * D : threadIdx.x; idx < ncols * D; idx += W * 32) {

@@ -43,8 +43,10 @@ struct DecodeParams {
     int num_sinks;                 // pa_decode_sinks: first rows that stay visible (else 0); `window` then
                                    //   counts the rows that any of the num_queries tokens' windows holds
     float* row_weights;            // pa_decode_weights: [num_blocks][num_kv_heads][block_size] (else null),
-    float* scores;                 //   scores [B][Hkv][score_rows][columns], base 2, of every row
+    float* scores;                 //   scores [B][Hkv][score_rows][columns], base 2, of every row,
     int score_rows;
+    int32_t* item_count;           //   the tile ring's number of work items,
+    float2* final_ml;              //   [B][Q][Hq] max and sum of merged sequences
     int num_heads;
     int num_kv_heads;
     int head_dim;
@@ -250,8 +252,10 @@ cudaError_t launch_decode_weights(const CUtensorMap& tk, const CUtensorMap& tv, 
 bool has_rows_instance(pa_dtype dtype, int head_dim, int group, int num_queries);
 
 // Accumulates the row weights of pa_decode_weights from the scores and the
-// partitions' maxima and sums.
-cudaError_t launch_row_weights(const DecodeParams& p, cudaStream_t stream);
+// partitions' maxima and sums. item_count: how many work items the tile ring listed
+// (p.items), null after the plain kernel, which lists none.
+cudaError_t launch_row_weights(const DecodeParams& p, const int32_t* item_count, cudaStream_t stream);
+constexpr float kNoSum = -1.0f;      // in place of a partition's sum: it has a block outside the pool
 
 // Merge of partition partials for sequences longer than one partition.
 cudaError_t launch_combine(const DecodeParams& p, pa_dtype dtype, cudaStream_t stream);

@@ -73,7 +73,8 @@ def test_workspaces(lib, B, Q, hq, D, mcl):
     seqs, parts = min(B, 4096), max(1, -(-mcl // 512))
     units = seqs * hq * parts
     base = 256 + 16 * units + 8 * units * Q + (4 * units * Q * D if parts > 1 else 0)
-    assert need == -(-base // 16) * 16 + 4 * seqs * hq * Q * (-(-mcl // 16) * 16)
+    states = -(-8 * seqs * hq * Q // 16) * 16
+    assert need == -(-base // 16) * 16 + states + 4 * seqs * hq * Q * (-(-mcl // 16) * 16)
     mb = -(-mcl // 16)
     sizes = dict(B=B, Q=Q, Hq=hq, Hkv=1, D=D, mcl=mcl, mb=mb)
     assert weights(lib, **sizes, ws=P, wsb=need - 1) == WORKSPACE and weights(lib, **sizes, ws=P + 8, wsb=need) == WORKSPACE
