@@ -58,11 +58,14 @@ struct RowsMmaMath : MmaMath<D, G, true> {
         }
         if constexpr (SCORES) {
             // Rows past the sequence too: the scratch has whole tiles.
-            float* at = scores + static_cast<size_t>(row0 + gid) * cols + 2 * t4;
-            if (2 * t4 + 1 < cols && (cols & 1) == 0) {
-                *reinterpret_cast<float2*>(at) = make_float2(c[0], c[1]);
-                *reinterpret_cast<float2*>(at + 8 * cols) = make_float2(c[2], c[3]);
+            if (G > 1 && cols == G) {
+                float* at = scores + static_cast<size_t>(row0 + gid) * G + 2 * t4;
+                if (2 * t4 < G) {
+                    *reinterpret_cast<float2*>(at) = make_float2(c[0], c[1]);
+                    *reinterpret_cast<float2*>(at + 8 * G) = make_float2(c[2], c[3]);
+                }
             } else {
+                float* at = scores + static_cast<size_t>(row0 + gid) * cols + 2 * t4;
                 if (2 * t4 < cols) {
                     at[0] = c[0];
                     at[8 * cols] = c[2];
