@@ -8,7 +8,7 @@
 // Sums are pairs of fp32 values, a sum and its error: the difference p - q and each
 // addition leave an exact error term, and what is lost is below 2^-44 of a sum. (An fp64
 // instruction holds the SM's fp64 pipe for 16 cycles a warp: with fp64 lanes the
-// additions took as long as the loads.) Borders are compared in 64 bits, or pair to pair.
+// additions took as long as the loads.)
 //
 // A cluster of CTAs shares a sequence's row, a CTA a run of its segments of 512
 // (or 256) values, a warp a segment at a time. Running sums over the CTA's segments, then over
@@ -59,8 +59,12 @@ struct Sum {
         r.lo = lo - (r.hi - hi);
         return r;
     }
+    __device__ __forceinline__ Sum minus(const Sum& o) const { return plus(Sum{-o.hi, -o.lo}); }
+    __device__ __forceinline__ Sum times(float u) const {
+        const float p = hi * u;
+        return Sum{p, fmaf(hi, u, -p) + lo * u}.order();
+    }
     __device__ __forceinline__ bool above(const Sum& o) const { return hi > o.hi || (hi == o.hi && lo > o.lo); }
-    __device__ __forceinline__ double value() const { return static_cast<double>(hi) + static_cast<double>(lo); }
 };
 
 // x - y for x > y, else nothing; NaN counts as nothing.
@@ -70,13 +74,8 @@ __device__ __forceinline__ void add_excess(Sum& sum, float x, float y) {
     if (diff > 0.f) sum.add(diff, (x - (diff + b)) + (b - y));
 }
 
-__device__ __forceinline__ double warp_scan(double v, int lane) {
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const double u = __shfl_up_sync(0xffffffffu, v, off);
-        if (lane >= off) v += u;
-    }
-    return v;
+__device__ __forceinline__ Sum shuffle(const Sum& v, int from) {
+    return Sum{__shfl_sync(0xffffffffu, v.hi, from), __shfl_sync(0xffffffffu, v.lo, from)};
 }
 
 __device__ __forceinline__ Sum warp_scan(Sum v, int lane) {
@@ -183,9 +182,8 @@ template <int THREADS>
 __global__ void __launch_bounds__(THREADS) verify_kernel(const VerifyParams p, int segs_per_cta) {
     constexpr int kSegment = THREADS;         // a value a thread, in the last step
     constexpr int kWarps = THREADS / 32;
-    extern __shared__ double seg_sum[];       // [segs_per_cta]: first each segment's Sum (its bits), then running sums
-    __shared__ double cta_total;
-    __shared__ Sum warp_total[kWarps], border_left;
+    extern __shared__ Sum seg_sum[];          // [segs_per_cta]: of each segment, then up to its end
+    __shared__ Sum cta_total, warp_total[kWarps], border_left;
     __shared__ int first_rejected, bad, chosen, owner;
     cg::cluster_group cluster = cg::this_cluster();
     const int ranks = cluster.num_blocks(), rank = cluster.block_rank();
@@ -259,40 +257,41 @@ __global__ void __launch_bounds__(THREADS) verify_kernel(const VerifyParams p, i
                 o.lo = __shfl_xor_sync(0xffffffffu, v.lo, off);
                 v = v.plus(o);
             }
-            if (lane == 0) seg_sum[g] = __hiloint2double(__float_as_int(v.hi), __float_as_int(v.lo));
+            if (lane == 0) seg_sum[g] = v;
         }
         __syncthreads();
         if (warp == 0) {
             // Running sums: each lane's run of segments, then the lanes'.
             const int run = (segs + 31) / 32, g0 = min(segs, lane * run), g1 = min(segs, g0 + run);
-            double own = 0.0;
+            Sum own{0.f, 0.f};
+            for (int g = g0; g < g1; ++g) own = own.plus(seg_sum[g]);
+            const Sum incl = warp_scan(own, lane);
+            Sum upto = shuffle(incl, lane > 0 ? lane - 1 : 0);
+            if (lane == 0) upto = Sum{0.f, 0.f};
             for (int g = g0; g < g1; ++g) {
-                const double bits = seg_sum[g];
-                own += Sum{__int_as_float(__double2hiint(bits)), __int_as_float(__double2loint(bits))}.value();
-                seg_sum[g] = own;
+                upto = upto.plus(seg_sum[g]);
+                seg_sum[g] = upto;
             }
-            const double before = warp_scan(own, lane) - own;
-            for (int g = g0; g < g1; ++g) seg_sum[g] += before;
             __syncwarp();
-            if (lane == 0) cta_total = segs > 0 ? seg_sum[segs - 1] : 0.0;
+            if (lane == 0) cta_total = segs > 0 ? seg_sum[segs - 1] : Sum{0.f, 0.f};
         }
         cluster.sync();
         if (warp == 0) {
             // Where u S falls: in this CTA's part, and in which of its segments?
-            const double mine = lane < ranks ? *cluster.map_shared_rank(&cta_total, lane) : 0.0;
-            double total = 0.0, base = 0.0, end = 0.0;
+            const Sum mine = lane < ranks ? *cluster.map_shared_rank(&cta_total, lane) : Sum{0.f, 0.f};
+            Sum total{0.f, 0.f}, base{0.f, 0.f}, end{0.f, 0.f};
             for (int r = 0; r < ranks; ++r) {
                 if (r == rank) base = total;
-                total += __shfl_sync(0xffffffffu, mine, r);
+                total = total.plus(shuffle(mine, r));
                 if (r == rank) end = total;
             }
-            const double u = fminf(fmaxf(u_last, 0.f), 0.99999994f);   // [0, 1)
-            const double border = u * total;
-            const bool here = base <= border && border < end;
+            // Sums that values are added to never shrink, and u S is below S: it falls into one part.
+            const Sum border = total.times(fminf(fmaxf(u_last, 0.f), 0.99999994f));   // u in [0, 1)
+            const bool here = !base.above(border) && end.above(border);
             int seg = segs - 1;
             if (here) {
                 for (int g0 = 0; g0 < segs; g0 += 32) {
-                    const unsigned hit = __ballot_sync(0xffffffffu, g0 + lane < segs && base + seg_sum[g0 + lane] > border);
+                    const unsigned hit = __ballot_sync(0xffffffffu, g0 + lane < segs && base.plus(seg_sum[g0 + lane]).above(border));
                     if (hit != 0u) {
                         seg = g0 + __ffs(hit) - 1;
                         break;
@@ -300,10 +299,8 @@ __global__ void __launch_bounds__(THREADS) verify_kernel(const VerifyParams p, i
                 }
             }
             if (lane == 0) {
-                const double left = border - (base + (here && seg > 0 ? seg_sum[seg - 1] : 0.0));
-                border_left.hi = static_cast<float>(left);
-                border_left.lo = static_cast<float>(left - static_cast<double>(border_left.hi));
-                owner = !(total > 0.0) ? -2 : here ? seg : -1;
+                border_left = border.minus(here && seg > 0 ? base.plus(seg_sum[seg - 1]) : base);
+                owner = !(total.hi > 0.f) ? -2 : here ? seg : -1;
                 chosen = INT_MAX;
             }
         }
@@ -374,7 +371,7 @@ cudaError_t launch(const VerifyParams& p, long long ctas, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(p.num_seqs) * ranks);
     cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = 8 * static_cast<size_t>(per_cta);   // 32 KB at most
+    cfg.dynamicSmemBytes = sizeof(Sum) * static_cast<size_t>(per_cta);   // 32 KB at most
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
