@@ -696,10 +696,10 @@ size_t pa_decode_workspace_size_weights(int num_seqs, int num_queries, int num_h
  * lens_out[s] = k. Rows of the pool that no kept row moves to are left as they are.
  *
  * out_tables: int32 [num_seqs][max_blocks_per_seq]. block_tables itself (or equal
- *   entries): in place. Else each entry is that of block_tables at the same place,
- *   or a block that holds no row of the batch's sequences and stands nowhere else in
- *   out_tables: sequences that share blocks with others move into blocks of their
- *   own. Entries past ceil(k / block_size) are not read.
+ *   entries): in place. Else each entry is that of block_tables at the same place, if
+ *   no other sequence holds that block, or a block that holds no row of the batch's
+ *   sequences and stands nowhere else in out_tables: where sequences share blocks
+ *   they move into blocks of their own. Entries past ceil(k / block_size) are not read.
  * lens_out: int32 [num_seqs], may be context_lens itself.
  * k_cache, v_cache: pools of dtype as the decode calls take them; k_params,
  *   v_params: 4 bytes per row and KV head [num_blocks][num_kv_heads][block_size]
@@ -753,7 +753,8 @@ size_t pa_evict_workspace_size(int num_seqs, int num_kv_heads, int max_context_l
  * [num_seqs][max_drafts + 1]; num_accepted, num_drafts, context_lens, lens_out:
  * int32 [num_seqs], lens_out may be context_lens. 0 <= max_drafts <= 64.
  * A drafted token outside [0, vocab_size) among the first d, d outside
- * [0, max_drafts], or a row p_a without a positive value flags PA_DEVERR_TOKEN,
+ * [0, max_drafts], or a row p_a without a positive or with an infinite value flags
+ * PA_DEVERR_TOKEN,
  * context_lens[s] < d - a PA_DEVERR_CONTEXT; nothing of that sequence is written.
  * No workspace.
  */
