@@ -187,7 +187,7 @@ static_assert(kDefaultPartition % kWeightUnit == 0 && kWeightThreads / 32 % kWei
 // (the plain kernel has no list) all that there may be.
 template <bool LISTED>
 __global__ void __launch_bounds__(kWeightThreads) row_weights_kernel(const DecodeParams p, const int32_t* item_count,
-                                                                     int most_items) {
+                                                                     int most_items, const Divisor by_block) {
     grid_dependency_wait();
     grid_launch_dependents();
     const int lane = threadIdx.x & 31;
@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(kWeightThreads) row_weights_kernel(const Decod
 #pragma unroll
         for (int u = 0; u < kWeightRows; ++u) {
             const int i = min(i0 + 32 * u, end - 1);
-            id[u] = __ldg(table + i / bs);
+            id[u] = __ldg(table + by_block.quotient(i));
             w[u] = 0.f;
         }
         const float* sc = p.scores + (static_cast<size_t>(s) * p.num_kv_heads + h) * p.score_rows * cols;
@@ -239,32 +239,32 @@ __global__ void __launch_bounds__(kWeightThreads) row_weights_kernel(const Decod
             }
             own.x = own.x == -INFINITY ? 0.f : own.x;
             own.y = 1.f / own.y;
-            auto take = [&](int u, float score, int c) {
+            auto take = [&](const float (&score)[kWeightRows], int c) {
                 const float m = __shfl_sync(0xffffffffu, own.x, c - c0), r = __shfl_sync(0xffffffffu, own.y, c - c0);
-                w[u] = fmaf(fast_exp2(score - m), r, w[u]);
+#pragma unroll
+                for (int u = 0; u < kWeightRows; ++u) w[u] = fmaf(fast_exp2(score[u] - m), r, w[u]);
             };
             const int ce = min(cols, c0 + 32);
             if (cols % 4 == 0) {
                 for (int c = c0; c < ce; c += 4) {
-                    float4 v[kWeightRows];
-#pragma unroll
-                    for (int u = 0; u < kWeightRows; ++u)
-                        v[u] = *reinterpret_cast<const float4*>(sc + static_cast<size_t>(min(i0 + 32 * u, end - 1)) * cols + c);
+                    float v[4][kWeightRows];
 #pragma unroll
                     for (int u = 0; u < kWeightRows; ++u) {
-                        take(u, v[u].x, c);
-                        take(u, v[u].y, c + 1);
-                        take(u, v[u].z, c + 2);
-                        take(u, v[u].w, c + 3);
+                        const float4 x = *reinterpret_cast<const float4*>(sc + static_cast<size_t>(min(i0 + 32 * u, end - 1)) * cols + c);
+                        v[0][u] = x.x;
+                        v[1][u] = x.y;
+                        v[2][u] = x.z;
+                        v[3][u] = x.w;
                     }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) take(v[e], c + e);
                 }
             } else {
                 for (int c = c0; c < ce; ++c) {
                     float v[kWeightRows];
 #pragma unroll
                     for (int u = 0; u < kWeightRows; ++u) v[u] = sc[static_cast<size_t>(min(i0 + 32 * u, end - 1)) * cols + c];
-#pragma unroll
-                    for (int u = 0; u < kWeightRows; ++u) take(u, v[u], c);
+                    take(v, c);
                 }
             }
         }
@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(kWeightThreads) row_weights_kernel(const Decod
         for (int u = 0; u < kWeightRows; ++u) {
             const int i = i0 + 32 * u;
             if (i >= end) continue;
-            float* at = p.row_weights + (static_cast<size_t>(id[u]) * p.num_kv_heads + h) * bs + i % bs;
+            float* at = p.row_weights + (static_cast<size_t>(id[u]) * p.num_kv_heads + h) * bs + by_block.rest(i, by_block.quotient(i));
             if (i >= n - Q)
                 *at = w[u];
             else
@@ -315,7 +315,7 @@ cudaError_t launch_row_weights(const DecodeParams& p, const int32_t* item_count,
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     const cudaError_t err = cudaLaunchKernelEx(&cfg, item_count != nullptr ? row_weights_kernel<true> : row_weights_kernel<false>,
-                                               p, item_count, static_cast<int>(most));
+                                               p, item_count, static_cast<int>(most), Divisor(static_cast<uint32_t>(p.block_size)));
     if (err != cudaSuccess) return err;
     return cudaGetLastError();
 }
