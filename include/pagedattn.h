@@ -645,8 +645,9 @@ pa_status pa_norm_rope_append_int4(const pa_norm_rope_args* args, const void* v,
  * window >= 1, num_sinks >= 0, 1 <= num_queries <= 8. Workspace:
  * pa_decode_workspace_size_multi. head_dim up to 256, any block_size >= 1, at most
  * 1024 heads per KV head * num_queries. The fast kernels need block_size a multiple of 16, head_dim 64 or
- * 128, and over bf16 heads per KV head * num_queries <= 8, over fp32 1, 2, 4 or
- * 8 heads per KV head and one query token; other shapes run a plain kernel.
+ * 128, up to 8 heads per KV head, over fp32 one query token, and over bf16, with
+ * t = 8 / (heads per KV head) tokens at a time, no more than heads per KV head
+ * times t of them; other shapes run a plain kernel.
  */
 pa_status pa_decode_sinks(const void* q, const void* k_cache, const void* v_cache,
                           const int32_t* block_tables, const int32_t* context_lens, float scale,

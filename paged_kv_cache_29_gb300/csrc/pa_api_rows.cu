@@ -132,8 +132,14 @@ pa_status rows_call(const void* q, const void* k_cache, const void* v_cache, con
     base.max_parts = static_cast<int>(parts);
     const size_t es = dtype == PA_DTYPE_F32 ? 4 : 2;
     const long long pool_rows = static_cast<long long>(num_blocks) * num_kv_heads * block_size;
-    const bool ring = block_size % 16 == 0 && pool_rows < INT_MAX &&
-                      pa::has_rows_instance(dtype, head_dim, group, num_queries);
+    // The tile ring, where an item takes whole heads of at least one token, and the items of
+    // all column groups fit the work list (sized for one per query head).
+    const int tokens = pa::rows_group_tokens(dtype, head_dim, group, num_queries);
+    const int groups = tokens > 0 ? static_cast<int>(ceil_div(num_queries, tokens)) : 0;
+    const bool ring = block_size % 16 == 0 && pool_rows < INT_MAX && groups > 0 && groups <= group &&
+                      parts * chunk * num_kv_heads * groups <= 0x3fffffffLL;
+    base.col_groups = groups;
+    base.group_tokens = tokens;
     CUtensorMap tk, tv;
     int sms = 0;
     if (ring) {

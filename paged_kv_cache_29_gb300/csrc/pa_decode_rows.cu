@@ -201,7 +201,8 @@ __global__ void __launch_bounds__(kWeightThreads) row_weights_kernel(const Decod
         if constexpr (LISTED) {
             const int4 it = p.items[k];
             s = it.x;
-            h = it.y;
+            h = it.y / p.col_groups;
+            if (it.y != h * p.col_groups) continue;                          // (the first column group takes them all)
             part = it.z;
             n = it.w;
         } else {

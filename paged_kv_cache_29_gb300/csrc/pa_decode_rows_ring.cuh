@@ -29,7 +29,7 @@ cudaError_t run_simt(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeP
 template <int D, bool SCORES>
 cudaError_t by_columns(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeParams& p, pa_dtype dtype,
                        int sm_count, cudaStream_t stream) {
-    const int cols = (p.num_heads / p.num_kv_heads) * p.num_queries;
+    const int cols = (p.num_heads / p.num_kv_heads) * p.group_tokens;
     const bool bf16 = dtype == PA_DTYPE_BF16;
     if (cols <= 1) return bf16 ? run_mma<D, 1, SCORES>(tk, tv, p, sm_count, stream)
                                : run_simt<D, 1, SCORES>(tk, tv, p, sm_count, stream);

@@ -1,6 +1,7 @@
 // pa_decode_sinks.cu -- instances of the tile-ring decode kernel for
-// pa_decode_sinks: a window and the first rows (bf16: up to 8 query columns, heads per
-// KV head x query tokens; fp32: 1, 2, 4 or 8 heads per KV head, one query token).
+// pa_decode_sinks: a window and the first rows. Up to 8 heads per KV head; bf16: the query
+// tokens of an item fill up to 8 columns, further ones are another item's, whose K and V
+// tiles the first one has brought into L2; fp32: one query token.
 #include "pa_decode_rows_ring.cuh"
 
 namespace pa {
@@ -10,10 +11,11 @@ cudaError_t launch_decode_sinks(const CUtensorMap& tk, const CUtensorMap& tv, co
     return launch_rows_ring<false>(tk, tv, p, dtype, sm_count, stream);
 }
 
-bool has_rows_instance(pa_dtype dtype, int head_dim, int group, int num_queries) {
-    if (head_dim != 64 && head_dim != 128) return false;
-    if (dtype == PA_DTYPE_BF16) return group * num_queries <= 8;
-    return num_queries == 1 && (group == 1 || group == 2 || group == 4 || group == 8);
+int rows_group_tokens(pa_dtype dtype, int head_dim, int group, int num_queries) {
+    if ((head_dim != 64 && head_dim != 128) || group > 8) return 0;
+    if (dtype != PA_DTYPE_BF16) return num_queries == 1 ? 1 : 0;
+    const int tokens = 8 / group;
+    return tokens < num_queries ? tokens : num_queries;
 }
 
 }  // namespace pa

@@ -86,7 +86,7 @@ __device__ __forceinline__ void cp_async_wait_all() {
 template <bool ROWS>
 __device__ __forceinline__ int4 first_item_by_warp(const DecodeParams& p, int c, int lane) {
     if (p.partition_long != p.partition_size) return make_int4(-1, 0, 0, 0);
-    const int Hkv = p.num_kv_heads;
+    const int Hkv = plan_heads<ROWS>(p);
     const int unit = c / Hkv;
     int carry = 0;
     for (int s0 = 0; s0 < p.num_seqs; s0 += 32) {
@@ -240,6 +240,8 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap tmap_k,
             hi = min(it.w, lo + P);
         }
     };
+    // The KV head of an item.
+    auto item_head = [&](const int4& it) { return Math::kRows ? it.y / p.col_groups : it.y; };
     auto gap_from = [&](int n, int v) { return Math::kRows && v >= sink_rows(p) ? seq_gap(p, n) : 0; };
     const uint32_t ring_addr = smem_addr(ring);
 
@@ -689,7 +691,7 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     // 0's expect_tx (ordered by the shuffle above).
                     if (data && lane < 2) {
                         const int id = ids[Math::kRows ? tt : tok / bs - b0];
-                        const int row = (id * p.num_kv_heads + cur.y) * bs + (tok + gap_from(cur.w, tok)) % bs;
+                        const int row = (id * p.num_kv_heads + item_head(cur)) * bs + (tok + gap_from(cur.w, tok)) % bs;
                         const uint32_t dst = ring_addr + stage * Geom::kStageBytes +
                                              (lane ? Geom::kTileBytes : 0);
                         tma_load_3d(dst, lane ? static_cast<const void*>(&tmap_v)
@@ -752,7 +754,12 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap tmap_k,
     // masking serve one query per sequence with exactly G heads.
     const int grp = Math::kCausal ? p.num_heads / p.num_kv_heads : G;
     const int Qn = Math::kCausal ? p.num_queries : 1;
-    const int ncols = Math::kCausal ? grp * Qn : G;
+    const int all_cols = Math::kCausal ? grp * Qn : G;
+    // With column groups: an item's first query token, and its columns.
+    auto first_token = [&](const int4& it) { return Math::kRows ? (it.y % p.col_groups) * p.group_tokens : 0; };
+    auto item_cols = [&](const int4& it) {
+        return Math::kRows ? grp * min(p.group_tokens, Qn - first_token(it)) : all_cols;
+    };
     auto item_at = own_item;
     int4 it = item_at(0);
     int4 it_next = item_at(1);
@@ -774,7 +781,7 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap tmap_k,
             }
             const bool have = landed && q0_sm[0] == it.x && q0_sm[1] == it.y;
             if (!have) {
-                math.stage_q(p, it.x, it.y, ncols, grp, smem_addr(qbuf), lane);
+                math.stage_q(p, it.x, it.y, all_cols, grp, smem_addr(qbuf), lane);
                 cp_async_wait_all();
             }
         }
@@ -784,7 +791,8 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap tmap_k,
     }
     int t0 = 0;                 // stream index of the current item's first tile (a multiple of W)
     for (int j = 0; it.x >= 0; ++j) {
-        const int s = it.x, h = it.y, part = it.z, n = it.w;
+        const int s = it.x, h = item_head(it), part = it.z, n = it.w;
+        const int token0 = first_token(it), ncols = item_cols(it);
         int lo, hi;
         item_rows(it, lo, hi);
         const int ntiles = (hi - lo + kTileRows - 1) / kTileRows;
@@ -794,15 +802,15 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap tmap_k,
             // The other buffer was last read when item j - 1 began, before the
             // previous item's closing barrier.
             if (warp == 0 && it_next.x >= 0)
-                math.stage_q(p, it_next.x, it_next.y, ncols, grp,
+                math.stage_q(p, it_next.x, it_next.y, all_cols, grp,
                              smem_addr(qbuf + ((j + 1) & 1) * Math::kQBufBytes), lane);
         } else {
             math.begin(p, q_next);
             if (it_next.x >= 0) math.load_q(p, it_next.x, it_next.y, q_next);
         }
-        if constexpr (Math::kRows) math.begin_rows(p, s, h, ncols);
+        if constexpr (Math::kRows) math.begin_rows(p, s, h, token0, ncols, grp);
         const int span = ((ntiles + W - 1) / W) * W;   // padded as the producer pads
-        const int limit0 = n - Qn;                      // the last row query token 0 sees
+        const int limit0 = n - Qn + token0;             // the last row the first query token sees
         bool bad = false;
         if (!aborted) {
             for (int t = t0 + warp; t < t0 + span; t += W) {
@@ -851,7 +859,7 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap tmap_k,
         // any_bad: flagged by the producer; output left unspecified
         if constexpr (Math::kRows) {
             if (any_bad && p.scores != nullptr && threadIdx.x < ncols)
-                p.part_ml[2 * (query_row(p, s, h, threadIdx.x, grp) * p.max_parts + part) + 1] = kNoSum;
+                p.part_ml[2 * (query_row(p, s, h, token0 * grp + threadIdx.x, grp) * p.max_parts + part) + 1] = kNoSum;
         }
         const int P = Math::kRows ? p.partition_size : part_rows(n);
         const int nparts = (plan_span<Math::kRows>(p, n) + P - 1) / P;
@@ -873,7 +881,7 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 O = fmaf(cw, sw[2 * G + g * D + d], O);
             }
             const size_t row = Math::kCausal
-                                   ? query_row(p, s, h, g, grp)
+                                   ? query_row(p, s, h, token0 * grp + g, grp)
                                    : static_cast<size_t>(s) * p.num_heads + h * G + g;
             const size_t slot = row * p.max_parts + part;
             if (nparts == 1)

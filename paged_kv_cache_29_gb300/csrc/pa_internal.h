@@ -42,6 +42,8 @@ struct DecodeParams {
     int window;                    // sliding window: attend to the last `window` rows (0 = all)
     int num_sinks;                 // pa_decode_sinks: first rows that stay visible (else 0); `window` then
                                    //   counts the rows that any of the num_queries tokens' windows holds
+    int col_groups;                // tile ring of those calls: items of a KV head share its query columns in
+    int group_tokens;              //   col_groups groups of up to group_tokens tokens (item.y: head * col_groups + group)
     float* row_weights;            // pa_decode_weights: [num_blocks][num_kv_heads][block_size] (else null),
     float* scores;                 //   scores [B][Hkv][score_rows][columns], base 2, of every row,
     int score_rows;
@@ -244,12 +246,13 @@ size_t generic_smem_bytes(int group, int head_dim, int partition_size, int block
 // query tokens (head dim <= 256).
 cudaError_t launch_decode_rows(const DecodeParams& p, pa_dtype dtype, cudaStream_t stream);
 
-// Their tile-ring instances (head dim 64 or 128, block size a multiple of 16).
+// Their tile-ring instances (block size a multiple of 16), and how many query tokens an
+// item of theirs takes (0: no instance).
 cudaError_t launch_decode_sinks(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeParams& p,
                                 pa_dtype dtype, int sm_count, cudaStream_t stream);
 cudaError_t launch_decode_weights(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeParams& p,
                                   pa_dtype dtype, int sm_count, cudaStream_t stream);
-bool has_rows_instance(pa_dtype dtype, int head_dim, int group, int num_queries);
+int rows_group_tokens(pa_dtype dtype, int head_dim, int group, int num_queries);
 
 // Accumulates the row weights of pa_decode_weights from the scores and the
 // partitions' maxima and sums. item_count: how many work items the tile ring listed

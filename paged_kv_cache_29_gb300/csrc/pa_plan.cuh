@@ -68,6 +68,13 @@ __device__ __forceinline__ int plan_span(const DecodeParams& p, int n) {
     return n - seq_row_base(n, p.window);
 }
 
+// Items per sequence and partition: KV heads, with ROWS times their column groups.
+template <bool ROWS>
+__device__ __forceinline__ int plan_heads(const DecodeParams& p) {
+    if constexpr (ROWS) return p.num_kv_heads * p.col_groups;
+    return p.num_kv_heads;
+}
+
 // Context length of sequence s, or -1 (flagged) when it is out of range
 // (negative, past max_context_len, or shorter than the query tokens it holds).
 __device__ __forceinline__ int plan_len(const DecodeParams& p, int s, bool flag) {
@@ -141,7 +148,7 @@ __device__ int plan_cta(const DecodeParams& p, int c, int C, int* sm, int4* firs
     // full partitions so far (pass 2, after the long ones), [3] total items
     int* carry = brun + kPlanBuckets;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int B = p.num_seqs, Hkv = p.num_kv_heads;
+    const int B = p.num_seqs, Hkv = plan_heads<ROWS>(p);
     const int Pb = p.partition_size;
     if (tid < kPlanBuckets) {
         bcount[tid] = 0;

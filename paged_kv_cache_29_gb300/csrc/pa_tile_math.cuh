@@ -93,14 +93,14 @@ __device__ __forceinline__ size_t query_row(const DecodeParams& p, int s, int h,
 // into a staging buffer whose rows are ROW_BYTES apart, with cp.async.
 template <int D, int ROW_BYTES>
 __device__ __forceinline__ void stage_q_rows(const DecodeParams& p, int s, int h, int ncols,
-                                             int grp, uint32_t qbuf, int lane) {
+                                             int grp, uint32_t qbuf, int lane, int col0 = 0) {
     constexpr int kChunksPerRow = D * 2 / 16;
     const uint8_t* q = reinterpret_cast<const uint8_t*>(p.q);
     for (int c = lane; c < ncols * kChunksPerRow; c += 32) {
         const int col = c / kChunksPerRow, ch = c - col * kChunksPerRow;
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
                          qbuf + static_cast<uint32_t>(col * ROW_BYTES + ch * 16)),
-                     "l"(q + query_row(p, s, h, col, grp) * D * 2 + ch * 16)
+                     "l"(q + query_row(p, s, h, col0 + col, grp) * D * 2 + ch * 16)
                      : "memory");
     }
     asm volatile("cp.async.commit_group;" ::: "memory");

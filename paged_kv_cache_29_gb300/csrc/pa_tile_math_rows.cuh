@@ -29,16 +29,27 @@ struct RowsMmaMath : MmaMath<D, G, true> {
     using Base::gid;
     using Base::t4;
 
-    float* scores;                // of the item's sequence and KV head, [row][cols]
-    int cols, tokens, window, sinks;
+    float* scores;                // of the item's sequence, KV head and first column, [row][all columns]
+    int cols, all_cols, tokens, window, sinks;
 
-    __device__ __forceinline__ void begin_rows(const DecodeParams& p, int s, int h, int ncols) {
+    // q of an item (head: with its column group), up to all its columns.
+    __device__ __forceinline__ void stage_q(const DecodeParams& p, int s, int head, int /*all columns*/, int grp,
+                                            uint32_t qbuf, int lane) const {
+        const int h = head / p.col_groups, token0 = (head - h * p.col_groups) * p.group_tokens;
+        stage_q_rows<D, Base::kQRowBytes>(p, s, h, grp * min(p.group_tokens, p.num_queries - token0), grp, qbuf, lane,
+                                          token0 * grp);
+    }
+
+    __device__ __forceinline__ void begin_rows(const DecodeParams& p, int s, int h, int token0, int ncols, int grp) {
         cols = ncols;
-        tokens = p.num_queries;
-        window = p.window > 0 ? p.window - p.num_queries + 1 : 0;   // of one token
-        sinks = p.num_sinks;
-        if constexpr (SCORES)
-            scores = p.scores + (static_cast<size_t>(s) * p.num_kv_heads + h) * p.score_rows * ncols;
+        if constexpr (!SCORES) {                  // (pa_decode_weights has no window)
+            window = p.window > 0 ? p.window - p.num_queries + 1 : 0;   // of one token
+            sinks = p.num_sinks;
+            tokens = ncols / grp;
+        } else {
+            all_cols = grp * p.num_queries;
+            scores = p.scores + (static_cast<size_t>(s) * p.num_kv_heads + h) * p.score_rows * all_cols + token0 * grp;
+        }
     }
 
     __device__ __forceinline__ void tile(uint32_t kbase, uint32_t vbase, int /*valid*/,
@@ -47,10 +58,11 @@ struct RowsMmaMath : MmaMath<D, G, true> {
         float c[4];
         Base::qk(kbase, scale_log2, lane, c);
         const bool whole = row0 + kTileRows - 1 <= limit0 &&
-                           (window == 0 || row0 + kTileRows <= sinks || row0 > limit0 + tokens - 1 - window);
+                           (SCORES || window == 0 || row0 + kTileRows <= sinks || row0 > limit0 + tokens - 1 - window);
+        auto seen_by = [&](int last) { return SCORES ? rows_seen(row0, last, 0, 0) : rows_seen(row0, last, window, sinks); };
         if (!whole) {
-            const uint32_t s0 = rows_seen(row0, limit0 + (2 * t4) / grp, window, sinks) >> gid;
-            const uint32_t s1 = rows_seen(row0, limit0 + (2 * t4 + 1) / grp, window, sinks) >> gid;
+            const uint32_t s0 = seen_by(limit0 + (2 * t4) / grp) >> gid;
+            const uint32_t s1 = seen_by(limit0 + (2 * t4 + 1) / grp) >> gid;
             if (!(s0 & 1u)) c[0] = -INFINITY;
             if (!(s1 & 1u)) c[1] = -INFINITY;
             if (!(s0 & 256u)) c[2] = -INFINITY;
@@ -58,21 +70,21 @@ struct RowsMmaMath : MmaMath<D, G, true> {
         }
         if constexpr (SCORES) {
             // Rows past the sequence too: the scratch has whole tiles.
-            if (G > 1 && cols == G) {
+            if (G > 1 && all_cols == G) {
                 float* at = scores + static_cast<size_t>(row0 + gid) * G + 2 * t4;
                 if (2 * t4 < G) {
                     *reinterpret_cast<float2*>(at) = make_float2(c[0], c[1]);
                     *reinterpret_cast<float2*>(at + 8 * G) = make_float2(c[2], c[3]);
                 }
             } else {
-                float* at = scores + static_cast<size_t>(row0 + gid) * cols + 2 * t4;
+                float* at = scores + static_cast<size_t>(row0 + gid) * all_cols + 2 * t4;
                 if (2 * t4 < cols) {
                     at[0] = c[0];
-                    at[8 * cols] = c[2];
+                    at[8 * all_cols] = c[2];
                 }
                 if (2 * t4 + 1 < cols) {
                     at[1] = c[1];
-                    at[8 * cols + 1] = c[3];
+                    at[8 * all_cols + 1] = c[3];
                 }
             }
         }
@@ -80,12 +92,12 @@ struct RowsMmaMath : MmaMath<D, G, true> {
         Base::softmax(c, b0, b1);
         if (whole) {
             Base::pv(vbase, lane, b0, b1);
-        } else if (tokens == 1) {
-            Base::pv_rows(vbase, lane, b0, b1, rows_seen(row0, limit0, window, sinks));
+        } else if (cols == grp) {
+            Base::pv_rows(vbase, lane, b0, b1, seen_by(limit0));
         } else {
             // Each token's columns with the rows that it sees.
-            for (int j = 0; j < tokens; ++j) {
-                const uint32_t seen = rows_seen(row0, limit0 + j, window, sinks);
+            for (int j = 0; j * grp < cols; ++j) {
+                const uint32_t seen = seen_by(limit0 + j);
                 if (seen != 0u)
                     Base::template pv_rows<true>(vbase, lane, b0, b1, seen, (2 * t4) / grp == j, (2 * t4 + 1) / grp == j);
             }
@@ -93,20 +105,64 @@ struct RowsMmaMath : MmaMath<D, G, true> {
     }
 };
 
-// fp32 on the CUDA cores, G query heads of one token.
+// fp32 on the CUDA cores, up to G query heads of one token.
 template <int D, int G, bool SCORES>
 struct RowsSimtMath : SimtMath<float, D, G> {
     using Base = SimtMath<float, D, G>;
+    using QRegs = typename Base::QRegs;
     static constexpr bool kRows = true;
+    static constexpr bool kCausal = true;         // columns are the item's, not G of them
 
     float* scores;
-    int window, sinks;
+    int cols, window, sinks;
 
-    __device__ __forceinline__ void begin_rows(const DecodeParams& p, int s, int h, int /*ncols: G*/) {
+    // The group's q rows; a column past them is zero.
+    __device__ __forceinline__ void load_heads(const DecodeParams& p, int s, int h, float (&dst)[G][Base::kEpc]) const {
+        const int grp = p.num_heads / p.num_kv_heads;
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+#pragma unroll
+            for (int e = 0; e < Base::kEpc; ++e) dst[g][e] = 0.f;
+            if (g < grp) {
+                const float* row = static_cast<const float*>(p.q) + (static_cast<size_t>(s) * p.num_heads + h * grp + g) * D;
+                const uint4 raw = __ldg(reinterpret_cast<const uint4*>(row) + Base::ch);
+                Base::E::unpack(raw, dst[g]);
+#pragma unroll
+                for (int e = 0; e < Base::kEpc; ++e) dst[g][e] *= p.scale_log2;
+            }
+        }
+    }
+
+    __device__ __forceinline__ void load_q(const DecodeParams& p, int s, int h, QRegs& r) const {
+        r.s = s;
+        r.h = h;
+        if constexpr (Base::kPrefetch) load_heads(p, s, h, r.f);
+    }
+
+    __device__ __forceinline__ void begin(const DecodeParams& p, const QRegs& r) {
+        if constexpr (Base::kPrefetch) {
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+#pragma unroll
+                for (int e = 0; e < Base::kEpc; ++e) Base::qf[g][e] = r.f[g][e];
+        } else {
+            load_heads(p, r.s, r.h, Base::qf);
+        }
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+#pragma unroll
+            for (int e = 0; e < Base::kEpc; ++e) Base::o[g][e] = 0.f;
+            Base::m[g] = -INFINITY;
+            Base::l[g] = 0.f;
+        }
+    }
+
+    __device__ __forceinline__ void begin_rows(const DecodeParams& p, int s, int h, int /*token0: 0*/, int ncols, int /*grp*/) {
+        cols = ncols;
         window = p.window;
         sinks = p.num_sinks;
         if constexpr (SCORES)
-            scores = p.scores + (static_cast<size_t>(s) * p.num_kv_heads + h) * p.score_rows * G;
+            scores = p.scores + (static_cast<size_t>(s) * p.num_kv_heads + h) * p.score_rows * ncols;
     }
 
     __device__ __forceinline__ void tile(uint32_t kbase, uint32_t vbase, int /*valid*/,
@@ -116,7 +172,8 @@ struct RowsSimtMath : SimtMath<float, D, G> {
             if constexpr (SCORES) {
                 if (Base::ch == 0) {
 #pragma unroll
-                    for (int g = 0; g < G; ++g) scores[static_cast<size_t>(row0 + row) * G + g] = sc[g];
+                    for (int g = 0; g < G; ++g)
+                        if (g < cols) scores[static_cast<size_t>(row0 + row) * cols + g] = sc[g];
                 }
             }
         });

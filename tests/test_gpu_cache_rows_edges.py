@@ -92,7 +92,7 @@ def test_drafts_verified_in_a_window_and_rejected_rows_taken_back():
         lens.copy_(i32(sv.lens()))
         q, hq = sv.values(B, Q + 1, sv.hq, sv.D)
         out = torch.empty_like(q)
-        # Heads per KV head x tokens is 16: more than the tensor-core kernel's columns.
+        # Heads per KV head x tokens is 16: two groups of the tensor-core kernel's columns.
         pa.pa_decode_sinks(q, sv.kc, sv.vc, tables_of(sv.m, sv.names, sv.width), lens, sv.scale, window, sinks, out, 1000, error_word=sv.err)
         sv.check(out.double().cpu().numpy(), hq, window, sinks)
         target = torch.from_numpy(sv.r.dirichlet(np.full(V, 0.05), (B, Q + 1)).astype(np.float32)).cuda()
