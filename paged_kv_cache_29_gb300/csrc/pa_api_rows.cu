@@ -163,7 +163,7 @@ pa_status rows_call(const void* q, const void* k_cache, const void* v_cache, con
                                 : weights ? pa::launch_decode_weights(tk, tv, p, dtype, sms, stream_of(stream))
                                           : pa::launch_decode_sinks(tk, tv, p, dtype, sms, stream_of(stream));
         if (err != cudaSuccess) return PA_ERR_CUDA;
-        if (parts > 1 && pa::launch_combine(p, dtype, stream_of(stream)) != cudaSuccess) return PA_ERR_CUDA;
+        if (parts > 1 && pa::launch_combine(p, dtype, stream_of(stream), true) != cudaSuccess) return PA_ERR_CUDA;
         if (weights && pa::launch_row_weights(p, ring ? p.item_count : nullptr, stream_of(stream)) != cudaSuccess)
             return PA_ERR_CUDA;
     }

@@ -177,7 +177,9 @@ __host__ __device__ __forceinline__ int combine_warps(int np, int chunk) {
 // Each warp merges its chunks (lane q holds partition q's max and sum; the o
 // rows are loaded kCombineBatch partitions at a time), then the warp results
 // are merged in warp order.
-template <typename T, int E, int HPB>
+// ROWS: the partitions leave the rows out that seq_gap counts, and final_ml takes the
+// merged maximum and sum where it is set.
+template <typename T, int E, int HPB, bool ROWS = false>
 __global__ void __launch_bounds__(kCombineMaxWarps * 32) combine_kernel(const DecodeParams p) {
     extern __shared__ float sm[];                // [nw][2 + head_dim]
     const int qh = HPB > 1 ? blockIdx.x * HPB + (threadIdx.x >> 5) : blockIdx.x;
@@ -194,7 +196,7 @@ __global__ void __launch_bounds__(kCombineMaxWarps * 32) combine_kernel(const De
     // (0, 0) always waits, so that this grid never completes before the
     // decode kernel does.
     const int n = __ldg(p.context_lens + s);
-    const int span = n - seq_gap(p, n);                   // rows of the partitions
+    const int span = n - (ROWS ? seq_gap(p, n) : seq_row_base(n, p.window));   // rows of the partitions
     const int P = seq_partition(p, span);
     const bool merge = n <= p.context_cap && n >= p.num_queries &&
                        span > P + p.partition_tail;           // else flagged or one partition
@@ -264,7 +266,9 @@ __global__ void __launch_bounds__(kCombineMaxWarps * 32) combine_kernel(const De
                 const int d = lane + 32 * e;
                 if (d < D) ElemTraits<T>::store(out + d, acc[e] / L);
             }
-            if (p.final_ml != nullptr && lane == 0) p.final_ml[row] = make_float2(M, L);
+            if constexpr (ROWS) {
+                if (p.final_ml != nullptr && lane == 0) p.final_ml[row] = make_float2(M, L);
+            }
         } else {
             float* st = sm + warp * (D + 2);
             if (lane == 0) {
@@ -284,7 +288,9 @@ __global__ void __launch_bounds__(kCombineMaxWarps * 32) combine_kernel(const De
     for (int w = 0; w < nw; ++w) M = fmaxf(M, sm[w * (D + 2)]);
     float L = 0.f;
     for (int w = 0; w < nw; ++w) L = fmaf(fast_exp2(sm[w * (D + 2)] - M), sm[w * (D + 2) + 1], L);
-    if (p.final_ml != nullptr && threadIdx.x == 0) p.final_ml[row] = make_float2(M, L);
+    if constexpr (ROWS) {
+        if (p.final_ml != nullptr && threadIdx.x == 0) p.final_ml[row] = make_float2(M, L);
+    }
     T* out = static_cast<T*>(p.out) + row * D;
     for (int d = threadIdx.x; d < D; d += blockDim.x) {
         float a = 0.f;
@@ -326,7 +332,7 @@ cudaError_t launch_decode_generic(const DecodeParams& p, pa_dtype dtype, cudaStr
     return cudaGetLastError();
 }
 
-cudaError_t launch_combine(const DecodeParams& p, pa_dtype dtype, cudaStream_t stream) {
+cudaError_t launch_combine(const DecodeParams& p, pa_dtype dtype, cudaStream_t stream, bool rows) {
     if (p.max_parts <= 1 || p.num_seqs == 0) return cudaSuccess;
     const int warps = combine_warps(p.max_parts, combine_chunk(p));   // enough for the longest sequence
     // One warp per head merges every partition: several heads per CTA.
@@ -350,6 +356,12 @@ cudaError_t launch_combine(const DecodeParams& p, pa_dtype dtype, cudaStream_t s
         // At most 16 warps x (256 + 2) floats: within the default shared-memory limit.
         auto run = [&](auto kernel) -> cudaError_t { return cudaLaunchKernelEx(&cfg, kernel, p); };
         constexpr int H = kCombineHeadsPerCta;
+        if (rows) {
+            if (p.head_dim == 128) return packed ? run(combine_kernel<T, 4, H, true>) : run(combine_kernel<T, 4, 1, true>);
+            if (p.head_dim == 64) return packed ? run(combine_kernel<T, 2, H, true>) : run(combine_kernel<T, 2, 1, true>);
+            return packed ? run(combine_kernel<T, kCombineMaxElems, H, true>)
+                          : run(combine_kernel<T, kCombineMaxElems, 1, true>);
+        }
         if (p.head_dim == 128) return packed ? run(combine_kernel<T, 4, H>) : run(combine_kernel<T, 4, 1>);
         if (p.head_dim == 64) return packed ? run(combine_kernel<T, 2, H>) : run(combine_kernel<T, 2, 1>);
         return packed ? run(combine_kernel<T, kCombineMaxElems, H>)

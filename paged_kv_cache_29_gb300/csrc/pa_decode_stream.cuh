@@ -227,22 +227,11 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap tmap_k,
     const int bs = p.block_size;
     // Rows per partition of the sequence an item belongs to (n rows).
     auto part_rows = [&](int n) { return seq_partition(p, n - seq_row_base(n, p.window)); };
-    // The rows of an item: [lo, hi), numbered within its sequence, or with
-    // Math::kRows within the rows that its partitions cover (seq_gap), of which row v
-    // is row v + gap_from(n, v) of the sequence.
-    auto item_rows = [&](const int4& it, int& lo, int& hi) {
-        if constexpr (Math::kRows) {
-            lo = it.z * p.partition_size;
-            hi = min(it.w - seq_gap(p, it.w), lo + p.partition_size);
-        } else {
-            const int P = part_rows(it.w);
-            lo = seq_row_base(it.w, p.window) + it.z * P;
-            hi = min(it.w, lo + P);
-        }
-    };
+    // With Math::kRows an item's rows are numbered within the rows that its sequence's
+    // partitions cover (seq_gap): row v of those is row v + gap_from(n, v) of the sequence.
+    auto gap_from = [&](int n, int v) { return Math::kRows && v >= sink_rows(p) ? seq_gap(p, n) : 0; };
     // The KV head of an item.
     auto item_head = [&](const int4& it) { return Math::kRows ? it.y / p.col_groups : it.y; };
-    auto gap_from = [&](int n, int v) { return Math::kRows && v >= sink_rows(p) ? seq_gap(p, n) : 0; };
     const uint32_t ring_addr = smem_addr(ring);
 
     if (warp == W) {
@@ -545,20 +534,23 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap tmap_k,
             // with cp.async one item ahead of their use.
             auto prefetch_ids = [&](const int4& it, int32_t* buf) {
                 if (it.x >= 0) {
-                    int lo, hi;
-                    item_rows(it, lo, hi);
-                    const int32_t* bt = p.block_tables + static_cast<size_t>(it.x) * p.max_blocks_per_seq;
                     if constexpr (Math::kRows) {
                         // An id per tile (an item's rows may be two runs of the sequence's).
+                        const int lo = it.z * p.partition_size;
+                        const int hi = min(it.w - seq_gap(p, it.w), lo + p.partition_size);
+                        const int32_t* bt = p.block_tables + static_cast<size_t>(it.x) * p.max_blocks_per_seq;
                         const int ntiles = (hi - lo + kTileRows - 1) / kTileRows;
                         for (int i = lane; i < ntiles; i += 32) {
                             const int v = lo + kTileRows * i;
                             cp_async_4(smem_addr(buf + i), bt + (v + gap_from(it.w, v)) / bs);
                         }
                     } else {
+                        const int P = part_rows(it.w);
+                        const int lo = seq_row_base(it.w, p.window) + it.z * P;
+                        const int hi = min(it.w, lo + P);
                         const int b0 = lo / bs;
                         const int nblk = (hi - 1) / bs - b0 + 1;
-                        bt += b0;
+                        const int32_t* bt = p.block_tables + static_cast<size_t>(it.x) * p.max_blocks_per_seq + b0;
                         for (int i = lane; i < nblk; i += 32) cp_async_4(smem_addr(buf + i), bt + i);
                     }
                 }
@@ -602,14 +594,15 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     cp_async_wait_all();                // the first item's ids, the only group
                 }
                 __syncwarp();
-                int lo, hi;
-                item_rows(cur, lo, hi);
+                const int P = Math::kRows ? p.partition_size : part_rows(cur.w);
+                const int lo = (Math::kRows ? 0 : seq_row_base(cur.w, p.window)) + cur.z * P;
+                const int hi = min(Math::kRows ? cur.w - seq_gap(p, cur.w) : cur.w, lo + P);
                 const int b0 = lo / bs;
-                const int ntiles = (hi - lo + kTileRows - 1) / kTileRows;
-                const int nids = Math::kRows ? ntiles : (hi - 1) / bs - b0 + 1;
+                const int nblk = Math::kRows ? (hi - lo + kTileRows - 1) / kTileRows : (hi - 1) / bs - b0 + 1;   // ids
                 bool bad_lane = false;
-                for (int i = lane; i < nids; i += 32) bad_lane |= (ids[i] < 0) | (ids[i] >= p.num_blocks);
+                for (int i = lane; i < nblk; i += 32) bad_lane |= (ids[i] < 0) | (ids[i] >= p.num_blocks);
                 const int cur_bad = __any_sync(0xffffffffu, bad_lane) ? 1 : 0;
+                const int ntiles = (hi - lo + kTileRows - 1) / kTileRows;
                 if (cur_bad && lane == 0) raise_error(p.error_word, PA_DEVERR_BLOCK_ID);
                 // Fused append: the item holding the sequence's last row writes
                 // this KV head's new K and V rows into their slot before the
@@ -793,8 +786,10 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap tmap_k,
     for (int j = 0; it.x >= 0; ++j) {
         const int s = it.x, h = item_head(it), part = it.z, n = it.w;
         const int token0 = first_token(it), ncols = item_cols(it);
-        int lo, hi;
-        item_rows(it, lo, hi);
+        const int base = Math::kRows ? seq_gap(p, n) : seq_row_base(n, p.window);   // (rows that no partition covers)
+        const int P = Math::kRows ? p.partition_size : seq_partition(p, n - base);
+        const int lo = (Math::kRows ? 0 : base) + part * P;
+        const int hi = min(Math::kRows ? n - base : n, lo + P);
         const int ntiles = (hi - lo + kTileRows - 1) / kTileRows;
         const int4 it_after = item_at(j + 2);
         if constexpr (Math::kQInSmem) {
@@ -823,9 +818,9 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 if (stage_bad[stage]) {
                     bad = true;
                 } else if (t - t0 < ntiles) {
-                    int row0 = lo + kTileRows * (t - t0);
-                    const int valid = min(kTileRows, hi - row0);
-                    row0 += gap_from(n, row0);
+                    const int v0 = lo + kTileRows * (t - t0);
+                    const int valid = min(kTileRows, hi - v0);
+                    const int row0 = v0 + gap_from(n, v0);
                     const uint32_t kb = ring_addr + stage * Geom::kStageBytes;
                     // Rows of the tile before a sliding window (<= 0: none).
                     const int skip = p.window > 0 ? n - p.window - row0 : 0;
@@ -861,8 +856,7 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap tmap_k,
             if (any_bad && p.scores != nullptr && threadIdx.x < ncols)
                 p.part_ml[2 * (query_row(p, s, h, token0 * grp + threadIdx.x, grp) * p.max_parts + part) + 1] = kNoSum;
         }
-        const int P = Math::kRows ? p.partition_size : part_rows(n);
-        const int nparts = (plan_span<Math::kRows>(p, n) + P - 1) / P;
+        const int nparts = (n - base + P - 1) / P;
         for (int idx = any_bad ? ncols * D : threadIdx.x; idx < ncols * D; idx += W * 32) {
             const int g = idx / D;            // query column
             const int d = idx - g * D;
@@ -883,15 +877,22 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap tmap_k,
             const size_t row = Math::kCausal
                                    ? query_row(p, s, h, token0 * grp + g, grp)
                                    : static_cast<size_t>(s) * p.num_heads + h * G + g;
-            const size_t slot = row * p.max_parts + part;
-            if (nparts == 1)
+            if (nparts == 1) {
                 ElemTraits<T>::store(static_cast<T*>(p.out) + row * D + d, O / L);
-            else
+                if constexpr (Math::kRows) {
+                    // pa_decode_weights takes the state of a single partition too.
+                    if (d == 0 && p.scores != nullptr) {
+                        p.part_ml[2 * (row * p.max_parts + part)] = M;
+                        p.part_ml[2 * (row * p.max_parts + part) + 1] = L;
+                    }
+                }
+            } else {
+                const size_t slot = row * p.max_parts + part;
                 p.part_o[slot * D + d] = O;
-            // (pa_decode_weights takes the state of a single partition too.)
-            if (d == 0 && (nparts > 1 || (Math::kRows && p.scores != nullptr))) {
-                p.part_ml[2 * slot] = M;
-                p.part_ml[2 * slot + 1] = L;
+                if (d == 0) {
+                    p.part_ml[2 * slot] = M;
+                    p.part_ml[2 * slot + 1] = L;
+                }
             }
         }
         // The next item's warp states overwrite the merge area.

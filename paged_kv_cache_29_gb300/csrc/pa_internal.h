@@ -40,15 +40,6 @@ struct DecodeParams {
     int num_seqs;
     int num_queries;               // query tokens per sequence, the last rows of each (>= 1)
     int window;                    // sliding window: attend to the last `window` rows (0 = all)
-    int num_sinks;                 // pa_decode_sinks: first rows that stay visible (else 0); `window` then
-                                   //   counts the rows that any of the num_queries tokens' windows holds
-    int col_groups;                // tile ring of those calls: items of a KV head share its query columns in
-    int group_tokens;              //   col_groups groups of up to group_tokens tokens (item.y: head * col_groups + group)
-    float* row_weights;            // pa_decode_weights: [num_blocks][num_kv_heads][block_size] (else null),
-    float* scores;                 //   scores [B][Hkv][score_rows][columns], base 2, of every row,
-    int score_rows;
-    int32_t* item_count;           //   the tile ring's number of work items,
-    float2* final_ml;              //   [B][Q][Hq] max and sum of merged sequences
     int num_heads;
     int num_kv_heads;
     int head_dim;
@@ -66,6 +57,16 @@ struct DecodeParams {
     // its stream tile withhold_tile without copying it or completing its
     // barrier, so the consumer's bounded wait expires.
     int withhold_tile = -1;
+    // pa_decode_sinks and pa_decode_weights only.
+    int num_sinks;                 // first rows that stay visible; `window` then counts the rows that any of the
+                                   //   num_queries tokens' windows holds
+    int col_groups;                // tile ring: items of a KV head share its query columns in
+    int group_tokens;              //   col_groups groups of up to group_tokens tokens (item.y: head * col_groups + group)
+    float* row_weights;            // pa_decode_weights: [num_blocks][num_kv_heads][block_size] (else null),
+    float* scores;                 //   scores [B][Hkv][score_rows][columns], base 2, of every row,
+    int score_rows;
+    int32_t* item_count;           //   the tile ring's number of work items,
+    float2* final_ml;              //   [B][Q][Hq] max and sum of merged sequences
 };
 
 // Launch result: cudaSuccess or the launch error.
@@ -260,8 +261,9 @@ int rows_group_tokens(pa_dtype dtype, int head_dim, int group, int num_queries);
 cudaError_t launch_row_weights(const DecodeParams& p, const int32_t* item_count, cudaStream_t stream);
 constexpr float kNoSum = -1.0f;      // in place of a partition's sum: it has a block outside the pool
 
-// Merge of partition partials for sequences longer than one partition.
-cudaError_t launch_combine(const DecodeParams& p, pa_dtype dtype, cudaStream_t stream);
+// Merge of partition partials for sequences longer than one partition. rows: of
+// pa_decode_sinks and pa_decode_weights.
+cudaError_t launch_combine(const DecodeParams& p, pa_dtype dtype, cudaStream_t stream, bool rows = false);
 
 // Rows per partition of a sequence whose partitions cover `span` rows (its
 // rows from seq_row_base on): partition_size, or partition_long for spans
