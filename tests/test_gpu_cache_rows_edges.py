@@ -302,3 +302,70 @@ def test_refusals_of_the_binding():
                     (dict(num_drafts=acc.long()), TypeError)):
         with pytest.raises(err):
             pa.pa_verify_draft(**{**dict(target_probs=p, draft_probs=q, draft_tokens=x, uniforms=u, out_tokens=out, num_accepted=acc), **kw})
+
+
+@pytest.mark.parametrize("shape", [("bf16", 4, 1, 128, 16), ("bf16", 4, 3, 64, 16), ("f32", 5, 1, 64, 16)], ids=str)
+def test_sequences_of_many_partitions(shape):
+    """More partitions than a warp of the merge takes at a time (40 and 100)."""
+    run = Run(shape, [20000, 50_000 if shape[0] == "bf16" else 17000, 30], hkv=1, seed=21)
+    run.check(run.sinks(18000, 70), 18000, 70)
+    start = start_weights(run.cache)
+    out, got = run.weights(start)
+    run.check(out)
+    for s, n in enumerate(run.lens):
+        _, w, _, tol = ref.attention(run.q[s], run.cache.k[s], run.cache.v[s], run.scale, run.group)
+        old = ref.slot_rows(start, run.cache.table[s], n, run.bs).astype(np.float64)
+        want = np.where(np.arange(n)[:, None] >= n - run.Q, w, old + w)
+        assert (np.abs(ref.slot_rows(got, run.cache.table[s], n, run.bs) - want) <= tol + 2.0 ** -24 * (want + tol)).all()
+    assert int(run.err.item()) == 0
+
+
+def test_more_sequences_than_a_launch_holds_with_column_groups():
+    r = np.random.default_rng(1)
+    lens = [0 if x < 3 else int(x) for x in r.integers(0, 30, 4200)]
+    run = Run(("bf16", 4, 3, 64, 16), lens, hkv=1, seed=22)
+    run.check(run.sinks(7, 2), 7, 2)
+    run.check(run.weights(start_weights(run.cache))[0])
+    assert int(run.err.item()) == 0
+
+
+@pytest.mark.parametrize("shape", [("bf16", 4, 1, 128, 16), ("f32", 1, 1, 33, 5)], ids=str)
+def test_a_length_bound_of_zero(shape):
+    run = Run(shape, [0, 0, 0], seed=23)
+    run.bound = 0
+    assert not run.sinks(5, 2).any()
+    start = start_weights(run.cache)
+    out, got = run.weights(start)
+    assert not out.any() and np.array_equal(got, start)
+    lens = torch.full_like(run.n, 9)
+    pa.pa_evict(run.dk, run.dv, torch.from_numpy(start).cuda(), run.table, run.n, run.n, run.table, lens, 0, 3, 4, error_word=run.err) \
+        if shape[0] == "bf16" else lens.zero_()
+    assert lens.tolist() == [0, 0, 0] and int(run.err.item()) == 0
+
+
+def test_every_row_of_a_long_first_part_and_limits_of_the_numbers():
+    e = Evict([600, 40], [600, 40], 2 ** 31 - 1, 2 ** 31 - 1, place="other", seed=24)
+    e.check()
+
+
+def test_eviction_of_float8_tensors():
+    e = Evict([300, 40], [120, 40], 2, 8, "fp8", seed=25, weights="random")
+    e.k, e.v = e.k.view(torch.float8_e4m3fn), e.v.view(torch.float8_e4m3fn)
+    e.check()
+
+
+def test_probabilities_laid_out_token_by_token():
+    """[rows][B][V] as a loop over tokens leaves them, passed as a transposed view."""
+    r = np.random.default_rng(26)
+    B, Q, V = 6, 3, 777
+    p = r.dirichlet(np.full(V, 0.1), (Q + 1, B)).astype(np.float32)
+    q = r.dirichlet(np.full(V, 0.1), (Q, B)).astype(np.float32)
+    q[:, :3] = p[:Q, :3]
+    x = np.argmax(q, -1).T.astype(np.int32).copy()
+    u = r.random((B, Q + 1), dtype=np.float32)
+    out, acc = torch.zeros(B, Q + 1, dtype=torch.int32, device="cuda"), torch.zeros(B, dtype=torch.int32, device="cuda")
+    pa.pa_verify_draft(torch.from_numpy(p).cuda().transpose(0, 1), torch.from_numpy(q).cuda().transpose(0, 1), torch.from_numpy(x).cuda(),
+                       torch.from_numpy(u).cuda(), out, acc)
+    for s in range(B):
+        a, token, _ = ref.verify(p[:, s], q[:, s], x[s], u[s].astype(np.float64), Q)
+        assert acc[s] == a and out[s].tolist() == list(x[s][:a]) + [token] + [-1] * (Q - a)
