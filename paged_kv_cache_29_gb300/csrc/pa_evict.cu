@@ -37,9 +37,11 @@ constexpr int kFew = 256;                     // candidates that are ranked agai
 constexpr int kCopies = 2;                    // of the counts: 16 lanes at most meet in one
 constexpr int kApart = -1;                    // in place of a first move: no block is moved from and to
 constexpr uint32_t kStays = 0xffffffffu;      // key of a row that stays in any case; no weight has it
-// Keys that a CTA holds. Sequences of more rows than a cluster holds read their weights
-// again in every pass.
+// Keys that a CTA holds at most. Where the bound on the lengths allows more than a cluster
+// holds, it holds those of sequences with up to kShortKeys rows a CTA; longer ones read their
+// weights again in every pass.
 constexpr int kMaxKeys = 48 * 1024;
+constexpr int kShortKeys = 8 * 1024;
 
 // 32 bits in the order of the weights: NaN as -infinity, -0 as +0.
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -50,11 +52,12 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 
 // One cluster per (sequence, KV head): the list of its rows' moves, and from where on rows
 // change their place.
-template <int kSelectThreads>
-__global__ void __launch_bounds__(kSelectThreads, kSelectThreads == 256 ? 4 : 2) evict_select_kernel(const EvictParams p, int max_keys) {
+// HELD: every CTA's keys fit its shared memory, by the bound on the lengths.
+template <int kSelectThreads, bool HELD>
+__global__ void __launch_bounds__(kSelectThreads, kSelectThreads == 256 ? 4 : 2) evict_select_kernel(const EvictParams p) {
     constexpr int kSelectWarps = kSelectThreads / 32;
     static_assert(kSelectThreads >= 256, "a thread per part, a warp per CTA of the cluster");
-    extern __shared__ uint32_t keys[];        // [max_keys]
+    extern __shared__ uint32_t keys[];        // of the CTA's rows (HELD)
     __shared__ uint32_t hist[256 * kCopies];
     __shared__ uint32_t parts[2][256];       // this CTA's counts by part, of two passes
     __shared__ uint32_t few[2][kFew];         // candidates: this CTA's, the cluster's
@@ -106,7 +109,7 @@ __global__ void __launch_bounds__(kSelectThreads, kSelectThreads == 256 ? 4 : 2)
     const int row0 = min(n, rank * share), row1 = min(n, row0 + share);
     const int warp_share = ((row1 - row0 + kSelectWarps - 1) / kSelectWarps + 31) / 32 * 32;
     const int w0 = min(row1, row0 + warp * warp_share), w1 = min(row1, w0 + warp_share);
-    const bool held = share <= max_keys;
+    const bool held = HELD || share <= kShortKeys;
     if (tid == 0) {
         flags = 0;
         first_move = INT_MAX;
@@ -131,7 +134,7 @@ __global__ void __launch_bounds__(kSelectThreads, kSelectThreads == 256 ? 4 : 2)
         outside |= id < 0 || id >= p.num_blocks;
         same |= id == __ldg(from + b);
     }
-    constexpr int kRows = 8;                  // rows of a thread whose loads are on the way together
+    constexpr int kRows = kSelectThreads == 256 ? 4 : 8;   // rows of a thread whose loads are on the way together
     for (int i0 = row0 + tid; i0 < row1; i0 += kRows * kSelectThreads) {
         int id[kRows];
         uint32_t k[kRows];
@@ -462,9 +465,15 @@ cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream) {
     int ranks = 1;
     while (ranks < kMaxCluster && static_cast<long long>(heads) * ranks < 2 * sms && p.context_cap / ranks > 2048) ranks *= 2;
     const int share = ((p.context_cap + ranks - 1) / ranks + 31) / 32 * 32;
-    const int max_keys = share < kMaxKeys ? share : kMaxKeys;
+    // Many CTAs hold few keys each, so that several fit an SM: 1,024 of them with a bound of
+    // 32,768 rows and lengths of 1,640 take 189 us so, 202 with room for the bound.
+    const int most_keys = static_cast<long long>(heads) * ranks <= 4LL * sms ? kMaxKeys : kShortKeys;
+    const bool all_held = share <= most_keys;
+    const int max_keys = all_held ? share : kShortKeys;
     // More threads where a CTA has many rows; else smaller CTAs, more of them to an SM.
-    auto* select = share > 8192 ? evict_select_kernel<512> : evict_select_kernel<256>;
+    auto* select = !all_held      ? evict_select_kernel<512, false>
+                   : share > 8192 ? evict_select_kernel<512, true>
+                                  : evict_select_kernel<256, true>;
     cudaError_t err = cudaSuccess;
     if (max_keys > 8192) {                    // beyond the shared memory that needs no asking
         err = cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * kMaxKeys);
@@ -482,12 +491,12 @@ cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream) {
     // Programmatic dependents where the keys take little shared memory. Where they take
     // much, moving CTAs beside selecting ones have little of the SM's memory left for loads
     // on their way: 128 sequences of 1,640 rows then take 350 us, and 226 without.
-    const bool early = max_keys <= 2048;
+    const bool early = share <= 2048;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = early ? 2 : 1;
-    err = cudaLaunchKernelEx(&cfg, select, p, max_keys);
+    err = cudaLaunchKernelEx(&cfg, select, p);
     if (err != cudaSuccess) return err;
     // Slices of 128 bytes, or what divides the rows. Few sequences: of 32 bytes (a sector), larger
     // CTAs and more of them.

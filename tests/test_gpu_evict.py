@@ -219,3 +219,13 @@ def test_weights_that_are_close_together(kind, n, place):
     e = Evict([n, n // 2, 3], [n // 3, n // 2 - 1, 1], 1, 0, "bf16", hkv=2, D=8, place=place, seed=n, weights="equal")
     e.w = narrow(kind, np.random.default_rng(n), e.w.shape)
     e.check()
+
+
+@pytest.mark.parametrize("weights", ["random", "odd"])
+def test_a_bound_beyond_what_clusters_hold(weights):
+    """Lengths bounded at a million rows (the keys are read again in every pass), and one of 450,000."""
+    e = Evict([450_000, 90, 0, 5000], [1000, 40, 0, 4990], 2, 20, "int4", hkv=1, D=32, place="other", seed=14, weights=weights)
+    e.table = np.pad(e.table, ((0, 0), (0, 70_000 - e.table.shape[1])), constant_values=-1)
+    e.to = np.pad(e.to, ((0, 0), (0, 70_000 - e.to.shape[1])), constant_values=-1)
+    e.bound = 1_000_000
+    e.check()
