@@ -11,7 +11,7 @@
 // additions took as long as the loads.)
 //
 // A cluster of CTAs shares a sequence's row, a CTA a run of its segments of 512
-// (or 256) values, a warp a segment at a time. Running sums over the CTA's segments, then over
+// values, a warp a segment at a time. Running sums over the CTA's segments, then over
 // the cluster's CTAs through their shared memory, find the one segment that u S falls
 // into; its CTA scans that, a value a thread. Every order of addition is fixed by the
 // row's length and the cluster's size.
@@ -29,15 +29,17 @@ namespace pa {
 
 namespace {
 
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kSegment = kThreads;            // a value a thread, in the last step
 constexpr int kMaxCluster = 8;
-// Segments of a CTA: their running sums fit the default shared memory, and 2^22 values
-// (2^14 segments of 256) fit a cluster.
+// Segments of a CTA: their running sums fit the default shared memory.
 constexpr int kMaxSegments = 4096;
 
 // A sum of fp32 values as hi + lo, |lo| at most half a step of hi.
 struct Sum {
     float hi, lo;
-    // + x + err; lo is left to grow (take() or plus() bring the pair to order)
+    // + x + err; lo is left to grow (order() or plus() bring the pair to order)
     __device__ __forceinline__ void add(float x, float err) {
         const float s = hi + x;
         const float b = s - hi;
@@ -178,10 +180,7 @@ __device__ __forceinline__ Sum sum_some(const float* pr, const float* qr, int v0
     return sum.order();
 }
 
-template <int THREADS>
-__global__ void __launch_bounds__(THREADS) verify_kernel(const VerifyParams p, int segs_per_cta) {
-    constexpr int kSegment = THREADS;         // a value a thread, in the last step
-    constexpr int kWarps = THREADS / 32;
+__global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams p, int segs_per_cta) {
     extern __shared__ Sum seg_sum[];          // [segs_per_cta]: of each segment, then up to its end
     __shared__ Sum cta_total, warp_total[kWarps], border_left;
     __shared__ int first_rejected, bad, chosen, owner;
@@ -344,13 +343,13 @@ __global__ void __launch_bounds__(THREADS) verify_kernel(const VerifyParams p, i
             __syncthreads();                  // every thread has read `chosen`
             if (tid == 0) chosen = -1;
             __syncthreads();
-            for (int v = seg0 * kSegment + tid; last_positive < 0 && v < min(V, (seg0 + seg) * kSegment); v += THREADS)
+            for (int v = seg0 * kSegment + tid; last_positive < 0 && v < min(V, (seg0 + seg) * kSegment); v += kThreads)
                 if (v != left_out && __ldg(pr + v) > (qr != nullptr ? __ldg(qr + v) : 0.f)) atomicMax(&chosen, v);
             if (last_positive >= 0) atomicMax(&chosen, last_positive);
             __syncthreads();
             token = chosen;
         }
-        for (int i = tid; i <= Q; i += THREADS)
+        for (int i = tid; i <= Q; i += kThreads)
             p.out_tokens[static_cast<size_t>(s) * (Q + 1) + i] = i < a ? __ldg(tokens + i) : i == a ? token : -1;
         if (tid == 0) {
             p.num_accepted[s] = a;
@@ -360,17 +359,26 @@ __global__ void __launch_bounds__(THREADS) verify_kernel(const VerifyParams p, i
     cluster.barrier_wait(std::move(arrived));
 }
 
-template <int THREADS>
-cudaError_t launch(const VerifyParams& p, long long ctas, cudaStream_t stream) {
-    const int segs = (p.vocab + THREADS - 1) / THREADS;
+}  // namespace
+
+cudaError_t launch_verify(const VerifyParams& p, cudaStream_t stream) {
+    if (p.num_seqs == 0) return cudaSuccess;
+    const long long sms = device_sms();
+    if (sms <= 0) return cudaErrorInvalidDevice;
+    const int segs = (p.vocab + kSegment - 1) / kSegment;
+    // CTAs of a sequence: until they are one for each SM, two fit one. The last doubling only
+    // where its clusters of eight all find room at once (37 sequences of 50,021 values: 12.7 us
+    // with clusters of eight, 9 with four).
     int ranks = 1;
-    while (ranks < kMaxCluster && ranks < segs &&
-           (static_cast<long long>(p.num_seqs) * ranks < ctas || segs > kMaxSegments * ranks))
+    while (ranks < kMaxCluster && ranks < segs) {
+        const bool room = ranks < 4 || 5LL * p.num_seqs * 2 * ranks <= 8 * sms;
+        if ((p.num_seqs * static_cast<long long>(ranks) >= sms || !room) && segs <= kMaxSegments * ranks) break;
         ranks *= 2;
+    }
     const int per_cta = (segs + ranks - 1) / ranks;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(p.num_seqs) * ranks);
-    cfg.blockDim = dim3(THREADS);
+    cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = sizeof(Sum) * static_cast<size_t>(per_cta);   // 32 KB at most
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
@@ -381,21 +389,9 @@ cudaError_t launch(const VerifyParams& p, long long ctas, cudaStream_t stream) {
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    cudaError_t err = cudaLaunchKernelEx(&cfg, verify_kernel<THREADS>, p, per_cta);
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, verify_kernel, p, per_cta);
     if (err != cudaSuccess) return err;
     return cudaGetLastError();
-}
-
-}  // namespace
-
-cudaError_t launch_verify(const VerifyParams& p, cudaStream_t stream) {
-    if (p.num_seqs == 0) return cudaSuccess;
-    const int sms = device_sms();
-    if (sms <= 0) return cudaErrorInvalidDevice;
-    // Few sequences: the CTAs of a largest cluster do not fill the device, so that each has
-    // more loads on the way. Many: smaller CTAs, several to an SM, spread evenly.
-    return static_cast<long long>(p.num_seqs) * kMaxCluster <= sms ? launch<512>(p, sms, stream)
-                                                                   : launch<256>(p, 2LL * sms, stream);
 }
 
 }  // namespace pa
