@@ -12,40 +12,40 @@ constexpr int kWarps = 4;            // consumer warps, ring stages and CTAs per
 constexpr int kStages = 4;           // decode kernels have them (pa_decode_mma.cu, pa_decode_simt.cu)
 constexpr int kMinCtasPerSm = 4;
 
-template <int D, int G, bool SCORES>
+template <int D, int G, bool SCORES, bool ENDS>
 cudaError_t run_mma(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeParams& p, int sm_count,
                     cudaStream_t stream) {
-    return launch_stream_instance<RowsMmaMath<D, G, SCORES>, D, G, kWarps, kStages, kMinCtasPerSm, false>(
+    return launch_stream_instance<RowsMmaMath<D, G, SCORES, ENDS>, D, G, kWarps, kStages, kMinCtasPerSm, false>(
         tk, tv, p, sm_count, stream);
 }
 
-template <int D, int G, bool SCORES>
+template <int D, int G, bool SCORES, bool ENDS>
 cudaError_t run_simt(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeParams& p, int sm_count,
                      cudaStream_t stream) {
-    return launch_stream_instance<RowsSimtMath<D, G, SCORES>, D, G, kWarps, kWarps, 1, false>(tk, tv, p, sm_count,
+    return launch_stream_instance<RowsSimtMath<D, G, SCORES, ENDS>, D, G, kWarps, kWarps, 1, false>(tk, tv, p, sm_count,
                                                                                               stream);
 }
 
-template <int D, bool SCORES>
+template <int D, bool SCORES, bool ENDS>
 cudaError_t by_columns(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeParams& p, pa_dtype dtype,
                        int sm_count, cudaStream_t stream) {
     const int cols = (p.num_heads / p.num_kv_heads) * p.group_tokens;
     const bool bf16 = dtype == PA_DTYPE_BF16;
-    if (cols <= 1) return bf16 ? run_mma<D, 1, SCORES>(tk, tv, p, sm_count, stream)
-                               : run_simt<D, 1, SCORES>(tk, tv, p, sm_count, stream);
-    if (cols <= 2) return bf16 ? run_mma<D, 2, SCORES>(tk, tv, p, sm_count, stream)
-                               : run_simt<D, 2, SCORES>(tk, tv, p, sm_count, stream);
-    if (cols <= 4) return bf16 ? run_mma<D, 4, SCORES>(tk, tv, p, sm_count, stream)
-                               : run_simt<D, 4, SCORES>(tk, tv, p, sm_count, stream);
-    return bf16 ? run_mma<D, 8, SCORES>(tk, tv, p, sm_count, stream)
-                : run_simt<D, 8, SCORES>(tk, tv, p, sm_count, stream);
+    if (cols <= 1) return bf16 ? run_mma<D, 1, SCORES, ENDS>(tk, tv, p, sm_count, stream)
+                               : run_simt<D, 1, SCORES, ENDS>(tk, tv, p, sm_count, stream);
+    if (cols <= 2) return bf16 ? run_mma<D, 2, SCORES, ENDS>(tk, tv, p, sm_count, stream)
+                               : run_simt<D, 2, SCORES, ENDS>(tk, tv, p, sm_count, stream);
+    if (cols <= 4) return bf16 ? run_mma<D, 4, SCORES, ENDS>(tk, tv, p, sm_count, stream)
+                               : run_simt<D, 4, SCORES, ENDS>(tk, tv, p, sm_count, stream);
+    return bf16 ? run_mma<D, 8, SCORES, ENDS>(tk, tv, p, sm_count, stream)
+                : run_simt<D, 8, SCORES, ENDS>(tk, tv, p, sm_count, stream);
 }
 
-template <bool SCORES>
+template <bool SCORES, bool ENDS = false>
 cudaError_t launch_rows_ring(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeParams& p, pa_dtype dtype,
                              int sm_count, cudaStream_t stream) {
-    return p.head_dim == 64 ? by_columns<64, SCORES>(tk, tv, p, dtype, sm_count, stream)
-                            : by_columns<128, SCORES>(tk, tv, p, dtype, sm_count, stream);
+    return p.head_dim == 64 ? by_columns<64, SCORES, ENDS>(tk, tv, p, dtype, sm_count, stream)
+                            : by_columns<128, SCORES, ENDS>(tk, tv, p, dtype, sm_count, stream);
 }
 }  // namespace
 

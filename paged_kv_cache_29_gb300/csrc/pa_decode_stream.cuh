@@ -895,6 +895,11 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 }
             }
         }
+        if constexpr (Math::kRows) {
+            if constexpr (Math::kEnds) {
+                if (!any_bad) math.template end_rows<W, Smem::kState>(p, buf, s, h, n, ncols);
+            }
+        }
         // The next item's warp states overwrite the merge area.
         named_barrier(1, W * 32);
     }

@@ -253,6 +253,9 @@ cudaError_t launch_decode_sinks(const CUtensorMap& tk, const CUtensorMap& tv, co
                                 pa_dtype dtype, int sm_count, cudaStream_t stream);
 cudaError_t launch_decode_weights(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeParams& p,
                                   pa_dtype dtype, int sm_count, cudaStream_t stream);
+// (Every sequence of one partition: adds the row weights too.)
+cudaError_t launch_decode_weights_short(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeParams& p,
+                                        pa_dtype dtype, int sm_count, cudaStream_t stream);
 int rows_group_tokens(pa_dtype dtype, int head_dim, int group, int num_queries);
 
 // Accumulates the row weights of pa_decode_weights from the scores and the

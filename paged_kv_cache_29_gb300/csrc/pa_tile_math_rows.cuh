@@ -6,7 +6,7 @@
 // tokens; the others (the one that the window begins in, the last one, a last
 // tile of first rows) mask scores, and take the products with V a token at a time, over
 // the rows that it sees: 0 * NaN would reach the other tokens' sums. With SCORES every row's scores go
-// to p.scores, for the row weights.
+// to p.scores, for the row weights; with ENDS too an item's end adds them.
 #pragma once
 
 #include "pa_tile_math.cuh"
@@ -21,11 +21,49 @@ __device__ __forceinline__ uint32_t rows_seen(int row0, int last, int window, in
     return seen;
 }
 
+// The row weights of a sequence of one partition, by the CTA's consumer warps at its
+// item's end: the columns' maxima and sums are those of the CTA's W warps (states of STATE
+// floats, maxima then sums of G columns, in `buf`), the scores its own. For calls
+// whose sequences all have one partition: a sequence of 17 rows takes 8.5 us, 10.5 with
+// row_weights_kernel behind the decode kernel. In an instance for longer sequences
+// it costs registers that their tiles need (32 sequences of 4096 rows: 182 us instead of 171).
+template <int W, int STATE, int G>
+__device__ __forceinline__ void item_row_weights(const DecodeParams& p, const float* buf, int s, int h, int n, int cols) {
+    float M[G], R[G];
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        M[g] = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < W; ++w) M[g] = fmaxf(M[g], buf[w * STATE + g]);
+        M[g] = g < cols && M[g] != -INFINITY ? M[g] : 0.f;
+        float L = 0.f;
+#pragma unroll
+        for (int w = 0; w < W; ++w) L = fmaf(fast_exp2(buf[w * STATE + g] - M[g]), buf[w * STATE + G + g], L);
+        R[g] = 1.f / L;
+    }
+    const int bs = p.block_size;
+    const int32_t* table = p.block_tables + static_cast<size_t>(s) * p.max_blocks_per_seq;
+    const float* scores = p.scores + (static_cast<size_t>(s) * p.num_kv_heads + h) * p.score_rows * cols;
+    for (int i = threadIdx.x; i < n; i += W * 32) {
+        const int b = i / bs;
+        float* at = p.row_weights + (static_cast<size_t>(__ldg(table + b)) * p.num_kv_heads + h) * bs + (i - b * bs);
+        float w = 0.f;
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+            if (g < cols) w = fmaf(fast_exp2(scores[static_cast<size_t>(i) * cols + g] - M[g]), R[g], w);
+        if (i >= n - p.num_queries)
+            *at = w;
+        else
+            atomicAdd(at, w);
+    }
+}
+
 // bf16 tensor-core products, up to G query columns.
-template <int D, int G, bool SCORES>
+template <int D, int G, bool SCORES, bool ENDS>
 struct RowsMmaMath : MmaMath<D, G, true> {
     using Base = MmaMath<D, G, true>;
     static constexpr bool kRows = true;
+    static constexpr bool kEnds = ENDS;           // an item's end adds its row weights
     using Base::gid;
     using Base::t4;
 
@@ -38,6 +76,11 @@ struct RowsMmaMath : MmaMath<D, G, true> {
         const int h = head / p.col_groups, token0 = (head - h * p.col_groups) * p.group_tokens;
         stage_q_rows<D, Base::kQRowBytes>(p, s, h, grp * min(p.group_tokens, p.num_queries - token0), grp, qbuf, lane,
                                           token0 * grp);
+    }
+
+    template <int W, int STATE>
+    __device__ __forceinline__ void end_rows(const DecodeParams& p, const float* buf, int s, int h, int n, int ncols) const {
+        item_row_weights<W, STATE, G>(p, buf, s, h, n, ncols);
     }
 
     __device__ __forceinline__ void begin_rows(const DecodeParams& p, int s, int h, int token0, int ncols, int grp) {
@@ -106,11 +149,12 @@ struct RowsMmaMath : MmaMath<D, G, true> {
 };
 
 // fp32 on the CUDA cores, up to G query heads of one token.
-template <int D, int G, bool SCORES>
+template <int D, int G, bool SCORES, bool ENDS>
 struct RowsSimtMath : SimtMath<float, D, G> {
     using Base = SimtMath<float, D, G>;
     using QRegs = typename Base::QRegs;
     static constexpr bool kRows = true;
+    static constexpr bool kEnds = ENDS;
     static constexpr bool kCausal = true;         // columns are the item's, not G of them
 
     float* scores;
@@ -155,6 +199,11 @@ struct RowsSimtMath : SimtMath<float, D, G> {
             Base::m[g] = -INFINITY;
             Base::l[g] = 0.f;
         }
+    }
+
+    template <int W, int STATE>
+    __device__ __forceinline__ void end_rows(const DecodeParams& p, const float* buf, int s, int h, int n, int ncols) const {
+        item_row_weights<W, STATE, G>(p, buf, s, h, n, ncols);
     }
 
     __device__ __forceinline__ void begin_rows(const DecodeParams& p, int s, int h, int /*token0: 0*/, int ncols, int /*grp*/) {

@@ -261,3 +261,48 @@ def test_on_another_stream_with_scratch_of_its_own():
     pa.pa_decode_sinks(run.dq, run.dk, run.dv, run.table, run.n, run.scale, 77, 3, o, run.bound, stream=side)
     side.synchronize()
     run.check(o.double().cpu().numpy(), 77, 3)
+
+
+@pytest.mark.parametrize("shape", RING, ids=str)
+def test_weights_of_short_sequences(shape):
+    """Sequences of one partition each: as in 64 bits, flagged ones left out, and the bits of the
+    same call with a length bound that allows more partitions."""
+    Q = shape[2]
+    lens = [0, Q, Q + 1, 15 + Q, 17 + Q, 64, 511, 512, 300, 90]
+    run = Run(shape, lens, seed=15)
+    start = start_weights(run.cache)
+    out, got = run.weights(start)
+    run.check(out)
+    check_weights(run, start, got)
+    run.table = torch.nn.functional.pad(run.table, (0, 1), value=-1)
+    run.bound = 513
+    for a, b in zip(run.weights(start), (out, got)):
+        assert np.array_equal(a, b)
+    run.bound = 512
+    run.n[8] = Q - 1 if Q > 1 else -1
+    run.n[9] = run.bound + 1
+    run.table[7, 1] = run.cache.num_blocks
+    out1, got1 = run.weights(start)
+    assert int(run.err.item()) == pa.PA_DEVERR_CONTEXT | pa.PA_DEVERR_BLOCK_ID
+    for s, n in enumerate(lens):
+        rows = lambda w: ref.slot_rows(w, run.cache.table[s], n, run.bs)
+        assert np.array_equal(rows(got1), rows(start if s in (7, 8, 9) else got))
+        assert s in (7, 8, 9) or np.array_equal(out1[s], out[s])
+
+
+@pytest.mark.parametrize("shape", [RING[1], RING[3], RING[-1]], ids=str)
+def test_short_sequences_alone_and_in_a_large_batch(shape):
+    r = np.random.default_rng(3)
+    lens = [int(x) for x in r.integers(1, 60, 700)] + [512]
+    run = Run(shape, lens, seed=16)
+    start = start_weights(run.cache)
+    out, got = run.weights(start)
+    run.check(out)
+    check_weights(run, start, got)
+    dq, table, n = run.dq, run.table, run.n
+    for a, b in ((0, 1), (40, 300), (600, 701)):
+        run.dq, run.table, run.n = dq[a:b], table[a:b], n[a:b]
+        out1, got1 = run.weights(start)
+        assert np.array_equal(out1, out[a:b])
+        for s in range(a, b):
+            assert np.array_equal(*(ref.slot_rows(w, run.cache.table[s], lens[s], run.bs) for w in (got1, got)))
