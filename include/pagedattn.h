@@ -639,9 +639,10 @@ pa_status pa_norm_rope_append_int4(const pa_norm_rope_args* args, const void* v,
  * q, out: dtype [num_seqs][num_queries][num_heads][head_dim], fp32 or bf16.
  * n == 0 gives zero rows; 0 < n < Q is flagged PA_DEVERR_CONTEXT. Only the rows
  * of the 16-row tiles that hold a visible row are read. A row that is not finite
- * reaches the query tokens that attend to it and no other. Partitions of 512
- * rows, counted without the rows between the first ones and the window, are merged as
- * in pa_decode: a sequence's result does not depend on the rest of the batch.
+ * reaches the query tokens that attend to it and no other. Partitions (of 512 rows or
+ * more, by window, num_sinks and num_queries; the rows between the first ones and the window
+ * are not counted) are merged as in pa_decode: a sequence's result does not depend on the
+ * rest of the batch.
  * window >= 1, num_sinks >= 0, 1 <= num_queries <= 8. Workspace:
  * pa_decode_workspace_size_multi. head_dim up to 256, any block_size >= 1, at most
  * 1024 heads per KV head * num_queries. The fast kernels need block_size a multiple of 16, head_dim 64 or
@@ -744,8 +745,8 @@ size_t pa_evict_workspace_size(int num_seqs, int num_kv_heads, int max_context_l
  *   cache (context_lens counts the rows of all d; both null: no such output).
  * draft_probs null: the drafts were not drawn (a lookup), q_i is 1 at x_i and 0
  * elsewhere. Products are exact, sums keep 44 bits or more: only where u comes nearer
- * than that to the border between two tokens may either be drawn. A NaN or negative r
- * counts as 0.
+ * than that to the border between two tokens may either be drawn (for sums from 2^-100
+ * to 2^127). A NaN or negative r counts as 0.
  *
  * target_probs: fp32 [num_seqs][max_drafts + 1][vocab_size], draft_probs: fp32
  * [num_seqs][max_drafts][vocab_size], with any strides (elements) between

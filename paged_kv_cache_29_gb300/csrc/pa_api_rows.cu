@@ -79,14 +79,14 @@ pa_status rows_call(const void* q, const void* k_cache, const void* v_cache, con
     const int sinks = all ? 0 : (num_sinks < max_context_len ? num_sinks : max_context_len);
     // Rows of the longest sequence's partitions: its first rows in whole tiles,
     // its windows' and up to 15 before them in the same tile.
-    const long long seen = (static_cast<long long>(rows_seen) + 30) / 16 * 16 + (static_cast<long long>(sinks) + 15) / 16 * 16;
+    const long long seen = (static_cast<long long>(window) + num_queries + 29) / 16 * 16 + (static_cast<long long>(num_sinks) + 15) / 16 * 16;
     const long long most = all || seen > max_context_len ? max_context_len : seen;
-    // A windowed sequence in equal partitions of 512 rows or more: 128 sequences with a window
+    // A window's rows in equal partitions of 512 rows or more: 128 sequences with a window
     // of 1,024 rows and 4 first ones, 1,056 with their tiles, take 87 us in two partitions, 91
-    // in 512 + 512 + 32. By the window alone, so that a sequence's partitions do not depend on
-    // the batch.
-    int P = pa::kDefaultPartition;
-    if (!all) {
+    // in 512 + 512 + 32. By the window and the first rows alone, so that a sequence's partitions do
+    // not depend on the batch, nor on the bound on its lengths.
+    int P = pa::kDefaultPartition;                // (752 at most)
+    if (!weights) {
         const long long equal = (seen + P / 2) / P;
         const long long rows = equal > 0 ? ceil_div(ceil_div(seen, equal), 16) * 16 : 0;
         if (rows > P) P = static_cast<int>(rows);

@@ -273,7 +273,8 @@ __global__ void __launch_bounds__(kWeightThreads) row_weights_kernel(const Decod
 #pragma unroll
         for (int u = 0; u < kWeightRows; ++u) {
             const int i = i0 + 32 * u;
-            if (i >= end) continue;
+            // (An id outside the pool: its sequence is flagged, or the ring gave up before its partition.)
+            if (i >= end || id[u] < 0 || id[u] >= p.num_blocks) continue;
             float* at = p.row_weights + (static_cast<size_t>(id[u]) * p.num_kv_heads + h) * bs + by_block.rest(i, by_block.quotient(i));
             if (i >= n - Q)
                 *at = w[u];
@@ -290,7 +291,7 @@ cudaError_t launch_decode_rows(const DecodeParams& p, pa_dtype dtype, cudaStream
     const long long grid = static_cast<long long>(p.max_parts) * p.num_seqs * p.num_kv_heads;
     if (grid <= 0) return cudaSuccess;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    // At most 8 x (256 + 512 + 2) floats and 512 row numbers: within the default limit.
+    // At most 8 x (256 + 752 + 2) floats and 752 row numbers: within the default limit.
     if (dtype == PA_DTYPE_BF16)
         decode_rows_kernel<__nv_bfloat16><<<static_cast<unsigned>(grid), kThreads, smem, stream>>>(p);
     else

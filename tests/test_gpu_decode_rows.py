@@ -213,10 +213,11 @@ def test_more_sequences_than_a_launch_holds():
 
 def test_a_window_that_holds_every_row_is_none():
     run = Run(("bf16", 4, 1, 128, 16), [1551, 512, 7, 0], seed=13)
-    whole = run.sinks(1551, 0)
-    run.check(whole)
-    assert np.array_equal(run.sinks(2 ** 31 - 1, 2 ** 31 - 1), whole)
-    assert np.array_equal(run.weights(start_weights(run.cache))[0], whole)
+    for got in (run.sinks(1551, 0), run.sinks(2 ** 31 - 1, 2 ** 31 - 1), run.weights(start_weights(run.cache))[0]):
+        run.check(got)
+    # Windows of 1,000 rows lie in partitions of 512, as decoding without one has them: the same bits.
+    run = Run(("bf16", 4, 1, 128, 16), [991, 512, 7, 0], seed=13)
+    assert np.array_equal(run.weights(start_weights(run.cache))[0], run.sinks(1000, 0))
 
 
 @pytest.mark.parametrize("shape", [RING[1], RING[5], RING[11], RING[-1], PLAIN[2]], ids=str)
@@ -306,3 +307,16 @@ def test_short_sequences_alone_and_in_a_large_batch(shape):
         assert np.array_equal(out1, out[a:b])
         for s in range(a, b):
             assert np.array_equal(*(ref.slot_rows(w, run.cache.table[s], lens[s], run.bs) for w in (got1, got)))
+
+
+@pytest.mark.parametrize("shape", [RING[1], RING[5], RING[-1], PLAIN[0], PLAIN[4]], ids=str)
+@pytest.mark.parametrize("window,sinks", [(700, 4), (660, 0), (1024, 4), (30, 2000), (1600, 100)])
+def test_a_sequence_does_not_depend_on_the_bound_of_the_lengths(shape, window, sinks):
+    """Also where no row can be outside the window, or the first rows are all there are."""
+    run = Run(shape, [690, 40, 600, 513], seed=17)
+    run.table = torch.nn.functional.pad(run.table, (0, 5000 // shape[4] + 1), value=-1)
+    want = run.sinks(window, sinks)
+    for bound in (701, 752, 1025, 2500, 5000):
+        run.bound = bound
+        assert np.array_equal(run.sinks(window, sinks), want)
+    assert int(run.err.item()) == 0
