@@ -22,29 +22,31 @@ from ._binding import (  # noqa: F401
     pa_decode_int8,
     pa_decode_multi,
     pa_decode_noalloc,
-    pa_decode_sinks,
-    pa_decode_weights,
     pa_append_decode,
     pa_append_decode_fp8,
     pa_append_decode_int8,
     pa_decode_window,
-    pa_evict,
-    pa_evict_workspace_size,
     pa_gather_int4,
     pa_norm_rope,
     pa_norm_rope_append,
     pa_norm_rope_append_int4,
     pa_decode_workspace_size,
     pa_decode_workspace_size_multi,
-    pa_decode_workspace_size_weights,
     pa_reshape_and_cache,
     pa_reshape_and_cache_fp8,
     pa_reshape_and_cache_int4,
     pa_reshape_and_cache_int8,
     pa_default_partition_size,
     pa_status_string,
-    pa_verify_draft,
     pa_version,
+)
+from ._binding_rows import (  # noqa: F401
+    pa_decode_sinks,
+    pa_decode_weights,
+    pa_evict,
+    pa_evict_workspace_size,
+    pa_decode_workspace_size_weights,
+    pa_verify_draft,
 )
 
 __all__ = ["pa_reshape_and_cache", "pa_reshape_and_cache_int8", "pa_decode_int8", "pa_decode_window", "pa_decode_multi", "pa_reshape_and_cache_fp8", "pa_decode_fp8", "pa_copy_blocks", "pa_decode", "pa_decode_noalloc", "pa_append_decode", "pa_append_decode_fp8", "pa_append_decode_int8", "pa_decode_workspace_size", "pa_decode_workspace_size_multi", "pa_status_string",

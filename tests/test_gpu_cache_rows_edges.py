@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import cache_rows_reference as ref
+import paged_kv_cache_29_gb300 as pkg
 from paged_kv_cache_29_gb300 import _binding as pa
 from paged_kv_cache_29_gb300.block_manager import BlockManager
 from test_gpu_decode_rows import Run, start_weights
@@ -93,7 +94,7 @@ def test_drafts_verified_in_a_window_and_rejected_rows_taken_back():
         q, hq = sv.values(B, Q + 1, sv.hq, sv.D)
         out = torch.empty_like(q)
         # Heads per KV head x tokens is 16: two groups of the tensor-core kernel's columns.
-        pa.pa_decode_sinks(q, sv.kc, sv.vc, tables_of(sv.m, sv.names, sv.width), lens, sv.scale, window, sinks, out, 1000, error_word=sv.err)
+        pkg.pa_decode_sinks(q, sv.kc, sv.vc, tables_of(sv.m, sv.names, sv.width), lens, sv.scale, window, sinks, out, 1000, error_word=sv.err)
         sv.check(out.double().cpu().numpy(), hq, window, sinks)
         target = torch.from_numpy(sv.r.dirichlet(np.full(V, 0.05), (B, Q + 1)).astype(np.float32)).cuda()
         draft = torch.from_numpy(sv.r.dirichlet(np.full(V, 0.05), (B, Q)).astype(np.float32)).cuda()
@@ -101,7 +102,7 @@ def test_drafts_verified_in_a_window_and_rejected_rows_taken_back():
         tokens = torch.multinomial(draft.flatten(0, 1) + 1e-20, 1).view(B, Q).int()
         u = torch.from_numpy(sv.r.random((B, Q + 1), dtype=np.float32)).cuda()
         new, accepted = torch.zeros(B, Q + 1, dtype=torch.int32, device="cuda"), torch.zeros(B, dtype=torch.int32, device="cuda")
-        pa.pa_verify_draft(target, draft, tokens, u, new, accepted, context_lens=lens, lens_out=lens, error_word=sv.err)
+        pkg.pa_verify_draft(target, draft, tokens, u, new, accepted, context_lens=lens, lens_out=lens, error_word=sv.err)
         for s, a in enumerate(accepted.tolist()):
             want, token, _ = ref.verify(target[s].cpu().numpy(), draft[s].cpu().numpy(), tokens[s].tolist(), u[s].double().cpu().numpy(), Q)
             assert (a, int(new[s, a])) == (want, token)
@@ -130,7 +131,7 @@ def test_a_cache_kept_to_a_budget(shared):
         out = torch.empty_like(q)
         lens = i32(sv.lens())
         table = tables_of(sv.m, sv.names, sv.width)
-        pa.pa_decode_weights(q, sv.kc, sv.vc, table, lens, sv.scale, out, sv.w, 1000, error_word=sv.err)
+        pkg.pa_decode_weights(q, sv.kc, sv.vc, table, lens, sv.scale, out, sv.w, 1000, error_word=sv.err)
         sv.check(out.double().cpu().numpy()[:, None], hq[:, None])
         for s in range(B):
             _, w, _, tol = ref.attention(hq[s][None], sv.k[s], sv.v[s], sv.scale, sv.group)
@@ -142,7 +143,7 @@ def test_a_cache_kept_to_a_budget(shared):
         pool_w = sv.w.cpu().numpy()
         old = [sv.m.block_table(x) for x in sv.names]
         sv.m.evict(dict(zip(sv.names, keep)))
-        pa.pa_evict(sv.kc, sv.vc, sv.w, table, lens, i32(keep), tables_of(sv.m, sv.names, sv.width), lens, 1000, sinks, recent, error_word=sv.err)
+        pkg.pa_evict(sv.kc, sv.vc, sv.w, table, lens, i32(keep), tables_of(sv.m, sv.names, sv.width), lens, 1000, sinks, recent, error_word=sv.err)
         assert lens.tolist() == keep
         for s in range(B):
             n = len(sv.k[s])
@@ -176,12 +177,12 @@ def test_rows_past_32_bits():
     run.table = run.table + high
     run.check(run.sinks(100, 4), 100, 4)
     o = run.out()
-    pa.pa_decode_weights(run.dq, kc, vc, run.table, run.n, run.scale, o, w, run.bound, error_word=run.err)
+    pkg.pa_decode_weights(run.dq, kc, vc, run.table, run.n, run.scale, o, w, run.bound, error_word=run.err)
     run.check(o.double().cpu().numpy())
     got = w[high:].cpu().numpy()
     before = kc[high:].cpu()
     lens = run.n.clone()
-    pa.pa_evict(kc, vc, w, run.table, run.n, i32([200, 10, 500]), run.table, lens, run.bound, 1, 4, error_word=run.err)
+    pkg.pa_evict(kc, vc, w, run.table, run.n, i32([200, 10, 500]), run.table, lens, run.bound, 1, 4, error_word=run.err)
     assert lens.tolist() == [200, 10, 500] and int(run.err.item()) == 0
     after = kc[high:].cpu()
     for s, k in enumerate(lens.tolist()):
@@ -203,18 +204,18 @@ def test_scratch_of_calls_on_another_stream_is_theirs(handle):
     want_out, want_w = run.weights(start)
     w, o = torch.from_numpy(start).cuda(), run.out()
     keep, lens = i32([2500, 20, 2999, 100] * 8), torch.zeros_like(run.n)
-    need = pa.pa_decode_workspace_size_weights(32, 1, 8, 128, run.bound)
+    need = pkg.pa_decode_workspace_size_weights(32, 1, 8, 128, run.bound)
     torch.cuda.synchronize()
     on = side.cuda_stream if handle else side
-    pa.pa_decode_weights(run.dq, run.dk, run.dv, run.table, run.n, run.scale, o, w, run.bound, error_word=run.err, stream=on)
+    pkg.pa_decode_weights(run.dq, run.dk, run.dv, run.table, run.n, run.scale, o, w, run.bound, error_word=run.err, stream=on)
     for _ in range(3):
         torch.full((need,), 255, dtype=torch.uint8, device="cuda")
     k_before = run.dk.clone()
     side.synchronize()
     assert np.array_equal(o.double().cpu().numpy(), want_out) and np.array_equal(w.cpu().numpy(), want_w)
-    pa.pa_evict(run.dk, run.dv, w, run.table, run.n, keep, run.table, lens, run.bound, error_word=run.err, stream=on)
+    pkg.pa_evict(run.dk, run.dv, w, run.table, run.n, keep, run.table, lens, run.bound, error_word=run.err, stream=on)
     for _ in range(3):
-        torch.full((pa.pa_evict_workspace_size(32, 2, run.bound),), 255, dtype=torch.uint8, device="cuda")
+        torch.full((pkg.pa_evict_workspace_size(32, 2, run.bound),), 255, dtype=torch.uint8, device="cuda")
     side.synchronize()
     assert lens.tolist() == [2500, 20, 2999, 100] * 8 and int(run.err.item()) == 0
     for s in (0, 1, 2, 3, 31):
@@ -236,12 +237,12 @@ def test_two_streams_at_once_with_workspaces_of_their_own():
     torch.cuda.synchronize()
     for r, s, st in ((a, sa, streams[0]), (b, sb, streams[1])):
         w, o = torch.from_numpy(s).cuda(), r.out()
-        ws = torch.empty(pa.pa_decode_workspace_size_weights(40, 1, 8, 128, r.bound), dtype=torch.uint8, device="cuda")
+        ws = torch.empty(pkg.pa_decode_workspace_size_weights(40, 1, 8, 128, r.bound), dtype=torch.uint8, device="cuda")
         got.append((r, o, w, ws, st))
     torch.cuda.synchronize()
     for _ in range(3):
         for r, o, w, ws, st in got:
-            pa.pa_decode_weights(r.dq, r.dk, r.dv, r.table, r.n, r.scale, o, w, r.bound, workspace=ws, stream=st)
+            pkg.pa_decode_weights(r.dq, r.dk, r.dv, r.table, r.n, r.scale, o, w, r.bound, workspace=ws, stream=st)
     torch.cuda.synchronize()
     for (r, o, w, _, _), (wo, ww), s in zip(got, want, (sa, sb)):
         assert np.array_equal(o.double().cpu().numpy(), wo)
@@ -260,10 +261,10 @@ def test_refusals_of_the_binding():
     args = dict(q=run.dq, k_cache=run.dk, v_cache=run.dv, block_tables=run.table, context_lens=run.n, scale=0.1, out=o, max_context_len=40)
 
     def sinks(**kw):
-        pa.pa_decode_sinks(**{**args, "window": 8, "num_sinks": 2, **kw})
+        pkg.pa_decode_sinks(**{**args, "window": 8, "num_sinks": 2, **kw})
 
     def weights(**kw):
-        pa.pa_decode_weights(**{**args, "row_weights": w, **kw})
+        pkg.pa_decode_weights(**{**args, "row_weights": w, **kw})
 
     for call in (sinks, weights):
         for kw, err in ((dict(q=run.dq.float()), TypeError), (dict(q=run.dq.cpu()), ValueError), (dict(q=run.dq[0, 0]), ValueError),
@@ -291,7 +292,7 @@ def test_refusals_of_the_binding():
                     (dict(k_cache=e.k.view(torch.int8), v_cache=e.v.view(torch.int8)), ValueError),
                     (dict(k_cache=e.k.view(torch.uint8), v_cache=e.v.view(torch.uint8), k_params=scales, v_params=scales), TypeError)):
         with pytest.raises(err):
-            pa.pa_evict(**{**good, **kw})
+            pkg.pa_evict(**{**good, **kw})
     assert np.array_equal(raw(e.k), before)
     p, q = torch.rand(2, 4, 50, device="cuda"), torch.rand(2, 3, 50, device="cuda")
     x, u = torch.zeros(2, 3, dtype=torch.int32, device="cuda"), torch.rand(2, 4, device="cuda")
@@ -301,7 +302,7 @@ def test_refusals_of_the_binding():
                     (dict(uniforms=u[:, :3].contiguous()), ValueError), (dict(num_accepted=acc[:1]), ValueError), (dict(context_lens=acc), pa.PagedAttentionError),
                     (dict(num_drafts=acc.long()), TypeError)):
         with pytest.raises(err):
-            pa.pa_verify_draft(**{**dict(target_probs=p, draft_probs=q, draft_tokens=x, uniforms=u, out_tokens=out, num_accepted=acc), **kw})
+            pkg.pa_verify_draft(**{**dict(target_probs=p, draft_probs=q, draft_tokens=x, uniforms=u, out_tokens=out, num_accepted=acc), **kw})
 
 
 @pytest.mark.parametrize("shape", [("bf16", 4, 1, 128, 16), ("bf16", 4, 3, 64, 16), ("f32", 5, 1, 64, 16)], ids=str)
@@ -338,7 +339,7 @@ def test_a_length_bound_of_zero(shape):
     out, got = run.weights(start)
     assert not out.any() and np.array_equal(got, start)
     lens = torch.full_like(run.n, 9)
-    pa.pa_evict(run.dk, run.dv, torch.from_numpy(start).cuda(), run.table, run.n, run.n, run.table, lens, 0, 3, 4, error_word=run.err) \
+    pkg.pa_evict(run.dk, run.dv, torch.from_numpy(start).cuda(), run.table, run.n, run.n, run.table, lens, 0, 3, 4, error_word=run.err) \
         if shape[0] == "bf16" else lens.zero_()
     assert lens.tolist() == [0, 0, 0] and int(run.err.item()) == 0
 
@@ -364,7 +365,7 @@ def test_probabilities_laid_out_token_by_token():
     x = np.argmax(q, -1).T.astype(np.int32).copy()
     u = r.random((B, Q + 1), dtype=np.float32)
     out, acc = torch.zeros(B, Q + 1, dtype=torch.int32, device="cuda"), torch.zeros(B, dtype=torch.int32, device="cuda")
-    pa.pa_verify_draft(torch.from_numpy(p).cuda().transpose(0, 1), torch.from_numpy(q).cuda().transpose(0, 1), torch.from_numpy(x).cuda(),
+    pkg.pa_verify_draft(torch.from_numpy(p).cuda().transpose(0, 1), torch.from_numpy(q).cuda().transpose(0, 1), torch.from_numpy(x).cuda(),
                        torch.from_numpy(u).cuda(), out, acc)
     for s in range(B):
         a, token, _ = ref.verify(p[:, s], q[:, s], x[s], u[s].astype(np.float64), Q)

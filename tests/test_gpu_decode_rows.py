@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import cache_rows_reference as ref
+import paged_kv_cache_29_gb300 as pkg
 from paged_kv_cache_29_gb300 import _binding as pa
 
 pytestmark = pytest.mark.gpu
@@ -40,12 +41,12 @@ class Run:
 
     def sinks(self, window, sinks, **kw):
         o = self.out()
-        pa.pa_decode_sinks(self.dq, self.dk, self.dv, self.table, self.n, self.scale, window, sinks, o, self.bound, error_word=self.err, **kw)
+        pkg.pa_decode_sinks(self.dq, self.dk, self.dv, self.table, self.n, self.scale, window, sinks, o, self.bound, error_word=self.err, **kw)
         return o.double().cpu().numpy()
 
     def weights(self, start, **kw):
         o, w = self.out(), torch.from_numpy(start).cuda()
-        pa.pa_decode_weights(self.dq, self.dk, self.dv, self.table, self.n, self.scale, o, w, self.bound, error_word=self.err, **kw)
+        pkg.pa_decode_weights(self.dq, self.dk, self.dv, self.table, self.n, self.scale, o, w, self.bound, error_word=self.err, **kw)
         return o.double().cpu().numpy(), w.cpu().numpy()
 
     def check(self, got, window=0, sinks=0, only=None):
@@ -225,15 +226,15 @@ def test_captured_and_replayed(shape):
     """Both calls in one graph over one workspace, replayed with other queries."""
     run = Run(shape, [900, 64, 0, 513], seed=14)
     hq = run.group * run.hkv
-    need = max(pa.pa_decode_workspace_size_weights(4, run.Q, hq, run.D, run.bound), pa.pa_decode_workspace_size_multi(4, run.Q, hq, run.D, run.bound))
+    need = max(pkg.pa_decode_workspace_size_weights(4, run.Q, hq, run.D, run.bound), pa.pa_decode_workspace_size_multi(4, run.Q, hq, run.D, run.bound))
     ws = torch.empty(need, dtype=torch.uint8, device="cuda")
     start = start_weights(run.cache)
     o1, o2, w = run.out(), run.out(), torch.from_numpy(start).cuda()
     args = (run.dq, run.dk, run.dv, run.table, run.n, run.scale)
 
     def both():
-        pa.pa_decode_sinks(*args, 100, 4, o1, run.bound, workspace=ws, error_word=run.err)
-        pa.pa_decode_weights(*args, o2, w, run.bound, workspace=ws, error_word=run.err)
+        pkg.pa_decode_sinks(*args, 100, 4, o1, run.bound, workspace=ws, error_word=run.err)
+        pkg.pa_decode_weights(*args, o2, w, run.bound, workspace=ws, error_word=run.err)
 
     side = torch.cuda.Stream()
     with torch.cuda.stream(side):
@@ -259,7 +260,7 @@ def test_on_another_stream_with_scratch_of_its_own():
     side.wait_stream(torch.cuda.current_stream())
     o = run.out()
     torch.cuda.synchronize()
-    pa.pa_decode_sinks(run.dq, run.dk, run.dv, run.table, run.n, run.scale, 77, 3, o, run.bound, stream=side)
+    pkg.pa_decode_sinks(run.dq, run.dk, run.dv, run.table, run.n, run.scale, 77, 3, o, run.bound, stream=side)
     side.synchronize()
     run.check(o.double().cpu().numpy(), 77, 3)
 

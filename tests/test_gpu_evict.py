@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import cache_rows_reference as ref
+import paged_kv_cache_29_gb300 as pkg
 from paged_kv_cache_29_gb300 import _binding as pa
 
 pytestmark = pytest.mark.gpu
@@ -69,7 +70,7 @@ class Evict:
         to = table if same_table else torch.from_numpy(self.to).cuda()
         n, keep = (torch.tensor(x, dtype=torch.int32).cuda() for x in (self.lens, self.keep))
         out = n if in_place_lens else torch.full_like(n, -7)
-        pa.pa_evict(self.k, self.v, w, table, n, keep, to, out, self.bound, self.sinks, self.recent, self.kp, self.vp,
+        pkg.pa_evict(self.k, self.v, w, table, n, keep, to, out, self.bound, self.sinks, self.recent, self.kp, self.vp,
                     error_word=self.err, **kw)
         after = [raw(t) for t in rows] + [w.cpu().numpy().view(np.uint8).reshape(*self.w.shape, 4)]
         before.append(self.w.view(np.uint8).reshape(*self.w.shape, 4))
@@ -183,11 +184,11 @@ def test_captured_and_replayed_in_place():
     table = torch.from_numpy(e.table).cuda()
     n, keep = (torch.tensor(x, dtype=torch.int32).cuda() for x in (e.lens, e.keep))
     out = torch.zeros_like(n)
-    ws = torch.empty(pa.pa_evict_workspace_size(2, 2, 300), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(pkg.pa_evict_workspace_size(2, 2, 300), dtype=torch.uint8, device="cuda")
     keep_k = e.k.clone()
 
     def call():
-        pa.pa_evict(e.k, e.v, w, table, n, keep, table, out, 300, 2, 8, workspace=ws)
+        pkg.pa_evict(e.k, e.v, w, table, n, keep, table, out, 300, 2, 8, workspace=ws)
 
     call()
     torch.cuda.synchronize()

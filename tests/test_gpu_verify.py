@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import cache_rows_reference as ref
+import paged_kv_cache_29_gb300 as pkg
 from paged_kv_cache_29_gb300 import _binding as pa
 
 pytestmark = pytest.mark.gpu
@@ -42,7 +43,7 @@ class Verify:
         accepted = torch.full((B,), -9, dtype=torch.int32, device="cuda")
         lens = torch.from_numpy(self.lens).cuda()
         lens_out = lens if in_place else torch.full_like(lens, -9)
-        pa.pa_verify_draft(probs(self.target), probs(self.draft), torch.from_numpy(self.tokens).cuda(), torch.from_numpy(self.uniforms).cuda(), out,
+        pkg.pa_verify_draft(probs(self.target), probs(self.draft), torch.from_numpy(self.tokens).cuda(), torch.from_numpy(self.uniforms).cuda(), out,
                            accepted, num_drafts=None if self.count is None else torch.from_numpy(self.count).cuda(), context_lens=lens,
                            lens_out=lens_out, error_word=self.err, **kw)
         return out.cpu().numpy(), accepted.cpu().numpy(), lens_out.cpu().numpy()
@@ -137,11 +138,11 @@ def test_without_lengths_captured_and_replayed():
     v = Verify(5, 4, 3000, seed=6)
     t, d, x, u = (torch.from_numpy(a).cuda() for a in (v.target, v.draft, v.tokens, v.uniforms))
     out, acc = torch.zeros(5, 5, dtype=torch.int32, device="cuda"), torch.zeros(5, dtype=torch.int32, device="cuda")
-    pa.pa_verify_draft(t, d, x, u, out, acc)
+    pkg.pa_verify_draft(t, d, x, u, out, acc)
     torch.cuda.synchronize()
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
-        pa.pa_verify_draft(t, d, x, u, out, acc)
+        pkg.pa_verify_draft(t, d, x, u, out, acc)
     w = Verify(5, 4, 3000, seed=7)
     for a, b in ((t, w.target), (d, w.draft), (x, w.tokens), (u, w.uniforms)):
         a.copy_(torch.from_numpy(b))
@@ -161,7 +162,7 @@ def test_drawn_tokens_are_distributed_as_the_targets():
     u = torch.from_numpy(r.random((B, 2), dtype=np.float32)).cuda()
     out, acc = torch.zeros(B, 2, dtype=torch.int32, device="cuda"), torch.zeros(B, dtype=torch.int32, device="cuda")
     target = torch.from_numpy(p).cuda().expand(B, 2, V)
-    pa.pa_verify_draft(target, torch.from_numpy(q).cuda().expand(B, 1, V), tokens, u, out, acc)
+    pkg.pa_verify_draft(target, torch.from_numpy(q).cuda().expand(B, 1, V), tokens, u, out, acc)
     counts = np.bincount(out[:, 0].cpu().numpy(), minlength=V)
     assert (np.abs(counts - B * p) <= 5 * np.sqrt(B * p * (1 - p))).all(), counts
 
@@ -174,7 +175,7 @@ def test_the_largest_vocabulary(B):
     p = softmax(2 * r.standard_normal(V))
     u = r.random((B, 1), dtype=np.float32)
     out, acc = torch.zeros(B, 1, dtype=torch.int32, device="cuda"), torch.ones(B, dtype=torch.int32, device="cuda")
-    pa.pa_verify_draft(torch.from_numpy(p).cuda().expand(B, 1, V), None, torch.zeros(B, 0, dtype=torch.int32, device="cuda"), torch.from_numpy(u).cuda(),
+    pkg.pa_verify_draft(torch.from_numpy(p).cuda().expand(B, 1, V), None, torch.zeros(B, 0, dtype=torch.int32, device="cuda"), torch.from_numpy(u).cuda(),
                        out, acc)
     run = np.cumsum(p.astype(np.float64))
     want = np.searchsorted(run, u[:, 0].astype(np.float64) * run[-1], side="right")
