@@ -34,7 +34,7 @@ def _rows_args(q, k_cache, v_cache, block_tables, context_lens, out, dev):
     else:
         raise ValueError(f"q must have 3 or 4 dimensions, got {len(shape)}")
     rows, mb = block_tables.shape
-    if dq != d or out.shape != shape or v_cache.shape != pool or rows != B or context_lens.shape[0] != B:
+    if dq != d or out.shape != shape or v_cache.shape != pool or rows != B or context_lens.numel() != B:
         raise ValueError("shape mismatch between q/out/block_tables/context_lens and the caches")
     return (qp, kc, vc, bt, cl), op, (B, Q, hq, hkv, d, bs, nb, mb), _b._plain_dtype_code(k_cache)
 
@@ -131,7 +131,7 @@ def pa_evict(k_cache, v_cache, row_weights, block_tables, context_lens, keep_len
     lo = _b._arg("lens_out", lens_out, dev, torch.int32, 1)
     B, mb = block_tables.shape
     if v_cache.shape != pool or row_weights.shape != pool[:3] or out_tables.shape != block_tables.shape \
-            or context_lens.shape[0] != B or keep_lens.shape[0] != B or lens_out.shape[0] != B:
+            or context_lens.numel() != B or keep_lens.numel() != B or lens_out.numel() != B:
         raise ValueError("shape mismatch between the caches, row_weights, the tables and the lengths")
     bound = _b._int32("max_context_len", max_context_len)
     if workspace is None:
@@ -150,6 +150,13 @@ def _probs_arg(name, t, dev):
     """Pointer and (sequence, row) strides of fp32 probabilities [B][rows][V] whose
     rows are contiguous and may lie any distance apart."""
     import torch
+    try:
+        if t.get_device() == dev and t.dtype is torch.float32:
+            seq, row, one = t.stride()
+            if one == 1:
+                return t.data_ptr(), seq, row
+    except (AttributeError, ValueError):
+        pass
     if t is None:
         raise ValueError(f"{name} is required")
     if not t.is_cuda:
@@ -158,8 +165,7 @@ def _probs_arg(name, t, dev):
         raise TypeError(f"{name} must be {torch.float32}, got {t.dtype}")
     if t.dim() != 3:
         raise ValueError(f"{name} must have 3 dimensions, got {t.dim()}")
-    if t.get_device() != dev:
-        _b._check_device(None, t)
+    _b._check_device(None, t)
     seq, row, one = t.stride()
     if one != 1 and t.shape[2] > 1:
         raise ValueError(f"{name}: the values of a row must be contiguous")
@@ -191,8 +197,8 @@ def pa_verify_draft(target_probs, draft_probs, draft_tokens, uniforms, out_token
     cl = _b._opt_arg("context_lens", context_lens, dev, torch.int32, 1)
     lo = _b._opt_arg("lens_out", lens_out, dev, torch.int32, 1)
     if Q < 0 or draft_tokens.shape != (B, Q) or uniforms.shape != (B, rows) or out_tokens.shape != (B, rows) \
-            or (draft_probs is not None and draft_probs.shape != (B, Q, V)) or num_accepted.shape[0] != B \
-            or any(t is not None and t.shape[0] != B for t in (num_drafts, context_lens, lens_out)):
+            or (draft_probs is not None and draft_probs.shape != (B, Q, V)) or num_accepted.numel() != B \
+            or any(t is not None and t.numel() != B for t in (num_drafts, context_lens, lens_out)):
         raise ValueError("shape mismatch between the probabilities, the drafted tokens and the outputs")
     rc = _b.lib().pa_verify_draft(tp, t_seq, t_row, dp, d_seq, d_row, dt, nd, un, ot, na, cl, lo, B, Q,
                                   V, _b._opt_arg("error_word", error_word, dev, torch.int32),

@@ -19,6 +19,10 @@
 // of later stretches may come before them too. Bytes of a row at different offsets
 // never meet: CTAs move slices of the rows under one KV head through the whole list, with
 // no barrier between them.
+//
+// 128 sequences of 1,640 rows to half, in place, 8 KV heads of 128, bf16: selection 28 us, bound by
+// latencies (six trips to memory and some 20 barriers a CTA, in 1.7 rounds of CTAs); moves 143 us for 854 MB,
+// 6.0 TB/s, bound by memory.
 #include <climits>
 
 #include <cooperative_groups.h>
@@ -490,7 +494,7 @@ cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream) {
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     // Programmatic dependents where the keys take little shared memory. Where they take
     // much, moving CTAs beside selecting ones have little of the SM's memory left for loads
-    // on their way: 128 sequences of 1,640 rows then take 350 us, and 226 without.
+    // on their way: those of 128 sequences of 1,640 rows then take 325 us, and 143 without.
     const bool early = share <= 2048;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;

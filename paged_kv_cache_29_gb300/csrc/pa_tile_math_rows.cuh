@@ -26,7 +26,7 @@ __device__ __forceinline__ uint32_t rows_seen(int row0, int last, int window, in
 // floats, maxima then sums of G columns, in `buf`), the scores its own. For calls
 // whose sequences all have one partition: a sequence of 17 rows takes 8.5 us, 10.5 with
 // row_weights_kernel behind the decode kernel. In an instance for longer sequences
-// it costs registers that their tiles need (32 sequences of 4096 rows: 182 us instead of 171).
+// it costs registers that their tiles need (128 sequences of 1,640 rows: 182 us instead of 171).
 template <int W, int STATE, int G>
 __device__ __forceinline__ void item_row_weights(const DecodeParams& p, const float* buf, int s, int h, int n, int cols) {
     float M[G], R[G];

