@@ -218,8 +218,8 @@ size_t pa_decode_workspace_size_weights(int num_seqs, int num_queries, int num_h
 size_t pa_evict_workspace_size(int num_seqs, int num_kv_heads, int max_context_len) {
     if (num_seqs <= 0 || num_kv_heads <= 0 || max_context_len < 0) return 0;
     const size_t heads = static_cast<size_t>(num_seqs) * num_kv_heads;
-    // the moves, then where they start per sequence and KV head and a length per sequence
-    return heads * max_context_len * sizeof(uint2) + 4 * (heads + num_seqs);
+    // the moves, then where they start per sequence and KV head, a length and a place per sequence
+    return heads * max_context_len * sizeof(uint2) + 4 * (heads + 2 * static_cast<size_t>(num_seqs));
 }
 
 pa_status pa_evict(void* k_cache, void* v_cache, void* k_params, void* v_params, float* row_weights,
@@ -270,6 +270,7 @@ pa_status pa_evict(void* k_cache, void* v_cache, void* k_params, void* v_params,
     p.moves = static_cast<uint2*>(workspace);
     p.starts = reinterpret_cast<int32_t*>(p.moves + heads * max_context_len);
     p.new_lens = p.starts + heads;
+    p.order = p.new_lens + num_seqs;
     p.error_word = error_word;
     p.num_sinks = num_sinks;
     p.num_recent = num_recent;

@@ -46,6 +46,7 @@ constexpr uint32_t kStays = 0xffffffffu;      // key of a row that stays in any 
 // weights again in every pass.
 constexpr int kMaxKeys = 48 * 1024;
 constexpr int kShortKeys = 8 * 1024;
+constexpr int kMaxOrdered = 256;              // sequences that are taken in the order of their lengths
 
 // 32 bits in the order of the weights: NaN as -infinity, -0 as +0.
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -84,13 +85,60 @@ __global__ void __launch_bounds__(kSelectThreads, kSelectThreads == 256 ? 4 : 2)
     };
     grid_dependency_wait();
     grid_launch_dependents();
-    const int sh = blockIdx.x / ranks;
-    const int s = sh / p.num_kv_heads;
-    const int h = sh - s * p.num_kv_heads;
+    const int sh = blockIdx.x / ranks;        // (what the list and the lengths are kept by)
+    const int unit = sh / p.num_kv_heads;
+    const int h = sh - unit * p.num_kv_heads;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int bs = p.block_size;
-    const int n = __ldg(p.context_lens + s);
-    int keep = __ldg(p.keep_lens + s);
+    int s = unit, n, keep;
+    if (p.order != nullptr) {
+        // The unit-th sequence when the longest come first, by eight classes of lengths, each half
+        // the one before it; a warp counts 32 sequences' classes, all warps add up the counts.
+        __shared__ uint2 counts[32];          // [class][warp]
+        __shared__ int own[3];
+        int cls = 8;
+        n = keep = 0;
+        if (tid < p.num_seqs) {
+            n = __ldg(p.context_lens + tid);
+            keep = __ldg(p.keep_lens + tid);
+            cls = n <= 0 ? 7 : min(7, max(0, __clz(n) - __clz(p.context_cap)));
+        }
+        uint32_t peers = 0, count = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const uint32_t in = __ballot_sync(0xffffffffu, cls == k);
+            if (cls == k) peers = in;
+            if (lane == k) count = __popc(in);
+        }
+        if (warp < 8 && lane < 8) reinterpret_cast<uint32_t*>(counts)[lane * 8 + warp] = count;
+        __syncthreads();
+        if (warp < 8) {
+            const uint2 c = counts[lane];
+            uint32_t before = c.x + c.y;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const uint32_t u = __shfl_up_sync(0xffffffffu, before, off);
+                if (lane >= off) before += u;
+            }
+            const int at = (cls * 8 + warp) & 63;
+            const uint32_t upto = __shfl_sync(0xffffffffu, before - c.x - c.y, at / 2);
+            const uint32_t even = __shfl_sync(0xffffffffu, c.x, at / 2);
+            const uint32_t place = upto + (at & 1 ? even : 0u) + __popc(peers & ((1u << lane) - 1u));
+            if (cls < 8 && place == static_cast<uint32_t>(unit)) {
+                own[0] = tid;
+                own[1] = n;
+                own[2] = keep;
+            }
+        }
+        __syncthreads();
+        s = own[0];
+        n = own[1];
+        keep = own[2];
+        if (tid == 0 && rank == 0 && h == 0) p.order[unit] = s;
+    } else {
+        n = __ldg(p.context_lens + s);
+        keep = __ldg(p.keep_lens + s);
+    }
     const bool odd = n < 0 || n > p.context_cap || keep < 0;
     keep = min(keep, n);
     const int first = odd ? 0 : min(n, p.num_sinks);             // rows [first, last) may leave
@@ -100,7 +148,7 @@ __global__ void __launch_bounds__(kSelectThreads, kSelectThreads == 256 ? 4 : 2)
         if (tid == 0 && rank == 0) {
             if (h == 0) {
                 raise_error(p.error_word, PA_DEVERR_CONTEXT);
-                p.new_lens[s] = n;
+                p.new_lens[unit] = n;
             }
             p.starts[sh] = INT_MAX;
         }
@@ -189,7 +237,7 @@ __global__ void __launch_bounds__(kSelectThreads, kSelectThreads == 256 ? 4 : 2)
         if (tid == 0 && rank == 0) {
             if (h == 0) {
                 raise_error(p.error_word, PA_DEVERR_BLOCK_ID);
-                p.new_lens[s] = n;
+                p.new_lens[unit] = n;
             }
             p.starts[sh] = INT_MAX;
         }
@@ -360,7 +408,7 @@ __global__ void __launch_bounds__(kSelectThreads, kSelectThreads == 256 ? 4 : 2)
         int start = INT_MAX;
         for (int r = 0; r < ranks; ++r) start = min(start, *cluster.map_shared_rank(&first_move, r));
         p.starts[sh] = all_flags & kSame ? start : kApart;
-        if (h == 0) p.new_lens[s] = keep;
+        if (h == 0) p.new_lens[unit] = keep;
     }
     meet();                           // no CTA ends before rank 0 has read it
 }
@@ -419,11 +467,12 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? 3 : 4) evict_move_ker
     grid_launch_dependents();
     const int sh = blockIdx.x / ctas;
     const int part = blockIdx.x - sh * ctas;
-    const int s = sh / p.num_kv_heads;
-    int count = p.new_lens[s];
+    const int unit = sh / p.num_kv_heads;
+    int count = p.new_lens[unit];
     int start = p.starts[sh];
     // Nothing reads the lengths any more: lens_out may be the array they are in.
-    if (part == 0 && sh == s * p.num_kv_heads && threadIdx.x == 0) p.lens_out[s] = count;
+    if (part == 0 && sh == unit * p.num_kv_heads && threadIdx.x == 0)
+        p.lens_out[p.order != nullptr ? p.order[unit] : unit] = count;
     const int pieces = 2 * (p.row_bytes / 16);
     int slice = part, step = ctas - 1;
     bool values = part == ctas - 1;
@@ -461,7 +510,7 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? 3 : 4) evict_move_ker
 
 }  // namespace
 
-cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream) {
+cudaError_t launch_evict(EvictParams p, cudaStream_t stream) {
     const int heads = p.num_seqs * p.num_kv_heads;
     if (heads == 0) return cudaSuccess;
     const int sms = device_sms();
@@ -471,6 +520,10 @@ cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream) {
     const int share = ((p.context_cap + ranks - 1) / ranks + 31) / 32 * 32;
     // Many CTAs hold few keys each, so that several fit an SM: 1,024 of them with a bound of
     // 32,768 rows and lengths of 1,640 take 189 us so, 202 with room for the bound.
+    // Longest sequences first, where CTAs wait for room and lengths may differ much (128 sequences of
+    // 1,640 rows take 171 us so, 177 as they come, 256 of them 340 and 365; but 256 of 300
+    // rows and a bound of 600 124 and 121).
+    if (p.num_seqs > kMaxOrdered || static_cast<long long>(heads) * ranks <= 4LL * sms || share <= 2048) p.order = nullptr;
     const int most_keys = static_cast<long long>(heads) * ranks <= 4LL * sms ? kMaxKeys : kShortKeys;
     const bool all_held = share <= most_keys;
     const int max_keys = all_held ? share : kShortKeys;

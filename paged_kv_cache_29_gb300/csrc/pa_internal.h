@@ -200,13 +200,14 @@ struct EvictParams {
     uint2* moves;                  // [B][Hkv][context_cap]
     int32_t* starts;               // [B][Hkv]
     int32_t* new_lens;             // [B]
+    int32_t* order;                // [B]: the sequences as moves, starts and new_lens have them (null: in order)
     int32_t* error_word;
     int num_sinks, num_recent;
     int num_seqs, num_kv_heads, row_bytes;
     int block_size, num_blocks, max_blocks_per_seq, context_cap;
     Divisor by_block;              // block_size
 };
-cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream);
+cudaError_t launch_evict(EvictParams p, cudaStream_t stream);
 
 // Verification of drafted tokens (pa_verify_draft in the header).
 struct VerifyParams {

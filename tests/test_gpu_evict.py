@@ -230,3 +230,23 @@ def test_a_bound_beyond_what_clusters_hold(weights):
     e.to = np.pad(e.to, ((0, 0), (0, 70_000 - e.to.shape[1])), constant_values=-1)
     e.bound = 1_000_000
     e.check()
+
+
+@pytest.mark.parametrize("place", ["same", "other", "some same"])
+@pytest.mark.parametrize("num_seqs,hkv", [(96, 8), (255, 3), (256, 3), (257, 3)])
+def test_batches_beyond_the_sms(num_seqs, hkv, place):
+    """More sequences and KV heads than CTAs at a time: taken in the order of their lengths,
+    up to 256 sequences; equal, empty and flagged ones among them."""
+    r = np.random.default_rng(num_seqs)
+    lens = [int(n) for n in r.choice([0, 1, 16, 33, 40, 40, 40, 100, 257], num_seqs)]
+    lens[7], lens[30], lens[50] = 2100, 70, 333
+    keep = [min(n, max(6, int(n * r.random()))) for n in lens]
+    e = Evict(lens, keep, 2, 4, hkv=hkv, D=16, place=place, seed=num_seqs)
+    e.check(in_place_lens=True)
+    e = Evict(lens, keep, 2, 4, "int8", hkv=hkv, D=16, place=place, seed=num_seqs + 1)
+    e.keep[30] = -1                                    # no length
+    e.table[50, 20] = e.k.shape[0]                     # outside the pool
+    e.check(flagged=(30, 50))
+    assert int(e.err.item()) == pa.PA_DEVERR_CONTEXT | pa.PA_DEVERR_BLOCK_ID
+    e.lens[7], e.lens[30] = -5, 2101                   # none, and above the bound
+    e.check(flagged=(7, 30, 50))
