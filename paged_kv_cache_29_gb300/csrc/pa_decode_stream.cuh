@@ -604,6 +604,16 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 const int cur_bad = __any_sync(0xffffffffu, bad_lane) ? 1 : 0;
                 const int ntiles = (hi - lo + kTileRows - 1) / kTileRows;
                 if (cur_bad && lane == 0) raise_error(p.error_word, PA_DEVERR_BLOCK_ID);
+                if constexpr (Math::kRows) {
+                    // The tiles' first pool rows in place of their ids, a lane a tile: found
+                    // between two copies they take the producer's time.
+                    const int head = item_head(cur);
+                    for (int i = lane; i < nblk; i += 32) {
+                        const int v = lo + kTileRows * i;
+                        ids[i] = cur_bad ? 0 : (ids[i] * p.num_kv_heads + head) * bs + (v + gap_from(cur.w, v)) % bs;
+                    }
+                    __syncwarp();
+                }
                 // Fused append: the item holding the sequence's last row writes
                 // this KV head's new K and V rows into their slot before the
                 // tile that holds them is loaded (the slot must be that row's).
@@ -683,8 +693,11 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     // (all 128-byte column halves of 16 rows), issued after lane
                     // 0's expect_tx (ordered by the shuffle above).
                     if (data && lane < 2) {
-                        const int id = ids[Math::kRows ? tt : tok / bs - b0];
-                        const int row = (id * p.num_kv_heads + item_head(cur)) * bs + (tok + gap_from(cur.w, tok)) % bs;
+                        int row;
+                        if constexpr (Math::kRows)
+                            row = ids[tt];
+                        else
+                            row = (ids[tok / bs - b0] * p.num_kv_heads + cur.y) * bs + (tok % bs);
                         const uint32_t dst = ring_addr + stage * Geom::kStageBytes +
                                              (lane ? Geom::kTileBytes : 0);
                         tma_load_3d(dst, lane ? static_cast<const void*>(&tmap_v)
