@@ -12,6 +12,13 @@ constexpr int kWarps = 4;            // consumer warps, ring stages and CTAs per
 constexpr int kStages = 4;           // decode kernels have them (pa_decode_mma.cu, pa_decode_simt.cu)
 constexpr int kMinCtasPerSm = 4;
 
+// Ring stages over fp32. Where registers or 64 dims leave room for them more than a tile a warp is on its way
+// (8 KV heads, 210,000 rows of 64 dims: 1, 2, 4 and 8 heads each 154, 165, 302, 483 us with 12
+// stages, 186, 224, 447, 623 with four; 105,000 rows of 128 dims, 4 and 8 heads 282 and 556 with
+// eight, 365 and 624 with four, but 1 and 2 heads 156 and 192 instead of 149 and 175).
+template <int D, int G>
+constexpr int kSimtStages = (D == 64 ? 3 : G >= 4 ? 2 : 1) * kWarps;
+
 template <int D, int G, bool SCORES, bool ENDS>
 cudaError_t run_mma(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeParams& p, int sm_count,
                     cudaStream_t stream) {
@@ -22,8 +29,8 @@ cudaError_t run_mma(const CUtensorMap& tk, const CUtensorMap& tv, const DecodePa
 template <int D, int G, bool SCORES, bool ENDS>
 cudaError_t run_simt(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeParams& p, int sm_count,
                      cudaStream_t stream) {
-    return launch_stream_instance<RowsSimtMath<D, G, SCORES, ENDS>, D, G, kWarps, kWarps, 1, false>(tk, tv, p, sm_count,
-                                                                                              stream);
+    return launch_stream_instance<RowsSimtMath<D, G, SCORES, ENDS>, D, G, kWarps, kSimtStages<D, G>, 1, false>(
+        tk, tv, p, sm_count, stream);
 }
 
 template <int D, bool SCORES, bool ENDS>
