@@ -8,9 +8,13 @@
 namespace pa {
 
 namespace {
-constexpr int kWarps = 4;            // consumer warps, ring stages and CTAs per SM as the plain
-constexpr int kStages = 4;           // decode kernels have them (pa_decode_mma.cu, pa_decode_simt.cu)
-constexpr int kMinCtasPerSm = 4;
+constexpr int kWarps = 4;            // consumer warps and CTAs per SM as the plain decode
+constexpr int kMinCtasPerSm = 4;     // kernels have them (pa_decode_mma.cu, pa_decode_simt.cu)
+
+// Ring stages over bf16: 32 KB of tiles on their way to each CTA (8 KV heads, 210,000 rows of 64
+// dims: 1, 4 and 8 heads each 95, 101, 110 us with eight stages, 108, 115, 124 with four).
+template <int D>
+constexpr int kMmaStages = (D == 64 ? 2 : 1) * kWarps;
 
 // Ring stages over fp32. Where registers or 64 dims leave room for them more than a tile a warp is on its way
 // (8 KV heads, 210,000 rows of 64 dims: 1, 2, 4 and 8 heads each 154, 165, 302, 483 us with 12
@@ -22,7 +26,7 @@ constexpr int kSimtStages = (D == 64 ? 3 : G >= 4 ? 2 : 1) * kWarps;
 template <int D, int G, bool SCORES, bool ENDS>
 cudaError_t run_mma(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeParams& p, int sm_count,
                     cudaStream_t stream) {
-    return launch_stream_instance<RowsMmaMath<D, G, SCORES, ENDS>, D, G, kWarps, kStages, kMinCtasPerSm, false>(
+    return launch_stream_instance<RowsMmaMath<D, G, SCORES, ENDS>, D, G, kWarps, kMmaStages<D>, kMinCtasPerSm, false>(
         tk, tv, p, sm_count, stream);
 }
 
