@@ -685,6 +685,14 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap tmap_k,
                             else if (!withheld)
                                 mbar_arrive(fb);          // no data: consumers skip the slot
                             issued = t + 1;
+                            if constexpr (Math::kRows) {
+                                if (data) {
+                                    const uint32_t dst = ring_addr + stage * Geom::kStageBytes;
+                                    const int row = ids[tt];
+                                    tma_load_3d(dst, &tmap_k, fb, 0, row, 0);
+                                    tma_load_3d(dst + Geom::kTileBytes, &tmap_v, fb, 0, row, 0);
+                                }
+                            }
                         }
                     }
                     ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -692,12 +700,8 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     // Lane 0 copies the K tile, lane 1 the V tile: one 3D box each
                     // (all 128-byte column halves of 16 rows), issued after lane
                     // 0's expect_tx (ordered by the shuffle above).
-                    if (data && lane < 2) {
-                        int row;
-                        if constexpr (Math::kRows)
-                            row = ids[tt];
-                        else
-                            row = (ids[tok / bs - b0] * p.num_kv_heads + cur.y) * bs + (tok % bs);
+                    if (!Math::kRows && data && lane < 2) {
+                        const int row = (ids[tok / bs - b0] * p.num_kv_heads + cur.y) * bs + (tok % bs);
                         const uint32_t dst = ring_addr + stage * Geom::kStageBytes +
                                              (lane ? Geom::kTileBytes : 0);
                         tma_load_3d(dst, lane ? static_cast<const void*>(&tmap_v)
