@@ -16,12 +16,15 @@ constexpr int kMinCtasPerSm = 4;     // kernels have them (pa_decode_mma.cu, pa_
 template <int D>
 constexpr int kMmaStages = (D == 64 ? 2 : 1) * kWarps;
 
-// Ring stages over fp32. Where registers or 64 dims leave room for them more than a tile a warp is on its way
-// (8 KV heads, 210,000 rows of 64 dims: 1, 2, 4 and 8 heads each 154, 165, 302, 483 us with 12
-// stages, 186, 224, 447, 623 with four; 105,000 rows of 128 dims, 4 and 8 heads 282 and 556 with
-// eight, 365 and 624 with four, but 1 and 2 heads 156 and 192 instead of 149 and 175).
+// Ring stages and CTAs per SM over fp32, whose tiles take twice the room: bound by the consumers'
+// latencies from four heads per KV head on, they need warps more than tiles on their way (8 KV
+// heads, 105,000 rows of 128 dims: 1, 2, 4 and 8 heads 150, 169, 230, 377 us with four stages in two CTAs,
+// 158, 182, 269, 498 with eight in one; 210,000 rows of 64 dims 153, 177, 246, 373 us as they stand here,
+// 157, 197, 246, 381 with eight stages in three CTAs, 153, 216, 280, 390 with twelve in two).
 template <int D, int G>
-constexpr int kSimtStages = (D == 64 ? 3 : G >= 4 ? 2 : 1) * kWarps;
+constexpr int kSimtStages = (D == 128 || G == 2 ? 1 : G == 1 ? 3 : 2) * kWarps;
+template <int D, int G>
+constexpr int kSimtCtas = D == 64 && (G == 2 || G == 4) ? 3 : 2;
 
 template <int D, int G, bool SCORES, bool ENDS>
 cudaError_t run_mma(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeParams& p, int sm_count,
@@ -33,7 +36,7 @@ cudaError_t run_mma(const CUtensorMap& tk, const CUtensorMap& tv, const DecodePa
 template <int D, int G, bool SCORES, bool ENDS>
 cudaError_t run_simt(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeParams& p, int sm_count,
                      cudaStream_t stream) {
-    return launch_stream_instance<RowsSimtMath<D, G, SCORES, ENDS>, D, G, kWarps, kSimtStages<D, G>, 1, false>(
+    return launch_stream_instance<RowsSimtMath<D, G, SCORES, ENDS>, D, G, kWarps, kSimtStages<D, G>, kSimtCtas<D, G>, false>(
         tk, tv, p, sm_count, stream);
 }
 

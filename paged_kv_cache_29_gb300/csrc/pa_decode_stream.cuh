@@ -820,7 +820,8 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap tmap_k,
             math.begin(p, q_next);
             if (it_next.x >= 0) math.load_q(p, it_next.x, it_next.y, q_next);
         }
-        if constexpr (Math::kRows) math.begin_rows(p, s, h, token0, ncols, grp);
+        if constexpr (Math::kRows)          // (the warp's place of the merge area is free until the item's end)
+            math.begin_rows(p, s, h, token0, ncols, grp, merge + warp * Smem::kState);
         const int span = ((ntiles + W - 1) / W) * W;   // padded as the producer pads
         const int limit0 = n - Qn + token0;             // the last row the first query token sees
         bool bad = false;

@@ -441,22 +441,6 @@ struct SimtMath {
                                          float /*scale_log2*/, int /*lane*/, int /*row0*/,
                                          int /*limit0*/, int /*grp*/, int skip,
                                          uint32_t /*xb: none*/) {
-        fold_rows(kbase, vbase, [&](int row) { return row < valid && row >= skip; },
-                  [&](int row) { return row < valid; }, valid < kTileRows || skip > 0, [](int, const float (&)[G]) {});
-    }
-
-    // One query per sequence: the rows of `seen` (a bit each); on_scores(row, the
-    // row's masked scores) in every lane of the row.
-    template <class OnScores>
-    __device__ __forceinline__ void fold(uint32_t kbase, uint32_t vbase, uint32_t seen, OnScores&& on_scores) {
-        auto sees = [&](int row) { return ((seen >> row) & 1u) != 0u; };
-        fold_rows(kbase, vbase, sees, sees, seen != 0xffffu, on_scores);
-    }
-
-    // sees(row): its score counts; reads(row): its V row is read; masked: some are not.
-    template <class Sees, class Reads, class OnScores>
-    __device__ __forceinline__ void fold_rows(uint32_t kbase, uint32_t vbase, Sees&& sees, Reads&& reads, bool masked,
-                                              OnScores&& on_scores) {
         const uint32_t kbox = kbase + (ch >> 3) * kBoxBytes;
         const uint32_t vbox = vbase + (ch >> 3) * kBoxBytes;
         const int cc = ch & 7;
@@ -483,17 +467,15 @@ struct SimtMath {
 #pragma unroll
                     for (int off = 1; off < kLpr; off <<= 1)
                         sc[j][g] += __shfl_xor_sync(0xffffffffu, sc[j][g], off);
-            if (masked) {
+            if (valid < kTileRows || skip > 0) {
 #pragma unroll
                 for (int j = 0; j < kSub; ++j) {
                     const int row = (sub * kSub + j) * kRpp + rr;
-                    if (!sees(row))
+                    if (row >= valid || row < skip)
 #pragma unroll
                         for (int g = 0; g < G; ++g) sc[j][g] = -INFINITY;
                 }
             }
-#pragma unroll
-            for (int j = 0; j < kSub; ++j) on_scores((sub * kSub + j) * kRpp + rr, sc[j]);
 #pragma unroll
             for (int g = 0; g < G; ++g) {
                 float mx = sc[0][g];
@@ -520,7 +502,7 @@ struct SimtMath {
 #pragma unroll
             for (int j = 0; j < kSub; ++j) {
                 const int row = (sub * kSub + j) * kRpp + rr;
-                if (reads(row)) {
+                if (row < valid) {
                     float vv[kEpc];
                     E::unpack(lds128(swizzled(vbox, row, cc)), vv);
 #pragma unroll

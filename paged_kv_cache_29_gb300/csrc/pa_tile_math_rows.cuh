@@ -83,7 +83,7 @@ struct RowsMmaMath : MmaMath<D, G, true> {
         item_row_weights<W, STATE, G>(p, buf, s, h, n, ncols);
     }
 
-    __device__ __forceinline__ void begin_rows(const DecodeParams& p, int s, int h, int token0, int ncols, int grp) {
+    __device__ __forceinline__ void begin_rows(const DecodeParams& p, int s, int h, int token0, int ncols, int grp, float* /*scratch*/) {
         cols = ncols;
         if constexpr (!SCORES) {                  // (pa_decode_weights has no window)
             window = p.window > 0 ? p.window - p.num_queries + 1 : 0;   // of one token
@@ -149,56 +149,73 @@ struct RowsMmaMath : MmaMath<D, G, true> {
 };
 
 // fp32 on the CUDA cores, up to G query heads of one token.
+//
+// A row is split over LPR lanes, 16 bytes each; a warp takes RPP rows a pass. The lanes' parts of LPR
+// scores (of S passes and G heads) are added up by halves: each step a lane hands over half of its
+// scores and adds the other half's, so that every lane ends with one score (a butterfly for each
+// score took five times the shuffles). Maxima and sums are kept by the lanes of a head's scores, weights
+// pass through shared memory to the products with V.
 template <int D, int G, bool SCORES, bool ENDS>
-struct RowsSimtMath : SimtMath<float, D, G> {
-    using Base = SimtMath<float, D, G>;
-    using QRegs = typename Base::QRegs;
+struct RowsSimtMath {
+    using T = float;
     static constexpr bool kRows = true;
     static constexpr bool kEnds = ENDS;
     static constexpr bool kCausal = true;         // columns are the item's, not G of them
+    static constexpr bool kQuantAppend = false;
+    static constexpr int kExtraStageBytes = 0;
+    static constexpr bool kQInSmem = false;
+    static constexpr int kQBufBytes = 0;
+    using Geom = TileGeom<T, D>;
+    static constexpr int kLpr = D / 4;            // lanes per row
+    static constexpr int kRpp = 32 / kLpr;        // rows per pass
+    static constexpr int kPasses = kTileRows / kRpp;
+    static constexpr int kSub = kPasses < kLpr / G ? kPasses : kLpr / G;   // passes of a sum by halves
+    static constexpr int kSubs = kPasses / kSub;
+    static constexpr int kScoresOf = kSub * G;    // scores of one
+    static constexpr int kTwins = kLpr / kScoresOf;   // lanes with the same score
 
-    float* scores;
+    struct QRegs {
+        float f[G][4];
+    };
+
+    float qf[G][4], o[G][4];
+    float m, l;                   // of the lane's head; l: of the lane's scores
+    int rr, ch, own;              // row of a pass, chunk, the lane's score of a sum: pass own / G, head own % G
+    float* scores;                // of the item's sequence and KV head
+    float* weights;               // [row][head] of the warp's tile, in shared memory
     int cols, window, sinks;
 
+    __device__ __forceinline__ void setup(int lane, const DecodeParams&) {
+        rr = lane / kLpr;
+        ch = lane % kLpr;
+        own = ch / kTwins;
+    }
+
     // The group's q rows; a column past them is zero.
-    __device__ __forceinline__ void load_heads(const DecodeParams& p, int s, int h, float (&dst)[G][Base::kEpc]) const {
+    __device__ __forceinline__ void load_q(const DecodeParams& p, int s, int h, QRegs& r) const {
         const int grp = p.num_heads / p.num_kv_heads;
 #pragma unroll
         for (int g = 0; g < G; ++g) {
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (g < grp)
+                x = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + (static_cast<size_t>(s) * p.num_heads + h * grp + g) * D) + ch);
+            r.f[g][0] = x.x * p.scale_log2;
+            r.f[g][1] = x.y * p.scale_log2;
+            r.f[g][2] = x.z * p.scale_log2;
+            r.f[g][3] = x.w * p.scale_log2;
+        }
+    }
+
+    __device__ __forceinline__ void begin(const DecodeParams&, const QRegs& r) {
 #pragma unroll
-            for (int e = 0; e < Base::kEpc; ++e) dst[g][e] = 0.f;
-            if (g < grp) {
-                const float* row = static_cast<const float*>(p.q) + (static_cast<size_t>(s) * p.num_heads + h * grp + g) * D;
-                const uint4 raw = __ldg(reinterpret_cast<const uint4*>(row) + Base::ch);
-                Base::E::unpack(raw, dst[g]);
+        for (int g = 0; g < G; ++g)
 #pragma unroll
-                for (int e = 0; e < Base::kEpc; ++e) dst[g][e] *= p.scale_log2;
+            for (int e = 0; e < 4; ++e) {
+                qf[g][e] = r.f[g][e];
+                o[g][e] = 0.f;
             }
-        }
-    }
-
-    __device__ __forceinline__ void load_q(const DecodeParams& p, int s, int h, QRegs& r) const {
-        r.s = s;
-        r.h = h;
-        if constexpr (Base::kPrefetch) load_heads(p, s, h, r.f);
-    }
-
-    __device__ __forceinline__ void begin(const DecodeParams& p, const QRegs& r) {
-        if constexpr (Base::kPrefetch) {
-#pragma unroll
-            for (int g = 0; g < G; ++g)
-#pragma unroll
-                for (int e = 0; e < Base::kEpc; ++e) Base::qf[g][e] = r.f[g][e];
-        } else {
-            load_heads(p, r.s, r.h, Base::qf);
-        }
-#pragma unroll
-        for (int g = 0; g < G; ++g) {
-#pragma unroll
-            for (int e = 0; e < Base::kEpc; ++e) Base::o[g][e] = 0.f;
-            Base::m[g] = -INFINITY;
-            Base::l[g] = 0.f;
-        }
+        m = -INFINITY;
+        l = 0.f;
     }
 
     template <int W, int STATE>
@@ -206,10 +223,11 @@ struct RowsSimtMath : SimtMath<float, D, G> {
         item_row_weights<W, STATE, G>(p, buf, s, h, n, ncols);
     }
 
-    __device__ __forceinline__ void begin_rows(const DecodeParams& p, int s, int h, int /*token0: 0*/, int ncols, int /*grp*/) {
+    __device__ __forceinline__ void begin_rows(const DecodeParams& p, int s, int h, int /*token0: 0*/, int ncols, int /*grp*/, float* scratch) {
         cols = ncols;
         window = p.window;
         sinks = p.num_sinks;
+        weights = scratch;
         if constexpr (SCORES)
             scores = p.scores + (static_cast<size_t>(s) * p.num_kv_heads + h) * p.score_rows * ncols;
     }
@@ -217,15 +235,119 @@ struct RowsSimtMath : SimtMath<float, D, G> {
     __device__ __forceinline__ void tile(uint32_t kbase, uint32_t vbase, int /*valid*/,
                                          float /*scale_log2*/, int /*lane*/, int row0, int limit0,
                                          int /*grp*/, int /*skip*/, uint32_t /*xb: none*/) {
-        Base::fold(kbase, vbase, rows_seen(row0, limit0, window, sinks), [&](int row, const float (&sc)[G]) {
-            if constexpr (SCORES) {
-                if (Base::ch == 0) {
+        const uint32_t kbox = kbase + (ch >> 3) * kBoxBytes;
+        const uint32_t vbox = vbase + (ch >> 3) * kBoxBytes;
+        const int cc = ch & 7;
+        const uint32_t seen = rows_seen(row0, limit0, window, sinks);
+        float sc[kSubs];
+        float mx = -INFINITY;
 #pragma unroll
-                    for (int g = 0; g < G; ++g)
-                        if (g < cols) scores[static_cast<size_t>(row0 + row) * cols + g] = sc[g];
+        for (int sub = 0; sub < kSubs; ++sub) {
+            float part[kScoresOf];
+#pragma unroll
+            for (int j = 0; j < kSub; ++j) {
+                const uint4 raw = lds128(swizzled(kbox, (sub * kSub + j) * kRpp + rr, cc));
+                const float k[4] = {__uint_as_float(raw.x), __uint_as_float(raw.y), __uint_as_float(raw.z), __uint_as_float(raw.w)};
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
+                    float acc = qf[g][0] * k[0];
+#pragma unroll
+                    for (int e = 1; e < 4; ++e) acc = fmaf(qf[g][e], k[e], acc);
+                    part[j * G + g] = acc;
                 }
             }
-        });
+#pragma unroll
+            for (int n = kScoresOf / 2, off = kLpr / 2; off > 0; n /= 2, off /= 2) {
+                if (n > 0) {
+                    const bool high = (ch & off) != 0;
+#pragma unroll
+                    for (int i = 0; i < n; ++i) {
+                        const float give = high ? part[i] : part[i + n];
+                        part[i] = (high ? part[i + n] : part[i]) + __shfl_xor_sync(0xffffffffu, give, off);
+                    }
+                } else {
+                    part[0] += __shfl_xor_sync(0xffffffffu, part[0], off);
+                }
+            }
+            const int row = (sub * kSub + own / G) * kRpp + rr;
+            sc[sub] = (seen >> row) & 1u ? part[0] : -INFINITY;
+            mx = fmaxf(mx, sc[sub]);
+            if constexpr (SCORES) {
+                if (ch % kTwins == 0 && own % G < cols) scores[static_cast<size_t>(row0 + row) * cols + own % G] = sc[sub];
+            }
+        }
+        // Over the lanes of a head: those that differ in the pass, then in the row of a pass.
+#pragma unroll
+        for (int off = kTwins * G; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+        const float mn = fmaxf(m, mx);
+        // (A whole tile can be masked while the maximum is still -inf: weights 0 then.)
+        const float ref = mn == -INFINITY ? 0.f : mn;
+        const float al = fast_exp2(m - ref);
+        m = mn;
+        l *= al;
+#pragma unroll
+        for (int sub = 0; sub < kSubs; ++sub) {
+            const float w = fast_exp2(sc[sub] - ref);
+            l += w;
+            if (ch % kTwins == 0) weights[((sub * kSub + own / G) * kRpp + rr) * G + own % G] = w;
+        }
+        __syncwarp();
+        if (__any_sync(0xffffffffu, al != 1.f)) {
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                const float a = __shfl_sync(0xffffffffu, al, g * kTwins);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[g][e] *= a;
+            }
+        }
+        auto add = [&](int row) {
+            const uint4 raw = lds128(swizzled(vbox, row, cc));
+            const float v[4] = {__uint_as_float(raw.x), __uint_as_float(raw.y), __uint_as_float(raw.z), __uint_as_float(raw.w)};
+            float w[G];
+            if constexpr (G % 4 == 0) {
+#pragma unroll
+                for (int g = 0; g < G; g += 4)
+                    *reinterpret_cast<float4*>(w + g) = *reinterpret_cast<const float4*>(weights + row * G + g);
+            } else if constexpr (G == 2) {
+                *reinterpret_cast<float2*>(w) = *reinterpret_cast<const float2*>(weights + row * G);
+            } else {
+                w[0] = weights[row];
+            }
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[g][e] = fmaf(w[g], v[e], o[g][e]);
+        };
+        if (seen == 0xffffu) {
+#pragma unroll
+            for (int j = 0; j < kPasses; ++j) add(j * kRpp + rr);
+        } else {                                  // (0 * NaN would stay in the sums)
+            for (int j = 0; j < kPasses; ++j)
+                if ((seen >> (j * kRpp + rr)) & 1u) add(j * kRpp + rr);
+        }
+    }
+
+    // State layout as SimtMath's.
+    __device__ __forceinline__ void write_state(float* st, int lane, int /*ncols*/) {
+        __syncwarp();                             // the weights were in its place
+#pragma unroll
+        for (int off = kTwins * G; off < 32; off <<= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+#pragma unroll
+        for (int off = kLpr; off < 32; off <<= 1)
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[g][e] += __shfl_xor_sync(0xffffffffu, o[g][e], off);
+        if (lane % kTwins == 0 && lane / kTwins < G) {
+            st[own] = m;
+            st[G + own] = l;
+        }
+        if (rr == 0) {
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) st[2 * G + g * D + ch * 4 + e] = o[g][e];
+        }
     }
 };
 
