@@ -23,6 +23,7 @@
 // 128 sequences of 1,640 rows to half, in place, 8 KV heads of 128, bf16: selection 28 us, bound by
 // latencies (six trips to memory and some 20 barriers a CTA, in 1.7 rounds of CTAs); moves 143 us for 854 MB,
 // 6.0 TB/s, bound by memory.
+#include <atomic>
 #include <climits>
 
 #include <cooperative_groups.h>
@@ -532,9 +533,16 @@ cudaError_t launch_evict(EvictParams p, cudaStream_t stream) {
                    : share > 8192 ? evict_select_kernel<512, true>
                                   : evict_select_kernel<256, true>;
     cudaError_t err = cudaSuccess;
-    if (max_keys > 8192) {                    // beyond the shared memory that needs no asking
-        err = cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * kMaxKeys);
+    if (max_keys > 8192) {                    // beyond the shared memory that needs no asking: once per device
+        static std::atomic<bool> asked[kMaxDevices];   // (of evict_select_kernel<512, true>)
+        int dev = 0;
+        err = cudaGetDevice(&dev);
         if (err != cudaSuccess) return err;
+        if (dev >= kMaxDevices || !asked[dev].load(std::memory_order_relaxed)) {
+            err = cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * kMaxKeys);
+            if (err != cudaSuccess) return err;
+            if (dev < kMaxDevices) asked[dev].store(true, std::memory_order_relaxed);
+        }
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(heads) * ranks);
