@@ -4,7 +4,7 @@
 // tiles the first one has brought into L2; fp32: one query token.
 //
 // 128 sequences of 1,640 rows, 32 query heads over 8 KV heads of 128, window 1,024 and 4 first
-// rows, bf16: 87 us with the merge, 465 MB, bound by memory (5.6 TB/s between the ring's
+// rows, bf16: 86 us with the merge, 465 MB, bound by memory (5.7 TB/s between the ring's
 // start, 6 us, and the merge, 4); the plain kernel took 1,056.
 #include "pa_decode_rows_ring.cuh"
 

@@ -2,8 +2,8 @@
 // pa_decode_weights: the scores of every row go to the workspace (shapes as in
 // pa_decode_sinks.cu).
 //
-// 128 sequences of 1,640 rows, 32 query heads over 8 KV heads of 128, bf16: 156 us (5.9 TB/s of
-// DRAM traffic, bound by memory; 150 without the stores of 27 MB of scores), 172 with the merge and
+// 128 sequences of 1,640 rows, 32 query heads over 8 KV heads of 128, bf16: 152 us (6.1 TB/s of
+// DRAM traffic, bound by memory; 5 us of it for the stores of 27 MB of scores), 168 with the merge and
 // row_weights_kernel.
 #include "pa_decode_rows_ring.cuh"
 
