@@ -81,7 +81,7 @@ def test_workspaces(lib, B, Q, hq, D, mcl):
     need = lib.pa_decode_workspace_size_multi(B, Q, hq, D, mcl)
     assert sinks(lib, **sizes, ws=P, wsb=need - 1) == WORKSPACE and sinks(lib, **sizes, ws=P + 8, wsb=need) == WORKSPACE
     need = lib.pa_evict_workspace_size(B, hq, mcl)
-    assert need == 8 * B * hq * mcl + 4 * (B * hq + B)
+    assert need == 8 * B * hq * mcl + 4 * (B * hq + 2 * B)
     assert evict(lib, B=B, Hkv=hq, mcl=mcl, mb=mb, ws=P, wsb=need - 1) == WORKSPACE
     assert lib.pa_decode_workspace_size_weights(0, Q, hq, D, mcl) == 0 and lib.pa_evict_workspace_size(0, hq, mcl) == 0
 
