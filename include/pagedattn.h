@@ -671,8 +671,10 @@ pa_status pa_decode_sinks(const void* q, const void* k_cache, const void* v_cach
  * begin with what the caller puts there. A row in a block that several sequences of
  * the batch share gets the weights of all of them (in any order of addition). All
  * weights are fp32, from fp32 scores and the sequence's final maximum and sum.
- * A sequence that is flagged leaves its row weights as they are; other
- * arguments, shapes and errors as pa_decode_sinks without the window. Workspace:
+ * A sequence that is flagged leaves its row weights as they are; after
+ * PA_DEVERR_TIMEOUT each sequence has, under each KV head, the weights of the whole
+ * call or those of before. Other arguments, shapes and errors as pa_decode_sinks
+ * without the window. Workspace:
  * pa_decode_workspace_size_weights bytes (4 bytes of it per row of
  * max_context_len, query token and head of each sequence hold the scores).
  */
@@ -686,6 +688,17 @@ pa_status pa_decode_weights(const void* q, const void* k_cache, const void* v_ca
 
 size_t pa_decode_workspace_size_weights(int num_seqs, int num_queries, int num_heads,
                                         int head_dim, int max_context_len);
+
+/* The failure test of pa_test_withhold_tile, of pa_decode_weights. */
+pa_status pa_test_withhold_tile_weights(const void* q, const void* k_cache, const void* v_cache,
+                                        const int32_t* block_tables, const int32_t* context_lens,
+                                        float scale, void* out, float* row_weights, int num_seqs,
+                                        int num_queries, int num_heads, int num_kv_heads,
+                                        int head_dim, int block_size, int num_blocks,
+                                        int max_blocks_per_seq, int max_context_len, pa_dtype dtype,
+                                        void* workspace, size_t workspace_bytes,
+                                        int32_t* error_word, int withhold_tile,
+                                        struct CUstream_st* stream);
 
 /*
  * pa_evict -- cuts sequences to a number of rows, for each KV head the rows that were

@@ -148,6 +148,9 @@ def lib() -> ctypes.CDLL:
         L.pa_decode_weights.argtypes = [P, P, P, P, P, F, P, P, I, I, I, I, I, I, I, I, I, I, P, S,
                                         P, P]
         L.pa_decode_weights.restype = I
+        L.pa_test_withhold_tile_weights.argtypes = [P, P, P, P, P, F, P, P, I, I, I, I, I, I, I, I, I, I, P, S,
+                                                    P, I, P]
+        L.pa_test_withhold_tile_weights.restype = I
         L.pa_decode_workspace_size_weights.argtypes = [I, I, I, I, I]
         L.pa_decode_workspace_size_weights.restype = S
         L.pa_evict.argtypes = [P, P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, I, P, S, P, P]

@@ -55,7 +55,7 @@ pa_status rows_call(const void* q, const void* k_cache, const void* v_cache, con
                     float* row_weights, int num_seqs, int num_queries, int num_heads, int num_kv_heads,
                     int head_dim, int block_size, int num_blocks, int max_blocks_per_seq,
                     int max_context_len, pa_dtype dtype, void* workspace, size_t workspace_bytes,
-                    int32_t* error_word, bool weights, struct CUstream_st* stream) {
+                    int32_t* error_word, bool weights, struct CUstream_st* stream, int withhold_tile = -1) {
     if (num_seqs < 0 || num_queries < 1 || num_queries > 8 || num_heads <= 0 || num_kv_heads <= 0 ||
         head_dim <= 0 || block_size <= 0 || num_blocks <= 0 || max_blocks_per_seq < 0 ||
         max_context_len < 0 || num_heads % num_kv_heads != 0 || !std::isfinite(scale) ||
@@ -115,6 +115,7 @@ pa_status rows_call(const void* q, const void* k_cache, const void* v_cache, con
         base.item_count = reinterpret_cast<int32_t*>(ws);
     }
     base.error_word = error_word;
+    base.withhold_tile = withhold_tile;
     base.scale_log2 = scale * kLog2e;
     base.k_scale = base.v_scale = 1.0f;
     base.num_queries = num_queries;
@@ -206,6 +207,20 @@ pa_status pa_decode_weights(const void* q, const void* k_cache, const void* v_ca
                      num_queries, num_heads, num_kv_heads, head_dim, block_size, num_blocks,
                      max_blocks_per_seq, max_context_len, dtype, workspace, workspace_bytes, error_word,
                      true, stream);
+}
+
+pa_status pa_test_withhold_tile_weights(const void* q, const void* k_cache, const void* v_cache,
+                                        const int32_t* block_tables, const int32_t* context_lens, float scale,
+                                        void* out, float* row_weights, int num_seqs, int num_queries,
+                                        int num_heads, int num_kv_heads, int head_dim, int block_size,
+                                        int num_blocks, int max_blocks_per_seq, int max_context_len,
+                                        pa_dtype dtype, void* workspace, size_t workspace_bytes,
+                                        int32_t* error_word, int withhold_tile, struct CUstream_st* stream) {
+    if (withhold_tile < 0 || error_word == nullptr) return PA_ERR_INVALID_ARG;
+    return rows_call(q, k_cache, v_cache, block_tables, context_lens, scale, 0, 0, out, row_weights, num_seqs,
+                     num_queries, num_heads, num_kv_heads, head_dim, block_size, num_blocks,
+                     max_blocks_per_seq, max_context_len, dtype, workspace, workspace_bytes, error_word,
+                     true, stream, withhold_tile);
 }
 
 size_t pa_decode_workspace_size_weights(int num_seqs, int num_queries, int num_heads, int head_dim,

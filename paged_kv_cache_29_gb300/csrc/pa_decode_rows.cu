@@ -169,8 +169,8 @@ __global__ void __launch_bounds__(kThreads) decode_rows_kernel(const DecodeParam
 // the merge's, else its only partition's)
 //   w = sum_c 2^(score_c - M_c) / L_c
 // for every row, stored for the rows of this call's tokens, added for the others
-// (atomically: sequences may share a block). A partition with a block outside the pool, flagged
-// by the decode kernel, has the sum kNoSum: its sequence keeps its weights.
+// (atomically: sequences may share a block). A partition with a block outside the pool, or that the
+// decode kernel gave up before its end, both flagged, has the sum kNoSum: its sequence keeps its weights.
 //
 // A warp takes 128 rows of a partition under one KV head, four a lane; all that it loads
 // (states, scores, block ids) is on the way together, so that the time is some three
@@ -222,6 +222,10 @@ __global__ void __launch_bounds__(kWeightThreads) row_weights_kernel(const Decod
         const float2* states = reinterpret_cast<const float2*>(p.part_ml);
         bool no_sum = false;
         for (int i = lane; i < nparts; i += 32) no_sum |= states[row0 * p.max_parts + i].y == kNoSum;
+        if (LISTED && p.col_groups > 1)           // (an item of a further column group may have no sums of its own)
+            for (int j = p.group_tokens; j < Q; j += p.group_tokens)
+                for (int i = lane; i < nparts; i += 32)
+                    no_sum |= states[(row0 + static_cast<size_t>(j) * p.num_heads) * p.max_parts + i].y == kNoSum;
         const int32_t* table = p.block_tables + static_cast<size_t>(s) * p.max_blocks_per_seq;
         int id[kWeightRows];
         float w[kWeightRows];

@@ -799,8 +799,21 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap tmap_k,
     } else {
         if (it.x >= 0) math.load_q(p, it.x, it.y, q_next);
     }
+    // Where row_weights_kernel follows: marks the columns of the CTA's i-th item as without a sum, so
+    // that its sequence keeps its row weights under that KV head.
+    constexpr bool kSums = [] {
+        if constexpr (Math::kRows) return Math::kScores && !Math::kEnds;
+        return false;
+    }();
+    auto no_sums = [&](int i) {
+        const int4 x = own_item(i);
+        if (x.x >= 0 && threadIdx.x < item_cols(x))
+            p.part_ml[2 * (query_row(p, x.x, item_head(x), first_token(x) * grp + threadIdx.x, grp) * p.max_parts + x.z) + 1] = kNoSum;
+        return x.x >= 0;
+    };
     int t0 = 0;                 // stream index of the current item's first tile (a multiple of W)
-    for (int j = 0; it.x >= 0; ++j) {
+    int j = 0;
+    for (; it.x >= 0; ++j) {
         const int s = it.x, h = item_head(it), part = it.z, n = it.w;
         const int token0 = first_token(it), ncols = item_cols(it);
         const int base = Math::kRows ? seq_gap(p, n) : seq_row_base(n, p.window);   // (rows that no partition covers)
@@ -870,9 +883,8 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap tmap_k,
 #pragma unroll
         for (int w = 0; w < W; ++w) any_bad |= warp_bad[(j & 1) * W + w] != 0;
         // any_bad: flagged by the producer; output left unspecified
-        if constexpr (Math::kRows) {
-            if (any_bad && p.scores != nullptr && threadIdx.x < ncols)
-                p.part_ml[2 * (query_row(p, s, h, token0 * grp + threadIdx.x, grp) * p.max_parts + part) + 1] = kNoSum;
+        if constexpr (kSums) {
+            if (any_bad) no_sums(j);
         }
         const int nparts = (n - base + P - 1) / P;
         for (int idx = any_bad ? ncols * D : threadIdx.x; idx < ncols * D; idx += W * 32) {
@@ -920,6 +932,11 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap tmap_k,
         }
         // The next item's warp states overwrite the merge area.
         named_barrier(1, W * 32);
+    }
+    if constexpr (kSums) {
+        // Given up: the workspace may hold an earlier call's states for the items without an end.
+        // (No item is left otherwise.)
+        while (no_sums(j)) ++j;
     }
 }
 

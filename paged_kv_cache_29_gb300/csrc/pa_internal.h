@@ -263,7 +263,7 @@ int rows_group_tokens(pa_dtype dtype, int head_dim, int group, int num_queries);
 // partitions' maxima and sums. item_count: how many work items the tile ring listed
 // (p.items), null after the plain kernel, which lists none.
 cudaError_t launch_row_weights(const DecodeParams& p, const int32_t* item_count, cudaStream_t stream);
-constexpr float kNoSum = -1.0f;      // in place of a partition's sum: it has a block outside the pool
+constexpr float kNoSum = -1.0f;      // in place of a partition's sum: it has a block outside the pool, or was given up
 
 // Merge of partition partials for sequences longer than one partition. rows: of
 // pa_decode_sinks and pa_decode_weights.

@@ -63,6 +63,7 @@ template <int D, int G, bool SCORES, bool ENDS>
 struct RowsMmaMath : MmaMath<D, G, true> {
     using Base = MmaMath<D, G, true>;
     static constexpr bool kRows = true;
+    static constexpr bool kScores = SCORES;       // every row's scores are stored
     static constexpr bool kEnds = ENDS;           // an item's end adds its row weights
     using Base::gid;
     using Base::t4;
@@ -159,6 +160,7 @@ template <int D, int G, bool SCORES, bool ENDS>
 struct RowsSimtMath {
     using T = float;
     static constexpr bool kRows = true;
+    static constexpr bool kScores = SCORES;
     static constexpr bool kEnds = ENDS;
     static constexpr bool kCausal = true;         // columns are the item's, not G of them
     static constexpr bool kQuantAppend = false;
