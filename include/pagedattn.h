@@ -758,8 +758,8 @@ size_t pa_evict_workspace_size(int num_seqs, int num_kv_heads, int max_context_l
  *   cache (context_lens counts the rows of all d; both null: no such output).
  * draft_probs null: the drafts were not drawn (a lookup), q_i is 1 at x_i and 0
  * elsewhere. Products are exact, sums keep 44 bits or more: only where u comes nearer
- * than that to the border between two tokens may either be drawn (for sums from 2^-100
- * to 2^127). A NaN or negative r counts as 0.
+ * than that to the border between two tokens may either be drawn (for sums up to 2^127).
+ * A NaN or negative r counts as 0.
  *
  * target_probs: fp32 [num_seqs][max_drafts + 1][vocab_size], draft_probs: fp32
  * [num_seqs][max_drafts][vocab_size], with any strides (elements) between

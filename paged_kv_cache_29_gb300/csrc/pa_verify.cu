@@ -39,6 +39,7 @@ constexpr int kSegment = kThreads;            // a value a thread, in the last s
 constexpr int kMaxCluster = 8;
 // Segments of a CTA: their running sums fit the default shared memory.
 constexpr int kMaxSegments = 4096;
+constexpr float kUp = 0x1p100f;
 
 // A sum of fp32 values as hi + lo, |lo| at most half a step of hi.
 struct Sum {
@@ -70,6 +71,7 @@ struct Sum {
         const float p = hi * u;
         return Sum{p, fmaf(hi, u, -p) + lo * u}.order();
     }
+    __device__ __forceinline__ Sum scaled(float by) const { return Sum{hi * by, lo * by}; }   // by a power of two
     __device__ __forceinline__ bool above(const Sum& o) const { return hi > o.hi || (hi == o.hi && lo > o.lo); }
 };
 
@@ -187,6 +189,7 @@ __device__ __forceinline__ Sum sum_some(const float* pr, const float* qr, int v0
 __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams p, int segs_per_cta) {
     extern __shared__ Sum seg_sum[];          // [segs_per_cta]: of each segment, then up to its end
     __shared__ Sum cta_total, warp_total[kWarps], border_left;
+    __shared__ bool in_units;
     __shared__ int first_rejected, bad, chosen, owner;
     cg::cluster_group cluster = cg::this_cluster();
     const int ranks = cluster.num_blocks(), rank = cluster.block_rank();
@@ -288,6 +291,16 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams p, 
                 total = total.plus(shuffle(mine, r));
                 if (r == rank) end = total;
             }
+            // Sums of fp32 values lose nothing at the low end of fp32's range, but u S has bits
+            // below them: there all are compared in units of 2^-100.
+            const bool tiny = total.hi < 0x1p-60f;
+            if (tiny) {
+                total = total.scaled(kUp);
+                base = base.scaled(kUp);
+                end = end.scaled(kUp);
+                for (int g = lane; g < segs; g += 32) seg_sum[g] = seg_sum[g].scaled(kUp);
+                __syncwarp();
+            }
             // Sums that values are added to never shrink, and u S is below S: it falls into one part.
             const Sum border = total.times(fminf(fmaxf(u_last, 0.f), 0.99999994f));   // u in [0, 1)
             const bool here = !base.above(border) && end.above(border);
@@ -303,6 +316,7 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams p, 
             }
             if (lane == 0) {
                 border_left = border.minus(here && seg > 0 ? base.plus(seg_sum[seg - 1]) : base);
+                in_units = tiny;
                 owner = !(total.hi > 0.f) ? -2 : here ? seg : -1;
                 chosen = INT_MAX;
             }
@@ -326,6 +340,7 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams p, 
             const int v = (seg0 + g) * kSegment + tid;
             Sum r{0.f, 0.f};
             if (v < V && v != left_out) add_excess(r, __ldg(pr + v), qr != nullptr ? __ldg(qr + v) : 0.f);
+            if (in_units) r = r.scaled(kUp);
             Sum run = warp_scan(r, lane);
             if (lane == 31) warp_total[warp] = run;
             __syncthreads();
