@@ -186,7 +186,8 @@ static_assert(kDefaultPartition % kWeightUnit == 0 && kWeightThreads / 32 % kWei
 
 // LISTED: the partitions are those of the tile ring's work list, item_count[0] of them; else
 // (the plain kernel has no list) all that there may be.
-template <bool LISTED>
+// TOKENS: there may be several query tokens, and rows that not all of them see.
+template <bool LISTED, bool TOKENS>
 __global__ void __launch_bounds__(kWeightThreads) row_weights_kernel(const DecodeParams p, const int32_t* item_count,
                                                                      int most_items, const Divisor by_block) {
     grid_dependency_wait();
@@ -235,6 +236,9 @@ __global__ void __launch_bounds__(kWeightThreads) row_weights_kernel(const Decod
             id[u] = __ldg(table + by_block.quotient(i));
             w[u] = 0.f;
         }
+        // First column of a token that sees the lane's first row (others add nothing, not 0 times a sum that
+        // may be NaN); far before the tokens' rows all see the lane's rows, and no product leaves 32 bits.
+        const int first_col = TOKENS ? max(i0 - (n - Q), -kWeightUnit) * grp : 0;
         const float* sc = p.scores + (static_cast<size_t>(s) * p.num_kv_heads + h) * p.score_rows * cols;
         for (int c0 = 0; c0 < cols; c0 += 32) {
             float2 own = make_float2(0.f, 1.f);
@@ -248,7 +252,8 @@ __global__ void __launch_bounds__(kWeightThreads) row_weights_kernel(const Decod
             auto take = [&](const float (&score)[kWeightRows], int c) {
                 const float m = __shfl_sync(0xffffffffu, own.x, c - c0), r = __shfl_sync(0xffffffffu, own.y, c - c0);
 #pragma unroll
-                for (int u = 0; u < kWeightRows; ++u) w[u] = fmaf(fast_exp2(score[u] - m), r, w[u]);
+                for (int u = 0; u < kWeightRows; ++u)
+                    if (!TOKENS || c >= first_col + 32 * u * grp) w[u] = fmaf(fast_exp2(score[u] - m), r, w[u]);
             };
             const int ce = min(cols, c0 + 32);
             if (cols % 4 == 0) {
@@ -321,8 +326,9 @@ cudaError_t launch_row_weights(const DecodeParams& p, const int32_t* item_count,
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t err = cudaLaunchKernelEx(&cfg, item_count != nullptr ? row_weights_kernel<true> : row_weights_kernel<false>,
-                                               p, item_count, static_cast<int>(most), Divisor(static_cast<uint32_t>(p.block_size)));
+    auto* kernel = item_count != nullptr ? (p.num_queries > 1 ? row_weights_kernel<true, true> : row_weights_kernel<true, false>)
+                                         : (p.num_queries > 1 ? row_weights_kernel<false, true> : row_weights_kernel<false, false>);
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, p, item_count, static_cast<int>(most), Divisor(static_cast<uint32_t>(p.block_size)));
     if (err != cudaSuccess) return err;
     return cudaGetLastError();
 }

@@ -41,16 +41,17 @@ __device__ __forceinline__ void item_row_weights(const DecodeParams& p, const fl
         for (int w = 0; w < W; ++w) L = fmaf(fast_exp2(buf[w * STATE + g] - M[g]), buf[w * STATE + G + g], L);
         R[g] = 1.f / L;
     }
-    const int bs = p.block_size;
+    const int bs = p.block_size, grp = p.num_heads / p.num_kv_heads;
     const int32_t* table = p.block_tables + static_cast<size_t>(s) * p.max_blocks_per_seq;
     const float* scores = p.scores + (static_cast<size_t>(s) * p.num_kv_heads + h) * p.score_rows * cols;
     for (int i = threadIdx.x; i < n; i += W * 32) {
         const int b = i / bs;
         float* at = p.row_weights + (static_cast<size_t>(__ldg(table + b)) * p.num_kv_heads + h) * bs + (i - b * bs);
+        const int first = max(0, i - (n - p.num_queries)) * grp;   // column of a token that sees the row (another's sum may be NaN)
         float w = 0.f;
 #pragma unroll
         for (int g = 0; g < G; ++g)
-            if (g < cols) w = fmaf(fast_exp2(scores[static_cast<size_t>(i) * cols + g] - M[g]), R[g], w);
+            if (g < cols && g >= first) w = fmaf(fast_exp2(scores[static_cast<size_t>(i) * cols + g] - M[g]), R[g], w);
         if (i >= n - p.num_queries)
             *at = w;
         else
