@@ -100,8 +100,8 @@ __global__ void __launch_bounds__(kSelectThreads, kSelectThreads == 256 ? 4 : 2)
         int cls = 8;
         n = keep = 0;
         if (tid < p.num_seqs) {
-            n = __ldg(p.context_lens + tid);
-            keep = __ldg(p.keep_lens + tid);
+            n = p.context_lens[tid];          // (ordinary loads, as the plan of the decode kernels)
+            keep = p.keep_lens[tid];
             cls = n <= 0 ? 7 : min(7, max(0, __clz(n) - __clz(p.context_cap)));
         }
         uint32_t peers = 0, count = 0;
@@ -137,8 +137,8 @@ __global__ void __launch_bounds__(kSelectThreads, kSelectThreads == 256 ? 4 : 2)
         keep = own[2];
         if (tid == 0 && rank == 0 && h == 0) p.order[unit] = s;
     } else {
-        n = __ldg(p.context_lens + s);
-        keep = __ldg(p.keep_lens + s);
+        n = p.context_lens[s];
+        keep = p.keep_lens[s];
     }
     const bool odd = n < 0 || n > p.context_cap || keep < 0;
     keep = min(keep, n);

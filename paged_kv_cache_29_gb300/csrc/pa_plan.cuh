@@ -76,9 +76,12 @@ __device__ __forceinline__ int plan_heads(const DecodeParams& p) {
 }
 
 // Context length of sequence s, or -1 (flagged) when it is out of range
-// (negative, past max_context_len, or shorter than the query tokens it holds).
+// (negative, past max_context_len, or shorter than the query tokens it holds). An
+// ordinary load: pa_verify_draft and pa_evict write lengths, and a kernel launched as
+// their programmatic dependent is there before they have, when read-only loads
+// (of what does not change while the kernel runs) do not hold.
 __device__ __forceinline__ int plan_len(const DecodeParams& p, int s, bool flag) {
-    int n = __ldg(p.context_lens + s);
+    int n = p.context_lens[s];
     if (n < 0 || n > p.context_cap || (n > 0 && n < p.num_queries)) {
         if (flag) raise_error(p.error_word, PA_DEVERR_CONTEXT);
         n = -1;

@@ -203,10 +203,11 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams p, 
     const int32_t* tokens = p.tokens + static_cast<size_t>(s) * Q;
     const float* uniforms = p.uniforms + static_cast<size_t>(s) * (Q + 1);
     // Independent loads first. (lens_out may be context_lens: it is written behind the
-    // cluster's barrier, which every CTA reaches after this read.)
-    const int d = p.num_drafts != nullptr ? __ldg(p.num_drafts + s) : Q;
+    // cluster's barrier, which every CTA reaches after this read. What may be another call's
+    // output is read with ordinary loads, as in the plan of the decode kernels.)
+    const int d = p.num_drafts != nullptr ? p.num_drafts[s] : Q;
     const int rows = p.context_lens != nullptr ? p.context_lens[s] : 0;
-    const int x = tid < Q ? __ldg(tokens + tid) : 0;
+    const int x = tid < Q ? tokens[tid] : 0;
     const float ux = tid < Q ? __ldg(uniforms + tid) : 0.f;
     const float u_last = __ldg(uniforms + Q);
     const bool bad_count = d < 0 || d > Q;
@@ -235,7 +236,7 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams p, 
     const bool rejected = a < d;
     const float* pr = target + a * p.target_row;
     const float* qr = rejected && draft != nullptr ? draft + a * p.draft_row : nullptr;
-    int left_out = rejected && draft == nullptr ? __ldg(tokens + a) : -1;   // looked up: q is 1 there
+    int left_out = rejected && draft == nullptr ? tokens[a] : -1;   // looked up: q is 1 there
 
     const int seg0 = rank * segs_per_cta;
     const int segs = max(0, min((V + kSegment - 1) / kSegment - seg0, segs_per_cta));
@@ -369,7 +370,7 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams p, 
             token = chosen;
         }
         for (int i = tid; i <= Q; i += kThreads)
-            p.out_tokens[static_cast<size_t>(s) * (Q + 1) + i] = i < a ? __ldg(tokens + i) : i == a ? token : -1;
+            p.out_tokens[static_cast<size_t>(s) * (Q + 1) + i] = i < a ? tokens[i] : i == a ? token : -1;
         if (tid == 0) {
             p.num_accepted[s] = a;
             if (p.lens_out != nullptr) p.lens_out[s] = rows - (d - a);
