@@ -768,7 +768,7 @@ size_t pa_evict_workspace_size(int num_seqs, int num_kv_heads, int max_context_l
  * [num_seqs][max_drafts + 1]; num_accepted, num_drafts, context_lens, lens_out:
  * int32 [num_seqs], lens_out may be context_lens. 0 <= max_drafts <= 64.
  * A drafted token outside [0, vocab_size) among the first d, d outside
- * [0, max_drafts], or a row p_a without a positive or with an infinite value flags
+ * [0, max_drafts], a row p_a without a positive value or an infinite r flags
  * PA_DEVERR_TOKEN,
  * context_lens[s] < d - a PA_DEVERR_CONTEXT; nothing of that sequence is written.
  * No workspace.

@@ -40,6 +40,7 @@ constexpr int kMaxCluster = 8;
 // Segments of a CTA: their running sums fit the default shared memory.
 constexpr int kMaxSegments = 4096;
 constexpr float kUp = 0x1p100f;
+constexpr int kNothing = -2, kNoSums = -3;    // in place of a segment
 
 // A sum of fp32 values as hi + lo, |lo| at most half a step of hi.
 struct Sum {
@@ -240,7 +241,6 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams p, 
 
     const int seg0 = rank * segs_per_cta;
     const int segs = max(0, min((V + kSegment - 1) / kSegment - seg0, segs_per_cta));
-    bool some = false;
     for (int pass = 0; pass < 2; ++pass) {
         if (pass == 1) {                      // the difference leaves nothing: from p itself
             qr = nullptr;
@@ -318,19 +318,19 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams p, 
             if (lane == 0) {
                 border_left = border.minus(here && seg > 0 ? base.plus(seg_sum[seg - 1]) : base);
                 in_units = tiny;
-                owner = !(total.hi > 0.f) ? -2 : here ? seg : -1;
+                // A value that is infinite has left a sum that is NaN: nothing to draw from.
+                owner = total.hi > 0.f ? (here ? seg : -1) : total.hi == 0.f ? kNothing : kNoSums;
                 chosen = INT_MAX;
             }
         }
         __syncthreads();
-        some = owner != -2;
-        if (some) break;
+        if (owner != kNothing) break;
         cluster.sync();                       // every CTA has read the totals: the second pass writes them
     }
     // The totals are read; no CTA ends before all have said so.
     auto arrived = cluster.barrier_arrive();
     const int seg = owner;
-    if (!some && rank == 0 && tid == 0) raise_error(p.error_word, PA_DEVERR_TOKEN);
+    if (seg <= kNothing && rank == 0 && tid == 0) raise_error(p.error_word, PA_DEVERR_TOKEN);
     if (seg >= 0) {
         // The first value whose running sum passes the border. (Where the two ways to sum part
         // by a rounding the walk may go on to the next segment, or end behind the last.)
