@@ -175,6 +175,7 @@ pa_status pa_decode_int8(const void* q, const void* k_cache, const void* v_cache
  * be a multiple of 16 and the pools 16-byte aligned. Returns PA_OK or an
  * error; never blocks. For an INT8 cache (dtype PA_DTYPE_INT8) this copies
  * the codes; copy the row scales with a second call on the two scale arrays
+ * (row weights likewise, given as both pools)
  * viewed as fp32 pools of one KV head, one row and num_kv_heads * block_size
  * values per block (num_kv_heads * block_size a multiple of 4). For an INT4
  * cache (dtype PA_DTYPE_INT4, head_dim the number of dims, a multiple of 32)
@@ -669,8 +670,13 @@ pa_status pa_decode_sinks(const void* q, const void* k_cache, const void* v_cach
  * the rows of this step's tokens begin their sums, whatever their slots held.
  * row_weights: fp32 [num_blocks][num_kv_heads][block_size]; the rows of a prompt
  * begin with what the caller puts there. A row in a block that several sequences of
- * the batch share gets the weights of all of them (in any order of addition). All
- * weights are fp32, from fp32 scores and the sequence's final maximum and sum.
+ * the batch share gets the weights of all of them (in any order of addition); the slots of
+ * the rows i >= n - Q are their sequence's alone, as they are where those rows are appended
+ * (a batch is padded with empty sequences, not with copies of one). A block that is
+ * copied takes its weights along by a further pa_copy_blocks, like the scales of an INT8 cache.
+ * All Q tokens count, those that pa_verify_draft rejects afterwards too: what they added
+ * to earlier rows stays there, while their own rows leave and their slots begin again.
+ * All weights are fp32, from fp32 scores and the sequence's final maximum and sum.
  * A sequence that is flagged leaves its row weights as they are; after
  * PA_DEVERR_TIMEOUT each sequence has, under each KV head, the weights of the whole
  * call or those of before. Other arguments, shapes and errors as pa_decode_sinks

@@ -564,7 +564,8 @@ def pa_copy_blocks(k_cache, v_cache, block_mapping, error_word=None, stream=None
     """Copy-on-write: block dst := block src of both pools for each (src, dst)
     row of block_mapping (int64 [n][2]); negative entries skip a pair. The
     pools are [NB][Hkv][bs][D] (an INT4 cache's [NB][Hkv][bs][D / 2] bytes); for
-    an INT8 cache call it again on the row scales viewed as [NB][1][1][Hkv * bs],
+    an INT8 cache call it again on the row scales viewed as [NB][1][1][Hkv * bs]
+    (row weights likewise, given as both pools),
     for an INT4 cache on the params viewed as [NB][1][1][Hkv * bs * 2]."""
     import torch
     _check_cuda("k_cache", k_cache, ndim=4)

@@ -70,7 +70,8 @@ def pa_decode_weights(q, k_cache, v_cache, block_tables, context_lens, scale, ou
     """Decode attention (q/out as in pa_decode_sinks, every row up to the token's own)
     that adds each row's attention weight, summed over the query heads of its KV
     head and the Q tokens, to row_weights (fp32 [NB][Hkv][bs]); the rows of the last
-    Q tokens begin their sums. workspace: at least
+    Q tokens, whose slots no other sequence of the batch holds, begin their sums. What tokens that
+    are rejected afterwards added to earlier rows stays. workspace: at least
     pa_decode_workspace_size_weights(B, Q, Hq, D, max_context_len) bytes; None as in
     pa_decode_sinks."""
     import torch

@@ -233,7 +233,9 @@ class BlockManager:
         sequences' own. A block that a sequence has to itself stays its place; a shared
         one is replaced by a fresh one, which is no block that any of them held. Which
         tokens the rows hold is known to the device alone, so the blocks lose their
-        keys and the sequences no longer enter the prefix cache."""
+        keys and the sequences no longer enter the prefix cache. So it is for a sequence whose
+        rows[seq] is all that it has, too: leave out of ``rows`` (and of pa_evict's batch) those
+        that are within their budget."""
         for seq, n in rows.items():
             if not 0 <= n <= self.num_tokens(seq):
                 raise ValueError(f"sequence {seq!r} holds {self.num_tokens(seq)} rows, not {n} or more")
