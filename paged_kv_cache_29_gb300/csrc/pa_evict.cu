@@ -523,7 +523,7 @@ cudaError_t launch_evict(EvictParams p, cudaStream_t stream) {
     // 32,768 rows and lengths of 1,640 take 189 us so, 202 with room for the bound.
     // Longest sequences first, where CTAs wait for room and lengths may differ much (128 sequences of
     // 1,640 rows take 171 us so, 177 as they come, 256 of them 340 and 365; but 256 of 300
-    // rows and a bound of 600 124 and 121).
+    // rows and a bound of 600 124 and 121; with a copy of 5 us that restores the weights).
     if (p.num_seqs > kMaxOrdered || static_cast<long long>(heads) * ranks <= 4LL * sms || share <= 2048) p.order = nullptr;
     const int most_keys = static_cast<long long>(heads) * ranks <= 4LL * sms ? kMaxKeys : kShortKeys;
     const bool all_held = share <= most_keys;

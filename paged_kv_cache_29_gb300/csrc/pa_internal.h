@@ -164,7 +164,8 @@ struct NormRopeParams {
 };
 cudaError_t launch_norm_rope(const NormRopeParams& p, pa_dtype dtype, cudaStream_t stream);
 
-// Division of numbers below 2^31 by a divisor that a launch knows: n / d =
+// Division of numbers below 2^31 by a divisor that a launch knows, by the multiplication of
+// Granlund and Montgomery: n / d =
 // (hi32(n * mul) + n) >> shift with shift = ceil(log2 d), mul = floor(2^32 (2^shift - d) / d) + 1
 // (a kernel's own division by a number that it learns at run time takes some 20 instructions;
 // with it the walks over a sequence's rows in pa_evict took three times as long).

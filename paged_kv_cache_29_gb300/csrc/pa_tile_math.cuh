@@ -234,6 +234,10 @@ struct MmaMath {
                 o[mt][3] *= al1;
             }
         }
+        // Weights times V take the weights rounded to bf16, the type of V in these instructions; the
+        // sum l takes them as they are. (128 sequences with a window of 1,024 rows: error against 64
+        // bits 0.0021 of the output's size, of which 0.0017 is the output's own rounding. With
+        // what the rounding leaves as a second product 0.0017, and 103 us instead of 86.)
         // P^T as the B operand: lane (gid, t4) needs P[token 2t4, 2t4+1][head gid]
         // (b0) and P[token 2t4+8, 2t4+9][head gid] (b1). Lane (g', t') holds
         // P[token g'][heads 2t', 2t'+1] and P[token g'+8][same heads].
