@@ -93,26 +93,6 @@ def pa_decode_weights(q, k_cache, v_cache, block_tables, context_lens, scale, ou
         raise _b.PagedAttentionError(rc, "pa_decode_weights")
 
 
-def pa_test_withhold_tile_weights(q, k_cache, v_cache, block_tables, context_lens, scale, out, row_weights,
-                                  max_context_len, withhold_tile, error_word, workspace) -> None:
-    """pa_decode_weights as pa_test_withhold_tile runs pa_decode: CTA 0 of the tile ring
-    withholds tile `withhold_tile`, and the waiting consumer gives up after about 2 s. Not
-    for production use."""
-    import torch
-    dev = torch.cuda.current_device()
-    ptrs, op, sizes, code = _rows_args(q, k_cache, v_cache, block_tables, context_lens, out, dev)
-    rw = _b._arg("row_weights", row_weights, dev, torch.float32, 3)
-    if row_weights.shape != k_cache.shape[:3]:
-        raise ValueError("row_weights must be [NB][Hkv][bs]")
-    rc = _b.lib().pa_test_withhold_tile_weights(*ptrs, float(scale), op, rw, *sizes, _b._int32("max_context_len", max_context_len),
-                                                code, _b._arg("workspace", workspace, dev),
-                                                workspace.numel() * workspace.element_size(),
-                                                _b._arg("error_word", error_word, dev, torch.int32),
-                                                int(withhold_tile), _b._stream_on(None, dev))
-    if rc != _b.PA_OK:
-        raise _b.PagedAttentionError(rc, "pa_test_withhold_tile_weights")
-
-
 def pa_evict(k_cache, v_cache, row_weights, block_tables, context_lens, keep_lens, out_tables,
              lens_out, max_context_len, num_sinks=0, num_recent=0, k_params=None, v_params=None,
              workspace=None, error_word=None, stream=None) -> None:

@@ -5,11 +5,23 @@ import pytest
 import torch
 
 import cache_rows_reference as ref
+import paged_kv_cache_29_gb300 as pkg
 from paged_kv_cache_29_gb300 import _binding as pa
-from paged_kv_cache_29_gb300 import _binding_rows as rows
 from test_gpu_decode_rows import Run, start_weights
 
 pytestmark = pytest.mark.gpu
+
+
+def withhold(run, w, workspace, tile):
+    """pa_decode_weights whose CTA 0 withholds a tile: the waiting consumer gives up after about 2 s."""
+    ptr = lambda t: t.data_ptr()
+    nb, hkv, bs, d = run.dk.shape
+    out = run.out()
+    rc = pa.lib().pa_test_withhold_tile_weights(
+        ptr(run.dq), ptr(run.dk), ptr(run.dv), ptr(run.table), ptr(run.n), run.scale, ptr(out), ptr(w), len(run.lens), run.Q, run.group * hkv, hkv,
+        d, bs, nb, run.table.shape[1], run.bound, 0 if run.dtype == "f32" else 1, ptr(workspace), workspace.numel() * 4, ptr(run.err), tile,
+        torch.cuda.current_stream().cuda_stream)
+    assert rc == pa.PA_OK
 
 
 @pytest.mark.parametrize("shape,lens", [
@@ -23,10 +35,10 @@ def test_weights_of_a_call_that_gave_up_are_this_calls_or_as_before(shape, lens)
     start = start_weights(run.cache)
     _, clean = run.weights(start)
     assert int(run.err.item()) == 0
-    need = rows.pa_decode_workspace_size_weights(len(lens), run.Q, run.group * run.hkv, run.D, run.bound)
+    need = pkg.pa_decode_workspace_size_weights(len(lens), run.Q, run.group * run.hkv, run.D, run.bound)
     ws = torch.ones((need + 3) // 4, device="cuda")    # states and scores of an earlier call, all usable
     w = torch.from_numpy(start).cuda()
-    rows.pa_test_withhold_tile_weights(run.dq, run.dk, run.dv, run.table, run.n, run.scale, run.out(), w, run.bound, 5, run.err, ws)
+    withhold(run, w, ws, 5)
     torch.cuda.synchronize()
     assert int(run.err.item()) == pa.PA_DEVERR_TIMEOUT
     got, left = w.cpu().numpy(), 0
