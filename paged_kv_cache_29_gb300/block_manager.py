@@ -134,6 +134,7 @@ class BlockManager:
         prompt = [int(t) for t in prompt]
         bs = self.block_size
         table: list[int] = []
+        fresh: list[int] = []
         hits = 0
         try:
             for start in range(0, len(prompt), bs):
@@ -150,9 +151,12 @@ class BlockManager:
                     table.append(found)
                 else:
                     block = self._allocate(chunk)
+                    fresh.append(block)
                     self._seal_if_full(block, parent, salt)
                     table.append(block)
         except OutOfBlocks:
+            for b in fresh:                # nothing will be written there: no prefix to find
+                self._forget_key(b)
             self._drop(table)
             raise
         self._tables[seq] = table
